@@ -78,6 +78,21 @@ def lib():
         L.gscan_backward_workspace_bytes.restype = ctypes.c_size_t
         L.gscan_forward_workspace_bytes.argtypes = [i64, i64, i64, i64, ctypes.c_int]
         L.gscan_forward_workspace_bytes.restype = ctypes.c_size_t
+        sz = ctypes.c_size_t
+        L.gscan_state_scan_forward.argtypes = [vp] * 9 + [sz, vp]
+        L.gscan_state_scan_forward.restype = ctypes.c_int
+        L.gscan_state_scan_backward.argtypes = [vp] * 14 + [sz, vp]
+        L.gscan_state_scan_backward.restype = ctypes.c_int
+        for f in (L.gscan_state_scan_forward_workspace_bytes,
+                  L.gscan_state_scan_backward_workspace_bytes, L.gscan_qk_norm_rope_workspace_bytes):
+            f.argtypes = [vp]
+            f.restype = sz
+        L.gscan_state_scan_step.argtypes = [vp] * 6 + [i64, vp, vp, vp]
+        L.gscan_state_scan_step.restype = ctypes.c_int
+        L.gscan_qk_norm_rope_forward.argtypes = [vp] * 10
+        L.gscan_qk_norm_rope_forward.restype = ctypes.c_int
+        L.gscan_qk_norm_rope_backward.argtypes = [vp] * 14 + [sz, vp]
+        L.gscan_qk_norm_rope_backward.restype = ctypes.c_int
         L.gscan_status_string.argtypes = [ctypes.c_int]
         L.gscan_status_string.restype = ctypes.c_char_p
         L.gscan_last_error.argtypes = []

@@ -12,6 +12,7 @@
 
 #include "gscan.h"
 #include "gscan_internal.h"
+#include "gscan_state.h"
 
 namespace {
 
@@ -197,6 +198,176 @@ int run_forward(const gscan::Plan &plan, const void *hh, const void *hs2, const 
     }
     if (e != hipSuccess)
         return fail(GSCAN_ERR_HIP, "forward launch failed: %s", hipGetErrorString(e));
+    return GSCAN_OK;
+}
+
+
+// ------------------------------------------- matrix-state scan, norm, rotation
+
+int esize(int dtype) { return dtype == GSCAN_BF16 ? 2 : 4; }
+
+bool known(int dtype) { return dtype == GSCAN_F32 || dtype == GSCAN_BF16; }
+
+bool strides16(const int64_t *s, int n, int dtype)
+{
+    for (int i = 0; i < n; ++i)
+        if (s[i] * esize(dtype) % 16 != 0) return false;
+    return true;
+}
+
+constexpr int64_t kMaxTokens = 2147483647 - 128;
+constexpr int64_t kMaxGrid = 2147483647;
+
+// Sizes, types and strides of a scan (and of a step, which is a scan of one
+// token each).
+int check_state_desc(const gscan_state_scan_t *d, bool backward, gscan::StateArgs *a)
+{
+    if (!d) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null descriptor");
+    if (!known(d->dtype) || !known(d->gate_dtype))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d / %d", (int)d->dtype,
+                    (int)d->gate_dtype);
+    if (d->gate_form != GSCAN_GATE_SIGMOID && d->gate_form != GSCAN_GATE_LOG)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown gate form %d", (int)d->gate_form);
+    if (d->B < 1 || d->T < 0 || d->H < 1 || d->Hk < 1 || d->Dk < 1 || d->Dv < 1)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT,
+                    "need B, H, Hk, Dk, Dv >= 1 and T >= 0 (B=%lld T=%lld H=%lld Hk=%lld Dk=%lld "
+                    "Dv=%lld)", (long long)d->B, (long long)d->T, (long long)d->H,
+                    (long long)d->Hk, (long long)d->Dk, (long long)d->Dv);
+    if (d->Dk % 8 || d->Dv % 8 || d->Dk > 128 || d->Dv > 128 || d->H % d->Hk || d->H > (1 << 20) ||
+        d->B > kMaxTokens || d->T > kMaxTokens)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "unsupported shape B=%lld T=%lld H=%lld Hk=%lld Dk=%lld Dv=%lld (need Dk and "
+                    "Dv multiples of 8 up to 128, Hk dividing H <= 2^20, B and T below 2^31 - 128)",
+                    (long long)d->B, (long long)d->T, (long long)d->H, (long long)d->Hk,
+                    (long long)d->Dk, (long long)d->Dv);
+    if (!strides16(d->q_stride, 3, d->dtype) || !strides16(d->k_stride, 3, d->dtype) ||
+        !strides16(d->v_stride, 3, d->dtype) ||
+        (backward && !strides16(d->d_out_stride, 3, d->dtype)))
+        return fail(GSCAN_ERR_MISALIGNED, "strides of q, k, v, d_out must be multiples of 16 bytes");
+    auto st = [](const int64_t *s) { return gscan::Strides{s[0], s[1], s[2]}; };
+    a->qs = st(d->q_stride);
+    a->ks = st(d->k_stride);
+    a->vs = st(d->v_stride);
+    a->gs = st(d->gate_stride);
+    if (backward) a->ds = st(d->d_out_stride);
+    a->off = d->seq_offsets;
+    a->B = d->B;
+    a->T = d->T;
+    a->H = (int)d->H;
+    a->Hk = (int)d->Hk;
+    a->Dk = (int)d->Dk;
+    a->Dv = (int)d->Dv;
+    a->dtype = d->dtype;
+    a->gate_dtype = d->gate_dtype;
+    a->gate_form = d->gate_form;
+    a->gate_shift = d->gate_shift;
+    a->scale = d->scale;
+    return GSCAN_OK;
+}
+
+// The decomposition, refused where a launch or an index would not fit.
+int state_plan(const gscan::StateArgs &a, gscan::StatePlan *p)
+{
+    const int64_t nc = a.T / 32 + 1;  // at least the chunks of a sequence
+    const int64_t slots = a.off ? nc + a.B : nc > kMaxGrid / a.B ? kMaxGrid : nc * a.B;
+    // eight workgroups at most per chunk and head in any launch
+    if (slots > kMaxGrid / 8 / a.H)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "too many chunks times heads (B=%lld T=%lld H=%d)",
+                    (long long)a.B, (long long)a.T, a.H);
+    *p = gscan::make_state_plan(a);
+    return GSCAN_OK;
+}
+
+bool mis(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+int check_state_inputs(const gscan::StateArgs &a)
+{
+    // without tokens there is nothing to read
+    if (a.T > 0 && (!a.q || !a.k || !a.v || !a.gate))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null q, k, v or gate");
+    if (mis(a.q, 16) || mis(a.k, 16) || mis(a.v, 16) || mis(a.s0, 16) ||
+        mis(a.gate, (uintptr_t)esize(a.gate_dtype)) || mis(a.off, 4))
+        return fail(GSCAN_ERR_MISALIGNED, "q, k, v and states must be 16-byte aligned, the gate "
+                    "and seq_offsets aligned to their elements");
+    return GSCAN_OK;
+}
+
+// Runs `go(workspace)` with the caller's workspace or stream-ordered memory.
+template <class F>
+int with_workspace(const char *what, void *ws, size_t ws_bytes, size_t need, hipStream_t stream, F go)
+{
+    if (need && ws) {
+        if (ws_bytes < need)
+            return fail(GSCAN_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < required %zu", ws_bytes,
+                        need);
+        if (mis(ws, 256)) return fail(GSCAN_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+    }
+    clear_stale_error();
+    void *own = nullptr;
+    if (need && !ws) {
+        hipError_t e = hipMallocAsync(&own, need, stream);
+        if (e != hipSuccess)
+            return fail(GSCAN_ERR_HIP, "%s workspace allocation (%zu bytes) failed: %s", what, need,
+                        hipGetErrorString(e));
+    }
+    hipError_t e = go(own ? own : ws);
+    if (own) {
+        hipError_t f = hipFreeAsync(own, stream);
+        if (e == hipSuccess) e = f;
+    }
+    if (e != hipSuccess) return fail(GSCAN_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
+    g_last_error[0] = '\0';
+    return GSCAN_OK;
+}
+
+int check_norm(const gscan_qk_norm_t *d, const void *q, const void *k, const float *wq,
+               const float *wk, const void *pos, const float *freq, gscan::NormArgs *a)
+{
+    if (!d) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null descriptor");
+    if (!known(d->dtype)) return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d", (int)d->dtype);
+    if (d->layout != GSCAN_ROTATE_HALF && d->layout != GSCAN_ROTATE_INTERLEAVED)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown rotation layout %d", (int)d->layout);
+    if (d->tokens < 0 || d->Hq < 1 || d->Hk < 0 || d->D < 1 || d->rot < 0 || !(d->eps > 0.f))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT,
+                    "need tokens, Hk, rot >= 0, Hq, D >= 1, eps > 0 (tokens=%lld Hq=%lld Hk=%lld "
+                    "D=%lld rot=%lld eps=%g)", (long long)d->tokens, (long long)d->Hq,
+                    (long long)d->Hk, (long long)d->D, (long long)d->rot, (double)d->eps);
+    if (d->D % 8 || d->D > 256 || d->rot % 8 || d->rot > d->D || d->Hq > (1 << 20) ||
+        d->Hk > (1 << 20) || d->tokens > kMaxTokens)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "unsupported shape tokens=%lld Hq=%lld Hk=%lld D=%lld rot=%lld (need D a "
+                    "multiple of 8 up to 256, rot a multiple of 8 up to D, at most 2^20 heads)",
+                    (long long)d->tokens, (long long)d->Hq, (long long)d->Hk, (long long)d->D,
+                    (long long)d->rot);
+    if (d->tokens > 0 && (!q || (d->Hk > 0 && !k)))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null q or k");
+    if (d->tokens > 0 && d->rot > 0 && (!pos || !freq))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null positions or freq");
+    if (mis(q, 16) || mis(k, 16) || mis(wq, 16) || mis(wk, 16) || mis(pos, d->pos_int64 ? 8 : 4) ||
+        mis(freq, 4) || !strides16(d->q_stride, 2, d->dtype) ||
+        (d->Hk > 0 && !strides16(d->k_stride, 2, d->dtype)))
+        return fail(GSCAN_ERR_MISALIGNED, "q, k, weights and the strides of q, k must be multiples of "
+                    "16 bytes, positions and freq aligned to their elements");
+    a->x[0] = q;
+    a->x[1] = k;
+    a->w[0] = wq;
+    a->w[1] = wk;
+    a->xn[0] = d->q_stride[0];
+    a->xh[0] = d->q_stride[1];
+    a->xn[1] = d->k_stride[0];
+    a->xh[1] = d->k_stride[1];
+    a->pos = pos;
+    a->pos64 = d->pos_int64;
+    a->freq = freq;
+    a->tokens = d->tokens;
+    a->heads[0] = (int)d->Hq;
+    a->heads[1] = (int)d->Hk;
+    a->D = (int)d->D;
+    a->rot = (int)d->rot;
+    a->layout = d->layout;
+    a->dtype = d->dtype;
+    a->eps = d->eps;
+    a->magnitude = d->magnitude;
     return GSCAN_OK;
 }
 
@@ -569,6 +740,204 @@ int gscan_batched_cifg_update(float *C_batch, const float *H, const float *X, co
         return fail(GSCAN_ERR_HIP, "CIFG update launch failed: %s", hipGetErrorString(e));
     g_last_error[0] = '\0';
     return GSCAN_OK;
+}
+
+int gscan_state_scan_forward(const gscan_state_scan_t *desc, const void *q, const void *k,
+                             const void *v, const void *gate, const float *initial_state,
+                             void *out, float *final_state, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream)
+{
+    gscan::StateArgs a;
+    gscan::StatePlan p;
+    int st = check_state_desc(desc, false, &a);
+    if (st != GSCAN_OK) return st;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.gate = gate;
+    a.s0 = initial_state;
+    a.out = out;
+    a.sT = final_state;
+    if ((st = check_state_inputs(a)) != GSCAN_OK) return st;
+    if (a.T > 0 && !out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null out");
+    if (mis(out, 16) || mis(final_state, 16))
+        return fail(GSCAN_ERR_MISALIGNED, "out and final_state must be 16-byte aligned");
+    if ((st = state_plan(a, &p)) != GSCAN_OK) return st;
+    if (a.T == 0 && !final_state) return GSCAN_OK;
+    return with_workspace("state scan forward", workspace, workspace_bytes, p.fwd_bytes, stream,
+                          [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_state_forward(p, a, stream);
+                          });
+}
+
+int gscan_state_scan_backward(const gscan_state_scan_t *desc, const void *q, const void *k,
+                              const void *v, const void *gate, const float *initial_state,
+                              const void *d_out, const float *d_final_state, void *dq, void *dk,
+                              void *dv, void *dgate, float *d_initial_state, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream)
+{
+    gscan::StateArgs a;
+    gscan::StatePlan p;
+    int st = check_state_desc(desc, true, &a);
+    if (st != GSCAN_OK) return st;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.gate = gate;
+    a.s0 = initial_state;
+    a.dout = d_out;
+    a.dsT = d_final_state;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dgate = dgate;
+    a.ds0 = d_initial_state;
+    if ((st = check_state_inputs(a)) != GSCAN_OK) return st;
+    if (a.T > 0 && (!d_out || !dq || !dk || !dv || !dgate))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null d_out or gradient pointer");
+    if (mis(d_out, 16) || mis(d_final_state, 16) || mis(dq, 16) || mis(dk, 16) || mis(dv, 16) ||
+        mis(dgate, (uintptr_t)esize(a.gate_dtype)) || mis(d_initial_state, 16))
+        return fail(GSCAN_ERR_MISALIGNED, "gradients must be 16-byte aligned, dgate to its elements");
+    if ((st = state_plan(a, &p)) != GSCAN_OK) return st;
+    if (a.T == 0 && !d_initial_state) return GSCAN_OK;
+    return with_workspace("state scan backward", workspace, workspace_bytes, p.bwd_bytes, stream,
+                          [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_state_backward(p, a, stream);
+                          });
+}
+
+size_t gscan_state_scan_forward_workspace_bytes(const gscan_state_scan_t *desc)
+{
+    gscan::StateArgs a;
+    gscan::StatePlan p;
+    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, &p) != GSCAN_OK) return 0;
+    return p.fwd_bytes;
+}
+
+size_t gscan_state_scan_backward_workspace_bytes(const gscan_state_scan_t *desc)
+{
+    gscan::StateArgs a;
+    gscan::StatePlan p;
+    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, &p) != GSCAN_OK) return 0;
+    return p.bwd_bytes;
+}
+
+int gscan_state_scan_step(const gscan_state_scan_t *desc, const void *q, const void *k,
+                          const void *v, const void *gate, float *state, int64_t pool,
+                          const int32_t *slots, void *out, hipStream_t stream)
+{
+    gscan::StateArgs a;
+    int st = check_state_desc(desc, false, &a);
+    if (st != GSCAN_OK) return st;
+    if (a.T != 1 || a.off)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "a step takes T = 1 and no seq_offsets (T=%lld)",
+                    (long long)a.T);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.gate = gate;
+    a.s0 = state;
+    if ((st = check_state_inputs(a)) != GSCAN_OK) return st;
+    if (!state || !out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null state or out");
+    if (mis(out, 16) || mis(slots, 4))
+        return fail(GSCAN_ERR_MISALIGNED, "out must be 16-byte aligned, slots to its elements");
+    if (pool < 1 || (!slots && a.B > pool))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "pool of %lld states for %lld requests",
+                    (long long)pool, (long long)a.B);
+    if (a.B > kMaxGrid / 8 / a.H)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "too many requests times heads (%lld x %d)",
+                    (long long)a.B, a.H);
+    gscan::StepArgs s;
+    s.q = q;
+    s.k = k;
+    s.v = v;
+    s.gate = gate;
+    s.qn = a.qs.b;
+    s.qh = a.qs.h;
+    s.kn = a.ks.b;
+    s.kh = a.ks.h;
+    s.vn = a.vs.b;
+    s.vh = a.vs.h;
+    s.gn = a.gs.b;
+    s.gh = a.gs.h;
+    s.state = state;
+    s.slots = slots;
+    s.out = out;
+    s.N = a.B;
+    s.pool = pool;
+    s.H = a.H;
+    s.Hk = a.Hk;
+    s.Dk = a.Dk;
+    s.Dv = a.Dv;
+    s.dtype = a.dtype;
+    s.gate_dtype = a.gate_dtype;
+    s.gate_form = a.gate_form;
+    s.gate_shift = a.gate_shift;
+    s.scale = a.scale;
+    return with_workspace("state scan step", nullptr, 0, 0, stream,
+                          [&](void *) { return gscan::launch_state_step(s, stream); });
+}
+
+int gscan_qk_norm_rope_forward(const gscan_qk_norm_t *desc, const void *q, const void *k,
+                               const float *weight_q, const float *weight_k,
+                               const void *positions, const float *freq, void *q_out, void *k_out,
+                               hipStream_t stream)
+{
+    gscan::NormArgs a;
+    int st = check_norm(desc, q, k, weight_q, weight_k, positions, freq, &a);
+    if (st != GSCAN_OK) return st;
+    if (a.tokens > 0 && (!q_out || (a.heads[1] > 0 && !k_out)))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null output");
+    if (mis(q_out, 16) || mis(k_out, 16))
+        return fail(GSCAN_ERR_MISALIGNED, "outputs must be 16-byte aligned");
+    a.y[0] = q_out;
+    a.y[1] = k_out;
+    return with_workspace("query/key norm", nullptr, 0, 0, stream,
+                          [&](void *) { return gscan::launch_norm_forward(a, stream); });
+}
+
+int gscan_qk_norm_rope_backward(const gscan_qk_norm_t *desc, const void *q, const void *k,
+                                const float *weight_q, const float *weight_k,
+                                const void *positions, const float *freq, const void *dy_q,
+                                const void *dy_k, void *dq, void *dk, float *d_weight_q,
+                                float *d_weight_k, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream)
+{
+    gscan::NormArgs a;
+    int st = check_norm(desc, q, k, weight_q, weight_k, positions, freq, &a);
+    if (st != GSCAN_OK) return st;
+    const bool keys = a.heads[1] > 0;
+    if (a.tokens > 0 && (!dy_q || !dq || (keys && (!dy_k || !dk))))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null gradient pointer");
+    if (mis(dy_q, 16) || mis(dy_k, 16) || mis(dq, 16) || mis(dk, 16) || mis(d_weight_q, 4) ||
+        mis(d_weight_k, 4) || !strides16(desc->dy_q_stride, 2, a.dtype) ||
+        (keys && !strides16(desc->dy_k_stride, 2, a.dtype)))
+        return fail(GSCAN_ERR_MISALIGNED, "gradients and their strides must be multiples of 16 bytes");
+    a.dy[0] = dy_q;
+    a.dy[1] = dy_k;
+    a.dn[0] = desc->dy_q_stride[0];
+    a.dh[0] = desc->dy_q_stride[1];
+    a.dn[1] = desc->dy_k_stride[0];
+    a.dh[1] = desc->dy_k_stride[1];
+    a.y[0] = dq;
+    a.y[1] = dk;
+    a.dw[0] = d_weight_q;
+    a.dw[1] = d_weight_k;
+    const bool weights = d_weight_q || d_weight_k;
+    const size_t need = weights ? gscan::norm_workspace_bytes(a.tokens, a.D) : 0;
+    return with_workspace("query/key norm backward", weights ? workspace : nullptr, workspace_bytes,
+                          need, stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_norm_backward(a, stream);
+                          });
+}
+
+size_t gscan_qk_norm_rope_workspace_bytes(const gscan_qk_norm_t *desc)
+{
+    if (!desc || desc->tokens < 0 || desc->D < 1 || desc->D > 256) return 0;
+    return gscan::norm_workspace_bytes(desc->tokens, (int)desc->D);
 }
 
 const char *gscan_status_string(int status)

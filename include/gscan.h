@@ -293,6 +293,155 @@ int gscan_backward_noalloc(const void *h_history, const void *h_s2,
 size_t gscan_backward_workspace_bytes(int64_t B, int64_t K, int64_t SH2, int64_t D,
                                       gscan_dtype_t in_dtype);
 
+/*
+ * ----------------------------------------------------------------------
+ * Matrix-state scan: the gated recurrence with a state per head, an output
+ * per token and sequences of any length.
+ *
+ *   g_t = sigmoid(gate_t + gate_shift)   (GSCAN_GATE_SIGMOID), or
+ *   g_t = exp(gate_t + gate_shift)       (GSCAN_GATE_LOG: log decays)
+ *   S_t = g_t S_{t-1} + k_t v_t^T        S [Dk][Dv], S_0 = initial state or 0
+ *   out_t = scale * S_t^T q_t
+ *
+ * for every sequence and every one of H heads.  q and k may have fewer heads
+ * (Hk, dividing H): head h uses q, k of head h / (H / Hk).
+ *
+ * Tokens.  Dense (seq_offsets NULL): B sequences of T tokens; element
+ * (b, t, h, i) of an operand is at b * stride[0] + t * stride[1] + h *
+ * stride[2] + i, in elements (the width is contiguous).  Packed: T is the
+ * number of tokens of all B sequences and sequence b holds the tokens
+ * seq_offsets[b] .. seq_offsets[b + 1] - 1 (device int32 [B + 1], starting
+ * at 0, not decreasing, ending at T; stride[0] is not used).  The offsets
+ * are not read on the host: values outside 0 .. T are taken as the nearest
+ * valid ones, so nothing is accessed out of range, but what the outputs hold
+ * is then unspecified.  Sequences may be empty; their final state is their
+ * initial one.
+ *
+ * Types.  q, k, v, d_out and the outputs out, dq, dk, dv have one type
+ * (GSCAN_F32 or GSCAN_BF16), the gate and dgate another (either).  States
+ * and their gradients are fp32 [B][H][Dk][Dv].  Outputs are dense row-major
+ * ([tokens][H][Dv], [tokens][Hk][Dk], [tokens][H]).
+ *
+ * Shapes: Dk and Dv multiples of 8 up to 128; H >= 1, Hk dividing H; B >= 1,
+ * T >= 0, T < 2^31 - 128.  q, k, v, d_out pointers, and their strides in
+ * bytes, are multiples of 16; states 16-byte aligned.
+ *
+ * Non-finite inputs propagate as in the recurrence: a token's NaN or Inf
+ * reaches the outputs of its own and later tokens of its sequence and head,
+ * not of earlier ones.  A gate of exactly zero (GSCAN_GATE_LOG: minus
+ * infinity) forgets the state.  Log gates below -1000 count as -1000.
+ *
+ * Accuracy.  Sums, gates and states are fp32 or better.  With bf16 operands
+ * the products inside a chunk of tokens and of the state with q (backward:
+ * with the upstream gradient, v and k) take bf16 roundings of the decayed
+ * scores and of the state; the state itself, the final state and the
+ * gradient of the initial state are accumulated to fp32 accuracy.  Results
+ * are bitwise reproducible.
+ */
+typedef enum {
+    GSCAN_GATE_SIGMOID = 0,
+    GSCAN_GATE_LOG = 1
+} gscan_gate_t;
+
+typedef struct {
+    int64_t B, T;
+    int64_t H, Hk, Dk, Dv;
+    const int32_t *seq_offsets;  /* device, or NULL: dense */
+    int64_t q_stride[3], k_stride[3], v_stride[3], gate_stride[3];  /* batch, token, head */
+    int64_t d_out_stride[3];     /* backward only */
+    gscan_dtype_t dtype, gate_dtype;
+    gscan_gate_t gate_form;
+    float gate_shift, scale;
+} gscan_state_scan_t;
+
+/* Writes out and, if not NULL, final_state.  initial_state may be NULL
+ * (zero); it may be the same array as final_state.  workspace: at least
+ * gscan_state_scan_forward_workspace_bytes() bytes, 256-byte aligned, or NULL
+ * to allocate stream-ordered (ignored where the query returns 0). */
+int gscan_state_scan_forward(const gscan_state_scan_t *desc, const void *q, const void *k,
+                             const void *v, const void *gate, const float *initial_state,
+                             void *out, float *final_state, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of L = sum(d_out * out) + sum(d_final_state * final_state); the
+ * forward is replayed from its inputs.  d_final_state may be NULL (zero),
+ * d_initial_state may be NULL (not written).  Gradients of q and k heads that
+ * several heads share are summed over those heads.  workspace: at least
+ * gscan_state_scan_backward_workspace_bytes(), 256-byte aligned, or NULL to
+ * allocate stream-ordered. */
+int gscan_state_scan_backward(const gscan_state_scan_t *desc, const void *q, const void *k,
+                              const void *v, const void *gate, const float *initial_state,
+                              const void *d_out, const float *d_final_state, void *dq, void *dk,
+                              void *dv, void *dgate, float *d_initial_state, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of the two calls (0 for an invalid descriptor). */
+size_t gscan_state_scan_forward_workspace_bytes(const gscan_state_scan_t *desc);
+size_t gscan_state_scan_backward_workspace_bytes(const gscan_state_scan_t *desc);
+
+/*
+ * One token for each of desc->B requests (serving): updates in place the
+ * states state[slots[n]] of a pool [pool][H][Dk][Dv] (fp32) and writes
+ * out[n] = scale * S^T q_n.  desc->T must be 1 and seq_offsets NULL; strides
+ * [0] (request) and [2] (head) are used.  slots: device int32 [B], or NULL
+ * (request n uses state n; then B <= pool).  A slot outside 0 .. pool - 1 is
+ * a padding entry: nothing is updated and its output is zero.  No slot may
+ * occur twice.  Arithmetic is fp32.
+ */
+int gscan_state_scan_step(const gscan_state_scan_t *desc, const void *q, const void *k,
+                          const void *v, const void *gate, float *state, int64_t pool,
+                          const int32_t *slots, void *out, hipStream_t stream);
+
+/*
+ * RMS norm of every query and key head and the rotation by position, in one
+ * pass: for each row x of D elements (one head of one token)
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: ones)
+ * and then the first `rot` elements of y are turned in pairs (a, b) by the
+ * angle pos * freq[i], i < rot / 2:
+ *   a' = magnitude (a cos - b sin),  b' = magnitude (b cos + a sin);
+ * GSCAN_ROTATE_HALF pairs elements i and i + rot / 2, GSCAN_ROTATE_INTERLEAVED
+ * 2i and 2i + 1.  rot may be 0 (norm only).  Angles are reduced in fp64.
+ * x: q [tokens][Hq][D] and k [tokens][Hk][D] with token and head strides (in
+ * elements), fp32 or bf16; weights and freq fp32; positions int32 or int64
+ * [tokens].  Outputs are dense, of the inputs' type.  Arithmetic is fp32.
+ * Shapes: D a multiple of 8 up to 256, rot a multiple of 8 up to D, Hq >= 1,
+ * Hk >= 0 (0: no keys, k pointers NULL), tokens >= 0, eps > 0.  x and
+ * gradient pointers and strides in bytes multiples of 16.
+ */
+typedef enum {
+    GSCAN_ROTATE_HALF = 0,
+    GSCAN_ROTATE_INTERLEAVED = 1
+} gscan_rotate_t;
+
+typedef struct {
+    int64_t tokens, Hq, Hk, D, rot;
+    int64_t q_stride[2], k_stride[2];    /* token, head */
+    int64_t dy_q_stride[2], dy_k_stride[2];  /* backward only */
+    gscan_dtype_t dtype;
+    gscan_rotate_t layout;
+    int pos_int64;                       /* positions are int64 (else int32) */
+    float eps, magnitude;
+} gscan_qk_norm_t;
+
+int gscan_qk_norm_rope_forward(const gscan_qk_norm_t *desc, const void *q, const void *k,
+                               const float *weight_q, const float *weight_k,
+                               const void *positions, const float *freq, void *q_out, void *k_out,
+                               hipStream_t stream);
+
+/* dx of both, and the weights' gradients summed over tokens and heads
+ * (d_weight_q, d_weight_k: fp32 [D], NULL: not wanted; overwritten).
+ * workspace: at least gscan_qk_norm_rope_workspace_bytes() bytes, 256-byte
+ * aligned, or NULL to allocate stream-ordered; used only where a weight
+ * gradient is wanted.  Bitwise reproducible. */
+int gscan_qk_norm_rope_backward(const gscan_qk_norm_t *desc, const void *q, const void *k,
+                                const float *weight_q, const float *weight_k,
+                                const void *positions, const float *freq, const void *dy_q,
+                                const void *dy_k, void *dq, void *dk, float *d_weight_q,
+                                float *d_weight_k, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+size_t gscan_qk_norm_rope_workspace_bytes(const gscan_qk_norm_t *desc);
+
 /* Static description of a status code. */
 const char *gscan_status_string(int status);
 
