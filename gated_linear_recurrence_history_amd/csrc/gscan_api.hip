@@ -266,7 +266,7 @@ int check_state_desc(const gscan_state_scan_t *d, bool backward, gscan::StateArg
 }
 
 // The decomposition, refused where a launch or an index would not fit.
-int state_plan(const gscan::StateArgs &a, gscan::StatePlan *p)
+int state_plan(const gscan::StateArgs &a, bool backward, gscan::StatePlan *p)
 {
     const int64_t nc = a.T / 32 + 1;  // at least the chunks of a sequence
     const int64_t slots = a.off ? nc + a.B : nc > kMaxGrid / a.B ? kMaxGrid : nc * a.B;
@@ -274,7 +274,7 @@ int state_plan(const gscan::StateArgs &a, gscan::StatePlan *p)
     if (slots > kMaxGrid / 8 / a.H)
         return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "too many chunks times heads (B=%lld T=%lld H=%d)",
                     (long long)a.B, (long long)a.T, a.H);
-    *p = gscan::make_state_plan(a);
+    *p = gscan::make_state_plan(a, backward);
     return GSCAN_OK;
 }
 
@@ -762,9 +762,9 @@ int gscan_state_scan_forward(const gscan_state_scan_t *desc, const void *q, cons
     if (a.T > 0 && !out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null out");
     if (mis(out, 16) || mis(final_state, 16))
         return fail(GSCAN_ERR_MISALIGNED, "out and final_state must be 16-byte aligned");
-    if ((st = state_plan(a, &p)) != GSCAN_OK) return st;
+    if ((st = state_plan(a, false, &p)) != GSCAN_OK) return st;
     if (a.T == 0 && !final_state) return GSCAN_OK;
-    return with_workspace("state scan forward", workspace, workspace_bytes, p.fwd_bytes, stream,
+    return with_workspace("state scan forward", workspace, workspace_bytes, p.bytes, stream,
                           [&](void *ws) {
                               a.ws = ws;
                               return gscan::launch_state_forward(p, a, stream);
@@ -799,9 +799,9 @@ int gscan_state_scan_backward(const gscan_state_scan_t *desc, const void *q, con
     if (mis(d_out, 16) || mis(d_final_state, 16) || mis(dq, 16) || mis(dk, 16) || mis(dv, 16) ||
         mis(dgate, (uintptr_t)esize(a.gate_dtype)) || mis(d_initial_state, 16))
         return fail(GSCAN_ERR_MISALIGNED, "gradients must be 16-byte aligned, dgate to its elements");
-    if ((st = state_plan(a, &p)) != GSCAN_OK) return st;
+    if ((st = state_plan(a, true, &p)) != GSCAN_OK) return st;
     if (a.T == 0 && !d_initial_state) return GSCAN_OK;
-    return with_workspace("state scan backward", workspace, workspace_bytes, p.bwd_bytes, stream,
+    return with_workspace("state scan backward", workspace, workspace_bytes, p.bytes, stream,
                           [&](void *ws) {
                               a.ws = ws;
                               return gscan::launch_state_backward(p, a, stream);
@@ -812,16 +812,16 @@ size_t gscan_state_scan_forward_workspace_bytes(const gscan_state_scan_t *desc)
 {
     gscan::StateArgs a;
     gscan::StatePlan p;
-    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, &p) != GSCAN_OK) return 0;
-    return p.fwd_bytes;
+    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, false, &p) != GSCAN_OK) return 0;
+    return p.bytes;
 }
 
 size_t gscan_state_scan_backward_workspace_bytes(const gscan_state_scan_t *desc)
 {
     gscan::StateArgs a;
     gscan::StatePlan p;
-    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, &p) != GSCAN_OK) return 0;
-    return p.bwd_bytes;
+    if (check_state_desc(desc, false, &a) != GSCAN_OK || state_plan(a, true, &p) != GSCAN_OK) return 0;
+    return p.bytes;
 }
 
 int gscan_state_scan_step(const gscan_state_scan_t *desc, const void *q, const void *k,

@@ -27,6 +27,7 @@ struct StateArgs {
     float *ds0 = nullptr;          // gradient of the initial state (null: not written)
     void *ws = nullptr;
     int64_t B = 0, T = 0;          // packed: T is the number of tokens of all sequences
+    int64_t chunks = 0;            // chunk slots there are (StatePlan)
     int H = 0, Hk = 0, Dk = 0, Dv = 0;
     int dtype = 0, gate_dtype = 0, gate_form = 0;
     float gate_shift = 0.f, scale = 1.f;
@@ -36,13 +37,17 @@ struct StateArgs {
 struct StatePlan {
     int chunk = 64;           // tokens per chunk: 64 (bf16) or 32 (fp32)
     int nk = 2, nv = 2;       // 32-wide units of the padded widths: 2 or 4
-    int64_t units = 0;        // sequences as walked by the scan
+    int64_t per = 0;          // tokens per unit (a sequence, or a part of one)
+    int64_t units = 0;        // units over all sequences (an upper bound when packed)
+    bool split = false;       // some sequence may have several units
+    size_t st_part = 0, st_dec = 0;  // workspace: what the units add to the state, their decays
+    size_t st_part_r = 0, st_dec_r = 0;  // backward: the same of the state's gradient
     int64_t chunks = 0;       // chunk slots over all sequences (an upper bound when packed)
     size_t st_kv = 0, st_gt = 0, st_g = 0;  // workspace offsets of the backward's chunk states
-    size_t fwd_bytes = 0, bwd_bytes = 0;
+    size_t bytes = 0;
 };
 
-StatePlan make_state_plan(const StateArgs &a);
+StatePlan make_state_plan(const StateArgs &a, bool backward);
 hipError_t launch_state_forward(const StatePlan &p, const StateArgs &a, hipStream_t stream);
 hipError_t launch_state_backward(const StatePlan &p, const StateArgs &a, hipStream_t stream);
 

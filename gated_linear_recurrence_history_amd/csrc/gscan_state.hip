@@ -37,6 +37,7 @@
 // split in three bf16 parts (24 bits), so a state carried over a long
 // sequence has fp32 accuracy.
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 
 #include "gscan_state_dev.h"
@@ -273,7 +274,7 @@ __device__ f4 other_terms(const S *m, int pm, const S *b, int pb, int r0, int co
 struct Unit {
     int64_t tok0;  // first token of the sequence in [tokens][H][..] outputs
     int64_t in0;   // the same where inputs have a batch stride: packed first token, else 0
-    int seq, part, len, slot0;
+    int seq, part, parts, len, slot0;
 };
 
 // Whether unit u exists.  Offsets are clamped to the tokens there are, so
@@ -288,6 +289,7 @@ __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t
         if (seq >= a.B) return false;
         w->seq = (int)seq;
         w->part = (int)(u - seq * n);
+        w->parts = (int)n;
         w->len = (int)a.T;
         w->slot0 = (int)(seq * nc);
         w->tok0 = seq * a.T;
@@ -322,8 +324,11 @@ __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t
             const int64_t seq = i0 + l;
             if (seq >= a.B) return false;
             w->seq = (int)seq;
-            w->part = (int)(u - (ub + __shfl(su, l) - __shfl(nu, l)));
+            w->parts = __shfl(nu, l);
+            w->part = (int)(u - (ub + __shfl(su, l) - w->parts));
             w->slot0 = (int)(cb + __shfl(sc, l) - __shfl(nc, l));
+            // offsets that overlap could ask for more chunks than there are
+            if (w->slot0 + __shfl(nc, l) > a.chunks) return false;
             const int start = __shfl((int)s, l);
             w->len = __shfl((int)(e - s), l);
             w->tok0 = w->in0 = start;
@@ -382,18 +387,21 @@ struct Stage {
     }
 };
 
-// Decays of one chunk, in LDS: L (as a sum of two floats, so that differences
-// of far-down values keep fp32 accuracy), e^L, e^(L_end - L), e^(L_end).
+// Decays of one chunk, in LDS: L in units of log 2 (as a sum of two floats,
+// so that differences of far-down values keep fp32 accuracy), e^L,
+// e^(L_end - L), e^(L_end).
 template <int C>
-struct Decay {
+struct __align__(16) Decay {
     float hi[C], lo[C], e[C], d[C], g;
 };
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // x: the gate argument of token `lane` (ok: there is one).  One wavefront.
 template <int C>
 __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane)
 {
-    double L = ok ? (double)log_gate(x, form) : 0.0;
+    double L = ok ? (double)log_gate(x, form) * 1.44269504088896340736 : 0.0;
 #pragma unroll
     for (int d = 1; d < C; d *= 2) {
         const double y = __shfl_up(L, d);
@@ -404,9 +412,9 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
         const float h = (float)L;
         s.hi[lane] = h;
         s.lo[lane] = (float)(L - (double)h);
-        s.e[lane] = expf(h);
-        s.d[lane] = expf((float)(end - L));
-        if (lane == C - 1) s.g = expf((float)end);
+        s.e[lane] = exp2_(h);
+        s.d[lane] = exp2_((float)(end - L));
+        if (lane == C - 1) s.g = exp2_((float)end);
     }
 }
 
@@ -414,76 +422,106 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
 template <int C>
 __device__ __forceinline__ float decay(const Decay<C> &s, int t, int u)
 {
-    return __expf((s.hi[t] - s.hi[u]) + (s.lo[t] - s.lo[u]));
+    return exp2_((s.hi[t] - s.hi[u]) + (s.lo[t] - s.lo[u]));
 }
 
 // --------------------------------------------------------------- forward
 
-// One workgroup walks a sequence's chunks for one head and 64 columns of its
+// One workgroup walks a unit's chunks for one head and 64 columns of its
 // state: wavefront w keeps columns 16w .. 16w+15 of every row in
 // accumulators, which are operands of Q S as they are; Q K^T is split over
 // the wavefronts by rows and passes through LDS.  The next chunk's rows are
-// requested while this one is computed.
+// requested while this one is computed, its decays are formed by the
+// wavefront that has least of Q K^T to do, and the outputs leave through LDS
+// in 16-byte pieces while the next chunk is staged.
 template <class T, int NK>
-__global__ void __launch_bounds__(kSThreads) gscan_state_fwd_kernel(StateArgs a, int slices)
+__global__ void __launch_bounds__(kSThreads)
+gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
     constexpr int C = T::C, RT = C / 16, CS = 4 / RT, KS = C / 32;
     constexpr int PK = NK * 32 + T::kPad, PV = kSlice + T::kPad, PP = C + T::kPad;
-    __shared__ __align__(16) S qt[C * PK], kt[C * PK], vt[C * PV], pt[C * PP];
-    __shared__ Decay<C> dc;
+    constexpr int GW = CS == 1 ? 0 : RT;  // the wavefront of the decays
+    __shared__ __align__(16) S qt[C * PK], kt[C * PK], vt[C * PV], pt[C * PP], ot[C * PV];
+    __shared__ Decay<C> dcs[2];
     __shared__ int bad[2];
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int slice = blockIdx.x % slices;
     const int h = blockIdx.x / slices % a.H;
+    const int64_t unit = blockIdx.x / slices / a.H;
     Unit un;
-    if (!find_unit(a, blockIdx.x / slices / a.H, INT32_MAX, C, lane, &un)) return;
+    if (!find_unit(a, unit, per, C, lane, &un)) return;
     const bool packed = a.off != nullptr;
     const int hk = h / (a.H / a.Hk), c0 = slice * kSlice, vcols = a.Dv - c0;
     const S *qp = rows_of<S>(a.q, a.qs, un, packed, hk), *kp = rows_of<S>(a.k, a.ks, un, packed, hk);
     const S *vp = rows_of<S>(a.v, a.vs, un, packed, h) + c0;
     const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
+    S *op = reinterpret_cast<S *>(a.out) + (un.tok0 * a.H + h) * a.Dv + c0;
+    const int64_t ost = (int64_t)a.H * a.Dv;
     const int col = w * 16 + l16;  // this lane's column of the slice
+    const int tb = (int)(un.part * per);
+    const int te = un.len - tb > per ? (int)(tb + per) : un.len;
 
     // the state: row 16i + 4g + j of column `col`
     const int64_t srow = ((int64_t)un.seq * a.H + h) * a.Dk;
+    const float *init = a.s0 ? a.s0 + srow * a.Dv : nullptr;
+    if (un.part)
+        init = reinterpret_cast<const float *>(reinterpret_cast<const char *>(a.ws) + st_part) +
+               (unit * a.H + h) * a.Dk * a.Dv;
     f4 st[2 * NK];
 #pragma unroll
     for (int i = 0; i < 2 * NK; ++i) {
         st[i] = zf4();
-        if (a.s0 && col < vcols)
+        if (init && col < vcols)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (16 * i + g4 + j < a.Dk)
-                    st[i][j] = a.s0[(srow + 16 * i + g4 + j) * a.Dv + c0 + col];
+                if (16 * i + g4 + j < a.Dk) st[i][j] = init[(16 * i + g4 + j) * a.Dv + c0 + col];
     }
 
     Stage<T, NK> sq, sk;
     Stage<T, 2> sv;
     float gx = 0.f;
     auto request = [&](int t0) {
-        sq.load(qp, a.qs.t, t0, un.len, a.Dk, tid);
-        sk.load(kp, a.ks.t, t0, un.len, a.Dk, tid);
-        sv.load(vp, a.vs.t, t0, un.len, vcols, tid);
-        if (w == 0 && lane < C && t0 + lane < un.len)
+        sq.load(qp, a.qs.t, t0, te, a.Dk, tid);
+        sk.load(kp, a.ks.t, t0, te, a.Dk, tid);
+        sv.load(vp, a.vs.t, t0, te, vcols, tid);
+    };
+    auto request_gate = [&](int t0) {
+        if (w == GW && lane < C && t0 + lane < te)
             gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
     };
+    // outputs of the chunk at t0, from LDS
+    auto flush = [&](int t0) {
+        constexpr int ppr = kSlice / T::VE;
+#pragma unroll
+        for (int i = 0; i < C * ppr / kSThreads; ++i) {
+            const int p = tid + kSThreads * i, row = p / ppr, cc = p % ppr * T::VE;
+            if (t0 + row < te && cc < vcols)
+                *reinterpret_cast<u4 *>(op + (t0 + row) * ost + cc) =
+                    *reinterpret_cast<const u4 *>(ot + row * PV + cc);
+        }
+    };
     if (tid < 2) bad[tid] = 0;
-    request(0);
+    request_gate(tb);
+    request(tb);
+    if (w == GW) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
+    request_gate(tb + C);
     __syncthreads();
 
-    for (int t0 = 0, odd = 0; t0 < un.len; t0 += C, odd ^= 1) {
+    int odd = 0;
+    for (int t0 = tb; t0 < te; t0 += C, odd ^= 1) {
+        const Decay<C> &dc = dcs[odd];
         sq.store(qt, PK, tid);
         sk.store(kt, PK, tid);
         sv.store(vt, PV, tid);
         if (sv.bad()) bad[odd] = 1;
-        if (w == 0) gate_scan<C>(dc, gx, t0 + lane < un.len, a.gate_form, lane);
+        if (t0 > tb) flush(t0 - C);
         __syncthreads();
         if (tid == 0) bad[odd ^ 1] = 0;
-        if (t0 + C < un.len) request(t0 + C);
+        if (t0 + C < te) request(t0 + C);
 
         // P . D, rows 16rt .. of wavefront (rt, ct % CS)
         {
@@ -503,15 +541,20 @@ __global__ void __launch_bounds__(kSThreads) gscan_state_fwd_kernel(StateArgs a,
                     narrow(t >= s ? x[j] * decay(dc, t, s) : 0.f, &pt[t * PP + s]);
                 }
             }
+            if (w == GW && t0 + C < te) {
+                gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
+                request_gate(t0 + 2 * C);
+            }
         }
         __syncthreads();
 
+        const bool slow = bad[odd] != 0;
         Frag vf[KS], pf[KS];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-            vf[kk] = pf[kk] = ld_col(vt, PV, 32 * kk, 16 * w, lane);
-            if (bad[odd]) pf[kk] = finite_part(pf[kk]);
-        }
+        for (int kk = 0; kk < KS; ++kk) vf[kk] = pf[kk] = ld_col(vt, PV, 32 * kk, 16 * w, lane);
+        if (slow)
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) pf[kk] = finite_part(pf[kk]);
         {
             f4 o[RT];
 #pragma unroll
@@ -530,16 +573,15 @@ __global__ void __launch_bounds__(kSThreads) gscan_state_fwd_kernel(StateArgs a,
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk)
                     if (2 * kk <= r) o[r] = mma(ld_row(pt, PP, 16 * r, 32 * kk, lane), pf[kk], o[r]);
-                if (bad[odd]) o[r] += other_terms<true, false>(pt, PP, vt, PV, 16 * r + g4, col, C);
-                if (col < vcols)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t = t0 + 16 * r + g4 + j;
-                        if (t < un.len)
-                            narrow(a.scale * o[r][j],
-                                   reinterpret_cast<S *>(a.out) + ((un.tok0 + t) * a.H + h) * a.Dv + c0 + col);
-                    }
             }
+            if (slow)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    o[r] += other_terms<true, false>(pt, PP, vt, PV, 16 * r + g4, col, C);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) narrow(a.scale * o[r][j], &ot[(16 * r + g4 + j) * PV + col]);
         }
         // S' = e^(L_end) S + K^T (e^(L_end - L) V)
         typename PartsOf<T>::type vs[KS];
@@ -564,8 +606,9 @@ __global__ void __launch_bounds__(kSThreads) gscan_state_fwd_kernel(StateArgs a,
         }
         __syncthreads();
     }
+    if (te > tb) flush(tb + (te - tb - 1) / C * C);
 
-    if (a.sT && col < vcols) {
+    if (a.sT && te == un.len && col < vcols) {
 #pragma unroll
         for (int i = 0; i < 2 * NK; ++i)
 #pragma unroll
@@ -577,25 +620,28 @@ __global__ void __launch_bounds__(kSThreads) gscan_state_fwd_kernel(StateArgs a,
 
 // ------------------------------------------------- backward: chunk states
 
-// The states before every chunk (REV false) or the gradients of the states
-// after every chunk (REV true) of one head, as operands: X rows, 64 columns
-// of Y; acc += X^T (decay . Y).  Column tile n and 32-row unit kk of chunk
-// slot c and head h are operand ((c H + h) 2NY + n) NX + kk of `dst`.
+// A walk over a unit's chunks that keeps the state (REV false) or the gradient
+// of the state (REV true) of one head: X rows, 64 columns of Y, acc += X^T
+// (decay . Y).  STORE: before every chunk (after it, REV) the accumulators are
+// left as operands: column tile n and 32-row unit kk of chunk slot c and head
+// h are operand ((c H + h) 2NY + n) NX + kk of `dst`.
 struct PassJob {
     const void *x, *y;
     Strides xs, ys;
-    int xh, yh;        // heads of x, y
-    int xd, yd;        // widths
-    const float *init; // [B][H][Dk][Dv] or null
-    float *fin;        // the state after the last chunk walked, or null
-    int64_t rstr, cstr;  // strides of a row and a column in init and fin
+    int xh, yh;          // heads of x, y
+    int xd, yd;          // widths
+    const float *init;   // the state to begin with, or null
+    float *fin;          // for the state at the end, or null
+    float *dec;          // for the product of the unit's gates, or null
+    int rstr, cstr;      // strides of a row and a column in init and fin
     void *dst;
-    float mul;         // factor of what is added
+    float mul;           // factor of what is added
 };
 
-template <class T, int NX, bool REV>
+template <class T, int NX, bool REV, bool STORE>
 __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb, int ny, int slice,
-                                          int h, const Unit &un, char *smem, Decay<T::C> &dc)
+                                          int h, const Unit &un, int tb, int te, char *smem,
+                                          Decay<T::C> (&dcs)[2])
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
@@ -608,7 +654,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     const S *xp = rows_of<S>(jb.x, jb.xs, un, packed, jb.xh);
     const S *yp = rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0;
     const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-    const int64_t sb = ((int64_t)un.seq * a.H + h) * a.Dk * a.Dv + (int64_t)(c0 + col) * jb.cstr;
+    const int sb = (c0 + col) * jb.cstr;
     f4 st[2 * NX];
 #pragma unroll
     for (int i = 0; i < 2 * NX; ++i) {
@@ -618,32 +664,46 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             for (int j = 0; j < 4; ++j)
                 if (16 * i + g4 + j < jb.xd) st[i][j] = jb.init[sb + (16 * i + g4 + j) * jb.rstr];
     }
-    const int nc = un.len > C ? (un.len + C - 1) / C : 1;
+    const int cb = tb / C, ce = te > tb ? (te + C - 1) / C : cb + 1;  // chunks
     Stage<T, NX> sx;
     Stage<T, 2> sy;
-    float gx = 0.f;
+    float gx = 0.f, gall = 1.f;
     auto request = [&](int c) {
-        sx.load(xp, jb.xs.t, c * C, un.len, jb.xd, tid);
-        sy.load(yp, jb.ys.t, c * C, un.len, ycols, tid);
-        if (w == 0 && lane < C && c * C + lane < un.len)
+        sx.load(xp, jb.xs.t, c * C, te, jb.xd, tid);
+        sy.load(yp, jb.ys.t, c * C, te, ycols, tid);
+    };
+    auto request_gate = [&](int c) {
+        if (w == 0 && lane < C && c >= cb && c * C + lane < te)
             gx = load_scalar(a.gate, g0 + (int64_t)(c * C + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
     };
-    request(REV ? nc - 1 : 0);
-    for (int n = 0; n < nc; ++n) {
-        const int c = REV ? nc - 1 - n : n;
-        // the operands of this chunk, before its own tokens enter
-#pragma unroll
-        for (int kk = 0; kk < NX; ++kk) {
-            Frag f;
-            to_frag(st[2 * kk], st[2 * kk + 1], &f);
-            put_frag(jb.dst, (((int64_t)(un.slot0 + c) * a.H + h) * 2 * ny + slice * 4 + w) * NX + kk,
-                     lane, f);
-        }
+    constexpr int step = REV ? -1 : 1;
+    int c = REV ? ce - 1 : cb;
+    request_gate(c);
+    request(c);
+    if (w == 0) gate_scan<C>(dcs[0], gx, c * C + lane < te, a.gate_form, lane);
+    request_gate(c + step);
+    int odd = 0;
+    for (int n = ce - cb; n > 0; --n, c += step, odd ^= 1) {
+        const Decay<C> &dc = dcs[odd];
         sx.store(xt, PX, tid);
         sy.store(yt, PY, tid);
-        if (w == 0) gate_scan<C>(dc, gx, c * C + lane < un.len, a.gate_form, lane);
+        if constexpr (STORE) {  // the operands of this chunk, before its own tokens enter
+#pragma unroll
+            for (int kk = 0; kk < NX; ++kk) {
+                Frag f;
+                to_frag(st[2 * kk], st[2 * kk + 1], &f);
+                put_frag(jb.dst, (((int64_t)(un.slot0 + c) * a.H + h) * 2 * ny + slice * 4 + w) * NX + kk,
+                         lane, f);
+            }
+        }
         __syncthreads();
-        if (n + 1 < nc) request(REV ? c - 1 : c + 1);
+        if (n > 1) {
+            request(c + step);
+            if (w == 0) {
+                gate_scan<C>(dcs[odd ^ 1], gx, (c + step) * C + lane < te, a.gate_form, lane);
+                request_gate(c + 2 * step);
+            }
+        }
         typename PartsOf<T>::type ys[KS];
         const float *m = REV ? dc.e : dc.d;
 #pragma unroll
@@ -658,6 +718,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             to_parts(x, y, &ys[kk]);
         }
         const float ge = dc.g;
+        gall *= ge;
 #pragma unroll
         for (int i = 0; i < 2 * NX; ++i) {
             st[i] *= ge;
@@ -674,37 +735,144 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             for (int j = 0; j < 4; ++j)
                 if (16 * i + g4 + j < jb.xd) jb.fin[sb + (16 * i + g4 + j) * jb.rstr] = st[i][j];
     }
+    if (jb.dec && slice == 0 && tid == 0) *jb.dec = gall;
 }
 
-// Three walks per sequence and head: the states as operands of dO S^T, and
-// the gradients of the states as operands of V dS^T and of K dS.
+template <class T, int NM>
+struct PassLds {
+    static constexpr size_t bytes = T::C * (NM * 32 + kSlice + 2 * T::kPad) * sizeof(typename T::S);
+};
+
+// Units of split sequences, by themselves: what a unit adds to the state after
+// it (REV: to the gradient of the state before it) and the product of its
+// gates.  fp32 [units][H][Dk][Dv] and [units][H] at st_part, st_dec.
+template <class T, int NK, bool REV>
+__global__ void __launch_bounds__(kSThreads)
+gscan_state_part_kernel(StateArgs a, int slices, int64_t per, size_t st_part, size_t st_dec)
+{
+    __shared__ __align__(16) char smem[PassLds<T, NK>::bytes];
+    __shared__ Decay<T::C> dcs[2];
+    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices;
+    const int h = blockIdx.x / slices % a.H, hk = h / (a.H / a.Hk);
+    const int64_t unit = blockIdx.x / slices / a.H;
+    Unit un;
+    if (!find_unit(a, unit, per, T::C, lane, &un)) return;
+    if (un.part == (REV ? 0 : un.parts - 1)) return;  // nothing comes after it
+    const int tb = (int)(un.part * per);
+    const int te = un.len - tb > per ? (int)(tb + per) : un.len;
+    char *ws = reinterpret_cast<char *>(a.ws);
+    float *fin = reinterpret_cast<float *>(ws + st_part) + (unit * a.H + h) * a.Dk * a.Dv;
+    float *dec = reinterpret_cast<float *>(ws + st_dec) + unit * a.H + h;
+    const PassJob jb = {REV ? a.q : a.k, REV ? a.dout : a.v, REV ? a.qs : a.ks, REV ? a.ds : a.vs, hk, h,
+                        a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr, REV ? a.scale : 1.f};
+    pass_walk<T, NK, REV, false>(a, jb, 0, slice, h, un, tb, te, smem, dcs);
+}
+
+// Joins the units of split sequences: in place, what each adds becomes the
+// state it begins with (REV: the gradient of the state it ends with).
+template <bool REV>
+__global__ void __launch_bounds__(kSThreads)
+gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
+{
+    const int n4 = a.Dk * a.Dv / 4, blocks = (n4 + kSThreads - 1) / kSThreads;
+    const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H;
+    const int seq = blockIdx.x / blocks / a.H;
+    int64_t u0 = 0;
+    int n;
+    if (!a.off) {
+        n = (int)((a.T + per - 1) / per);
+        u0 = (int64_t)seq * n;
+    } else {  // units of the sequences before it
+        int64_t sum = 0;
+        n = 1;
+        for (int i = threadIdx.x & 63; i <= seq; i += 64) {
+            int64_t s = a.off[i], e = a.off[i + 1];
+            s = s < 0 ? 0 : s > a.T ? a.T : s;
+            e = e < s ? s : e > a.T ? a.T : e;
+            const int nu = e - s > per ? (int)((e - s + per - 1) / per) : 1;
+            if (i < seq) sum += nu;
+            else n = nu;
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+        u0 = sum;
+        n = __shfl(n, seq & 63);
+    }
+    const int64_t units = a.off ? a.T / per + a.B : u0 + n;  // what the workspace holds
+    const int i4 = part * kSThreads + threadIdx.x;
+    if (n < 2 || i4 >= n4 || u0 + n > units) return;
+    char *ws = reinterpret_cast<char *>(a.ws);
+    f4 *p = reinterpret_cast<f4 *>(ws + st_part) + (u0 * a.H + h) * n4 + i4;
+    const float *dec = reinterpret_cast<const float *>(ws + st_dec) + u0 * a.H + h;
+    const int64_t ps = (int64_t)a.H * n4;
+    const float *from = REV ? a.dsT : a.s0;
+    f4 st = from ? reinterpret_cast<const f4 *>(from)[((int64_t)seq * a.H + h) * n4 + i4] : zf4();
+    constexpr int B = 8;  // units in flight
+    for (int b = 0; b < n; b += B) {
+        f4 x[B];
+        float g[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const int i = REV ? n - 1 - b - j : b + j;
+            if (b + j < n - 1) {
+                x[j] = p[i * ps];
+                g[j] = dec[(int64_t)i * a.H];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const int i = REV ? n - 1 - b - j : b + j;
+            if (b + j < n) {
+                p[i * ps] = st;
+                if (b + j < n - 1) st = g[j] * st + x[j];
+            }
+        }
+    }
+}
+
+// Three walks per unit and head that leave operands: the states for dO S^T,
+// and the gradients of the states for V dS^T and for K dS.
+struct PassWs {
+    size_t kv, gt, g;      // operands
+    size_t part_f, part_r; // units' states and gradients of states (split sequences)
+};
+
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kSThreads)
-gscan_state_pass_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
+gscan_state_pass_kernel(StateArgs a, int64_t tokens, PassWs o)
 {
-    typedef typename T::S S;
     constexpr int NM = NK > NV ? NK : NV;
-    __shared__ __align__(16) char smem[T::C * (NM * 32 + kSlice + 2 * T::kPad) * sizeof(S)];
-    __shared__ Decay<T::C> dc;
+    __shared__ __align__(16) char smem[PassLds<T, NM>::bytes];
+    __shared__ Decay<T::C> dcs[2];
     constexpr int ks = NK / 2, vs = NV / 2, per = 2 * ks + vs;
     const int lane = threadIdx.x & 63;
-    int j = blockIdx.x % per;
+    const int j = blockIdx.x % per;
     const int h = blockIdx.x / per % a.H, hk = h / (a.H / a.Hk);
+    const int64_t unit = blockIdx.x / per / a.H;
     Unit un;
-    if (!find_unit(a, blockIdx.x / per / a.H, INT32_MAX, T::C, lane, &un)) return;
+    if (!find_unit(a, unit, tokens, T::C, lane, &un)) return;
+    const int tb = (int)(un.part * tokens);
+    const int te = un.len - tb > tokens ? (int)(tb + tokens) : un.len;
     char *ws = reinterpret_cast<char *>(a.ws);
+    const int64_t one = (int64_t)a.Dk * a.Dv, mine = (unit * a.H + h) * one;
+    const int64_t whole = ((int64_t)un.seq * a.H + h) * one;
+    const float *s0 = un.part ? reinterpret_cast<const float *>(ws + o.part_f) + mine
+                              : a.s0 ? a.s0 + whole : nullptr;
+    const float *ds = un.part + 1 < un.parts ? reinterpret_cast<const float *>(ws + o.part_r) + mine
+                                             : a.dsT ? a.dsT + whole : nullptr;
     if (j < ks) {
-        const PassJob jb = {a.v, a.k, a.vs, a.ks, h, hk, a.Dv, a.Dk, a.s0, nullptr, 1, a.Dv,
-                            ws + st_kv, 1.f};
-        pass_walk<T, NV, false>(a, jb, NK, j, h, un, smem, dc);
+        const PassJob jb = {a.v, a.k, a.vs, a.ks, h, hk, a.Dv, a.Dk, s0, nullptr, nullptr, 1, a.Dv,
+                            ws + o.kv, 1.f};
+        pass_walk<T, NV, false, true>(a, jb, NK, j, h, un, tb, te, smem, dcs);
     } else if (j < 2 * ks) {
-        const PassJob jb = {a.dout, a.q, a.ds, a.qs, h, hk, a.Dv, a.Dk, a.dsT, nullptr, 1, a.Dv,
-                            ws + st_gt, a.scale};
-        pass_walk<T, NV, true>(a, jb, NK, j - ks, h, un, smem, dc);
+        const PassJob jb = {a.dout, a.q, a.ds, a.qs, h, hk, a.Dv, a.Dk, ds, nullptr, nullptr, 1, a.Dv,
+                            ws + o.gt, a.scale};
+        pass_walk<T, NV, true, true>(a, jb, NK, j - ks, h, un, tb, te, smem, dcs);
     } else {
-        const PassJob jb = {a.q, a.dout, a.qs, a.ds, hk, h, a.Dk, a.Dv, a.dsT, a.ds0, a.Dv, 1,
-                            ws + st_g, a.scale};
-        pass_walk<T, NK, true>(a, jb, NV, j - 2 * ks, h, un, smem, dc);
+        const PassJob jb = {a.q, a.dout, a.qs, a.ds, hk, h, a.Dk, a.Dv, ds,
+                            a.ds0 && un.part == 0 ? a.ds0 + whole : nullptr, nullptr, a.Dv, 1,
+                            ws + o.g, a.scale};
+        pass_walk<T, NK, true, true>(a, jb, NV, j - 2 * ks, h, un, tb, te, smem, dcs);
     }
 }
 
@@ -1017,22 +1185,47 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
     }
 }
 
+template <class T, int NK, bool REV>
+hipError_t part_launch(const StatePlan &p, const StateArgs &a, size_t st_part, size_t st_dec,
+                       hipStream_t st)
+{
+    const int slices = (a.Dv + kSlice - 1) / kSlice;
+    hipLaunchKernelGGL((gscan_state_part_kernel<T, NK, REV>), dim3((unsigned)(p.units * a.H * slices)),
+                       dim3(kSThreads), 0, st, a, slices, p.per, st_part, st_dec);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t blocks = (a.Dk * a.Dv / 4 + kSThreads - 1) / kSThreads;
+    hipLaunchKernelGGL((gscan_state_join_kernel<REV>), dim3((unsigned)(a.B * a.H * blocks)),
+                       dim3(kSThreads), 0, st, a, p.per, st_part, st_dec);
+    return hipGetLastError();
+}
+
 template <class T, int NK>
 hipError_t fwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
     const int slices = (a.Dv + kSlice - 1) / kSlice;
+    if (p.split) {
+        const hipError_t e = part_launch<T, NK, false>(p, a, p.st_part, p.st_dec, st);
+        if (e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL((gscan_state_fwd_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices)),
-                       dim3(kSThreads), 0, st, a, slices);
+                       dim3(kSThreads), 0, st, a, slices, p.per, p.st_part);
     return hipGetLastError();
 }
 
 template <class T, int NK, int NV>
 hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
+    hipError_t e;
+    if (p.split) {
+        e = part_launch<T, NK, false>(p, a, p.st_part, p.st_dec, st);
+        if (e == hipSuccess) e = part_launch<T, NK, true>(p, a, p.st_part_r, p.st_dec_r, st);
+        if (e != hipSuccess) return e;
+    }
+    const PassWs o = {p.st_kv, p.st_gt, p.st_g, p.st_part, p.st_part_r};
     hipLaunchKernelGGL((gscan_state_pass_kernel<T, NK, NV>),
-                       dim3((unsigned)(p.units * a.H * (NK + NV / 2))), dim3(kSThreads), 0, st, a,
-                       p.st_kv, p.st_gt, p.st_g);
-    hipError_t e = hipGetLastError();
+                       dim3((unsigned)(p.units * a.H * (NK + NV / 2))), dim3(kSThreads), 0, st, a, p.per, o);
+    e = hipGetLastError();
     if (e != hipSuccess || a.T == 0) return e;
     hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(p.chunks * a.Hk)),
                        dim3(kSThreads), 0, st, a, p.st_kv, p.st_gt, p.st_g);
@@ -1048,33 +1241,64 @@ hipError_t bwd_widths(const StatePlan &p, const StateArgs &a, hipStream_t st)
 
 }  // namespace
 
-StatePlan make_state_plan(const StateArgs &a)
+// Sequences are split into units of `per` tokens, walked in parallel, where
+// there are too few of them to fill the card.
+StatePlan make_state_plan(const StateArgs &a, bool backward)
 {
     StatePlan p;
     p.chunk = a.dtype ? BF::C : FP::C;
     p.nk = a.Dk <= 64 ? 2 : 4;
     p.nv = a.Dv <= 64 ? 2 : 4;
-    p.units = a.B;
     const int64_t nc = a.T > p.chunk ? (a.T + p.chunk - 1) / p.chunk : 1;
     // packed: sum over sequences of max(1, ceil(len / C)) <= T / C + B
     p.chunks = a.off ? a.T / p.chunk + a.B : a.B * nc;
-    const size_t one = (size_t)p.chunks * (size_t)a.H * (size_t)(p.nk * p.nv) * 1024u *
-                       (a.dtype ? 2u : 4u);
-    p.st_kv = 0;
-    p.st_gt = one;
-    p.st_g = 2 * one;
-    p.bwd_bytes = 3 * one;
+    const int64_t walks = (int64_t)a.H * (backward ? p.nk + p.nv / 2 : (a.Dv + kSlice - 1) / kSlice);
+    static const int64_t tgt = getenv("GS_TGT") ? atoi(getenv("GS_TGT")) : 768;
+    static const int64_t mn = getenv("GS_MIN") ? atoi(getenv("GS_MIN")) : 4;
+    int64_t pc = p.chunks * walks / tgt;
+    pc = pc < mn ? mn : pc;
+    p.split = pc < nc;
+    p.per = p.split ? pc * p.chunk : (nc > 1 ? nc : 1) * p.chunk;
+    p.units = !p.split ? a.B : a.off ? a.T / p.per + a.B : a.B * ((a.T + p.per - 1) / p.per);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t r = at;
+        at += (n + 255) / 256 * 256;
+        return r;
+    };
+    if (p.split) {
+        const size_t states = (size_t)p.units * (size_t)a.H * (size_t)a.Dk * (size_t)a.Dv * 4u;
+        const size_t decs = (size_t)p.units * (size_t)a.H * 4u;
+        p.st_part = take(states);
+        p.st_dec = take(decs);
+        if (backward) {
+            p.st_part_r = take(states);
+            p.st_dec_r = take(decs);
+        }
+    }
+    if (backward) {
+        const size_t one = (size_t)p.chunks * (size_t)a.H * (size_t)(p.nk * p.nv) * 1024u *
+                           (a.dtype ? 2u : 4u);
+        p.st_kv = take(one);
+        p.st_gt = take(one);
+        p.st_g = take(one);
+    }
+    p.bytes = at;
     return p;
 }
 
-hipError_t launch_state_forward(const StatePlan &p, const StateArgs &a, hipStream_t st)
+hipError_t launch_state_forward(const StatePlan &p, const StateArgs &args, hipStream_t st)
 {
+    StateArgs a = args;
+    a.chunks = p.chunks;
     if (a.dtype) return p.nk == 2 ? fwd_launch<BF, 2>(p, a, st) : fwd_launch<BF, 4>(p, a, st);
     return p.nk == 2 ? fwd_launch<FP, 2>(p, a, st) : fwd_launch<FP, 4>(p, a, st);
 }
 
-hipError_t launch_state_backward(const StatePlan &p, const StateArgs &a, hipStream_t st)
+hipError_t launch_state_backward(const StatePlan &p, const StateArgs &args, hipStream_t st)
 {
+    StateArgs a = args;
+    a.chunks = p.chunks;
     return a.dtype ? bwd_widths<BF>(p, a, st) : bwd_widths<FP>(p, a, st);
 }
 
