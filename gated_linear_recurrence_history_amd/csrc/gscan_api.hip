@@ -217,6 +217,8 @@ bool strides16(const int64_t *s, int n, int dtype)
 
 constexpr int64_t kMaxTokens = 2147483647 - 128;
 constexpr int64_t kMaxGrid = 2147483647;
+constexpr int64_t kMaxHeads = 16384;        // a chunk's outputs stay below 2 GiB
+constexpr int64_t kMaxStride = 1 << 23;     // and so do a chunk's rows of an operand
 
 // Sizes, types and strides of a scan (and of a step, which is a scan of one
 // token each).
@@ -233,17 +235,21 @@ int check_state_desc(const gscan_state_scan_t *d, bool backward, gscan::StateArg
                     "need B, H, Hk, Dk, Dv >= 1 and T >= 0 (B=%lld T=%lld H=%lld Hk=%lld Dk=%lld "
                     "Dv=%lld)", (long long)d->B, (long long)d->T, (long long)d->H,
                     (long long)d->Hk, (long long)d->Dk, (long long)d->Dv);
-    if (d->Dk % 8 || d->Dv % 8 || d->Dk > 128 || d->Dv > 128 || d->H % d->Hk || d->H > (1 << 20) ||
+    if (d->Dk % 8 || d->Dv % 8 || d->Dk > 128 || d->Dv > 128 || d->H % d->Hk || d->H > kMaxHeads ||
         d->B > kMaxTokens || d->T > kMaxTokens)
         return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
                     "unsupported shape B=%lld T=%lld H=%lld Hk=%lld Dk=%lld Dv=%lld (need Dk and "
-                    "Dv multiples of 8 up to 128, Hk dividing H <= 2^20, B and T below 2^31 - 128)",
+                    "Dv multiples of 8 up to 128, Hk dividing H <= 16384, B and T below 2^31 - 128)",
                     (long long)d->B, (long long)d->T, (long long)d->H, (long long)d->Hk,
                     (long long)d->Dk, (long long)d->Dv);
     if (!strides16(d->q_stride, 3, d->dtype) || !strides16(d->k_stride, 3, d->dtype) ||
         !strides16(d->v_stride, 3, d->dtype) ||
         (backward && !strides16(d->d_out_stride, 3, d->dtype)))
         return fail(GSCAN_ERR_MISALIGNED, "strides of q, k, v, d_out must be multiples of 16 bytes");
+    auto far = [](const int64_t *s) { return s[1] < 0 || s[1] >= kMaxStride; };
+    if (d->T > 1 && (far(d->q_stride) || far(d->k_stride) || far(d->v_stride) ||
+                     (backward && far(d->d_out_stride))))
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "token strides of q, k, v, d_out must be 0 .. 2^23 - 1");
     auto st = [](const int64_t *s) { return gscan::Strides{s[0], s[1], s[2]}; };
     a->qs = st(d->q_stride);
     a->ks = st(d->k_stride);

@@ -51,6 +51,10 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 constexpr int kSThreads = 256;
 constexpr int kSlice = 64;  // columns of a state that one workgroup walks
 
+// Loads are not moved across this: without it the unrolled steps of a chunk
+// are all loaded at its beginning, for more registers than there are.
+#define GSCAN_STEP() asm volatile("" ::: "memory")
+
 __device__ __forceinline__ f4 zf4() { return f4{0.f, 0.f, 0.f, 0.f}; }
 __device__ __forceinline__ u4 zu4() { return u4{0u, 0u, 0u, 0u}; }
 
@@ -59,14 +63,14 @@ __device__ __forceinline__ u4 zu4() { return u4{0u, 0u, 0u, 0u}; }
 struct BF {
     typedef uint16_t S;   // storage
     typedef u4 Frag;      // eight bf16
-    static constexpr int kDtype = 1, C = 64, VE = 8, kPad = 8;
+    static constexpr int C = 64, VE = 8;  // tokens per chunk, elements of 16 bytes
 };
 struct FP {
     typedef float S;
     struct Frag {
         f4 a, b;
     };
-    static constexpr int kDtype = 0, C = 32, VE = 4, kPad = 4;
+    static constexpr int C = 32, VE = 4;
 };
 
 __device__ __forceinline__ f4 mma(const u4 &a, const u4 &b, f4 c)
@@ -84,47 +88,139 @@ __device__ __forceinline__ f4 mma(const FP::Frag &a, const FP::Frag &b, f4 c)
     return c;
 }
 
-// Row r0 + l%16 of a row-major tile, elements k0 + {4g.., 16+4g..}.
-__device__ __forceinline__ u4 ld_row(const uint16_t *t, int pitch, int r0, int k0, int lane)
-{
-    const uint16_t *p = t + (r0 + (lane & 15)) * pitch + k0 + 4 * (lane >> 4);
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    const uint2 y = *reinterpret_cast<const uint2 *>(p + 16);
-    return u4{x.x, x.y, y.x, y.y};
-}
-__device__ __forceinline__ FP::Frag ld_row(const float *t, int pitch, int r0, int k0, int lane)
-{
-    const float *p = t + (r0 + (lane & 15)) * pitch + k0 + 4 * (lane >> 4);
-    return FP::Frag{*reinterpret_cast<const f4 *>(p), *reinterpret_cast<const f4 *>(p + 16)};
-}
+// Tiles in LDS: rows of 64 or 128 elements (W), `bytes` a row apart.  bf16 rows
+// are not padded; the 8-byte pieces of each 128 bytes of row r are exchanged
+// by XOR with ((r & 3) << 2) | ((r >> 2) & 3), which puts the sixteen rows a
+// read along rows touches, and the four rows times four pieces a transposed
+// read touches, on different banks (32 of 4 bytes).  fp32 rows are 16 bytes
+// longer than their elements, which does the same for both reads.
+//
+// Per lane: byte offsets of the pieces it reads along a row (r[c]: elements
+// 16c + 4g of row l % 16) and down a column (c[i]: column 16i + l % 16 of rows
+// 4g ..); what a read adds to them is known at compile time.
+template <class T, int W>
+struct Tile;
 
-// Column c0 + l%16, elements of rows k0 + {4g.., 16+4g..}.  The transposed
-// read gives lane i of a 16-lane group element i%4 of the 8-byte pieces that
-// lanes 4j + i/4 address, j = 0..3: with lane p addressing row 4g + p/4,
-// columns 4(p%4).., it receives column p of rows 4g .. 4g+3.
-__device__ __forceinline__ uint2 read_tr(const uint16_t *p)
-{
-    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s4v *)(p)));
-}
-__device__ __forceinline__ u4 ld_col(const uint16_t *t, int pitch, int k0, int c0, int lane)
-{
-    const int p = lane & 15;
-    const uint16_t *a = t + (k0 + 4 * (lane >> 4) + (p >> 2)) * pitch + c0 + 4 * (p & 3);
-    const uint2 x = read_tr(a), y = read_tr(a + 16 * pitch);
-    return u4{x.x, x.y, y.x, y.y};
-}
-__device__ __forceinline__ FP::Frag ld_col(const float *t, int pitch, int k0, int c0, int lane)
-{
-    const float *a = t + (k0 + 4 * (lane >> 4)) * pitch + c0 + (lane & 15);
-    FP::Frag f;
+template <int W>
+struct Tile<BF, W> {
+    static constexpr int bytes = W * 2;
+    uint32_t r[4], c[4];
+    __device__ __forceinline__ explicit Tile(int lane)
+    {
+        const uint32_t l16 = lane & 15, g = lane >> 4, p4 = l16 >> 2;
+        const uint32_t fr = ((l16 & 3) << 2) | p4, fc = (p4 << 2) | g;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f.a[j] = a[j * pitch];
-        f.b[j] = a[(16 + j) * pitch];
+        for (uint32_t i = 0; i < 4; ++i) {
+            r[i] = l16 * bytes + ((g ^ (4 * i) ^ fr) << 3);
+            c[i] = (4 * g + p4) * bytes + (((l16 & 3) ^ (4 * i) ^ fc) << 3);
+        }
     }
-    return f;
-}
+    // byte offset of an 8-byte piece (four elements)
+    static __device__ __forceinline__ uint32_t piece(uint32_t row, uint32_t col)
+    {
+        const uint32_t f = ((row & 3) << 2) | ((row >> 2) & 3), p = col / 4;
+        return row * bytes + (p >> 4) * 128 + (((p & 15) ^ f) << 3);
+    }
+    static __device__ __forceinline__ void put(char *t, uint32_t row, uint32_t col, const u4 &x)
+    {
+        const uint32_t at = piece(row, col);
+        *reinterpret_cast<uint2 *>(t + at) = uint2{x[0], x[1]};
+        *reinterpret_cast<uint2 *>(t + (at ^ 8)) = uint2{x[2], x[3]};
+    }
+    // elements 16c + 4g .. +3 of row r0 + l % 16
+    __device__ __forceinline__ uint2 quad_bits(const char *t, int r0, int cc) const
+    {
+        return *reinterpret_cast<const uint2 *>(t + r[cc & 3] + (r0 * bytes + (cc >> 2) * 128));
+    }
+    __device__ __forceinline__ f4 quad(const char *t, int r0, int cc) const
+    {
+        const uint2 x = quad_bits(t, r0, cc);
+        return f4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
+    }
+    // row r0 + l%16, elements 32kk + {4g.., 16 + 4g..}
+    __device__ __forceinline__ u4 row(const char *t, int r0, int kk) const
+    {
+        const uint2 x = quad_bits(t, r0, 2 * kk), y = quad_bits(t, r0, 2 * kk + 1);
+        return u4{x.x, x.y, y.x, y.y};
+    }
+    // column 16i + l%16 of rows k0 + {4g.., 16 + 4g..}.  The transposed read
+    // gives lane i of a 16-lane group element i % 4 of the 8-byte pieces that
+    // lanes 4j + i/4 address, j = 0..3: with lane p addressing row 4g + p/4,
+    // columns 4 (p % 4).., it receives column p of rows 4g .. 4g+3.
+    __device__ __forceinline__ u4 at_col(const char *t, int k0, uint32_t off) const
+    {
+        const char *p = t + off + k0 * bytes;
+        const uint2 x = tr(p), y = tr(p + 16 * bytes);
+        return u4{x.x, x.y, y.x, y.y};
+    }
+    __device__ __forceinline__ u4 col(const char *t, int k0, int i) const
+    {
+        return at_col(t + (i >> 2) * 128, k0, c[i & 3]);
+    }
+    // the offset of a column tile known at run time only
+    __device__ __forceinline__ uint32_t col_off(int i) const
+    {
+        return (c[0] ^ ((i & 3) << 5)) + (i >> 2) * 128;
+    }
+    static __device__ __forceinline__ uint2 tr(const char *p)
+    {
+        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                             (__attribute__((address_space(3))) s4v *)(p)));
+    }
+    // replaces an infinity or NaN by zero
+    static __device__ __forceinline__ bool scrub(char *t, int row, int col)
+    {
+        uint16_t *x = reinterpret_cast<uint16_t *>(t + piece(row, col)) + (col & 3);
+        if ((*x & 0x7f80u) != 0x7f80u) return false;
+        *x = 0;
+        return true;
+    }
+};
+
+template <int W>
+struct Tile<FP, W> {
+    static constexpr int bytes = W * 4 + 16;
+    uint32_t r, c;
+    __device__ __forceinline__ explicit Tile(int lane)
+        : r((lane & 15) * bytes + (lane >> 4) * 16), c((lane >> 4) * 4 * bytes + (lane & 15) * 4)
+    {
+    }
+    static __device__ __forceinline__ void put(char *t, uint32_t row, uint32_t col, const u4 &x)
+    {
+        *reinterpret_cast<u4 *>(t + row * bytes + col * 4) = x;
+    }
+    __device__ __forceinline__ f4 quad(const char *t, int r0, int cc) const
+    {
+        return *reinterpret_cast<const f4 *>(t + r + (r0 * bytes + cc * 64));
+    }
+    __device__ __forceinline__ FP::Frag row(const char *t, int r0, int kk) const
+    {
+        return FP::Frag{quad(t, r0, 2 * kk), quad(t, r0, 2 * kk + 1)};
+    }
+    __device__ __forceinline__ FP::Frag at_col(const char *t, int k0, uint32_t off) const
+    {
+        const char *p = t + off + k0 * bytes;
+        FP::Frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.a[j] = *reinterpret_cast<const float *>(p + j * bytes);
+            f.b[j] = *reinterpret_cast<const float *>(p + (16 + j) * bytes);
+        }
+        return f;
+    }
+    __device__ __forceinline__ FP::Frag col(const char *t, int k0, int i) const
+    {
+        return at_col(t + i * 64, k0, c);
+    }
+    __device__ __forceinline__ uint32_t col_off(int i) const { return c + i * 64; }
+    static __device__ __forceinline__ bool scrub(char *t, int row, int col)
+    {
+        float *x = reinterpret_cast<float *>(t + row * bytes + col * 4);
+        if (isfinite(*x)) return false;
+        *x = 0.f;
+        return true;
+    }
+};
 
 // Two accumulators (rows 0..15 and 16..31 of a column) as an operand.
 __device__ __forceinline__ void to_frag(f4 x, f4 y, u4 *f)
@@ -146,21 +242,31 @@ __device__ __forceinline__ void from_frag(const FP::Frag &f, f4 *x, f4 *y)
 }
 
 // acc + A (x | y) with every bit of the fp32 values x, y: three bf16 parts,
-// each the rounding of what the parts before it leave (the differences are
-// exact in fp32).
+// each the rounding of what the parts before it leave.  The remainder of a
+// pair is -1 * part + 0 * (the other half) + x, one bf16 dot product per
+// element: the products and the difference are exact.  The selectors are
+// scalars, as an inline constant would be taken for fp32 -1.0.
 struct Parts {
     u4 p[3];
 };
 __device__ __forceinline__ void to_parts(f4 x, f4 y, Parts *s)
 {
+    uint32_t m0 = 0x0000bf80u, m1 = 0xbf800000u;
+    asm("" : "+s"(m0), "+s"(m1));
+    const bf16x2 lo = __builtin_bit_cast(bf16x2, m0), hi = __builtin_bit_cast(bf16x2, m1);
+    float r[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        to_frag(x, y, &s->p[i]);
-        f4 hx, hy;
-        from_frag(s->p[i], &hx, &hy);
-        x -= hx;
-        y -= hy;
-    }
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t h = pack_bf16(r[2 * j], r[2 * j + 1]);
+            s->p[i][j] = h;
+            if (i < 2) {
+                const bf16x2 hv = __builtin_bit_cast(bf16x2, h);
+                r[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(hv, lo, r[2 * j], false);
+                r[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(hv, hi, r[2 * j + 1], false);
+            }
+        }
 }
 __device__ __forceinline__ void to_parts(f4 x, f4 y, FP::Frag *s) { *s = FP::Frag{x, y}; }
 __device__ __forceinline__ f4 mma_parts(const u4 &a, const Parts &b, f4 c)
@@ -179,11 +285,6 @@ template <>
 struct PartsOf<FP> {
     typedef FP::Frag type;
 };
-
-__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ void narrow(float x, uint16_t *p) { *p = to_bf16(x); }
-__device__ __forceinline__ void narrow(float x, float *p) { *p = x; }
 
 // Operands kept in device memory: 16 bytes (bf16) or two planes of 16 bytes
 // (fp32) per lane.
@@ -206,63 +307,58 @@ __device__ __forceinline__ void get_frag(const void *base, int64_t i, int lane, 
     f->b = reinterpret_cast<const f4 *>(base)[i * 128 + 64 + lane];
 }
 
-// An infinity or NaN in sixteen bytes.
-__device__ __forceinline__ bool nonfinite(const u4 &x, const BF &)
+// Whether sixteen bytes hold an infinity or NaN: the largest magnitude's bits.
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void magnitude(const u4 &x, const BF &, uint32_t *m)
 {
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        bad |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+        *m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+                 __builtin_bit_cast(us2, *m), __builtin_bit_cast(us2, x[i] & 0x7fff7fffu)));
 }
-__device__ __forceinline__ bool nonfinite(const u4 &x, const FP &)
+__device__ __forceinline__ bool nonfinite(uint32_t m, const BF &)
 {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (x[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+    return (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u;
 }
-
-// A masked product (entries of m where k > r, or k < r, are zero) must not
-// carry an infinity or NaN of b's row k to the rows r that the mask keeps
-// from it, as 0 * b would.  Chunks that hold one take the product of b's
-// finite elements (the others as zeros, which leaves the other rows' bits
-// as they are) and then add the terms left out one by one.
-__device__ __forceinline__ u4 finite_part(u4 f)
+__device__ __forceinline__ void magnitude(const u4 &x, const FP &, uint32_t *m)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if ((f[i] & 0x7f80u) == 0x7f80u) f[i] &= 0xffff0000u;
-        if ((f[i] & 0x7f800000u) == 0x7f800000u) f[i] &= 0xffffu;
+        const uint32_t y = x[i] & 0x7fffffffu;
+        *m = y > *m ? y : *m;
     }
-    return f;
 }
-__device__ __forceinline__ FP::Frag finite_part(FP::Frag f)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (!isfinite(f.a[i])) f.a[i] = 0.f;
-        if (!isfinite(f.b[i])) f.b[i] = 0.f;
-    }
-    return f;
-}
+__device__ __forceinline__ bool nonfinite(uint32_t m, const FP &) { return m >= 0x7f800000u; }
 
-// The terms left out, for rows r0 .. r0+3 and column col: sum over the k of
-// non-finite b[k][col] with k <= r (LOWER) or k >= r of m[r][k] (TRANS:
-// m[k][r]) times it.
-template <bool LOWER, bool TRANS, class S>
-__device__ f4 other_terms(const S *m, int pm, const S *b, int pb, int r0, int col, int C)
+// ------------------------------------------------------------ device memory
+
+// A buffer of the 2 GiB from p: offsets of -1 read as zero and write nothing,
+// so rows past a sequence's end and columns past a width cost no branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p)
 {
-    f4 x = zf4();
-    for (int k = 0; k < C; ++k) {
-        const float v = widen(b[k * pb + col]);
-        if (isfinite(v)) continue;
-        for (int j = 0; j < 4; ++j) {
-            const int r = r0 + j;
-            if (LOWER ? k <= r : k >= r) x[j] += widen(TRANS ? m[k * pm + r] : m[r * pm + k]) * v;
-        }
-    }
-    return x;
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), 0, 0x80000000, 0x00027000);
+}
+constexpr uint32_t kNowhere = 0xffffffffu;
+
+// Four consecutive elements.
+__device__ __forceinline__ void put4(uint16_t *p, f4 x)
+{
+    *reinterpret_cast<uint2 *>(p) = uint2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+}
+__device__ __forceinline__ void put4(float *p, f4 x) { *reinterpret_cast<f4 *>(p) = x; }
+
+// The same at byte offset `at` of a buffer.
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t b, uint32_t at, f4 x, const BF &)
+{
+    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(u2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, b, at, 0, 0);
+}
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t b, uint32_t at, f4 x, const FP &)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), b, at, 0, 0);
 }
 
 // ------------------------------------------------------ sequences and units
@@ -355,99 +451,200 @@ __device__ __forceinline__ const S *rows_of(const void *p, const Strides &s, con
 template <class T, int NKU>
 struct Stage {
     u4 r[NKU];
+    uint32_t off[NKU];  // of the pieces from the chunk's first row
+    const typename T::S *base;  // that row
     static constexpr int kPpr = NKU * 32 / T::VE;  // pieces per row
 
-    // rows t0 .. of `base` (stride st), those before `len` and columns before
-    // `cols`; zero elsewhere
-    __device__ __forceinline__ void load(const typename T::S *base, int64_t st, int t0, int len,
-                                         int cols, int tid)
+    // row 0 of the tile is row t0 of `rows` (stride st, below 2^23); columns
+    // before `cols` are read, the others are zero
+    __device__ __forceinline__ void begin(const typename T::S *rows, int64_t st, int64_t t0, int cols,
+                                          int tid)
+    {
+        base = rows + t0 * st;
+#pragma unroll
+        for (int i = 0; i < NKU; ++i) {
+            const int q = tid + kSThreads * i, row = q / kPpr, col = q % kPpr * T::VE;
+            off[i] = col < cols ? (uint32_t)(row * (int)st + col) * (uint32_t)sizeof(typename T::S) : kNowhere;
+        }
+    }
+    // the first `left` rows of the tile (the others zero), and on by `step`
+    // elements to the next
+    __device__ __forceinline__ void load(int left, int64_t step, int tid)
+    {
+        const __amdgpu_buffer_rsrc_t b = buffer(base);
+#pragma unroll
+        for (int i = 0; i < NKU; ++i) {
+            const int row = (tid + kSThreads * i) / kPpr;
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, row < left ? off[i] : kNowhere, 0, 0);
+        }
+        base += step;
+    }
+    template <class TL>
+    __device__ __forceinline__ void store(char *tile, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < NKU; ++i) {
-            const int p = tid + kSThreads * i, row = p / kPpr, col = p % kPpr * T::VE;
-            r[i] = t0 + row < len && col < cols
-                       ? *reinterpret_cast<const u4 *>(base + (int64_t)(t0 + row) * st + col)
-                       : zu4();
+            const int q = tid + kSThreads * i;
+            TL::put(tile, q / kPpr, q % kPpr * T::VE, r[i]);
         }
     }
-    __device__ __forceinline__ void store(typename T::S *tile, int pitch, int tid) const
+    // Infinities and NaN of the stored tile become zero, and `found(row, column)`
+    // is called for each.  A product with scores that are zero above the
+    // diagonal would carry them to tokens they do not reach, as 0 * inf.  What
+    // they do reach is not finite in any case (the whole column of the state
+    // from that token on), so those results become NaN without being computed.
+    template <class TL, class F>
+    __device__ __forceinline__ void scrub(char *tile, int tid, F found) const
     {
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < NKU; ++i) {
-            const int p = tid + kSThreads * i;
-            *reinterpret_cast<u4 *>(tile + p / kPpr * pitch + p % kPpr * T::VE) = r[i];
+        for (int i = 0; i < NKU; ++i) magnitude(r[i], T(), &m);
+        if (!nonfinite(m, T())) return;
+#pragma unroll 1
+        for (int i = 0; i < NKU * T::VE; ++i) {
+            const int q = tid + kSThreads * (i / T::VE), row = q / kPpr, col = q % kPpr * T::VE + i % T::VE;
+            if (TL::scrub(tile, row, col)) found(row, col);
         }
-    }
-    __device__ __forceinline__ bool bad() const
-    {
-        bool b = false;
-#pragma unroll
-        for (int i = 0; i < NKU; ++i) b |= nonfinite(r[i], T());
-        return b;
     }
 };
 
-// Decays of one chunk, in LDS: L in units of log 2 (as a sum of two floats,
+// Four columns of a row, NaN where one of `where` reaches it (from that row on,
+// LAST: up to it), or everywhere (all).
+template <bool LAST>
+__device__ __forceinline__ f4 poison(f4 x, const int *where, int row, bool all = false)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (all || (LAST ? row <= where[j] : row >= where[j])) x[j] = __builtin_nanf("");
+    return x;
+}
+
+// Decays of one chunk, in LDS.  L in units of log 2 (as a sum of two floats,
 // so that differences of far-down values keep fp32 accuracy), e^L,
-// e^(L_end - L), e^(L_end).
+// e^(L_end - L), e^(L_end); and for tiles of 16 x 16 tokens below the
+// diagonal the two factors of e^(L_t - L_s) around the last token m of s's
+// tile, e^(L_m - L_s) and e^(L_t - L_m), neither above what the gates allow.
 template <int C>
 struct __align__(16) Decay {
-    float hi[C], lo[C], e[C], d[C], g;
+    float hi[C], lo[C], e[C], d[C], col[C], row[C / 16 - 1][C], g;
 };
 
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+// x of other lanes, zero where there is none: CTRL 0x110 + n, n lanes below in
+// the group of 16; 0x142 and 0x143, the last lane of the group (of the half)
+// before, taken by the groups of row mask RM.
+template <int CTRL, int RM = 0xf>
+__device__ __forceinline__ float dpp(float x)
+{
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, RM, 0xf, false));
+}
+template <int CTRL, int RM = 0xf>
+__device__ __forceinline__ double dpp(double x)
+{
+    const uint2 u = __builtin_bit_cast(uint2, x);
+    return __builtin_bit_cast(double, uint2{__builtin_amdgcn_update_dpp(0u, u.x, CTRL, RM, 0xf, false),
+                                            __builtin_amdgcn_update_dpp(0u, u.y, CTRL, RM, 0xf, false)});
+}
+__device__ __forceinline__ double of_lane(double x, int lane)
+{
+    const uint2 u = __builtin_bit_cast(uint2, x);
+    return __builtin_bit_cast(double, uint2{(uint32_t)__builtin_amdgcn_readlane(u.x, lane),
+                                            (uint32_t)__builtin_amdgcn_readlane(u.y, lane)});
+}
 
 // x: the gate argument of token `lane` (ok: there is one).  One wavefront.
 template <int C>
 __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane)
 {
     double L = ok ? (double)log_gate(x, form) * 1.44269504088896340736 : 0.0;
+    L += dpp<0x111>(L);
+    L += dpp<0x112>(L);
+    L += dpp<0x114>(L);
+    L += dpp<0x118>(L);
+    L += dpp<0x142, 0xa>(L);
+    if constexpr (C > 32) L += dpp<0x143, 0xc>(L);
+    const double end = of_lane(L, C - 1);
+    double m = end, mid[C / 16 - 1];
 #pragma unroll
-    for (int d = 1; d < C; d *= 2) {
-        const double y = __shfl_up(L, d);
-        if (lane >= d) L += y;
+    for (int i = C / 16 - 2; i >= 0; --i) {
+        mid[i] = of_lane(L, 16 * i + 15);
+        if (lane < 16 * i + 16) m = mid[i];
     }
-    const double end = __shfl(L, C - 1);
     if (lane < C) {
         const float h = (float)L;
         s.hi[lane] = h;
         s.lo[lane] = (float)(L - (double)h);
         s.e[lane] = exp2_(h);
         s.d[lane] = exp2_((float)(end - L));
+        s.col[lane] = exp2_((float)(m - L));
+#pragma unroll
+        for (int i = 0; i < C / 16 - 1; ++i) s.row[i][lane] = exp2_((float)(L - mid[i]));
         if (lane == C - 1) s.g = exp2_((float)end);
     }
 }
 
-// e^(L_t - L_s)
+// Factors e^(L_t - L_s) of a tile of scores, zero where s > t.  Rows s = 16ct +
+// 4g + j and columns t = 16rt + l16 (the tile's diagonal where ct == rt):
 template <int C>
-__device__ __forceinline__ float decay(const Decay<C> &s, int t, int u)
+__device__ __forceinline__ f4 decay_st(const Decay<C> &s, int rt, int ct, int l16, int g4)
 {
-    return exp2_((s.hi[t] - s.hi[u]) + (s.lo[t] - s.lo[u]));
+    const int t = 16 * rt + l16;
+    if (ct < rt) return *reinterpret_cast<const f4 *>(&s.col[16 * ct + g4]) * s.row[ct][t];
+    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * ct + g4]);
+    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * ct + g4]);
+    const float ht = s.hi[t], lt = s.lo[t];
+    f4 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = g4 + j <= l16 ? exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
+    return f;
+}
+// Rows t = 16rt + 4g + j and columns s = 16ct + l16:
+template <int C>
+__device__ __forceinline__ f4 decay_ts(const Decay<C> &s, int rt, int ct, int l16, int g4)
+{
+    const int u = 16 * ct + l16;
+    if (ct < rt) return *reinterpret_cast<const f4 *>(&s.row[ct][16 * rt + g4]) * s.col[u];
+    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * rt + g4]);
+    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * rt + g4]);
+    const float hs = s.hi[u], ls = s.lo[u];
+    f4 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = g4 + j >= l16 ? exp2_((hi[j] - hs) + (lo[j] - ls)) : 0.f;
+    return f;
+}
+// The factor zero also where the score is an infinity or NaN.
+__device__ __forceinline__ f4 times(f4 x, f4 f, bool diagonal)
+{
+    if (!diagonal) return x * f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = f[j] != 0.f ? x[j] * f[j] : 0.f;
+    return x;
 }
 
 // --------------------------------------------------------------- forward
 
 // One workgroup walks a unit's chunks for one head and 64 columns of its
-// state: wavefront w keeps columns 16w .. 16w+15 of every row in
-// accumulators, which are operands of Q S as they are; Q K^T is split over
-// the wavefronts by rows and passes through LDS.  The next chunk's rows are
-// requested while this one is computed, its decays are formed by the
-// wavefront that has least of Q K^T to do, and the outputs leave through LDS
-// in 16-byte pieces while the next chunk is staged.
+// state.  Wavefront w keeps columns 16w .. 16w+15 of every row in
+// accumulators, which are operands of S^T Q^T as they are.  It forms the
+// scores K Q^T of the whole chunk itself (in that order a tile's accumulators
+// are operands of V^T P^T, so scores go through no LDS and wait for no other
+// wavefront; the four-fold score products are a third of its MFMA time) and
+// the outputs transposed, four columns of a token per lane, stored as they
+// are.  The next chunk's rows are requested while this one is computed and
+// its decays are formed meanwhile by one wavefront.
 template <class T, int NK>
 __global__ void __launch_bounds__(kSThreads)
 gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
-    constexpr int C = T::C, RT = C / 16, CS = 4 / RT, KS = C / 32;
-    constexpr int PK = NK * 32 + T::kPad, PV = kSlice + T::kPad, PP = C + T::kPad;
-    constexpr int GW = CS == 1 ? 0 : RT;  // the wavefront of the decays
-    __shared__ __align__(16) S qt[C * PK], kt[C * PK], vt[C * PV], pt[C * PP], ot[C * PV];
+    typedef Tile<T, NK * 32> TK;
+    typedef Tile<T, kSlice> TV;
+    constexpr int C = T::C, RT = C / 16, KS = C / 32;
+    __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes];
     __shared__ Decay<C> dcs[2];
-    __shared__ int bad[2];
+    __shared__ int bad[2], first[kSlice];
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int slice = blockIdx.x % slices;
     const int h = blockIdx.x / slices % a.H;
@@ -456,14 +653,17 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     if (!find_unit(a, unit, per, C, lane, &un)) return;
     const bool packed = a.off != nullptr;
     const int hk = h / (a.H / a.Hk), c0 = slice * kSlice, vcols = a.Dv - c0;
-    const S *qp = rows_of<S>(a.q, a.qs, un, packed, hk), *kp = rows_of<S>(a.k, a.ks, un, packed, hk);
-    const S *vp = rows_of<S>(a.v, a.vs, un, packed, h) + c0;
     const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-    S *op = reinterpret_cast<S *>(a.out) + (un.tok0 * a.H + h) * a.Dv + c0;
-    const int64_t ost = (int64_t)a.H * a.Dv;
-    const int col = w * 16 + l16;  // this lane's column of the slice
+    const int col = w * 16 + l16;  // this lane's column of the slice in the state
     const int tb = (int)(un.part * per);
     const int te = un.len - tb > per ? (int)(tb + per) : un.len;
+    const TK lk(lane);
+    const uint32_t vcol = TV(lane).col_off(w);
+    // outputs: token 16r + l16, columns 16w + 4g .. +3
+    const S *op = reinterpret_cast<const S *>(a.out) + (un.tok0 + tb) * a.H * a.Dv;
+    const uint32_t ost = (uint32_t)(a.H * a.Dv * sizeof(S));
+    const uint32_t o0 = 16 * w + g4 < vcols
+        ? (uint32_t)(h * a.Dv + c0 + 16 * w + g4) * (uint32_t)sizeof(S) + l16 * ost : kNowhere;
 
     // the state: row 16i + 4g + j of column `col`
     const int64_t srow = ((int64_t)un.seq * a.H + h) * a.Dk;
@@ -484,104 +684,53 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     Stage<T, NK> sq, sk;
     Stage<T, 2> sv;
     float gx = 0.f;
+    sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, tb, a.Dk, tid);
+    sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, tb, a.Dk, tid);
+    sv.begin(rows_of<S>(a.v, a.vs, un, packed, h) + c0, a.vs.t, tb, vcols, tid);
     auto request = [&](int t0) {
-        sq.load(qp, a.qs.t, t0, te, a.Dk, tid);
-        sk.load(kp, a.ks.t, t0, te, a.Dk, tid);
-        sv.load(vp, a.vs.t, t0, te, vcols, tid);
+        sq.load(te - t0, C * a.qs.t, tid);
+        sk.load(te - t0, C * a.ks.t, tid);
+        sv.load(te - t0, C * a.vs.t, tid);
     };
-    auto request_gate = [&](int t0) {
-        if (w == GW && lane < C && t0 + lane < te)
-            gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
-    };
-    // outputs of the chunk at t0, from LDS
-    auto flush = [&](int t0) {
-        constexpr int ppr = kSlice / T::VE;
+    // outputs and state of the staged chunk
+    auto compute = [&](const Decay<C> &dc, int t0, bool nan) {
+        const __amdgpu_buffer_rsrc_t ob = buffer(op);
+        Frag vf[KS], sf[NK], kf[RT][NK];
 #pragma unroll
-        for (int i = 0; i < C * ppr / kSThreads; ++i) {
-            const int p = tid + kSThreads * i, row = p / ppr, cc = p % ppr * T::VE;
-            if (t0 + row < te && cc < vcols)
-                *reinterpret_cast<u4 *>(op + (t0 + row) * ost + cc) =
-                    *reinterpret_cast<const u4 *>(ot + row * PV + cc);
-        }
-    };
-    if (tid < 2) bad[tid] = 0;
-    request_gate(tb);
-    request(tb);
-    if (w == GW) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
-    request_gate(tb + C);
-    __syncthreads();
-
-    int odd = 0;
-    for (int t0 = tb; t0 < te; t0 += C, odd ^= 1) {
-        const Decay<C> &dc = dcs[odd];
-        sq.store(qt, PK, tid);
-        sk.store(kt, PK, tid);
-        sv.store(vt, PV, tid);
-        if (sv.bad()) bad[odd] = 1;
-        if (t0 > tb) flush(t0 - C);
-        __syncthreads();
-        if (tid == 0) bad[odd ^ 1] = 0;
-        if (t0 + C < te) request(t0 + C);
-
-        // P . D, rows 16rt .. of wavefront (rt, ct % CS)
-        {
-            const int rt = w % RT;
+        for (int kk = 0; kk < KS; ++kk) vf[kk] = TV(lane).at_col(vt, 32 * kk, vcol);
 #pragma unroll
-            for (int ct = w / RT; ct < RT; ct += CS) {
-                f4 x = zf4();
-                if (ct <= rt) {
+        for (int kk = 0; kk < NK; ++kk) to_frag(st[2 * kk], st[2 * kk + 1], &sf[kk]);
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk)
-                        x = mma(ld_row(qt, PK, 16 * rt, 32 * kk, lane),
-                                ld_row(kt, PK, 16 * ct, 32 * kk, lane), x);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 16 * rt + g4 + j, s = 16 * ct + l16;
-                    narrow(t >= s ? x[j] * decay(dc, t, s) : 0.f, &pt[t * PP + s]);
-                }
-            }
-            if (w == GW && t0 + C < te) {
-                gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
-                request_gate(t0 + 2 * C);
-            }
-        }
-        __syncthreads();
-
-        const bool slow = bad[odd] != 0;
-        Frag vf[KS], pf[KS];
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) vf[kk] = pf[kk] = ld_col(vt, PV, 32 * kk, 16 * w, lane);
-        if (slow)
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) pf[kk] = finite_part(pf[kk]);
-        {
-            f4 o[RT];
-#pragma unroll
-            for (int r = 0; r < RT; ++r) o[r] = zf4();
+        for (int r = 0; r < RT; ++r) {
+            Frag qf[NK];
+            f4 o = zf4(), p[RT];
+            GSCAN_STEP();
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) {
-                Frag sf;
-                to_frag(st[2 * kk], st[2 * kk + 1], &sf);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) o[r] = mma(ld_row(qt, PK, 16 * r, 32 * kk, lane), sf, o[r]);
+                qf[kk] = lk.row(qt, 16 * r, kk);
+                kf[r][kk] = lk.row(kt, 16 * r, kk);
             }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int kk = 0; kk < NK; ++kk) o = mma(sf[kk], qf[kk], o);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[r][j] *= dc.e[16 * r + g4 + j];
+            for (int ct = 0; ct < RT; ++ct) {
+                p[ct] = zf4();
+                if (ct > r) continue;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk <= r) o[r] = mma(ld_row(pt, PP, 16 * r, 32 * kk, lane), pf[kk], o[r]);
+                for (int kk = 0; kk < NK; ++kk) p[ct] = mma(kf[ct][kk], qf[kk], p[ct]);
+                p[ct] = times(p[ct], decay_st(dc, r, ct, l16, g4), ct == r);
             }
-            if (slow)
+            o *= dc.e[16 * r + l16];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    o[r] += other_terms<true, false>(pt, PP, vt, PV, 16 * r + g4, col, C);
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) narrow(a.scale * o[r][j], &ot[(16 * r + g4 + j) * PV + col]);
+            for (int kk = 0; kk < KS; ++kk) {
+                if (2 * kk > r) continue;
+                Frag pf;
+                to_frag(p[2 * kk], p[2 * kk + 1], &pf);
+                o = mma(vf[kk], pf, o);
+            }
+            if (nan) o = poison<false>(o, &first[16 * w + g4], 16 * r + l16);
+            store4(ob, t0 + 16 * r + l16 < te && o0 != kNowhere ? o0 + 16 * r * ost : kNowhere,
+                   a.scale * o, T());
         }
         // S' = e^(L_end) S + K^T (e^(L_end - L) V)
         typename PartsOf<T>::type vs[KS];
@@ -589,24 +738,62 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
         for (int kk = 0; kk < KS; ++kk) {
             f4 x, y;
             from_frag(vf[kk], &x, &y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] *= dc.d[32 * kk + g4 + j];
-                y[j] *= dc.d[32 * kk + 16 + g4 + j];
-            }
+            x *= *reinterpret_cast<const f4 *>(&dc.d[32 * kk + g4]);
+            y *= *reinterpret_cast<const f4 *>(&dc.d[32 * kk + 16 + g4]);
             to_parts(x, y, &vs[kk]);
         }
         const float ge = dc.g;
 #pragma unroll
         for (int i = 0; i < 2 * NK; ++i) {
+            if (i % 2 == 0) GSCAN_STEP();
             st[i] *= ge;
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-                st[i] = mma_parts(ld_col(kt, PK, 32 * kk, 16 * i, lane), vs[kk], st[i]);
+            for (int kk = 0; kk < KS; ++kk) st[i] = mma_parts(lk.col(kt, 32 * kk, i), vs[kk], st[i]);
         }
+        if (nan && first[col] < C)
+#pragma unroll
+            for (int i = 0; i < 2 * NK; ++i) st[i] = zf4() + __builtin_nanf("");
+    };
+    auto request_gate = [&](int t0) {
+        if (w == 0 && lane < C && t0 + lane < te)
+            gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
+    };
+    if (tid < 2) bad[tid] = 0;
+    if (tid < kSlice) first[tid] = C;
+    request_gate(tb);
+    request(tb);
+    if (w == 0) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
+    request_gate(tb + C);
+    __syncthreads();
+
+    int odd = 0;
+    for (int t0 = tb; t0 < te; t0 += C, odd ^= 1) {
+        const Decay<C> &dc = dcs[odd];
+        sq.template store<TK>(qt, tid);
+        sk.template store<TK>(kt, tid);
+        sv.template store<TV>(vt, tid);
+        sv.template scrub<TV>(vt, tid, [&](int row, int c) {
+            atomicMin(&first[c], row);
+            bad[odd] = 1;
+        });
         __syncthreads();
+        if (tid == 0) bad[odd ^ 1] = 0;
+        if (t0 + C < te) {
+            request(t0 + C);
+            if (w == 0) {
+                gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
+                request_gate(t0 + 2 * C);
+            }
+        }
+        const bool nan = bad[odd] != 0;
+        compute(dc, t0, nan);
+        op += (int64_t)C * a.H * a.Dv;
+        __syncthreads();
+        if (nan) {
+            if (tid < kSlice) first[tid] = C;
+            __syncthreads();
+        }
     }
-    if (te > tb) flush(tb + (te - tb - 1) / C * C);
 
     if (a.sT && te == un.len && col < vcols) {
 #pragma unroll
@@ -645,16 +832,18 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
-    constexpr int C = T::C, KS = C / 32, PX = NX * 32 + T::kPad, PY = kSlice + T::kPad;
-    S *xt = reinterpret_cast<S *>(smem), *yt = xt + C * PX;
+    typedef Tile<T, NX * 32> TX;
+    typedef Tile<T, kSlice> TY;
+    constexpr int C = T::C, KS = C / 32;
+    char *xt = smem, *yt = xt + C * TX::bytes;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const bool packed = a.off != nullptr;
     const int c0 = slice * kSlice, ycols = jb.yd - c0, col = 16 * w + l16;
-    const S *xp = rows_of<S>(jb.x, jb.xs, un, packed, jb.xh);
-    const S *yp = rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0;
     const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
     const int sb = (c0 + col) * jb.cstr;
+    const TX lx(lane);
+    const uint32_t ycol = TY(lane).col_off(w);
     f4 st[2 * NX];
 #pragma unroll
     for (int i = 0; i < 2 * NX; ++i) {
@@ -665,19 +854,21 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
                 if (16 * i + g4 + j < jb.xd) st[i][j] = jb.init[sb + (16 * i + g4 + j) * jb.rstr];
     }
     const int cb = tb / C, ce = te > tb ? (te + C - 1) / C : cb + 1;  // chunks
+    constexpr int step = REV ? -1 : 1;
     Stage<T, NX> sx;
     Stage<T, 2> sy;
     float gx = 0.f, gall = 1.f;
     auto request = [&](int c) {
-        sx.load(xp, jb.xs.t, c * C, te, jb.xd, tid);
-        sy.load(yp, jb.ys.t, c * C, te, ycols, tid);
+        sx.load(te - c * C, step * C * jb.xs.t, tid);
+        sy.load(te - c * C, step * C * jb.ys.t, tid);
     };
     auto request_gate = [&](int c) {
         if (w == 0 && lane < C && c >= cb && c * C + lane < te)
             gx = load_scalar(a.gate, g0 + (int64_t)(c * C + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
     };
-    constexpr int step = REV ? -1 : 1;
     int c = REV ? ce - 1 : cb;
+    sx.begin(rows_of<S>(jb.x, jb.xs, un, packed, jb.xh), jb.xs.t, c * C, jb.xd, tid);
+    sy.begin(rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0, jb.ys.t, c * C, ycols, tid);
     request_gate(c);
     request(c);
     if (w == 0) gate_scan<C>(dcs[0], gx, c * C + lane < te, a.gate_form, lane);
@@ -685,8 +876,8 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     int odd = 0;
     for (int n = ce - cb; n > 0; --n, c += step, odd ^= 1) {
         const Decay<C> &dc = dcs[odd];
-        sx.store(xt, PX, tid);
-        sy.store(yt, PY, tid);
+        sx.template store<TX>(xt, tid);
+        sy.template store<TY>(yt, tid);
         if constexpr (STORE) {  // the operands of this chunk, before its own tokens enter
 #pragma unroll
             for (int kk = 0; kk < NX; ++kk) {
@@ -709,12 +900,9 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
             f4 x, y;
-            from_frag(ld_col(yt, PY, 32 * kk, 16 * w, lane), &x, &y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] *= jb.mul * m[32 * kk + g4 + j];
-                y[j] *= jb.mul * m[32 * kk + 16 + g4 + j];
-            }
+            from_frag(TY(lane).at_col(yt, 32 * kk, ycol), &x, &y);
+            x *= jb.mul * *reinterpret_cast<const f4 *>(&m[32 * kk + g4]);
+            y *= jb.mul * *reinterpret_cast<const f4 *>(&m[32 * kk + 16 + g4]);
             to_parts(x, y, &ys[kk]);
         }
         const float ge = dc.g;
@@ -724,7 +912,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             st[i] *= ge;
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk)
-                st[i] = mma_parts(ld_col(xt, PX, 32 * kk, 16 * i, lane), ys[kk], st[i]);
+                st[i] = mma_parts(lx.col(xt, 32 * kk, i), ys[kk], st[i]);
         }
         __syncthreads();
     }
@@ -740,7 +928,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
 
 template <class T, int NM>
 struct PassLds {
-    static constexpr size_t bytes = T::C * (NM * 32 + kSlice + 2 * T::kPad) * sizeof(typename T::S);
+    static constexpr size_t bytes = T::C * (Tile<T, NM * 32>::bytes + Tile<T, kSlice>::bytes);
 };
 
 // Units of split sequences, by themselves: what a unit adds to the state after
@@ -878,273 +1066,324 @@ gscan_state_pass_kernel(StateArgs a, int64_t tokens, PassWs o)
 
 // ---------------------------------------------------- backward: gradients
 
-// x of the lane N below in its group of 16, 0 in the first N lanes
-template <int N>
-__device__ __forceinline__ float row_shr(float x)
-{
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x110 + N, 0xf, 0xf, false));
-}
-
-__device__ __forceinline__ float sum16(float x)
-{
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d);
-    return x;
-}
-
 // One workgroup per chunk and key head: its queries and keys stay in LDS
 // while it takes the value heads that share them one by one, so dQ and dK of
 // shared heads are summed in registers in a fixed order.  Wavefront (rt, cs)
-// owns token rows 16rt .. 16rt+15 and every CS-th 16-column tile.
+// owns token rows 16rt .. 16rt+15 and every CS-th 16-column tile, and forms
+// the scores it needs itself, in the order whose accumulators are operands:
+// dO V^T of its tokens with the tokens before them (for dQ), Q K^T and dO V^T
+// of its tokens with the tokens after them (for dK and dV), five tiles for
+// every wavefront.  Gradients are formed transposed, four columns of a token
+// per lane.
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kSThreads)
 gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
+    typedef Tile<T, NK * 32> TK;
+    typedef Tile<T, NV * 32> TV;
     constexpr int C = T::C, RT = C / 16, CS = 4 / RT, KS = C / 32;
-    constexpr int PK = NK * 32 + T::kPad, PV = NV * 32 + T::kPad, PP = C + T::kPad;
-    constexpr int TK = 2 * NK / CS, TV = 2 * NV / CS;  // column tiles per wavefront
-    __shared__ __align__(16) S qt[C * PK], kt[C * PK], vt[C * PV], ot[C * PV], pt[C * PP], dt[C * PP];
+    constexpr int NTK = 2 * NK / CS, NTV = 2 * NV / CS;  // column tiles per wavefront
+    __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
     __shared__ Decay<C> dc;
-    __shared__ float rsum[C][RT], csum[RT][C], asum[CS][C], bsum[CS][C], fsum[4];
-    __shared__ int bad_q, bad_o;
+    __shared__ float rsum[C][RT], inner[C], asum[CS][C], bsum[CS][C], fsum[4];
+    // what infinities and NaN reach: per column the first row of k and the last
+    // of q and d_out that hold one, which rows of k and d_out do, and the last
+    // row of q, of d_out, the first of k
+    __shared__ int first_k[NK * 32], last_q[NK * 32], last_o[NV * 32], row_k[C], row_o[C], ends[3], bad;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int rt = w % RT, cs = w / RT;
     const int hk = blockIdx.x % a.Hk;
     Unit un;
     if (!find_unit(a, blockIdx.x / a.Hk, C, C, lane, &un)) return;
     const bool packed = a.off != nullptr;
-    const int t0 = un.part * C, reps = a.H / a.Hk;
-    if (t0 >= un.len) return;  // a sequence without tokens
+    const int t0 = un.part * C, reps = a.H / a.Hk, left = un.len - t0;
+    if (left <= 0) return;  // a sequence without tokens
     const int64_t slot = un.slot0 + un.part;
     const char *ws = reinterpret_cast<const char *>(a.ws);
+    const TK lk(lane);
+    const TV lv(lane);
+    const bool mine = 16 * rt + l16 < left;  // this lane's token exists
 
-    if (tid == 0) bad_q = bad_o = 0;
+    Stage<T, NV> sv, so;
+    float gx = 0.f;
+    auto request = [&](int h) {
+        sv.begin(rows_of<S>(a.v, a.vs, un, packed, h), a.vs.t, t0, a.Dv, tid);
+        so.begin(rows_of<S>(a.dout, a.ds, un, packed, h), a.ds.t, t0, a.Dv, tid);
+        sv.load(left, 0, tid);
+        so.load(left, 0, tid);
+        if (w == 0) {
+            const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
+            if (lane < C && lane < left)
+                gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
+        }
+    };
+    if (tid < NK * 32) {
+        first_k[tid] = C;
+        last_q[tid] = -1;
+    }
+    if (tid < NV * 32) last_o[tid] = -1;
+    if (tid < C) row_k[tid] = row_o[tid] = 0;
+    if (tid < 3) ends[tid] = tid < 2 ? -1 : C;
+    if (tid == 0) bad = 0;
     __syncthreads();
     {
         Stage<T, NK> sq, sk;
-        sq.load(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, t0, un.len, a.Dk, tid);
-        sk.load(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, t0, un.len, a.Dk, tid);
-        sq.store(qt, PK, tid);
-        sk.store(kt, PK, tid);
-        if (sq.bad() || sk.bad()) bad_q = 1;
+        sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, t0, a.Dk, tid);
+        sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, t0, a.Dk, tid);
+        sq.load(left, 0, tid);
+        sk.load(left, 0, tid);
+        request(hk * reps);
+        sq.template store<TK>(qt, tid);
+        sk.template store<TK>(kt, tid);
+        sq.template scrub<TK>(qt, tid, [&](int row, int c) {
+            atomicMax(&last_q[c], row);
+            atomicMax(&ends[0], row);
+            bad = 1;
+        });
+        sk.template scrub<TK>(kt, tid, [&](int row, int c) {
+            atomicMin(&first_k[c], row);
+            atomicMin(&ends[2], row);
+            row_k[row] = 1;
+            bad = 1;
+        });
     }
-    f4 dq[TK], dk[TK];
+    f4 dq[NTK], dk[NTK];
 #pragma unroll
-    for (int i = 0; i < TK; ++i) dq[i] = dk[i] = zf4();
+    for (int i = 0; i < NTK; ++i) dq[i] = dk[i] = zf4();
 
-    for (int hr = 0; hr < reps; ++hr) {
-        const int h = hk * reps + hr;
-        {
-            Stage<T, NV> sv, so;
-            sv.load(rows_of<S>(a.v, a.vs, un, packed, h), a.vs.t, t0, un.len, a.Dv, tid);
-            so.load(rows_of<S>(a.dout, a.ds, un, packed, h), a.ds.t, t0, un.len, a.Dv, tid);
-            sv.store(vt, PV, tid);
-            so.store(ot, PV, tid);
-            if (so.bad()) bad_o = 1;
-        }
-        float gx = 0.f;
-        if (w == 0) {
-            const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-            const bool ok = lane < C && t0 + lane < un.len;
-            if (ok) gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
-            gate_scan<C>(dc, gx, ok, a.gate_form, lane);
-        }
-        __syncthreads();
-        const bool bq = bad_q != 0, bo = bad_o != 0;
-
-        // P . D and dP . D, and the sums of W: over s < t inside a tile's
-        // columns and u >= t (csum), and each row's whole tile (rsum)
-        {
+    // the staged head
+    auto compute = [&](int h, bool nan) {
+        const int64_t fh = (slot * a.H + h) * 2 * NK * NV;  // operands before this head's
+        const void *Sf = ws + st_kv, *Gt = ws + st_gt, *Gf = ws + st_g;
+        // the state operands of the next column tile are requested one tile ahead
+        Frag next[NK > NV ? NK : NV];
+        auto fetch = [&](const void *from, int n) {
 #pragma unroll
-            for (int ct = cs; ct < RT; ct += CS) {
-                f4 x = zf4(), y = zf4();
-                float cp = 0.f;
+            for (int kk = 0; kk < NV; ++kk) get_frag(from, fh + n * NV + kk, lane, &next[kk]);
+        };
+        auto fetch_g = [&](int n) {
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) get_frag(Gf, fh + n * NK + kk, lane, &next[kk]);
+        };
+        fetch(Sf, cs);
+        // dQ^T = K^T (dP . D)^T + scale e^L S dO^T
+        {
+            Frag of[NV], df[KS];
+            f4 p[RT];
+#pragma unroll
+            for (int kk = 0; kk < NV; ++kk) of[kk] = lv.row(ot, 16 * rt, kk);
+#pragma unroll
+            for (int ct = 0; ct < RT; ++ct) {
+                p[ct] = zf4();
+                GSCAN_STEP();
                 if (ct <= rt) {
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk)
-                        x = mma(ld_row(qt, PK, 16 * rt, 32 * kk, lane),
-                                ld_row(kt, PK, 16 * ct, 32 * kk, lane), x);
-#pragma unroll
-                    for (int kk = 0; kk < NV; ++kk)
-                        y = mma(ld_row(ot, PV, 16 * rt, 32 * kk, lane),
-                                ld_row(vt, PV, 16 * ct, 32 * kk, lane), y);
+                    for (int kk = 0; kk < NV; ++kk) p[ct] = mma(lv.row(vt, 16 * ct, kk), of[kk], p[ct]);
+                    p[ct] = times(p[ct], a.scale * decay_st(dc, rt, ct, l16, g4), ct == rt);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int u = 16 * rt + g4 + j, s = 16 * ct + l16;
-                    const float f = a.scale * decay(dc, u, s);
-                    narrow(u >= s ? x[j] * f : 0.f, &pt[u * PP + s]);
-                    narrow(u >= s ? y[j] * f : 0.f, &dt[u * PP + s]);
-                    float wv = u > s ? x[j] * y[j] * f : 0.f;
-                    wv += row_shr<1>(wv);
-                    wv += row_shr<2>(wv);
-                    wv += row_shr<4>(wv);
-                    wv += row_shr<8>(wv);
-                    const float before = row_shr<1>(wv);
-                    cp += u >= s ? before : 0.f;
-                    if (l16 == 15) rsum[u][ct] = wv;
-                }
-                cp += __shfl_xor(cp, 16);
-                cp += __shfl_xor(cp, 32);
-                if (lane < 16) csum[rt][16 * ct + lane] = cp;
             }
-        }
-        __syncthreads();
-
-        if (tid == 0) bad_o = 0;  // read by all before this barrier, set again after the last one
-        const void *Sf = ws + st_kv, *Gt = ws + st_gt, *Gf = ws + st_g;
-        const int64_t fh = (slot * a.H + h) * 2 * NK * NV;  // operands before this head's
-        // dQ: (dP . D) K + scale e^L dO S^T
-        {
-            Frag of[NV];
-            f4 as = zf4();
 #pragma unroll
-            for (int kk = 0; kk < NV; ++kk) of[kk] = ld_row(ot, PV, 16 * rt, 32 * kk, lane);
+            for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &df[kk]);
+            const float e = a.scale * dc.e[16 * rt + l16];
+            float as = 0.f;
 #pragma unroll
-            for (int i = 0; i < TK; ++i) {
+            for (int i = 0; i < NTK; ++i) {
                 const int n = i * CS + cs;
                 f4 x = zf4();
+                Frag sf[NV];
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) {
-                    Frag sf;
-                    get_frag(Sf, fh + n * NV + kk, lane, &sf);
-                    x = mma(of[kk], sf, x);
-                }
+                for (int kk = 0; kk < NV; ++kk) sf[kk] = next[kk];
+                GSCAN_STEP();
+                fetch(i + 1 < NTK ? Sf : Gt, i + 1 < NTK ? n + CS : cs);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] *= a.scale * dc.e[16 * rt + g4 + j];
-                    as[j] += x[j] * widen(qt[(16 * rt + g4 + j) * PK + 16 * n + l16]);
-                }
+                for (int kk = 0; kk < NV; ++kk) x = mma(sf[kk], of[kk], x);
+                x *= e;
+                const f4 qv = lk.quad(qt, 16 * rt, n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) as += x[j] * qv[j];
                 dq[i] += x;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk <= rt) {
-                        Frag f = ld_col(kt, PK, 32 * kk, 16 * n, lane);
-                        if (bq) f = finite_part(f);
-                        dq[i] = mma(ld_row(dt, PP, 16 * rt, 32 * kk, lane), f, dq[i]);
-                    }
-                if (bq) dq[i] += other_terms<true, false>(dt, PP, kt, PK, 16 * rt + g4, 16 * n + l16, C);
+                for (int kk = 0; kk < KS; ++kk) {
+                    if (2 * kk > rt) continue;
+                    dq[i] = mma(lk.col(kt, 32 * kk, n), df[kk], dq[i]);
+                }
+                if (nan) dq[i] = poison<false>(dq[i], &first_k[16 * n + g4], 16 * rt + l16, row_o[16 * rt + l16]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float r = sum16(as[j]);
-                if (l16 == 0) asum[cs][16 * rt + g4 + j] = r;
-            }
+            as += __shfl_xor(as, 16);
+            as += __shfl_xor(as, 32);
+            if (lane < 16) asum[cs][16 * rt + lane] = as;
         }
-        // dK: (dP . D)^T Q + e^(L_end - L) V dS^T
+        // the scores of this wavefront's tokens (columns) with later ones
+        Frag pf[KS], df[KS];
         {
-            Frag vf[NV];
-            f4 bs = zf4();
+            Frag kf[NK], vf[NV];
+            f4 p[RT], d[RT];
+            float in = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < NV; ++kk) vf[kk] = ld_row(vt, PV, 16 * rt, 32 * kk, lane);
+            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
-            for (int i = 0; i < TK; ++i) {
-                const int n = i * CS + cs;
-                f4 x = zf4();
+            for (int kk = 0; kk < NV; ++kk) vf[kk] = lv.row(vt, 16 * rt, kk);
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) {
-                    Frag gf;
-                    get_frag(Gt, fh + n * NV + kk, lane, &gf);
-                    x = mma(vf[kk], gf, x);
-                }
+            for (int ut = 0; ut < RT; ++ut) {
+                p[ut] = d[ut] = zf4();
+                GSCAN_STEP();
+                if (ut >= rt) {
+                    f4 x = zf4(), y = zf4();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] *= dc.d[16 * rt + g4 + j];
-                    bs[j] += x[j] * widen(kt[(16 * rt + g4 + j) * PK + 16 * n + l16]);
-                }
-                dk[i] += x;
+                    for (int kk = 0; kk < NK; ++kk) x = mma(lk.row(qt, 16 * ut, kk), kf[kk], x);
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk + 1 >= rt) {
-                        Frag f = ld_col(qt, PK, 32 * kk, 16 * n, lane);
-                        if (bq) f = finite_part(f);
-                        dk[i] = mma(ld_col(dt, PP, 32 * kk, 16 * rt, lane), f, dk[i]);
-                    }
-                if (bq) dk[i] += other_terms<false, true>(dt, PP, qt, PK, 16 * rt + g4, 16 * n + l16, C);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float r = sum16(bs[j]);
-                if (l16 == 0) bsum[cs][16 * rt + g4 + j] = r;
-            }
-        }
-        // dV: (P . D)^T dO + e^(L_end - L) K dS
-        {
-            Frag kf[NK];
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) kf[kk] = ld_row(kt, PK, 16 * rt, 32 * kk, lane);
-#pragma unroll
-            for (int i = 0; i < TV; ++i) {
-                const int n = i * CS + cs, col = 16 * n + l16;
-                f4 x = zf4();
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) {
-                    Frag gf;
-                    get_frag(Gf, fh + n * NK + kk, lane, &gf);
-                    x = mma(kf[kk], gf, x);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= dc.d[16 * rt + g4 + j];
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk + 1 >= rt) {
-                        Frag f = ld_col(ot, PV, 32 * kk, 16 * n, lane);
-                        if (bo) f = finite_part(f);
-                        x = mma(ld_col(pt, PP, 32 * kk, 16 * rt, lane), f, x);
-                    }
-                if (bo) x += other_terms<false, true>(pt, PP, ot, PV, 16 * rt + g4, col, C);
-                if (col < a.Dv)
+                    for (int kk = 0; kk < NV; ++kk) y = mma(lv.row(ot, 16 * ut, kk), vf[kk], y);
+                    const f4 f = a.scale * decay_ts(dc, ut, rt, l16, g4);
+                    p[ut] = times(x, f, ut == rt);
+                    d[ut] = times(y, f, ut == rt);
+                    // W below the diagonal: sums over s < t of the tile's
+                    // columns, for u >= t
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int t = t0 + 16 * rt + g4 + j;
-                        if (t < un.len)
-                            narrow(x[j], reinterpret_cast<S *>(a.dv) + ((un.tok0 + t) * a.H + h) * a.Dv + col);
+                        const bool low = ut > rt || g4 + j > l16;
+                        float v = low ? p[ut][j] * y[j] : 0.f;
+                        v += dpp<0x111>(v);
+                        v += dpp<0x112>(v);
+                        v += dpp<0x114>(v);
+                        v += dpp<0x118>(v);
+                        const float before = dpp<0x111>(v);
+                        in += ut > rt || g4 + j >= l16 ? before : 0.f;
+                        if (cs == 0 && l16 == 15) rsum[16 * ut + g4 + j][rt] = v;
                     }
+                }
+            }
+            in += __shfl_xor(in, 16);
+            in += __shfl_xor(in, 32);
+            if (cs == 0 && lane < 16) inner[16 * rt + lane] = in;
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
+                to_frag(d[2 * kk], d[2 * kk + 1], &df[kk]);
+            }
+        }
+        const float ds = dc.d[16 * rt + l16];
+        // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
+        {
+            Frag vf[NV];
+            float bs = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < NV; ++kk) vf[kk] = lv.row(vt, 16 * rt, kk);
+#pragma unroll
+            for (int i = 0; i < NTK; ++i) {
+                const int n = i * CS + cs;
+                f4 x = zf4();
+                Frag gf[NV];
+#pragma unroll
+                for (int kk = 0; kk < NV; ++kk) gf[kk] = next[kk];
+                GSCAN_STEP();
+                if (i + 1 < NTK) fetch(Gt, n + CS);
+                else fetch_g(cs);
+#pragma unroll
+                for (int kk = 0; kk < NV; ++kk) x = mma(gf[kk], vf[kk], x);
+                x *= ds;
+                const f4 kv = lk.quad(kt, 16 * rt, n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bs += x[j] * kv[j];
+                dk[i] += x;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    if (2 * kk + 1 < rt) continue;
+                    dk[i] = mma(lk.col(qt, 32 * kk, n), df[kk], dk[i]);
+                }
+                if (nan) dk[i] = poison<true>(dk[i], &last_q[16 * n + g4], 16 * rt + l16, 16 * rt + l16 <= ends[1]);
+            }
+            bs += __shfl_xor(bs, 16);
+            bs += __shfl_xor(bs, 32);
+            if (lane < 16) bsum[cs][16 * rt + lane] = bs;
+        }
+        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T
+        {
+            Frag kf[NK];
+            S *out = reinterpret_cast<S *>(a.dv) + ((un.tok0 + t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
+#pragma unroll
+            for (int i = 0; i < NTV; ++i) {
+                const int n = i * CS + cs;
+                f4 x = zf4();
+                Frag gf[NK];
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) gf[kk] = next[kk];
+                GSCAN_STEP();
+                if (i + 1 < NTV) fetch_g(n + CS);
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) x = mma(gf[kk], kf[kk], x);
+                x *= ds;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    if (2 * kk + 1 < rt) continue;
+                    x = mma(lv.col(ot, 32 * kk, n), pf[kk], x);
+                }
+                if (nan)
+                    x = poison<true>(x, &last_o[16 * n + g4], 16 * rt + l16,
+                                     16 * rt + l16 <= ends[0] || row_k[16 * rt + l16]);
+                if (mine && 16 * n + g4 < a.Dv) put4(out + 16 * n, x);
             }
         }
         // F = e^(L_end) <S, dS>
-        {
-            float f = 0.f;
-            for (int i = w; i < 2 * NK * NV; i += 4) {
-                Frag x, y;
-                f4 x0, x1, y0, y1;
-                get_frag(Sf, fh + i, lane, &x);
-                get_frag(Gt, fh + i, lane, &y);
-                from_frag(x, &x0, &x1);
-                from_frag(y, &y0, &y1);
+        float f = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f += x0[j] * y0[j] + x1[j] * y1[j];
-            }
+        for (int i = 0; i < NK * NV / 2; ++i) {
+            if (i % 4 == 0) GSCAN_STEP();
+            Frag x, y;
+            f4 x0, x1, y0, y1;
+            get_frag(Sf, fh + 4 * i + w, lane, &x);
+            get_frag(Gt, fh + 4 * i + w, lane, &y);
+            from_frag(x, &x0, &x1);
+            from_frag(y, &y0, &y1);
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
-            if (lane == 0) fsum[w] = f;
+            for (int j = 0; j < 4; ++j) f += x0[j] * y0[j] + x1[j] * y1[j];
         }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
+        if (lane == 0) fsum[w] = f;
+    };
+
+    for (int hr = 0; hr < reps; ++hr) {
+        const int h = hk * reps + hr;
+        sv.template store<TV>(vt, tid);
+        so.template store<TV>(ot, tid);
+        so.template scrub<TV>(ot, tid, [&](int row, int c) {
+            atomicMax(&last_o[c], row);
+            atomicMax(&ends[1], row);
+            row_o[row] = 1;
+            bad = 1;
+        });
+        const float x = gx;
+        if (w == 0) gate_scan<C>(dc, x, lane < left, a.gate_form, lane);
+        __syncthreads();
+        const bool nan = bad != 0;
+        if (hr + 1 < reps) request(h + 1);
+        compute(h, nan);
         __syncthreads();
         if (w == 0) {
-            float x = 0.f, b = 0.f, in = 0.f, rs[RT];
+            float su = 0.f, pb = 0.f, in = 0.f, rs[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i) rs[i] = 0.f;
             if (lane < C) {
 #pragma unroll
                 for (int i = 0; i < CS; ++i) {
-                    x += asum[i][lane];
-                    b += bsum[i][lane];
+                    su += asum[i][lane];
+                    pb += bsum[i][lane];
                 }
+                in = inner[lane];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    in += csum[i][lane];
-                    rs[i] = rsum[lane][i];
-                }
+                for (int i = 0; i + 1 < RT; ++i)
+                    rs[i] = lane >= 16 * i + 16 ? rsum[lane][i] : 0.f;  // rows below the tile
             }
-            float pb = b;
 #pragma unroll
             for (int d = 1; d < C; d *= 2) {
-                const float y = __shfl_down(x, d), z = __shfl_up(pb, d);
-                if (lane + d < 64) x += y;
+                const float y = __shfl_down(su, d), z = __shfl_up(pb, d);
+                if (lane + d < 64) su += y;
                 if (lane >= d) pb += z;
 #pragma unroll
                 for (int i = 0; i + 1 < RT; ++i) {
@@ -1152,36 +1391,39 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                     if (lane + d < 64) rs[i] += r;
                 }
             }
-            x += in;
+            su += in;
 #pragma unroll
             for (int i = 0; i + 1 < RT; ++i)
-                if (lane >= 16 * (i + 1)) x += rs[i];
+                if (lane >= 16 * (i + 1)) su += rs[i];
             const float F = dc.g * ((fsum[0] + fsum[1]) + (fsum[2] + fsum[3]));
             const float before = __shfl_up(pb, 1);
-            if (lane < C && t0 + lane < un.len) {
-                const float dl = x + (lane ? before : 0.f) + F;
-                const float r = dl * log_gate_slope(gx, a.gate_form);
+            if (lane < C && lane < left) {
+                float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
+                if (nan && (lane <= ends[0] || lane <= ends[1] || lane > ends[2])) r = __builtin_nanf("");
                 const int64_t at = (un.tok0 + t0 + lane) * a.H + h;
                 if (a.gate_dtype) reinterpret_cast<uint16_t *>(a.dgate)[at] = to_bf16(r);
                 else reinterpret_cast<float *>(a.dgate)[at] = r;
             }
         }
         __syncthreads();
+        if (nan) {  // d_out's of this head (q and k stay)
+            if (tid < NV * 32) last_o[tid] = -1;
+            if (tid < C) row_o[tid] = 0;
+            if (tid == 0) ends[1] = -1;
+            __syncthreads();
+        }
     }
 
+    if (mine) {
+        const int64_t at = ((un.tok0 + t0 + 16 * rt + l16) * a.Hk + hk) * a.Dk + g4;
 #pragma unroll
-    for (int i = 0; i < TK; ++i) {
-        const int col = 16 * (i * CS + cs) + l16;
-        if (col < a.Dk)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + 16 * rt + g4 + j;
-                if (t < un.len) {
-                    const int64_t at = ((un.tok0 + t) * a.Hk + hk) * a.Dk + col;
-                    narrow(dq[i][j], reinterpret_cast<S *>(a.dq) + at);
-                    narrow(dk[i][j], reinterpret_cast<S *>(a.dk) + at);
-                }
+        for (int i = 0; i < NTK; ++i) {
+            const int n = i * CS + cs;
+            if (16 * n + g4 < a.Dk) {
+                put4(reinterpret_cast<S *>(a.dq) + at + 16 * n, dq[i]);
+                put4(reinterpret_cast<S *>(a.dk) + at + 16 * n, dk[i]);
             }
+        }
     }
 }
 

@@ -34,15 +34,30 @@ __device__ __forceinline__ float load_scalar(const void *p, int64_t i, int dtype
                  : reinterpret_cast<const float *>(p)[i];
 }
 
-// log of the gate: x itself (log form), or log sigmoid(x) without
-// cancellation at either end.  Below -1000 the gate is zero in fp32 and far
-// beyond; the clamp keeps sums of log gates finite, so that differences
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// log of the gate: x itself (log form), or log sigmoid(x) = min(x, 0) -
+// log1p(e), e = exp(-|x|), without cancellation at either end: log1p(e) =
+// 2 atanh(s), s = e / (2 + e) <= 1/3, by its power series to s^15 (the next
+// term is below 2^-26 of the sum).  Below -1000 the gate is zero in fp32 and
+// far beyond; the clamp keeps sums of log gates finite, so that differences
 // behind a closed gate stay exact.  NaN passes.
 __device__ __forceinline__ float log_gate(float x, int form)
 {
-    const float l = form ? x : fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
-    const float y = x != x ? x : l;  // fminf would drop a NaN
-    return y < -1000.f ? -1000.f : y;
+    float l = x;
+    if (!form) {
+        const float e = exp2_(-1.44269504f * fabsf(x));
+        const float s = e * __builtin_amdgcn_rcpf(2.f + e), z = s * s;
+        float p = fmaf(z, 1.f / 15.f, 1.f / 13.f);
+        p = fmaf(z, p, 1.f / 11.f);
+        p = fmaf(z, p, 1.f / 9.f);
+        p = fmaf(z, p, 1.f / 7.f);
+        p = fmaf(z, p, 1.f / 5.f);
+        p = fmaf(z, p, 1.f / 3.f);
+        p = fmaf(z, p, 1.f);
+        l = (x < 0.f ? x : 0.f) - 2.f * s * p;
+    }
+    return l < -1000.f ? -1000.f : l;
 }
 
 // d(log gate)/dx: 1 - sigmoid(x) = sigmoid(-x), or 1

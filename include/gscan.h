@@ -322,13 +322,14 @@ size_t gscan_backward_workspace_bytes(int64_t B, int64_t K, int64_t SH2, int64_t
  * and their gradients are fp32 [B][H][Dk][Dv].  Outputs are dense row-major
  * ([tokens][H][Dv], [tokens][Hk][Dk], [tokens][H]).
  *
- * Shapes: Dk and Dv multiples of 8 up to 128; H >= 1, Hk dividing H; B >= 1,
- * T >= 0, T < 2^31 - 128.  q, k, v, d_out pointers, and their strides in
+ * Shapes: Dk and Dv multiples of 8 up to 128; 1 <= H <= 16384, Hk dividing H;
+ * B >= 1, T >= 0, T < 2^31 - 128; token strides below 2^23 elements.  q, k, v, d_out pointers, and their strides in
  * bytes, are multiples of 16; states 16-byte aligned.
  *
- * Non-finite inputs propagate as in the recurrence: a token's NaN or Inf
- * reaches the outputs of its own and later tokens of its sequence and head,
- * not of earlier ones.  A gate of exactly zero (GSCAN_GATE_LOG: minus
+ * Non-finite inputs reach what they reach in the recurrence and nothing else:
+ * an Inf or NaN of v leaves NaN in its column of the outputs of its own and
+ * later tokens of its sequence and head and of the state, not in earlier
+ * ones (backward: likewise, in the other direction).  A gate of exactly zero (GSCAN_GATE_LOG: minus
  * infinity) forgets the state.  Log gates below -1000 count as -1000.
  *
  * Accuracy.  Sums, gates and states are fp32 or better.  With bf16 operands
