@@ -350,7 +350,10 @@ __device__ __forceinline__ void put4(uint16_t *p, f4 x)
 }
 __device__ __forceinline__ void put4(float *p, f4 x) { *reinterpret_cast<f4 *>(p) = x; }
 
-// The same at byte offset `at` of a buffer.
+__device__ __forceinline__ void put1(uint16_t *p, float x) { *p = to_bf16(x); }
+__device__ __forceinline__ void put1(float *p, float x) { *p = x; }
+
+// Four elements at byte offset `at` of a buffer.
 __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t b, uint32_t at, f4 x, const BF &)
 {
     typedef unsigned int u2 __attribute__((ext_vector_type(2)));
@@ -582,57 +585,57 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
     }
 }
 
-// Factors e^(L_t - L_s) of a tile of scores, zero where s > t.  Rows s = 16ct +
-// 4g + j and columns t = 16rt + l16 (the tile's diagonal where ct == rt):
+// Scores of a tile times e^(L_t - L_s), zero where s > t.  Rows s = 16ct + 4g + j
+// and columns t = 16rt + l16 (on the diagonal where ct == rt):
 template <int C>
-__device__ __forceinline__ f4 decay_st(const Decay<C> &s, int rt, int ct, int l16, int g4)
+__device__ __forceinline__ f4 decayed_st(const Decay<C> &s, f4 x, int rt, int ct, int l16, int g4)
 {
     const int t = 16 * rt + l16;
-    if (ct < rt) return *reinterpret_cast<const f4 *>(&s.col[16 * ct + g4]) * s.row[ct][t];
+    if (ct < rt) return x * *reinterpret_cast<const f4 *>(&s.col[16 * ct + g4]) * s.row[ct][t];
     const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * ct + g4]);
     const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * ct + g4]);
     const float ht = s.hi[t], lt = s.lo[t];
-    f4 f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = g4 + j <= l16 ? exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
-    return f;
+    for (int j = 0; j < 4; ++j)
+        x[j] = g4 + j <= l16 ? x[j] * exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
+    return x;
 }
-// Rows t = 16rt + 4g + j and columns s = 16ct + l16:
+// Two tiles (x, y) with rows t = 16rt + 4g + j and columns s = 16ct + l16:
 template <int C>
-__device__ __forceinline__ f4 decay_ts(const Decay<C> &s, int rt, int ct, int l16, int g4)
+__device__ __forceinline__ void decayed_ts(const Decay<C> &s, f4 *x, f4 *y, int rt, int ct, int l16,
+                                           int g4)
 {
     const int u = 16 * ct + l16;
-    if (ct < rt) return *reinterpret_cast<const f4 *>(&s.row[ct][16 * rt + g4]) * s.col[u];
+    if (ct < rt) {
+        const f4 f = *reinterpret_cast<const f4 *>(&s.row[ct][16 * rt + g4]) * s.col[u];
+        *x *= f;
+        *y *= f;
+        return;
+    }
     const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * rt + g4]);
     const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * rt + g4]);
     const float hs = s.hi[u], ls = s.lo[u];
-    f4 f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = g4 + j >= l16 ? exp2_((hi[j] - hs) + (lo[j] - ls)) : 0.f;
-    return f;
-}
-// The factor zero also where the score is an infinity or NaN.
-__device__ __forceinline__ f4 times(f4 x, f4 f, bool diagonal)
-{
-    if (!diagonal) return x * f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = f[j] != 0.f ? x[j] * f[j] : 0.f;
-    return x;
+    for (int j = 0; j < 4; ++j) {
+        const float f = exp2_((hi[j] - hs) + (lo[j] - ls));
+        (*x)[j] = g4 + j >= l16 ? (*x)[j] * f : 0.f;
+        (*y)[j] = g4 + j >= l16 ? (*y)[j] * f : 0.f;
+    }
 }
 
 // --------------------------------------------------------------- forward
 
 // One workgroup walks a unit's chunks for one head and 64 columns of its
 // state.  Wavefront w keeps columns 16w .. 16w+15 of every row in
-// accumulators, which are operands of S^T Q^T as they are.  It forms the
-// scores K Q^T of the whole chunk itself (in that order a tile's accumulators
-// are operands of V^T P^T, so scores go through no LDS and wait for no other
-// wavefront; the four-fold score products are a third of its MFMA time) and
-// the outputs transposed, four columns of a token per lane, stored as they
-// are.  The next chunk's rows are requested while this one is computed and
-// its decays are formed meanwhile by one wavefront.
+// accumulators, which are operands of S^T Q^T as they are.  The ten (three)
+// tiles of scores K Q^T on and below the diagonal are shared out to the four
+// wavefronts; in that order a tile's accumulators are operands of V^T P^T, so
+// they pass through LDS as they are, sixteen bytes per lane.  Outputs are
+// formed transposed, four columns of a token per lane, stored as they are.
+// The next chunk's rows are requested while this one is computed, and its
+// decays are formed meanwhile by a wavefront with fewer tiles.
 template <class T, int NK>
-__global__ void __launch_bounds__(kSThreads)
+__global__ void __launch_bounds__(kSThreads, 2)
 gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 {
     typedef typename T::S S;
@@ -640,9 +643,12 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     typedef Tile<T, NK * 32> TK;
     typedef Tile<T, kSlice> TV;
     constexpr int C = T::C, RT = C / 16, KS = C / 32;
+    // operands of the scores: columns 16r .. of tokens 32kk .., at r + RT kk
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes];
+    __shared__ Frag pt[RT * KS][64];
     __shared__ Decay<C> dcs[2];
     __shared__ int bad[2], first[kSlice];
+    constexpr int GW = 3;  // the wavefront of the decays
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
@@ -692,43 +698,57 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
         sk.load(te - t0, C * a.ks.t, tid);
         sv.load(te - t0, C * a.vs.t, tid);
     };
+    // scores of columns 16r .. with tokens 32kk ..
+    auto score = [&](const Decay<C> &dc, int r, int kk) {
+        f4 p[2] = {zf4(), zf4()};
+        Frag qf[NK], f;
+        GSCAN_STEP();
+#pragma unroll
+        for (int k = 0; k < NK; ++k) qf[k] = lk.row(qt, 16 * r, k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int ct = 2 * kk + i;
+            if (ct > r) continue;
+#pragma unroll
+            for (int k = 0; k < NK; ++k) p[i] = mma(lk.row(kt, 16 * ct, k), qf[k], p[i]);
+            p[i] = decayed_st(dc, p[i], r, ct, l16, g4);
+        }
+        to_frag(p[0], p[1], &f);
+        pt[r + RT * kk][lane] = f;
+    };
+    auto scores = [&](const Decay<C> &dc) {
+        if constexpr (RT == 4) {
+            if (w == 0) {
+                score(dc, 0, 0);
+                score(dc, 1, 0);
+            } else if (w == 1) {
+                score(dc, 2, 0);
+                score(dc, 2, 1);
+            } else {
+                score(dc, 3, w - 2);
+            }
+        } else if (w < 2) {
+            score(dc, w, 0);
+        }
+    };
     // outputs and state of the staged chunk
     auto compute = [&](const Decay<C> &dc, int t0, bool nan) {
         const __amdgpu_buffer_rsrc_t ob = buffer(op);
-        Frag vf[KS], sf[NK], kf[RT][NK];
+        Frag vf[KS], sf[NK];
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) vf[kk] = TV(lane).at_col(vt, 32 * kk, vcol);
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) to_frag(st[2 * kk], st[2 * kk + 1], &sf[kk]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            Frag qf[NK];
-            f4 o = zf4(), p[RT];
-            GSCAN_STEP();
+            f4 o = zf4();
+            if (r % 2 == 0) GSCAN_STEP();
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) {
-                qf[kk] = lk.row(qt, 16 * r, kk);
-                kf[r][kk] = lk.row(kt, 16 * r, kk);
-            }
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) o = mma(sf[kk], qf[kk], o);
-#pragma unroll
-            for (int ct = 0; ct < RT; ++ct) {
-                p[ct] = zf4();
-                if (ct > r) continue;
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) p[ct] = mma(kf[ct][kk], qf[kk], p[ct]);
-                p[ct] = times(p[ct], decay_st(dc, r, ct, l16, g4), ct == r);
-            }
+            for (int kk = 0; kk < NK; ++kk) o = mma(sf[kk], lk.row(qt, 16 * r, kk), o);
             o *= dc.e[16 * r + l16];
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                if (2 * kk > r) continue;
-                Frag pf;
-                to_frag(p[2 * kk], p[2 * kk + 1], &pf);
-                o = mma(vf[kk], pf, o);
-            }
-            if (nan) o = poison<false>(o, &first[16 * w + g4], 16 * r + l16);
+            for (int kk = 0; kk < KS; ++kk)
+                if (2 * kk <= r) o = mma(vf[kk], pt[r + RT * kk][lane], o);
             store4(ob, t0 + 16 * r + l16 < te && o0 != kNowhere ? o0 + 16 * r * ost : kNowhere,
                    a.scale * o, T());
         }
@@ -750,19 +770,27 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) st[i] = mma_parts(lk.col(kt, 32 * kk, i), vs[kk], st[i]);
         }
-        if (nan && first[col] < C)
+        if (nan) {
+            for (int r = 0; r < RT; ++r)
+                for (int j = 0; j < 4; ++j)
+                    if (t0 + 16 * r + l16 < te && 16 * w + g4 + j < vcols &&
+                        16 * r + l16 >= first[16 * w + g4 + j])
+                        put1(const_cast<S *>(op) + (int64_t)(16 * r + l16) * a.H * a.Dv + h * a.Dv + c0 +
+                                 16 * w + g4 + j, __builtin_nanf(""));
+            if (first[col] < C)
 #pragma unroll
-            for (int i = 0; i < 2 * NK; ++i) st[i] = zf4() + __builtin_nanf("");
+                for (int i = 0; i < 2 * NK; ++i) st[i] = zf4() + __builtin_nanf("");
+        }
     };
     auto request_gate = [&](int t0) {
-        if (w == 0 && lane < C && t0 + lane < te)
+        if (w == GW && lane < C && t0 + lane < te)
             gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
     };
     if (tid < 2) bad[tid] = 0;
     if (tid < kSlice) first[tid] = C;
     request_gate(tb);
     request(tb);
-    if (w == 0) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
+    if (w == GW) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
     request_gate(tb + C);
     __syncthreads();
 
@@ -778,13 +806,13 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
         });
         __syncthreads();
         if (tid == 0) bad[odd ^ 1] = 0;
-        if (t0 + C < te) {
-            request(t0 + C);
-            if (w == 0) {
-                gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
-                request_gate(t0 + 2 * C);
-            }
+        if (t0 + C < te) request(t0 + C);
+        scores(dc);
+        if (w == GW && t0 + C < te) {
+            gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
+            request_gate(t0 + 2 * C);
         }
+        __syncthreads();
         const bool nan = bad[odd] != 0;
         compute(dc, t0, nan);
         op += (int64_t)C * a.H * a.Dv;
@@ -935,7 +963,7 @@ struct PassLds {
 // it (REV: to the gradient of the state before it) and the product of its
 // gates.  fp32 [units][H][Dk][Dv] and [units][H] at st_part, st_dec.
 template <class T, int NK, bool REV>
-__global__ void __launch_bounds__(kSThreads)
+__global__ void __launch_bounds__(kSThreads, 2)
 gscan_state_part_kernel(StateArgs a, int slices, int64_t per, size_t st_part, size_t st_dec)
 {
     __shared__ __align__(16) char smem[PassLds<T, NK>::bytes];
@@ -1026,7 +1054,7 @@ struct PassWs {
 };
 
 template <class T, int NK, int NV>
-__global__ void __launch_bounds__(kSThreads)
+__global__ void __launch_bounds__(kSThreads, 2)
 gscan_state_pass_kernel(StateArgs a, int64_t tokens, PassWs o)
 {
     constexpr int NM = NK > NV ? NK : NV;
@@ -1183,7 +1211,7 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                 if (ct <= rt) {
 #pragma unroll
                     for (int kk = 0; kk < NV; ++kk) p[ct] = mma(lv.row(vt, 16 * ct, kk), of[kk], p[ct]);
-                    p[ct] = times(p[ct], a.scale * decay_st(dc, rt, ct, l16, g4), ct == rt);
+                    p[ct] = decayed_st(dc, a.scale * p[ct], rt, ct, l16, g4);
                 }
             }
 #pragma unroll
@@ -1237,9 +1265,9 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                     for (int kk = 0; kk < NK; ++kk) x = mma(lk.row(qt, 16 * ut, kk), kf[kk], x);
 #pragma unroll
                     for (int kk = 0; kk < NV; ++kk) y = mma(lv.row(ot, 16 * ut, kk), vf[kk], y);
-                    const f4 f = a.scale * decay_ts(dc, ut, rt, l16, g4);
-                    p[ut] = times(x, f, ut == rt);
-                    d[ut] = times(y, f, ut == rt);
+                    p[ut] = a.scale * x;
+                    d[ut] = a.scale * y;
+                    decayed_ts(dc, &p[ut], &d[ut], ut, rt, l16, g4);
                     // W below the diagonal: sums over s < t of the tile's
                     // columns, for u >= t
 #pragma unroll
