@@ -269,14 +269,29 @@ __device__ __forceinline__ void to_parts(f4 x, f4 y, Parts *s)
         }
 }
 __device__ __forceinline__ void to_parts(f4 x, f4 y, FP::Frag *s) { *s = FP::Frag{x, y}; }
-__device__ __forceinline__ f4 mma_parts(const u4 &a, const Parts &b, f4 c)
+template <int N>
+__device__ __forceinline__ void mma_all(f4 (&st)[N], const u4 (&x)[N], const Parts &y)
 {
-    return mma(a, b.p[0], mma(a, b.p[1], mma(a, b.p[2], c)));
+#pragma unroll
+    for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int i = 0; i < N; ++i) st[i] = mma(x[i], y.p[p], st[i]);
 }
-__device__ __forceinline__ f4 mma_parts(const FP::Frag &a, const FP::Frag &b, f4 c)
+template <int N>
+__device__ __forceinline__ void mma_all(f4 (&st)[N], const FP::Frag (&x)[N], const FP::Frag &y)
 {
-    return mma(a, b, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) st[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i].a[j], y.a[j], st[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) st[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i].b[j], y.b[j], st[i], 0, 0, 0);
+    }
 }
+
 template <class T>
 struct PartsOf {
     typedef Parts type;
@@ -448,12 +463,49 @@ __device__ __forceinline__ const S *rows_of(const void *p, const Strides &s, con
            (int64_t)h * s.h;
 }
 
+// Gate arguments of a chunk's tokens, one per lane (those from `left` on: zero),
+// either type without a branch, so that the loads in flight can be counted.
+struct Gates {
+    const char *base;
+    uint32_t o32, o16;
+    int64_t step;
+    __device__ __forceinline__ void begin(const StateArgs &a, const Unit &w, int h, int64_t t0, int C,
+                                          int lane)
+    {
+        const int64_t e = a.gate_dtype ? 2 : 4;
+        base = reinterpret_cast<const char *>(a.gate) +
+               ((a.off ? w.in0 * a.gs.t : (int64_t)w.seq * a.gs.b) + (int64_t)h * a.gs.h + t0 * a.gs.t) * e;
+        const uint32_t at = (uint32_t)(lane * (int)a.gs.t) * (uint32_t)e;
+        o32 = lane < C && !a.gate_dtype ? at : kNowhere;
+        o16 = lane < C && a.gate_dtype ? at : kNowhere;
+        step = C * a.gs.t * e;
+    }
+    struct Raw {
+        uint32_t x32;
+        uint16_t x16;
+    };
+    // the next chunk's, and on by `dir` chunks
+    __device__ __forceinline__ Raw load(int left, int lane, int dir)
+    {
+        const __amdgpu_buffer_rsrc_t b = buffer(base);
+        Raw r;
+        r.x32 = __builtin_amdgcn_raw_buffer_load_b32(b, lane < left ? o32 : kNowhere, 0, 0);
+        r.x16 = __builtin_amdgcn_raw_buffer_load_b16(b, lane < left ? o16 : kNowhere, 0, 0);
+        base += dir * step;
+        return r;
+    }
+    static __device__ __forceinline__ float value(const Raw &r, const StateArgs &a)
+    {
+        return __uint_as_float(r.x32 | (uint32_t)r.x16 << 16) + a.gate_shift;
+    }
+};
+
 // ---------------------------------------------------------- staged tiles
 
 // C rows of NKU 32-wide units, 16 bytes at a time: NKU pieces per thread.
 template <class T, int NKU>
 struct Stage {
-    u4 r[NKU];
+    typedef u4 Regs[NKU];
     uint32_t off[NKU];  // of the pieces from the chunk's first row
     const typename T::S *base;  // that row
     static constexpr int kPpr = NKU * 32 / T::VE;  // pieces per row
@@ -472,7 +524,7 @@ struct Stage {
     }
     // the first `left` rows of the tile (the others zero), and on by `step`
     // elements to the next
-    __device__ __forceinline__ void load(int left, int64_t step, int tid)
+    __device__ __forceinline__ void load(Regs &r, int left, int64_t step, int tid)
     {
         const __amdgpu_buffer_rsrc_t b = buffer(base);
 #pragma unroll
@@ -483,7 +535,7 @@ struct Stage {
         base += step;
     }
     template <class TL>
-    __device__ __forceinline__ void store(char *tile, int tid) const
+    __device__ __forceinline__ void store(const Regs &r, char *tile, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < NKU; ++i) {
@@ -497,7 +549,7 @@ struct Stage {
     // they do reach is not finite in any case (the whole column of the state
     // from that token on), so those results become NaN without being computed.
     template <class TL, class F>
-    __device__ __forceinline__ void scrub(char *tile, int tid, F found) const
+    __device__ __forceinline__ void scrub(const Regs &r, char *tile, int tid, F found) const
     {
         uint32_t m = 0;
 #pragma unroll
@@ -623,19 +675,55 @@ __device__ __forceinline__ void decayed_ts(const Decay<C> &s, f4 *x, f4 *y, int 
     }
 }
 
+// st = g st + mul X^T (m . y) of a staged tile X: y is an operand of 16 columns of
+// the chunk, m a factor per token.  Accumulators in turn, so that products
+// which follow each other do not wait for each other.
+template <class T, int NX, class TX, class F>
+__device__ __forceinline__ void add_decayed(f4 (&st)[2 * NX], const F (&y)[T::C / 32], const float *m,
+                                            float mul, float g, const TX &lx, const char *xt, int g4)
+{
+    constexpr int KS = T::C / 32;
+    typename PartsOf<T>::type ys[KS];
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+        f4 a, b;
+        from_frag(y[kk], &a, &b);
+        a *= mul * *reinterpret_cast<const f4 *>(&m[32 * kk + g4]);
+        b *= mul * *reinterpret_cast<const f4 *>(&m[32 * kk + 16 + g4]);
+        to_parts(a, b, &ys[kk]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NX; ++i) st[i] *= g;
+    F xf[2][2 * NX];
+#pragma unroll
+    for (int i = 0; i < 2 * NX; ++i) xf[0][i] = lx.col(xt, 0, i);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+        if (kk + 1 < KS)
+#pragma unroll
+            for (int i = 0; i < 2 * NX; ++i) xf[1][i] = lx.col(xt, 32, i);
+        mma_all(st, xf[kk & 1], ys[kk]);
+    }
+}
+
 // --------------------------------------------------------------- forward
 
 // One workgroup walks a unit's chunks for one head and 64 columns of its
-// state.  Wavefront w keeps columns 16w .. 16w+15 of every row in
+// state.  What a chunk needs before its state is known does not wait for it:
+// wavefronts 4-7 bring chunk n + 1 (its rows into LDS, its decays, then its
+// scores) while wavefronts 0-3 finish chunk n (its outputs, then the state),
+// two steps a chunk with a barrier after each; tiles and scores are kept
+// twice, decays three times.  (All of it in turn by the same four wavefronts took 3 us a
+// chunk, one workgroup per CU, most of it waiting.)
+//
+// Wavefront w < 4 keeps columns 16w .. 16w+15 of every row of the state in
 // accumulators, which are operands of S^T Q^T as they are.  The ten (three)
-// tiles of scores K Q^T on and below the diagonal are shared out to the four
-// wavefronts; in that order a tile's accumulators are operands of V^T P^T, so
-// they pass through LDS as they are, sixteen bytes per lane.  Outputs are
-// formed transposed, four columns of a token per lane, stored as they are.
-// The next chunk's rows are requested while this one is computed, and its
-// decays are formed meanwhile by a wavefront with fewer tiles.
+// tiles of scores K Q^T on and below the diagonal are shared out to the other
+// four; in that order a tile's accumulators are operands of V^T P^T, so they
+// pass through LDS as they are, sixteen bytes per lane.  Outputs are formed
+// transposed, four columns of a token per lane, stored as they are.
 template <class T, int NK>
-__global__ void __launch_bounds__(kSThreads, 2)
+__global__ void __launch_bounds__(2 * kSThreads, 2)
 gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 {
     typedef typename T::S S;
@@ -643,14 +731,19 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     typedef Tile<T, NK * 32> TK;
     typedef Tile<T, kSlice> TV;
     constexpr int C = T::C, RT = C / 16, KS = C / 32;
+    constexpr int kQ = 0, kK = C * TK::bytes, kV = 2 * C * TK::bytes, kBuf = kV + C * TV::bytes;
+    // (the loads in flight are counted in order, so the chunks are walked in
+    // pairs without a branch around either)
+    __shared__ __align__(16) char tiles[2][kBuf];
     // operands of the scores: columns 16r .. of tokens 32kk .., at r + RT kk
-    __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes];
-    __shared__ Frag pt[RT * KS][64];
-    __shared__ Decay<C> dcs[2];
-    __shared__ int bad[2], first[kSlice];
-    constexpr int GW = 3;  // the wavefront of the decays
+    __shared__ Frag pts[2][RT * KS][64];
+    __shared__ Decay<C> dcs[3];  // of chunk n - 1 (its state), n (its scores), n + 1 (being formed)
+    __shared__ int bad[2], first[2][kSlice];
+    constexpr int GW = 3;  // the wavefront (of its four) that forms the decays
 
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x & (kSThreads - 1), lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool brings = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int slice = blockIdx.x % slices;
     const int h = blockIdx.x / slices % a.H;
@@ -658,20 +751,108 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     Unit un;
     if (!find_unit(a, unit, per, C, lane, &un)) return;
     const bool packed = a.off != nullptr;
-    const int hk = h / (a.H / a.Hk), c0 = slice * kSlice, vcols = a.Dv - c0;
-    const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-    const int col = w * 16 + l16;  // this lane's column of the slice in the state
+    const int c0 = slice * kSlice, vcols = a.Dv - c0;
     const int tb = (int)(un.part * per);
     const int te = un.len - tb > per ? (int)(tb + per) : un.len;
+    const int nc = (te - tb + C - 1) / C;
     const TK lk(lane);
-    const uint32_t vcol = TV(lane).col_off(w);
-    // outputs: token 16r + l16, columns 16w + 4g .. +3
-    const S *op = reinterpret_cast<const S *>(a.out) + (un.tok0 + tb) * a.H * a.Dv;
-    const uint32_t ost = (uint32_t)(a.H * a.Dv * sizeof(S));
-    const uint32_t o0 = 16 * w + g4 < vcols
-        ? (uint32_t)(h * a.Dv + c0 + 16 * w + g4) * (uint32_t)sizeof(S) + l16 * ost : kNowhere;
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+    if (threadIdx.x < 2 * kSlice) first[0][threadIdx.x] = C;
+    __syncthreads();
 
-    // the state: row 16i + 4g + j of column `col`
+    if (brings) {
+        const int hk = h / (a.H / a.Hk);
+        // rows are requested two chunks ahead, into two sets of registers
+        Stage<T, NK> sq, sk;
+        Stage<T, 2> sv;
+        u4 rq[2][NK], rk[2][NK], rv[2][2];
+        Gates gates;
+        Gates::Raw gx[2];
+        gates.begin(a, un, h, tb, C, lane);
+        sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, tb, a.Dk, tid);
+        sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, tb, a.Dk, tid);
+        sv.begin(rows_of<S>(a.v, a.vs, un, packed, h) + c0, a.vs.t, tb, vcols, tid);
+        auto request = [&](int t0, auto set) {
+            constexpr int O = decltype(set)::value;
+            sq.load(rq[O], te - t0, C * a.qs.t, tid);
+            sk.load(rk[O], te - t0, C * a.ks.t, tid);
+            sv.load(rv[O], te - t0, C * a.vs.t, tid);
+            gx[O] = gates.load(te - t0, lane, 1);
+        };
+        request(tb, std::integral_constant<int, 0>());
+        request(tb + C, std::integral_constant<int, 1>());
+        auto bring = [&](int n, auto set) {
+            constexpr int odd = decltype(set)::value;
+            const int t0 = tb + n * C;
+            char *tile = tiles[odd];
+            const Decay<C> &dc = dcs[n % 3];
+            sq.template store<TK>(rq[odd], tile + kQ, tid);
+            sk.template store<TK>(rk[odd], tile + kK, tid);
+            sv.template store<TV>(rv[odd], tile + kV, tid);
+            sv.template scrub<TV>(rv[odd], tile + kV, tid, [&](int row, int c) {
+                atomicMin(&first[odd][c], row);
+                bad[odd] = 1;
+            });
+            request(t0 + 2 * C, set);
+            __syncthreads();
+            // scores of columns 16r .. with tokens 32kk ..
+            auto score = [&](auto rc, auto kc) {
+                constexpr int r = decltype(rc)::value, kk = decltype(kc)::value;
+                f4 p[2] = {zf4(), zf4()};
+                Frag qf[NK], kf[2][NK], f;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    qf[k] = lk.row(tile + kQ, 16 * r, k);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (2 * kk + i <= r) kf[i][k] = lk.row(tile + kK, 32 * kk + 16 * i, k);
+                }
+#pragma unroll
+                for (int k = 0; k < NK; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (2 * kk + i <= r) p[i] = mma(kf[i][k], qf[k], p[i]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (2 * kk + i <= r) p[i] = decayed_st(dc, p[i], r, 2 * kk + i, l16, g4);
+                to_frag(p[0], p[1], &f);
+                pts[odd][r + RT * kk][lane] = f;
+            };
+            using I0 = std::integral_constant<int, 0>;
+            using I1 = std::integral_constant<int, 1>;
+            using I2 = std::integral_constant<int, 2>;
+            using I3 = std::integral_constant<int, 3>;
+            if (w == GW) {
+                gate_scan<C>(dcs[(n + 1) % 3], Gates::value(gx[odd ^ 1], a), t0 + C + lane < te, a.gate_form, lane);
+            } else if constexpr (RT == 4) {
+                if (w == 0) {
+                    score(I0(), I0());
+                    score(I1(), I0());
+                } else if (w == 1) {
+                    score(I2(), I0());
+                    score(I2(), I1());
+                } else {
+                    score(I3(), I0());
+                    score(I3(), I1());
+                }
+            } else {
+                if (w == 0) score(I0(), I0());
+                else if (w == 1) score(I1(), I0());
+            }
+            __syncthreads();
+        };
+        if (w == GW) gate_scan<C>(dcs[0], Gates::value(gx[0], a), tb + lane < te, a.gate_form, lane);
+        for (int n = 0; n < nc; n += 2) {
+            bring(n, std::integral_constant<int, 0>());
+            bring(n + 1, std::integral_constant<int, 1>());  // past the end: empty rows
+        }
+        __syncthreads();
+        __syncthreads();
+        return;
+    }
+
+    // the state: row 16i + 4g + j of column `col` of the slice
+    const int col = w * 16 + l16;
     const int64_t srow = ((int64_t)un.seq * a.H + h) * a.Dk;
     const float *init = a.s0 ? a.s0 + srow * a.Dv : nullptr;
     if (un.part)
@@ -686,141 +867,76 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
             for (int j = 0; j < 4; ++j)
                 if (16 * i + g4 + j < a.Dk) st[i][j] = init[(16 * i + g4 + j) * a.Dv + c0 + col];
     }
-
-    Stage<T, NK> sq, sk;
-    Stage<T, 2> sv;
-    float gx = 0.f;
-    sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, tb, a.Dk, tid);
-    sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, tb, a.Dk, tid);
-    sv.begin(rows_of<S>(a.v, a.vs, un, packed, h) + c0, a.vs.t, tb, vcols, tid);
-    auto request = [&](int t0) {
-        sq.load(te - t0, C * a.qs.t, tid);
-        sk.load(te - t0, C * a.ks.t, tid);
-        sv.load(te - t0, C * a.vs.t, tid);
-    };
-    // scores of columns 16r .. with tokens 32kk ..
-    auto score = [&](const Decay<C> &dc, int r, int kk) {
-        f4 p[2] = {zf4(), zf4()};
-        Frag qf[NK], f;
-        GSCAN_STEP();
-#pragma unroll
-        for (int k = 0; k < NK; ++k) qf[k] = lk.row(qt, 16 * r, k);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int ct = 2 * kk + i;
-            if (ct > r) continue;
-#pragma unroll
-            for (int k = 0; k < NK; ++k) p[i] = mma(lk.row(kt, 16 * ct, k), qf[k], p[i]);
-            p[i] = decayed_st(dc, p[i], r, ct, l16, g4);
+    const uint32_t vcol = TV(lane).col_off(w);
+    // outputs: token 16r + l16, columns 16w + 4g .. +3
+    const S *op = reinterpret_cast<const S *>(a.out) + (un.tok0 + tb) * a.H * a.Dv;
+    const uint32_t ost = (uint32_t)(a.H * a.Dv * sizeof(S));
+    const uint32_t o0 = 16 * w + g4 < vcols
+        ? (uint32_t)(h * a.Dv + c0 + 16 * w + g4) * (uint32_t)sizeof(S) + l16 * ost : kNowhere;
+    __syncthreads();
+    __syncthreads();
+    for (int n = 0; n < (nc + 1) / 2 * 2; ++n) {
+        if (n == nc) {  // an empty chunk
+            __syncthreads();
+            __syncthreads();
+            break;
         }
-        to_frag(p[0], p[1], &f);
-        pt[r + RT * kk][lane] = f;
-    };
-    auto scores = [&](const Decay<C> &dc) {
-        if constexpr (RT == 4) {
-            if (w == 0) {
-                score(dc, 0, 0);
-                score(dc, 1, 0);
-            } else if (w == 1) {
-                score(dc, 2, 0);
-                score(dc, 2, 1);
-            } else {
-                score(dc, 3, w - 2);
+        const int t0 = tb + n * C, odd = n & 1;
+        const char *tile = tiles[odd];
+        const Decay<C> &dc = dcs[n % 3];
+        const bool nan = bad[odd] != 0;
+        const bool gone = first[odd][col] < C;
+        Frag vf[KS];
+        {
+            const __amdgpu_buffer_rsrc_t ob = buffer(op);
+            f4 x[RT], y[RT];
+            Frag qf[2][RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                x[r] = y[r] = zf4();
+                qf[0][r] = lk.row(tile + kQ, 16 * r, 0);
             }
-        } else if (w < 2) {
-            score(dc, w, 0);
-        }
-    };
-    // outputs and state of the staged chunk
-    auto compute = [&](const Decay<C> &dc, int t0, bool nan) {
-        const __amdgpu_buffer_rsrc_t ob = buffer(op);
-        Frag vf[KS], sf[NK];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) vf[kk] = TV(lane).at_col(vt, 32 * kk, vcol);
+            for (int kk = 0; kk < KS; ++kk) vf[kk] = TV(lane).at_col(tile + kV, 32 * kk, vcol);
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) to_frag(st[2 * kk], st[2 * kk + 1], &sf[kk]);
+            for (int kk = 0; kk < NK; ++kk) {
+                Frag sf;
+                to_frag(st[2 * kk], st[2 * kk + 1], &sf);
+                if (kk + 1 < NK)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            f4 o = zf4();
-            if (r % 2 == 0) GSCAN_STEP();
+                    for (int r = 0; r < RT; ++r) qf[(kk + 1) & 1][r] = lk.row(tile + kQ, 16 * r, kk + 1);
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) o = mma(sf[kk], lk.row(qt, 16 * r, kk), o);
-            o *= dc.e[16 * r + l16];
+                for (int r = 0; r < RT; ++r) x[r] = mma(sf, qf[kk & 1][r], x[r]);
+            }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk)
-                if (2 * kk <= r) o = mma(vf[kk], pt[r + RT * kk][lane], o);
-            store4(ob, t0 + 16 * r + l16 < te && o0 != kNowhere ? o0 + 16 * r * ost : kNowhere,
-                   a.scale * o, T());
-        }
-        // S' = e^(L_end) S + K^T (e^(L_end - L) V)
-        typename PartsOf<T>::type vs[KS];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-            f4 x, y;
-            from_frag(vf[kk], &x, &y);
-            x *= *reinterpret_cast<const f4 *>(&dc.d[32 * kk + g4]);
-            y *= *reinterpret_cast<const f4 *>(&dc.d[32 * kk + 16 + g4]);
-            to_parts(x, y, &vs[kk]);
-        }
-        const float ge = dc.g;
+                for (int r = 2 * kk; r < RT; ++r) y[r] = mma(vf[kk], pts[odd][r + RT * kk][lane], y[r]);
 #pragma unroll
-        for (int i = 0; i < 2 * NK; ++i) {
-            if (i % 2 == 0) GSCAN_STEP();
-            st[i] *= ge;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) st[i] = mma_parts(lk.col(kt, 32 * kk, i), vs[kk], st[i]);
+            for (int r = 0; r < RT; ++r)
+                store4(ob, t0 + 16 * r + l16 < te && o0 != kNowhere ? o0 + 16 * r * ost : kNowhere,
+                       a.scale * (dc.e[16 * r + l16] * x[r] + y[r]), T());
         }
         if (nan) {
             for (int r = 0; r < RT; ++r)
                 for (int j = 0; j < 4; ++j)
                     if (t0 + 16 * r + l16 < te && 16 * w + g4 + j < vcols &&
-                        16 * r + l16 >= first[16 * w + g4 + j])
+                        16 * r + l16 >= first[odd][16 * w + g4 + j])
                         put1(const_cast<S *>(op) + (int64_t)(16 * r + l16) * a.H * a.Dv + h * a.Dv + c0 +
                                  16 * w + g4 + j, __builtin_nanf(""));
-            if (first[col] < C)
-#pragma unroll
-                for (int i = 0; i < 2 * NK; ++i) st[i] = zf4() + __builtin_nanf("");
         }
-    };
-    auto request_gate = [&](int t0) {
-        if (w == GW && lane < C && t0 + lane < te)
-            gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
-    };
-    if (tid < 2) bad[tid] = 0;
-    if (tid < kSlice) first[tid] = C;
-    request_gate(tb);
-    request(tb);
-    if (w == GW) gate_scan<C>(dcs[0], gx, tb + lane < te, a.gate_form, lane);
-    request_gate(tb + C);
-    __syncthreads();
-
-    int odd = 0;
-    for (int t0 = tb; t0 < te; t0 += C, odd ^= 1) {
-        const Decay<C> &dc = dcs[odd];
-        sq.template store<TK>(qt, tid);
-        sk.template store<TK>(kt, tid);
-        sv.template store<TV>(vt, tid);
-        sv.template scrub<TV>(vt, tid, [&](int row, int c) {
-            atomicMin(&first[c], row);
-            bad[odd] = 1;
-        });
-        __syncthreads();
-        if (tid == 0) bad[odd ^ 1] = 0;
-        if (t0 + C < te) request(t0 + C);
-        scores(dc);
-        if (w == GW && t0 + C < te) {
-            gate_scan<C>(dcs[odd ^ 1], gx, t0 + C + lane < te, a.gate_form, lane);
-            request_gate(t0 + 2 * C);
-        }
-        __syncthreads();
-        const bool nan = bad[odd] != 0;
-        compute(dc, t0, nan);
         op += (int64_t)C * a.H * a.Dv;
         __syncthreads();
+        // S' = e^(L_end) S + K^T (e^(L_end - L) V)
+        add_decayed<T, NK>(st, vf, dc.d, 1.f, dc.g, lk, tile + kK, g4);
         if (nan) {
-            if (tid < kSlice) first[tid] = C;
-            __syncthreads();
+            if (gone)
+#pragma unroll
+                for (int i = 0; i < 2 * NK; ++i) st[i] = zf4() + __builtin_nanf("");
+            first[odd][col] = C;
+            if (tid == 0) bad[odd] = 0;
         }
+        __syncthreads();
     }
 
     if (a.sT && te == un.len && col < vcols) {
@@ -885,10 +1001,11 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     constexpr int step = REV ? -1 : 1;
     Stage<T, NX> sx;
     Stage<T, 2> sy;
+    u4 rx[NX], ry[2];
     float gx = 0.f, gall = 1.f;
     auto request = [&](int c) {
-        sx.load(te - c * C, step * C * jb.xs.t, tid);
-        sy.load(te - c * C, step * C * jb.ys.t, tid);
+        sx.load(rx, te - c * C, step * C * jb.xs.t, tid);
+        sy.load(ry, te - c * C, step * C * jb.ys.t, tid);
     };
     auto request_gate = [&](int c) {
         if (w == 0 && lane < C && c >= cb && c * C + lane < te)
@@ -904,8 +1021,8 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     int odd = 0;
     for (int n = ce - cb; n > 0; --n, c += step, odd ^= 1) {
         const Decay<C> &dc = dcs[odd];
-        sx.template store<TX>(xt, tid);
-        sy.template store<TY>(yt, tid);
+        sx.template store<TX>(rx, xt, tid);
+        sy.template store<TY>(ry, yt, tid);
         if constexpr (STORE) {  // the operands of this chunk, before its own tokens enter
 #pragma unroll
             for (int kk = 0; kk < NX; ++kk) {
@@ -923,25 +1040,11 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
                 request_gate(c + 2 * step);
             }
         }
-        typename PartsOf<T>::type ys[KS];
-        const float *m = REV ? dc.e : dc.d;
+        Frag yf[KS];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-            f4 x, y;
-            from_frag(TY(lane).at_col(yt, 32 * kk, ycol), &x, &y);
-            x *= jb.mul * *reinterpret_cast<const f4 *>(&m[32 * kk + g4]);
-            y *= jb.mul * *reinterpret_cast<const f4 *>(&m[32 * kk + 16 + g4]);
-            to_parts(x, y, &ys[kk]);
-        }
-        const float ge = dc.g;
-        gall *= ge;
-#pragma unroll
-        for (int i = 0; i < 2 * NX; ++i) {
-            st[i] *= ge;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-                st[i] = mma_parts(lx.col(xt, 32 * kk, i), ys[kk], st[i]);
-        }
+        for (int kk = 0; kk < KS; ++kk) yf[kk] = TY(lane).at_col(yt, 32 * kk, ycol);
+        gall *= dc.g;
+        add_decayed<T, NX>(st, yf, REV ? dc.e : dc.d, jb.mul, dc.g, lx, xt, g4);
         __syncthreads();
     }
     if (jb.fin && col < ycols) {
@@ -1137,12 +1240,13 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
     const bool mine = 16 * rt + l16 < left;  // this lane's token exists
 
     Stage<T, NV> sv, so;
+    u4 rv[NV], ro[NV];
     float gx = 0.f;
     auto request = [&](int h) {
         sv.begin(rows_of<S>(a.v, a.vs, un, packed, h), a.vs.t, t0, a.Dv, tid);
         so.begin(rows_of<S>(a.dout, a.ds, un, packed, h), a.ds.t, t0, a.Dv, tid);
-        sv.load(left, 0, tid);
-        so.load(left, 0, tid);
+        sv.load(rv, left, 0, tid);
+        so.load(ro, left, 0, tid);
         if (w == 0) {
             const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
             if (lane < C && lane < left)
@@ -1160,19 +1264,20 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
     __syncthreads();
     {
         Stage<T, NK> sq, sk;
+        u4 rq[NK], rk[NK];
         sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, t0, a.Dk, tid);
         sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, t0, a.Dk, tid);
-        sq.load(left, 0, tid);
-        sk.load(left, 0, tid);
+        sq.load(rq, left, 0, tid);
+        sk.load(rk, left, 0, tid);
         request(hk * reps);
-        sq.template store<TK>(qt, tid);
-        sk.template store<TK>(kt, tid);
-        sq.template scrub<TK>(qt, tid, [&](int row, int c) {
+        sq.template store<TK>(rq, qt, tid);
+        sk.template store<TK>(rk, kt, tid);
+        sq.template scrub<TK>(rq, qt, tid, [&](int row, int c) {
             atomicMax(&last_q[c], row);
             atomicMax(&ends[0], row);
             bad = 1;
         });
-        sk.template scrub<TK>(kt, tid, [&](int row, int c) {
+        sk.template scrub<TK>(rk, kt, tid, [&](int row, int c) {
             atomicMin(&first_k[c], row);
             atomicMin(&ends[2], row);
             row_k[row] = 1;
@@ -1378,9 +1483,9 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
 
     for (int hr = 0; hr < reps; ++hr) {
         const int h = hk * reps + hr;
-        sv.template store<TV>(vt, tid);
-        so.template store<TV>(ot, tid);
-        so.template scrub<TV>(ot, tid, [&](int row, int c) {
+        sv.template store<TV>(rv, vt, tid);
+        so.template store<TV>(ro, ot, tid);
+        so.template scrub<TV>(ro, ot, tid, [&](int row, int c) {
             atomicMax(&last_o[c], row);
             atomicMax(&ends[1], row);
             row_o[row] = 1;
@@ -1479,7 +1584,7 @@ hipError_t fwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((gscan_state_fwd_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices)),
-                       dim3(kSThreads), 0, st, a, slices, p.per, p.st_part);
+                       dim3(2 * kSThreads), 0, st, a, slices, p.per, p.st_part);
     return hipGetLastError();
 }
 
