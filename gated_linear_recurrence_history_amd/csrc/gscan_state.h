@@ -43,7 +43,7 @@ struct StatePlan {
     size_t st_part = 0, st_dec = 0;  // workspace: what the units add to the state, their decays
     size_t st_part_r = 0, st_dec_r = 0;  // backward: the same of the state's gradient
     int64_t chunks = 0;       // chunk slots over all sequences (an upper bound when packed)
-    size_t st_kv = 0, st_gt = 0, st_g = 0;  // workspace offsets of the backward's chunk states
+    size_t st_s = 0, st_ds = 0;  // workspace: the backward's chunk states and their gradients
     size_t bytes = 0;
 };
 

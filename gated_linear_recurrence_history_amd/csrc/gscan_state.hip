@@ -502,11 +502,12 @@ struct Gates {
 
 // ---------------------------------------------------------- staged tiles
 
-// C rows of NKU 32-wide units, 16 bytes at a time: NKU pieces per thread.
-template <class T, int NKU>
+// C rows of NKU 32-wide units, 16 bytes at a time, by TH threads.
+template <class T, int NKU, int TH = kSThreads>
 struct Stage {
-    typedef u4 Regs[NKU];
-    uint32_t off[NKU];  // of the pieces from the chunk's first row
+    static constexpr int N = NKU * kSThreads / TH;  // pieces per thread
+    typedef u4 Regs[N];
+    uint32_t off[N];  // of the pieces from the chunk's first row
     const typename T::S *base;  // that row
     static constexpr int kPpr = NKU * 32 / T::VE;  // pieces per row
 
@@ -517,8 +518,8 @@ struct Stage {
     {
         base = rows + t0 * st;
 #pragma unroll
-        for (int i = 0; i < NKU; ++i) {
-            const int q = tid + kSThreads * i, row = q / kPpr, col = q % kPpr * T::VE;
+        for (int i = 0; i < N; ++i) {
+            const int q = tid + TH * i, row = q / kPpr, col = q % kPpr * T::VE;
             off[i] = col < cols ? (uint32_t)(row * (int)st + col) * (uint32_t)sizeof(typename T::S) : kNowhere;
         }
     }
@@ -528,8 +529,8 @@ struct Stage {
     {
         const __amdgpu_buffer_rsrc_t b = buffer(base);
 #pragma unroll
-        for (int i = 0; i < NKU; ++i) {
-            const int row = (tid + kSThreads * i) / kPpr;
+        for (int i = 0; i < N; ++i) {
+            const int row = (tid + TH * i) / kPpr;
             r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, row < left ? off[i] : kNowhere, 0, 0);
         }
         base += step;
@@ -538,8 +539,8 @@ struct Stage {
     __device__ __forceinline__ void store(const Regs &r, char *tile, int tid) const
     {
 #pragma unroll
-        for (int i = 0; i < NKU; ++i) {
-            const int q = tid + kSThreads * i;
+        for (int i = 0; i < N; ++i) {
+            const int q = tid + TH * i;
             TL::put(tile, q / kPpr, q % kPpr * T::VE, r[i]);
         }
     }
@@ -553,11 +554,11 @@ struct Stage {
     {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < NKU; ++i) magnitude(r[i], T(), &m);
+        for (int i = 0; i < N; ++i) magnitude(r[i], T(), &m);
         if (!nonfinite(m, T())) return;
 #pragma unroll 1
-        for (int i = 0; i < NKU * T::VE; ++i) {
-            const int q = tid + kSThreads * (i / T::VE), row = q / kPpr, col = q % kPpr * T::VE + i % T::VE;
+        for (int i = 0; i < N * T::VE; ++i) {
+            const int q = tid + TH * (i / T::VE), row = q / kPpr, col = q % kPpr * T::VE + i % T::VE;
             if (TL::scrub(tile, row, col)) found(row, col);
         }
     }
@@ -694,15 +695,12 @@ __device__ __forceinline__ void add_decayed(f4 (&st)[2 * NX], const F (&y)[T::C 
     }
 #pragma unroll
     for (int i = 0; i < 2 * NX; ++i) st[i] *= g;
-    F xf[2][2 * NX];
-#pragma unroll
-    for (int i = 0; i < 2 * NX; ++i) xf[0][i] = lx.col(xt, 0, i);
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
-        if (kk + 1 < KS)
+        F xf[2 * NX];
 #pragma unroll
-            for (int i = 0; i < 2 * NX; ++i) xf[1][i] = lx.col(xt, 32, i);
-        mma_all(st, xf[kk & 1], ys[kk]);
+        for (int i = 0; i < 2 * NX; ++i) xf[i] = lx.col(xt, 32 * kk, i);
+        mma_all(st, xf, ys[kk]);
     }
 }
 
@@ -969,23 +967,72 @@ struct PassJob {
     float mul;           // factor of what is added
 };
 
+// Wavefronts 4-7 bring the next chunk's rows and decays into LDS while
+// wavefronts 0-3 add this one's, one barrier a chunk.
+template <class T, int NX>
+struct PassLds {
+    static constexpr int kX = T::C * Tile<T, NX * 32>::bytes, kBuf = kX + T::C * Tile<T, kSlice>::bytes;
+    char tile[2][kBuf];
+};
+
 template <class T, int NX, bool REV, bool STORE>
 __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb, int ny, int slice,
-                                          int h, const Unit &un, int tb, int te, char *smem,
+                                          int h, const Unit &un, int tb, int te, void *smem,
                                           Decay<T::C> (&dcs)[2])
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
     typedef Tile<T, NX * 32> TX;
     typedef Tile<T, kSlice> TY;
-    constexpr int C = T::C, KS = C / 32;
-    char *xt = smem, *yt = xt + C * TX::bytes;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    typedef PassLds<T, NX> Lds;
+    constexpr int C = T::C, KS = C / 32, step = REV ? -1 : 1, GW = 3;
+    Lds &lds = *reinterpret_cast<Lds *>(smem);
+    const int tid = threadIdx.x & (kSThreads - 1), lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool brings = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const bool packed = a.off != nullptr;
-    const int c0 = slice * kSlice, ycols = jb.yd - c0, col = 16 * w + l16;
-    const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-    const int sb = (c0 + col) * jb.cstr;
+    const int c0 = slice * kSlice, ycols = jb.yd - c0;
+    const int cb = tb / C, nc = te > tb ? (te + C - 1) / C - cb : 1;  // chunks, at least one
+    const int c1 = REV ? cb + nc - 1 : cb;                           // the first walked
+
+    if (brings) {
+        Stage<T, NX> sx;
+        Stage<T, 2> sy;
+        Gates gates;
+        u4 rx[2][NX], ry[2][2];
+        Gates::Raw gx[2];
+        sx.begin(rows_of<S>(jb.x, jb.xs, un, packed, jb.xh), jb.xs.t, c1 * C, jb.xd, tid);
+        sy.begin(rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0, jb.ys.t, c1 * C, ycols, tid);
+        gates.begin(a, un, h, c1 * C, C, lane);
+        // chunks past the end (in either direction) have no rows
+        auto request = [&](int n, auto set) {
+            constexpr int O = decltype(set)::value;
+            const int left = n < nc ? te - (c1 + step * n) * C : 0;
+            sx.load(rx[O], left, step * C * jb.xs.t, tid);
+            sy.load(ry[O], left, step * C * jb.ys.t, tid);
+            gx[O] = gates.load(left, lane, step);
+        };
+        auto bring = [&](int n, auto set) {
+            constexpr int odd = decltype(set)::value;
+            sx.template store<TX>(rx[odd], lds.tile[odd], tid);
+            sy.template store<TY>(ry[odd], lds.tile[odd] + Lds::kX, tid);
+            if (w == GW)
+                gate_scan<C>(dcs[odd], Gates::value(gx[odd], a), lane < te - (c1 + step * n) * C,
+                             a.gate_form, lane);
+            request(n + 2, set);
+            __syncthreads();
+        };
+        request(0, std::integral_constant<int, 0>());
+        request(1, std::integral_constant<int, 1>());
+        for (int n = 0; n < nc; n += 2) {
+            bring(n, std::integral_constant<int, 0>());
+            bring(n + 1, std::integral_constant<int, 1>());
+        }
+        return;
+    }
+
+    const int col = 16 * w + l16, sb = (c0 + col) * jb.cstr;
     const TX lx(lane);
     const uint32_t ycol = TY(lane).col_off(w);
     f4 st[2 * NX];
@@ -997,55 +1044,26 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             for (int j = 0; j < 4; ++j)
                 if (16 * i + g4 + j < jb.xd) st[i][j] = jb.init[sb + (16 * i + g4 + j) * jb.rstr];
     }
-    const int cb = tb / C, ce = te > tb ? (te + C - 1) / C : cb + 1;  // chunks
-    constexpr int step = REV ? -1 : 1;
-    Stage<T, NX> sx;
-    Stage<T, 2> sy;
-    u4 rx[NX], ry[2];
-    float gx = 0.f, gall = 1.f;
-    auto request = [&](int c) {
-        sx.load(rx, te - c * C, step * C * jb.xs.t, tid);
-        sy.load(ry, te - c * C, step * C * jb.ys.t, tid);
-    };
-    auto request_gate = [&](int c) {
-        if (w == 0 && lane < C && c >= cb && c * C + lane < te)
-            gx = load_scalar(a.gate, g0 + (int64_t)(c * C + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
-    };
-    int c = REV ? ce - 1 : cb;
-    sx.begin(rows_of<S>(jb.x, jb.xs, un, packed, jb.xh), jb.xs.t, c * C, jb.xd, tid);
-    sy.begin(rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0, jb.ys.t, c * C, ycols, tid);
-    request_gate(c);
-    request(c);
-    if (w == 0) gate_scan<C>(dcs[0], gx, c * C + lane < te, a.gate_form, lane);
-    request_gate(c + step);
-    int odd = 0;
-    for (int n = ce - cb; n > 0; --n, c += step, odd ^= 1) {
+    float gall = 1.f;
+    for (int n = 0; n < (nc + 1) / 2 * 2; ++n) {
+        __syncthreads();
+        if (n == nc) break;  // the empty chunk of the last pair
+        const int odd = n & 1;
         const Decay<C> &dc = dcs[odd];
-        sx.template store<TX>(rx, xt, tid);
-        sy.template store<TY>(ry, yt, tid);
         if constexpr (STORE) {  // the operands of this chunk, before its own tokens enter
 #pragma unroll
             for (int kk = 0; kk < NX; ++kk) {
                 Frag f;
                 to_frag(st[2 * kk], st[2 * kk + 1], &f);
-                put_frag(jb.dst, (((int64_t)(un.slot0 + c) * a.H + h) * 2 * ny + slice * 4 + w) * NX + kk,
-                         lane, f);
-            }
-        }
-        __syncthreads();
-        if (n > 1) {
-            request(c + step);
-            if (w == 0) {
-                gate_scan<C>(dcs[odd ^ 1], gx, (c + step) * C + lane < te, a.gate_form, lane);
-                request_gate(c + 2 * step);
+                put_frag(jb.dst, (((int64_t)(un.slot0 + c1 + step * n) * a.H + h) * 2 * ny +
+                                  slice * 4 + w) * NX + kk, lane, f);
             }
         }
         Frag yf[KS];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) yf[kk] = TY(lane).at_col(yt, 32 * kk, ycol);
+        for (int kk = 0; kk < KS; ++kk) yf[kk] = TY(lane).at_col(lds.tile[odd] + Lds::kX, 32 * kk, ycol);
         gall *= dc.g;
-        add_decayed<T, NX>(st, yf, REV ? dc.e : dc.d, jb.mul, dc.g, lx, xt, g4);
-        __syncthreads();
+        add_decayed<T, NX>(st, yf, REV ? dc.e : dc.d, jb.mul, dc.g, lx, lds.tile[odd], g4);
     }
     if (jb.fin && col < ycols) {
 #pragma unroll
@@ -1057,45 +1075,49 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     if (jb.dec && slice == 0 && tid == 0) *jb.dec = gall;
 }
 
-template <class T, int NM>
-struct PassLds {
-    static constexpr size_t bytes = T::C * (Tile<T, NM * 32>::bytes + Tile<T, kSlice>::bytes);
+// Units of split sequences, by themselves: what a unit adds to the state after
+// it and, in the backward (ways == 2), to the gradient of the state before it;
+// and the product of its gates.  fp32 [units][H][Dk][Dv] and [units][H].
+struct Parts2 {
+    size_t st[2], dec[2];  // workspace offsets, forwards and backwards
 };
 
-// Units of split sequences, by themselves: what a unit adds to the state after
-// it (REV: to the gradient of the state before it) and the product of its
-// gates.  fp32 [units][H][Dk][Dv] and [units][H] at st_part, st_dec.
-template <class T, int NK, bool REV>
-__global__ void __launch_bounds__(kSThreads, 2)
-gscan_state_part_kernel(StateArgs a, int slices, int64_t per, size_t st_part, size_t st_dec)
+template <class T, int NK>
+__global__ void __launch_bounds__(2 * kSThreads, 2)
+gscan_state_part_kernel(StateArgs a, int slices, int ways, int64_t per, Parts2 o)
 {
-    __shared__ __align__(16) char smem[PassLds<T, NK>::bytes];
+    __shared__ __align__(16) PassLds<T, NK> smem;
     __shared__ Decay<T::C> dcs[2];
-    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices;
-    const int h = blockIdx.x / slices % a.H, hk = h / (a.H / a.Hk);
-    const int64_t unit = blockIdx.x / slices / a.H;
+    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices, way = blockIdx.x / slices % ways;
+    const int64_t b = blockIdx.x / slices / ways;
+    const int h = (int)(b % a.H), hk = h / (a.H / a.Hk);
+    const int64_t unit = b / a.H;
     Unit un;
     if (!find_unit(a, unit, per, T::C, lane, &un)) return;
-    if (un.part == (REV ? 0 : un.parts - 1)) return;  // nothing comes after it
+    if (un.part == (way ? 0 : un.parts - 1)) return;  // nothing comes after it
     const int tb = (int)(un.part * per);
     const int te = un.len - tb > per ? (int)(tb + per) : un.len;
     char *ws = reinterpret_cast<char *>(a.ws);
-    float *fin = reinterpret_cast<float *>(ws + st_part) + (unit * a.H + h) * a.Dk * a.Dv;
-    float *dec = reinterpret_cast<float *>(ws + st_dec) + unit * a.H + h;
-    const PassJob jb = {REV ? a.q : a.k, REV ? a.dout : a.v, REV ? a.qs : a.ks, REV ? a.ds : a.vs, hk, h,
-                        a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr, REV ? a.scale : 1.f};
-    pass_walk<T, NK, REV, false>(a, jb, 0, slice, h, un, tb, te, smem, dcs);
+    float *fin = reinterpret_cast<float *>(ws + o.st[way]) + (unit * a.H + h) * a.Dk * a.Dv;
+    float *dec = reinterpret_cast<float *>(ws + o.dec[way]) + unit * a.H + h;
+    if (!way) {
+        const PassJob jb = {a.k, a.v, a.ks, a.vs, hk, h, a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr, 1.f};
+        pass_walk<T, NK, false, false>(a, jb, 0, slice, h, un, tb, te, &smem, dcs);
+    } else {
+        const PassJob jb = {a.q, a.dout, a.qs, a.ds, hk, h, a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr,
+                            a.scale};
+        pass_walk<T, NK, true, false>(a, jb, 0, slice, h, un, tb, te, &smem, dcs);
+    }
 }
 
 // Joins the units of split sequences: in place, what each adds becomes the
-// state it begins with (REV: the gradient of the state it ends with).
-template <bool REV>
+// state it begins with (backwards: the gradient of the state it ends with).
 __global__ void __launch_bounds__(kSThreads)
-gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
+gscan_state_join_kernel(StateArgs a, int ways, int64_t per, Parts2 o)
 {
     const int n4 = a.Dk * a.Dv / 4, blocks = (n4 + kSThreads - 1) / kSThreads;
-    const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % a.H;
-    const int seq = blockIdx.x / blocks / a.H;
+    const int part = blockIdx.x % blocks, way = blockIdx.x / blocks % ways;
+    const int h = blockIdx.x / blocks / ways % a.H, seq = blockIdx.x / blocks / ways / a.H;
     int64_t u0 = 0;
     int n;
     if (!a.off) {
@@ -1121,10 +1143,10 @@ gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
     const int i4 = part * kSThreads + threadIdx.x;
     if (n < 2 || i4 >= n4 || u0 + n > units) return;
     char *ws = reinterpret_cast<char *>(a.ws);
-    f4 *p = reinterpret_cast<f4 *>(ws + st_part) + (u0 * a.H + h) * n4 + i4;
-    const float *dec = reinterpret_cast<const float *>(ws + st_dec) + u0 * a.H + h;
+    f4 *p = reinterpret_cast<f4 *>(ws + o.st[way]) + (u0 * a.H + h) * n4 + i4;
+    const float *dec = reinterpret_cast<const float *>(ws + o.dec[way]) + u0 * a.H + h;
     const int64_t ps = (int64_t)a.H * n4;
-    const float *from = REV ? a.dsT : a.s0;
+    const float *from = way ? a.dsT : a.s0;
     f4 st = from ? reinterpret_cast<const f4 *>(from)[((int64_t)seq * a.H + h) * n4 + i4] : zf4();
     constexpr int B = 8;  // units in flight
     for (int b = 0; b < n; b += B) {
@@ -1132,7 +1154,7 @@ gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
         float g[B];
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            const int i = REV ? n - 1 - b - j : b + j;
+            const int i = way ? n - 1 - b - j : b + j;
             if (b + j < n - 1) {
                 x[j] = p[i * ps];
                 g[j] = dec[(int64_t)i * a.H];
@@ -1140,7 +1162,7 @@ gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
         }
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            const int i = REV ? n - 1 - b - j : b + j;
+            const int i = way ? n - 1 - b - j : b + j;
             if (b + j < n) {
                 p[i * ps] = st;
                 if (b + j < n - 1) st = g[j] * st + x[j];
@@ -1149,76 +1171,145 @@ gscan_state_join_kernel(StateArgs a, int64_t per, size_t st_part, size_t st_dec)
     }
 }
 
-// Three walks per unit and head that leave operands: the states for dO S^T,
-// and the gradients of the states for V dS^T and for K dS.
+// Two walks per unit and head that leave operands for every chunk: the state
+// before it and the gradient of the state after it, both with the columns of
+// S^T: operand (n, kk) holds columns (keys) 16n .. and rows (values) 32kk ...
 struct PassWs {
-    size_t kv, gt, g;      // operands
-    size_t part_f, part_r; // units' states and gradients of states (split sequences)
+    size_t s, ds;  // operands
+    Parts2 parts;  // units' states and gradients of states (split sequences)
 };
 
 template <class T, int NK, int NV>
-__global__ void __launch_bounds__(kSThreads, 2)
-gscan_state_pass_kernel(StateArgs a, int64_t tokens, PassWs o)
+__global__ void __launch_bounds__(2 * kSThreads, 2)
+gscan_state_pass_kernel(StateArgs a, int64_t per, PassWs o)
 {
-    constexpr int NM = NK > NV ? NK : NV;
-    __shared__ __align__(16) char smem[PassLds<T, NM>::bytes];
+    __shared__ __align__(16) PassLds<T, NV> smem;
     __shared__ Decay<T::C> dcs[2];
-    constexpr int ks = NK / 2, vs = NV / 2, per = 2 * ks + vs;
-    const int lane = threadIdx.x & 63;
-    const int j = blockIdx.x % per;
-    const int h = blockIdx.x / per % a.H, hk = h / (a.H / a.Hk);
-    const int64_t unit = blockIdx.x / per / a.H;
+    constexpr int slices = NK / 2;
+    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices, way = blockIdx.x / slices & 1;
+    const int64_t b = blockIdx.x / slices / 2;
+    const int h = (int)(b % a.H), hk = h / (a.H / a.Hk);
+    const int64_t unit = b / a.H;
     Unit un;
-    if (!find_unit(a, unit, tokens, T::C, lane, &un)) return;
-    const int tb = (int)(un.part * tokens);
-    const int te = un.len - tb > tokens ? (int)(tb + tokens) : un.len;
+    if (!find_unit(a, unit, per, T::C, lane, &un)) return;
+    const int tb = (int)(un.part * per);
+    const int te = un.len - tb > per ? (int)(tb + per) : un.len;
     char *ws = reinterpret_cast<char *>(a.ws);
-    const int64_t one = (int64_t)a.Dk * a.Dv, mine = (unit * a.H + h) * one;
-    const int64_t whole = ((int64_t)un.seq * a.H + h) * one;
-    const float *s0 = un.part ? reinterpret_cast<const float *>(ws + o.part_f) + mine
-                              : a.s0 ? a.s0 + whole : nullptr;
-    const float *ds = un.part + 1 < un.parts ? reinterpret_cast<const float *>(ws + o.part_r) + mine
-                                             : a.dsT ? a.dsT + whole : nullptr;
-    if (j < ks) {
-        const PassJob jb = {a.v, a.k, a.vs, a.ks, h, hk, a.Dv, a.Dk, s0, nullptr, nullptr, 1, a.Dv,
-                            ws + o.kv, 1.f};
-        pass_walk<T, NV, false, true>(a, jb, NK, j, h, un, tb, te, smem, dcs);
-    } else if (j < 2 * ks) {
-        const PassJob jb = {a.dout, a.q, a.ds, a.qs, h, hk, a.Dv, a.Dk, ds, nullptr, nullptr, 1, a.Dv,
-                            ws + o.gt, a.scale};
-        pass_walk<T, NV, true, true>(a, jb, NK, j - ks, h, un, tb, te, smem, dcs);
+    const int64_t one = (int64_t)a.Dk * a.Dv, whole = ((int64_t)un.seq * a.H + h) * one;
+    const bool outer = un.part == (way ? un.parts - 1 : 0);  // begins with the caller's
+    const float *from = way ? a.dsT : a.s0;
+    const float *init = !outer ? reinterpret_cast<const float *>(ws + o.parts.st[way]) + (unit * a.H + h) * one
+                               : from ? from + whole : nullptr;
+    if (!way) {
+        const PassJob jb = {a.v, a.k, a.vs, a.ks, h, hk, a.Dv, a.Dk, init, nullptr, nullptr, 1, a.Dv,
+                            ws + o.s, 1.f};
+        pass_walk<T, NV, false, true>(a, jb, NK, slice, h, un, tb, te, &smem, dcs);
     } else {
-        const PassJob jb = {a.q, a.dout, a.qs, a.ds, hk, h, a.Dk, a.Dv, ds,
-                            a.ds0 && un.part == 0 ? a.ds0 + whole : nullptr, nullptr, a.Dv, 1,
-                            ws + o.g, a.scale};
-        pass_walk<T, NK, true, true>(a, jb, NV, j - 2 * ks, h, un, tb, te, smem, dcs);
+        const PassJob jb = {a.dout, a.q, a.ds, a.qs, h, hk, a.Dv, a.Dk, init,
+                            a.ds0 && un.part == 0 ? a.ds0 + whole : nullptr, nullptr, 1, a.Dv,
+                            ws + o.ds, a.scale};
+        pass_walk<T, NV, true, true>(a, jb, NK, slice, h, un, tb, te, &smem, dcs);
     }
 }
 
 // ---------------------------------------------------- backward: gradients
 
+// The operands of a state in LDS: operand (n, kk) at 64 (n NV + kk) lanes of
+// sixteen bytes (fp32: two planes).  Within an operand lane l sits at
+// `place(l)`, so that reading four keys of a value (the transposed operand)
+// meets fewer banks twice.
+template <class T, int NV>
+struct States;
+
+__device__ __forceinline__ uint32_t place(uint32_t lane) { return lane ^ ((lane >> 4 & 1) << 2); }
+
+template <int NV>
+struct States<BF, NV> {
+    // keys 16n + l16, values 32kk + {4g.., 16 + 4g..}
+    static __device__ __forceinline__ u4 get(const u4 *t, int n, int kk, int lane)
+    {
+        return t[(n * NV + kk) * 64 + place(lane)];
+    }
+    // value 16m + l16, keys 32kk + {4g.., 16 + 4g..}
+    static __device__ __forceinline__ u4 turned(const u4 *t, int m, int kk, int lane)
+    {
+        const uint32_t l16 = lane & 15, g = lane >> 4;
+        const char *p = reinterpret_cast<const char *>(t) + (2 * kk * NV + m / 2) * 1024 + (m & 1) * 8 +
+                        place((l16 & 3) * 16 + 4 * g + (l16 >> 2)) * 16;
+        const uint2 x = Tile<BF, 64>::tr(p), y = Tile<BF, 64>::tr(p + NV * 1024);
+        return u4{x.x, x.y, y.x, y.y};
+    }
+};
+template <int NV>
+struct States<FP, NV> {
+    static __device__ __forceinline__ FP::Frag get(const u4 *t, int n, int kk, int lane)
+    {
+        const f4 *p = reinterpret_cast<const f4 *>(t) + (n * NV + kk) * 128 + place(lane);
+        return FP::Frag{p[0], p[64]};
+    }
+    static __device__ __forceinline__ FP::Frag turned(const u4 *t, int m, int kk, int lane)
+    {
+        const uint32_t l16 = lane & 15, g = lane >> 4;
+        const float *p = reinterpret_cast<const float *>(t) + (2 * kk * NV + m / 2) * 512 + (m & 1) * 256 + (l16 & 3);
+        FP::Frag f;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t at = place((l16 >> 2) * 16 + 4 * g + j) * 4;
+            f.a[j] = p[at];
+            f.b[j] = p[at + NV * 512];
+        }
+        return f;
+    }
+};
+
+__device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const BF &)
+{
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += bf_lo(x[i]) * bf_lo(y[i]) + bf_hi(x[i]) * bf_hi(y[i]);
+    return s;
+}
+__device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
+{
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += __uint_as_float(x[i]) * __uint_as_float(y[i]);
+    return s;
+}
+
 // One workgroup per chunk and key head: its queries and keys stay in LDS
 // while it takes the value heads that share them one by one, so dQ and dK of
-// shared heads are summed in registers in a fixed order.  Wavefront (rt, cs)
-// owns token rows 16rt .. 16rt+15 and every CS-th 16-column tile, and forms
-// the scores it needs itself, in the order whose accumulators are operands:
-// dO V^T of its tokens with the tokens before them (for dQ), Q K^T and dO V^T
-// of its tokens with the tokens after them (for dK and dV), five tiles for
-// every wavefront.  Gradients are formed transposed, four columns of a token
+// shared heads are summed in registers in a fixed order.  All of a head's
+// rows and state operands are requested at once, the next head's while this
+// one is computed.
+//
+// Eight wavefronts: `rt` owns token rows 16rt .. 16rt+15, half of them dQ and
+// half dK, each half of dV (and, fp32 with its two rows of tiles, each every
+// other column tile).  A wavefront forms the scores it needs itself, in the
+// order whose accumulators are operands: dO V^T of its tokens with the tokens
+// before them (for dQ), Q K^T and dO V^T of its tokens with those after them
+// (for dV and dK).  Gradients are formed transposed, four columns of a token
 // per lane.
+constexpr int kGThreads = 512;
+
 template <class T, int NK, int NV>
-__global__ void __launch_bounds__(kSThreads)
-gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
+__global__ void __launch_bounds__(kGThreads, 2)
+gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
     typedef Tile<T, NK * 32> TK;
     typedef Tile<T, NV * 32> TV;
-    constexpr int C = T::C, RT = C / 16, CS = 4 / RT, KS = C / 32;
-    constexpr int NTK = 2 * NK / CS, NTV = 2 * NV / CS;  // column tiles per wavefront
+    typedef States<T, NV> ST;
+    constexpr int C = T::C, RT = C / 16, KS = C / 32;
+    constexpr int CH = 8 / (2 * RT);                // column halves
+    constexpr int NTK = 2 * NK / CH, NTV = NV / CH; // column tiles per wavefront
+    constexpr int kOps = 2 * NK * NV * (int)sizeof(Frag) / 16 * 64;  // 16-byte pieces of a state
+    constexpr int NS = kOps / kGThreads;
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
+    __shared__ u4 state[kOps];
     __shared__ Decay<C> dc;
-    __shared__ float rsum[C][RT], inner[C], asum[CS][C], bsum[CS][C], fsum[4];
+    __shared__ float rsum[C][RT], inner[C], asum[CH][C], bsum[CH][C], fsum[8];
     // what infinities and NaN reach: per column the first row of k and the last
     // of q and d_out that hold one, which rows of k and d_out do, and the last
     // row of q, of d_out, the first of k
@@ -1226,7 +1317,8 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int rt = w % RT, cs = w / RT;
+    const int rt = w % RT, ch = w / (2 * RT);
+    const bool keys = (w / RT) & 1;
     const int hk = blockIdx.x % a.Hk;
     Unit un;
     if (!find_unit(a, blockIdx.x / a.Hk, C, C, lane, &un)) return;
@@ -1239,37 +1331,54 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
     const TV lv(lane);
     const bool mine = 16 * rt + l16 < left;  // this lane's token exists
 
-    Stage<T, NV> sv, so;
-    u4 rv[NV], ro[NV];
+    Stage<T, NV, kGThreads> sv, so;
+    typename Stage<T, NV, kGThreads>::Regs rv, ro;
+    u4 rs[NS], rd[NS];
     float gx = 0.f;
     auto request = [&](int h) {
         sv.begin(rows_of<S>(a.v, a.vs, un, packed, h), a.vs.t, t0, a.Dv, tid);
         so.begin(rows_of<S>(a.dout, a.ds, un, packed, h), a.ds.t, t0, a.Dv, tid);
         sv.load(rv, left, 0, tid);
         so.load(ro, left, 0, tid);
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + (slot * a.H + h) * kOps;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) rs[i] = p[tid + kGThreads * i];
         if (w == 0) {
             const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
             if (lane < C && lane < left)
                 gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
         }
     };
-    if (tid < NK * 32) {
-        first_k[tid] = C;
-        last_q[tid] = -1;
+    auto request_ds = [&](int h) {
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + (slot * a.H + h) * kOps;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) rd[i] = p[tid + kGThreads * i];
+    };
+    auto keep = [&](const u4 (&r)[NS]) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int q = tid + kGThreads * i;
+            state[(q & ~63) + place(q & 63)] = r[i];
+        }
+    };
+    for (int i = tid; i < NK * 32; i += kGThreads) {
+        first_k[i] = C;
+        last_q[i] = -1;
     }
     if (tid < NV * 32) last_o[tid] = -1;
     if (tid < C) row_k[tid] = row_o[tid] = 0;
     if (tid < 3) ends[tid] = tid < 2 ? -1 : C;
     if (tid == 0) bad = 0;
-    __syncthreads();
     {
-        Stage<T, NK> sq, sk;
-        u4 rq[NK], rk[NK];
+        Stage<T, NK, kGThreads> sq, sk;
+        typename Stage<T, NK, kGThreads>::Regs rq, rk;
         sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, t0, a.Dk, tid);
         sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, t0, a.Dk, tid);
         sq.load(rq, left, 0, tid);
         sk.load(rk, left, 0, tid);
         request(hk * reps);
+        request_ds(hk * reps);
+        __syncthreads();
         sq.template store<TK>(rq, qt, tid);
         sk.template store<TK>(rk, kt, tid);
         sq.template scrub<TK>(rq, qt, tid, [&](int row, int c) {
@@ -1284,28 +1393,39 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
             bad = 1;
         });
     }
-    f4 dq[NTK], dk[NTK];
+    f4 acc[NTK];  // dQ or dK of the wavefront's tokens
 #pragma unroll
-    for (int i = 0; i < NTK; ++i) dq[i] = dk[i] = zf4();
+    for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
-    // the staged head
-    auto compute = [&](int h, bool nan) {
-        const int64_t fh = (slot * a.H + h) * 2 * NK * NV;  // operands before this head's
-        const void *Sf = ws + st_kv, *Gt = ws + st_gt, *Gf = ws + st_g;
-        // the state operands of the next column tile are requested one tile ahead
-        Frag next[NK > NV ? NK : NV];
-        auto fetch = [&](const void *from, int n) {
+    for (int hr = 0; hr < reps; ++hr) {
+        const int h = hk * reps + hr;
+        sv.template store<TV>(rv, vt, tid);
+        so.template store<TV>(ro, ot, tid);
+        so.template scrub<TV>(ro, ot, tid, [&](int row, int c) {
+            atomicMax(&last_o[c], row);
+            atomicMax(&ends[1], row);
+            row_o[row] = 1;
+            bad = 1;
+        });
+        keep(rs);
+        const float x = gx;
+        if (w == 0) gate_scan<C>(dc, x, lane < left, a.gate_form, lane);
+        {  // F = e^(L_end) <S, dS>
+            float f = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < NV; ++kk) get_frag(from, fh + n * NV + kk, lane, &next[kk]);
-        };
-        auto fetch_g = [&](int n) {
+            for (int i = 0; i < NS; ++i) f += dot16(rs[i], rd[i], T());
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) get_frag(Gf, fh + n * NK + kk, lane, &next[kk]);
-        };
-        fetch(Sf, cs);
-        // dQ^T = K^T (dP . D)^T + scale e^L S dO^T
-        {
-            Frag of[NV], df[KS];
+            for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
+            if (lane == 0) fsum[w] = f;
+        }
+        __syncthreads();
+        const bool nan = bad != 0;
+        if (hr + 1 < reps) request(h + 1);
+
+        Frag pf[KS], df[KS];
+        if (!keys) {
+            // dQ^T = K^T (dP . D)^T + scale e^L S dO^T
+            Frag of[NV];
             f4 p[RT];
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) of[kk] = lv.row(ot, 16 * rt, kk);
@@ -1325,34 +1445,47 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
             float as = 0.f;
 #pragma unroll
             for (int i = 0; i < NTK; ++i) {
-                const int n = i * CS + cs;
-                f4 x = zf4();
-                Frag sf[NV];
-#pragma unroll
-                for (int kk = 0; kk < NV; ++kk) sf[kk] = next[kk];
+                const int n = i * CH + ch;
+                f4 y = zf4();
                 GSCAN_STEP();
-                fetch(i + 1 < NTK ? Sf : Gt, i + 1 < NTK ? n + CS : cs);
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) x = mma(sf[kk], of[kk], x);
-                x *= e;
+                for (int kk = 0; kk < NV; ++kk) y = mma(ST::get(state, n, kk, lane), of[kk], y);
+                y *= e;
                 const f4 qv = lk.quad(qt, 16 * rt, n);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) as += x[j] * qv[j];
-                dq[i] += x;
+                for (int j = 0; j < 4; ++j) as += y[j] * qv[j];
+                acc[i] += y;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    if (2 * kk > rt) continue;
-                    dq[i] = mma(lk.col(kt, 32 * kk, n), df[kk], dq[i]);
-                }
-                if (nan) dq[i] = poison<false>(dq[i], &first_k[16 * n + g4], 16 * rt + l16, row_o[16 * rt + l16]);
+                for (int kk = 0; kk < KS; ++kk)
+                    if (2 * kk <= rt) acc[i] = mma(lk.col(kt, 32 * kk, n), df[kk], acc[i]);
             }
+            if (nan)
+#pragma unroll
+                for (int i = 0; i < NTK; ++i)
+                    acc[i] = poison<false>(acc[i], &first_k[16 * (i * CH + ch) + g4], 16 * rt + l16,
+                                           row_o[16 * rt + l16]);
             as += __shfl_xor(as, 16);
             as += __shfl_xor(as, 32);
-            if (lane < 16) asum[cs][16 * rt + lane] = as;
-        }
-        // the scores of this wavefront's tokens (columns) with later ones
-        Frag pf[KS], df[KS];
-        {
+            if (lane < 16) asum[ch][16 * rt + lane] = as;
+            // P . D of its tokens (columns) with later ones, for dV
+            Frag kf[NK];
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
+#pragma unroll
+            for (int ut = 0; ut < RT; ++ut) {
+                p[ut] = zf4();
+                GSCAN_STEP();
+                if (ut >= rt) {
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk) p[ut] = mma(lk.row(qt, 16 * ut, kk), kf[kk], p[ut]);
+                    p[ut] *= a.scale;
+                    f4 none = zf4();
+                    decayed_ts(dc, &p[ut], &none, ut, rt, l16, g4);
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
+        } else {
             Frag kf[NK], vf[NV];
             f4 p[RT], d[RT];
             float in = 0.f;
@@ -1365,75 +1498,79 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                 p[ut] = d[ut] = zf4();
                 GSCAN_STEP();
                 if (ut >= rt) {
-                    f4 x = zf4(), y = zf4();
+                    f4 y = zf4();
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk) x = mma(lk.row(qt, 16 * ut, kk), kf[kk], x);
+                    for (int kk = 0; kk < NK; ++kk) p[ut] = mma(lk.row(qt, 16 * ut, kk), kf[kk], p[ut]);
 #pragma unroll
                     for (int kk = 0; kk < NV; ++kk) y = mma(lv.row(ot, 16 * ut, kk), vf[kk], y);
-                    p[ut] = a.scale * x;
+                    p[ut] *= a.scale;
                     d[ut] = a.scale * y;
                     decayed_ts(dc, &p[ut], &d[ut], ut, rt, l16, g4);
                     // W below the diagonal: sums over s < t of the tile's
                     // columns, for u >= t
+                    if (ch == 0)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool low = ut > rt || g4 + j > l16;
-                        float v = low ? p[ut][j] * y[j] : 0.f;
-                        v += dpp<0x111>(v);
-                        v += dpp<0x112>(v);
-                        v += dpp<0x114>(v);
-                        v += dpp<0x118>(v);
-                        const float before = dpp<0x111>(v);
-                        in += ut > rt || g4 + j >= l16 ? before : 0.f;
-                        if (cs == 0 && l16 == 15) rsum[16 * ut + g4 + j][rt] = v;
-                    }
+                        for (int j = 0; j < 4; ++j) {
+                            const bool low = ut > rt || g4 + j > l16;
+                            float v = low ? p[ut][j] * y[j] : 0.f;
+                            v += dpp<0x111>(v);
+                            v += dpp<0x112>(v);
+                            v += dpp<0x114>(v);
+                            v += dpp<0x118>(v);
+                            const float before = dpp<0x111>(v);
+                            in += ut > rt || g4 + j >= l16 ? before : 0.f;
+                            if (l16 == 15) rsum[16 * ut + g4 + j][rt] = v;
+                        }
                 }
             }
-            in += __shfl_xor(in, 16);
-            in += __shfl_xor(in, 32);
-            if (cs == 0 && lane < 16) inner[16 * rt + lane] = in;
+            if (ch == 0) {
+                in += __shfl_xor(in, 16);
+                in += __shfl_xor(in, 32);
+                if (lane < 16) inner[16 * rt + lane] = in;
+            }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
                 to_frag(d[2 * kk], d[2 * kk + 1], &df[kk]);
             }
         }
+        __syncthreads();  // the states have been read
+        keep(rd);
+        __syncthreads();
+        if (hr + 1 < reps) request_ds(h + 1);
         const float ds = dc.d[16 * rt + l16];
-        // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
-        {
+        if (keys) {
+            // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
             Frag vf[NV];
             float bs = 0.f;
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) vf[kk] = lv.row(vt, 16 * rt, kk);
 #pragma unroll
             for (int i = 0; i < NTK; ++i) {
-                const int n = i * CS + cs;
-                f4 x = zf4();
-                Frag gf[NV];
-#pragma unroll
-                for (int kk = 0; kk < NV; ++kk) gf[kk] = next[kk];
+                const int n = i * CH + ch;
+                f4 y = zf4();
                 GSCAN_STEP();
-                if (i + 1 < NTK) fetch(Gt, n + CS);
-                else fetch_g(cs);
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) x = mma(gf[kk], vf[kk], x);
-                x *= ds;
+                for (int kk = 0; kk < NV; ++kk) y = mma(ST::get(state, n, kk, lane), vf[kk], y);
+                y *= ds;
                 const f4 kv = lk.quad(kt, 16 * rt, n);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bs += x[j] * kv[j];
-                dk[i] += x;
+                for (int j = 0; j < 4; ++j) bs += y[j] * kv[j];
+                acc[i] += y;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    if (2 * kk + 1 < rt) continue;
-                    dk[i] = mma(lk.col(qt, 32 * kk, n), df[kk], dk[i]);
-                }
-                if (nan) dk[i] = poison<true>(dk[i], &last_q[16 * n + g4], 16 * rt + l16, 16 * rt + l16 <= ends[1]);
+                for (int kk = 0; kk < KS; ++kk)
+                    if (2 * kk + 1 >= rt) acc[i] = mma(lk.col(qt, 32 * kk, n), df[kk], acc[i]);
             }
+            if (nan)
+#pragma unroll
+                for (int i = 0; i < NTK; ++i)
+                    acc[i] = poison<true>(acc[i], &last_q[16 * (i * CH + ch) + g4], 16 * rt + l16,
+                                          16 * rt + l16 <= ends[1]);
             bs += __shfl_xor(bs, 16);
             bs += __shfl_xor(bs, 32);
-            if (lane < 16) bsum[cs][16 * rt + lane] = bs;
+            if (lane < 16) bsum[ch][16 * rt + lane] = bs;
         }
-        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T
+        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, half of the columns
         {
             Frag kf[NK];
             S *out = reinterpret_cast<S *>(a.dv) + ((un.tok0 + t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
@@ -1441,77 +1578,40 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
             for (int i = 0; i < NTV; ++i) {
-                const int n = i * CS + cs;
-                f4 x = zf4();
-                Frag gf[NK];
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) gf[kk] = next[kk];
+                const int m = (i * CH + ch) * 2 + keys;
+                f4 y = zf4();
                 GSCAN_STEP();
-                if (i + 1 < NTV) fetch_g(n + CS);
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) x = mma(gf[kk], kf[kk], x);
-                x *= ds;
+                for (int kk = 0; kk < NK; ++kk) y = mma(ST::turned(state, m, kk, lane), kf[kk], y);
+                y *= ds;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    if (2 * kk + 1 < rt) continue;
-                    x = mma(lv.col(ot, 32 * kk, n), pf[kk], x);
-                }
-                if (nan)
-                    x = poison<true>(x, &last_o[16 * n + g4], 16 * rt + l16,
-                                     16 * rt + l16 <= ends[0] || row_k[16 * rt + l16]);
-                if (mine && 16 * n + g4 < a.Dv) put4(out + 16 * n, x);
+                for (int kk = 0; kk < KS; ++kk)
+                    if (2 * kk + 1 >= rt) y = mma(lv.col(ot, 32 * kk, m), pf[kk], y);
+                if (mine && 16 * m + g4 < a.Dv) put4(out + 16 * m, y);
             }
+            if (nan && mine)
+#pragma unroll 1
+                for (int i = 0; i < 4 * NTV; ++i) {
+                    const int c = 16 * ((i / 4 * CH + ch) * 2 + keys) + g4 + i % 4;
+                    if (c < a.Dv && (16 * rt + l16 <= last_o[c] || 16 * rt + l16 <= ends[0] || row_k[16 * rt + l16]))
+                        put1(out - g4 + c, __builtin_nanf(""));
+                }
         }
-        // F = e^(L_end) <S, dS>
-        float f = 0.f;
-#pragma unroll
-        for (int i = 0; i < NK * NV / 2; ++i) {
-            if (i % 4 == 0) GSCAN_STEP();
-            Frag x, y;
-            f4 x0, x1, y0, y1;
-            get_frag(Sf, fh + 4 * i + w, lane, &x);
-            get_frag(Gt, fh + 4 * i + w, lane, &y);
-            from_frag(x, &x0, &x1);
-            from_frag(y, &y0, &y1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f += x0[j] * y0[j] + x1[j] * y1[j];
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
-        if (lane == 0) fsum[w] = f;
-    };
-
-    for (int hr = 0; hr < reps; ++hr) {
-        const int h = hk * reps + hr;
-        sv.template store<TV>(rv, vt, tid);
-        so.template store<TV>(ro, ot, tid);
-        so.template scrub<TV>(ro, ot, tid, [&](int row, int c) {
-            atomicMax(&last_o[c], row);
-            atomicMax(&ends[1], row);
-            row_o[row] = 1;
-            bad = 1;
-        });
-        const float x = gx;
-        if (w == 0) gate_scan<C>(dc, x, lane < left, a.gate_form, lane);
-        __syncthreads();
-        const bool nan = bad != 0;
-        if (hr + 1 < reps) request(h + 1);
-        compute(h, nan);
         __syncthreads();
         if (w == 0) {
-            float su = 0.f, pb = 0.f, in = 0.f, rs[RT];
+            float su = 0.f, pb = 0.f, in = 0.f, rw[RT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) rs[i] = 0.f;
+            for (int i = 0; i < RT; ++i) rw[i] = 0.f;
             if (lane < C) {
 #pragma unroll
-                for (int i = 0; i < CS; ++i) {
+                for (int i = 0; i < CH; ++i) {
                     su += asum[i][lane];
                     pb += bsum[i][lane];
                 }
                 in = inner[lane];
 #pragma unroll
                 for (int i = 0; i + 1 < RT; ++i)
-                    rs[i] = lane >= 16 * i + 16 ? rsum[lane][i] : 0.f;  // rows below the tile
+                    rw[i] = lane >= 16 * i + 16 ? rsum[lane][i] : 0.f;  // rows below the tile
             }
 #pragma unroll
             for (int d = 1; d < C; d *= 2) {
@@ -1520,15 +1620,18 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                 if (lane >= d) pb += z;
 #pragma unroll
                 for (int i = 0; i + 1 < RT; ++i) {
-                    const float r = __shfl_down(rs[i], d);
-                    if (lane + d < 64) rs[i] += r;
+                    const float r = __shfl_down(rw[i], d);
+                    if (lane + d < 64) rw[i] += r;
                 }
             }
             su += in;
 #pragma unroll
             for (int i = 0; i + 1 < RT; ++i)
-                if (lane >= 16 * (i + 1)) su += rs[i];
-            const float F = dc.g * ((fsum[0] + fsum[1]) + (fsum[2] + fsum[3]));
+                if (lane >= 16 * (i + 1)) su += rw[i];
+            float F = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) F += fsum[i];
+            F *= dc.g;
             const float before = __shfl_up(pb, 1);
             if (lane < C && lane < left) {
                 float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
@@ -1538,40 +1641,44 @@ gscan_state_grad_kernel(StateArgs a, size_t st_kv, size_t st_gt, size_t st_g)
                 else reinterpret_cast<float *>(a.dgate)[at] = r;
             }
         }
-        __syncthreads();
-        if (nan) {  // d_out's of this head (q and k stay)
-            if (tid < NV * 32) last_o[tid] = -1;
-            if (tid < C) row_o[tid] = 0;
-            if (tid == 0) ends[1] = -1;
+        if (hr + 1 < reps) {
             __syncthreads();
+            if (nan) {  // d_out's of this head (q's and k's stay)
+                if (tid < NV * 32) last_o[tid] = -1;
+                if (tid < C) row_o[tid] = 0;
+                if (tid == 0) ends[1] = -1;
+                __syncthreads();
+            }
         }
     }
 
     if (mine) {
-        const int64_t at = ((un.tok0 + t0 + 16 * rt + l16) * a.Hk + hk) * a.Dk + g4;
+        S *out = reinterpret_cast<S *>(keys ? a.dk : a.dq) +
+                 ((un.tok0 + t0 + 16 * rt + l16) * a.Hk + hk) * a.Dk + g4;
 #pragma unroll
         for (int i = 0; i < NTK; ++i) {
-            const int n = i * CS + cs;
-            if (16 * n + g4 < a.Dk) {
-                put4(reinterpret_cast<S *>(a.dq) + at + 16 * n, dq[i]);
-                put4(reinterpret_cast<S *>(a.dk) + at + 16 * n, dk[i]);
-            }
+            const int n = i * CH + ch;
+            if (16 * n + g4 < a.Dk) put4(out + 16 * n, acc[i]);
         }
     }
 }
 
-template <class T, int NK, bool REV>
-hipError_t part_launch(const StatePlan &p, const StateArgs &a, size_t st_part, size_t st_dec,
-                       hipStream_t st)
+Parts2 parts_of(const StatePlan &p)
+{
+    return Parts2{{p.st_part, p.st_part_r}, {p.st_dec, p.st_dec_r}};
+}
+
+template <class T, int NK>
+hipError_t part_launch(const StatePlan &p, const StateArgs &a, int ways, hipStream_t st)
 {
     const int slices = (a.Dv + kSlice - 1) / kSlice;
-    hipLaunchKernelGGL((gscan_state_part_kernel<T, NK, REV>), dim3((unsigned)(p.units * a.H * slices)),
-                       dim3(kSThreads), 0, st, a, slices, p.per, st_part, st_dec);
+    hipLaunchKernelGGL((gscan_state_part_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices * ways)),
+                       dim3(2 * kSThreads), 0, st, a, slices, ways, p.per, parts_of(p));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t blocks = (a.Dk * a.Dv / 4 + kSThreads - 1) / kSThreads;
-    hipLaunchKernelGGL((gscan_state_join_kernel<REV>), dim3((unsigned)(a.B * a.H * blocks)),
-                       dim3(kSThreads), 0, st, a, p.per, st_part, st_dec);
+    hipLaunchKernelGGL(gscan_state_join_kernel, dim3((unsigned)(a.B * a.H * blocks * ways)),
+                       dim3(kSThreads), 0, st, a, ways, p.per, parts_of(p));
     return hipGetLastError();
 }
 
@@ -1580,7 +1687,7 @@ hipError_t fwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
     const int slices = (a.Dv + kSlice - 1) / kSlice;
     if (p.split) {
-        const hipError_t e = part_launch<T, NK, false>(p, a, p.st_part, p.st_dec, st);
+        const hipError_t e = part_launch<T, NK>(p, a, 1, st);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((gscan_state_fwd_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices)),
@@ -1593,17 +1700,16 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
     hipError_t e;
     if (p.split) {
-        e = part_launch<T, NK, false>(p, a, p.st_part, p.st_dec, st);
-        if (e == hipSuccess) e = part_launch<T, NK, true>(p, a, p.st_part_r, p.st_dec_r, st);
+        e = part_launch<T, NK>(p, a, 2, st);
         if (e != hipSuccess) return e;
     }
-    const PassWs o = {p.st_kv, p.st_gt, p.st_g, p.st_part, p.st_part_r};
-    hipLaunchKernelGGL((gscan_state_pass_kernel<T, NK, NV>),
-                       dim3((unsigned)(p.units * a.H * (NK + NV / 2))), dim3(kSThreads), 0, st, a, p.per, o);
+    const PassWs o = {p.st_s, p.st_ds, parts_of(p)};
+    hipLaunchKernelGGL((gscan_state_pass_kernel<T, NK, NV>), dim3((unsigned)(p.units * a.H * NK)),
+                       dim3(2 * kSThreads), 0, st, a, p.per, o);
     e = hipGetLastError();
     if (e != hipSuccess || a.T == 0) return e;
     hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(p.chunks * a.Hk)),
-                       dim3(kSThreads), 0, st, a, p.st_kv, p.st_gt, p.st_g);
+                       dim3(kGThreads), 0, st, a, p.st_s, p.st_ds);
     return hipGetLastError();
 }
 
@@ -1627,7 +1733,7 @@ StatePlan make_state_plan(const StateArgs &a, bool backward)
     const int64_t nc = a.T > p.chunk ? (a.T + p.chunk - 1) / p.chunk : 1;
     // packed: sum over sequences of max(1, ceil(len / C)) <= T / C + B
     p.chunks = a.off ? a.T / p.chunk + a.B : a.B * nc;
-    const int64_t walks = (int64_t)a.H * (backward ? p.nk + p.nv / 2 : (a.Dv + kSlice - 1) / kSlice);
+    const int64_t walks = (int64_t)a.H * (backward ? p.nk : (a.Dv + kSlice - 1) / kSlice);
     static const int64_t tgt = getenv("GS_TGT") ? atoi(getenv("GS_TGT")) : 768;
     static const int64_t mn = getenv("GS_MIN") ? atoi(getenv("GS_MIN")) : 4;
     int64_t pc = p.chunks * walks / tgt;
@@ -1654,9 +1760,8 @@ StatePlan make_state_plan(const StateArgs &a, bool backward)
     if (backward) {
         const size_t one = (size_t)p.chunks * (size_t)a.H * (size_t)(p.nk * p.nv) * 1024u *
                            (a.dtype ? 2u : 4u);
-        p.st_kv = take(one);
-        p.st_gt = take(one);
-        p.st_g = take(one);
+        p.st_s = take(one);
+        p.st_ds = take(one);
     }
     p.bytes = at;
     return p;
