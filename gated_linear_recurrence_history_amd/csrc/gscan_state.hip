@@ -397,9 +397,9 @@ __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t
                                           int lane, Unit *w)
 {
     if (!a.off) {
-        const int64_t n = a.T > per ? (a.T + per - 1) / per : 1;
-        const int64_t nc = a.T > C ? (a.T + C - 1) / C : 1;
-        const int64_t seq = u / n;
+        const uint32_t T = (uint32_t)a.T, p = (uint32_t)per;
+        const uint32_t n = T > p ? (T + p - 1) / p : 1, nc = T > (uint32_t)C ? (T + C - 1) / C : 1;
+        const int64_t seq = (uint32_t)u / n;
         if (seq >= a.B) return false;
         w->seq = (int)seq;
         w->part = (int)(u - seq * n);
@@ -579,10 +579,11 @@ __device__ __forceinline__ f4 poison(f4 x, const int *where, int row, bool all =
 // so that differences of far-down values keep fp32 accuracy), e^L,
 // e^(L_end - L), e^(L_end); and for tiles of 16 x 16 tokens below the
 // diagonal the two factors of e^(L_t - L_s) around the last token m of s's
-// tile, e^(L_m - L_s) and e^(L_t - L_m), neither above what the gates allow.
+// tile, e^(L_m - L_s) and (zero where t is not below the tile) e^(L_t - L_m),
+// neither above what the gates allow.
 template <int C>
 struct __align__(16) Decay {
-    float hi[C], lo[C], e[C], d[C], col[C], row[C / 16 - 1][C], g;
+    float hi[C], lo[C], e[C], d[C], col[C], row[C / 16][C], g;
 };
 
 // x of other lanes, zero where there is none: CTRL 0x110 + n, n lanes below in
@@ -633,7 +634,9 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
         s.d[lane] = exp2_((float)(end - L));
         s.col[lane] = exp2_((float)(m - L));
 #pragma unroll
-        for (int i = 0; i < C / 16 - 1; ++i) s.row[i][lane] = exp2_((float)(L - mid[i]));
+        for (int i = 0; i < C / 16 - 1; ++i)
+            s.row[i][lane] = lane >= 16 * i + 16 ? exp2_((float)(L - mid[i])) : 0.f;
+        s.row[C / 16 - 1][lane] = 0.f;
         if (lane == C - 1) s.g = exp2_((float)end);
     }
 }
@@ -653,26 +656,51 @@ __device__ __forceinline__ f4 decayed_st(const Decay<C> &s, f4 x, int rt, int ct
         x[j] = g4 + j <= l16 ? x[j] * exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
     return x;
 }
-// Two tiles (x, y) with rows t = 16rt + 4g + j and columns s = 16ct + l16:
-template <int C>
-__device__ __forceinline__ void decayed_ts(const Decay<C> &s, f4 *x, f4 *y, int rt, int ct, int l16,
-                                           int g4)
+// The same for a wavefront that holds all tiles of its tokens `own` (16 of
+// them, known at run time only) without a branch: `ST` tokens t = 16own + l16
+// are the columns and s the rows of tiles p[0 ..], tiles behind the diagonal
+// zero; otherwise the columns are s = 16own + l16 and the rows t.
+template <bool ST, int C>
+__device__ __forceinline__ void decay_tiles(const Decay<C> &s, f4 (&p)[C / 16], int own, int l16, int g4)
 {
-    const int u = 16 * ct + l16;
-    if (ct < rt) {
-        const f4 f = *reinterpret_cast<const f4 *>(&s.row[ct][16 * rt + g4]) * s.col[u];
-        *x *= f;
-        *y *= f;
-        return;
-    }
-    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * rt + g4]);
-    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * rt + g4]);
-    const float hs = s.hi[u], ls = s.lo[u];
+    constexpr int RT = C / 16;
+    const int me = 16 * own + l16;
+    f4 x = p[0];
+#pragma unroll
+    for (int i = 1; i < RT; ++i) x = own == i ? p[i] : x;
+    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * own + g4]);
+    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * own + g4]);
+    const float hm = s.hi[me], lm = s.lo[me];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float f = exp2_((hi[j] - hs) + (lo[j] - ls));
-        (*x)[j] = g4 + j >= l16 ? (*x)[j] * f : 0.f;
-        (*y)[j] = g4 + j >= l16 ? (*y)[j] * f : 0.f;
+        const float f = exp2_(ST ? (hm - hi[j]) + (lm - lo[j]) : (hi[j] - hm) + (lo[j] - lm));
+        x[j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? x[j] * f : 0.f;
+    }
+    const float c = s.col[me];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const f4 f = ST ? *reinterpret_cast<const f4 *>(&s.col[16 * i + g4]) * s.row[i][me]
+                        : *reinterpret_cast<const f4 *>(&s.row[own][16 * i + g4]) * c;
+        p[i] = own == i ? x : (ST ? i < own : i > own) ? p[i] * f : zf4();
+    }
+}
+
+// y[i] += A(i, k) b[k], the operands A of step k + 1 requested before the
+// products of step k; those of a step do not wait for each other.
+template <int N, int K, class F, class LD>
+__device__ __forceinline__ void mma_group(f4 (&y)[N], const F (&b)[K], LD ld)
+{
+    F x[2][N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[0][i] = ld(i, 0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (k + 1 < K)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[(k + 1) & 1][i] = ld(i, k + 1);
+        GSCAN_STEP();
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = mma(x[k & 1][i], b[k], y[i]);
     }
 }
 
@@ -1304,6 +1332,8 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
     constexpr int C = T::C, RT = C / 16, KS = C / 32;
     constexpr int CH = 8 / (2 * RT);                // column halves
     constexpr int NTK = 2 * NK / CH, NTV = NV / CH; // column tiles per wavefront
+    constexpr int G = sizeof(Frag) == 16 && NK * NV < 16 ? 4 : 2;  // of them at a time
+    constexpr int GV = NTV < G ? NTV : G;
     constexpr int kOps = 2 * NK * NV * (int)sizeof(Frag) / 16 * 64;  // 16-byte pieces of a state
     constexpr int NS = kOps / kGThreads;
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
@@ -1317,7 +1347,7 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int rt = w % RT, ch = w / (2 * RT);
+    const int rt = w % RT, ch = CH == 1 ? 0 : w / (2 * RT);
     const bool keys = (w / RT) & 1;
     const int hk = blockIdx.x % a.Hk;
     Unit un;
@@ -1430,34 +1460,30 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) of[kk] = lv.row(ot, 16 * rt, kk);
 #pragma unroll
-            for (int ct = 0; ct < RT; ++ct) {
-                p[ct] = zf4();
-                GSCAN_STEP();
-                if (ct <= rt) {
+            for (int ct = 0; ct < RT; ++ct) p[ct] = zf4();
+            mma_group(p, of, [&](int ct, int kk) { return lv.row(vt, 16 * ct, kk); });
+            decay_tiles<true>(dc, p, rt, l16, g4);
 #pragma unroll
-                    for (int kk = 0; kk < NV; ++kk) p[ct] = mma(lv.row(vt, 16 * ct, kk), of[kk], p[ct]);
-                    p[ct] = decayed_st(dc, a.scale * p[ct], rt, ct, l16, g4);
-                }
-            }
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &df[kk]);
+            for (int kk = 0; kk < KS; ++kk) to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &df[kk]);
             const float e = a.scale * dc.e[16 * rt + l16];
             float as = 0.f;
 #pragma unroll
-            for (int i = 0; i < NTK; ++i) {
-                const int n = i * CH + ch;
-                f4 y = zf4();
-                GSCAN_STEP();
+            for (int i0 = 0; i0 < NTK; i0 += G) {
+                f4 y[G];
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) y = mma(ST::get(state, n, kk, lane), of[kk], y);
-                y *= e;
-                const f4 qv = lk.quad(qt, 16 * rt, n);
+                for (int i = 0; i < G; ++i) y[i] = zf4();
+                mma_group(y, of, [&](int i, int kk) { return ST::get(state, (i0 + i) * CH + ch, kk, lane); });
 #pragma unroll
-                for (int j = 0; j < 4; ++j) as += y[j] * qv[j];
-                acc[i] += y;
+                for (int i = 0; i < G; ++i) {
+                    y[i] *= e;
+                    const f4 qv = lk.quad(qt, 16 * rt, (i0 + i) * CH + ch);
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk <= rt) acc[i] = mma(lk.col(kt, 32 * kk, n), df[kk], acc[i]);
+                    for (int j = 0; j < 4; ++j) as += y[i][j] * qv[j];
+                    y[i] += acc[i0 + i];
+                }
+                mma_group(y, df, [&](int i, int kk) { return lk.col(kt, 32 * kk, (i0 + i) * CH + ch); });
+#pragma unroll
+                for (int i = 0; i < G; ++i) acc[i0 + i] = y[i];
             }
             if (nan)
 #pragma unroll
@@ -1472,66 +1498,51 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
-            for (int ut = 0; ut < RT; ++ut) {
-                p[ut] = zf4();
-                GSCAN_STEP();
-                if (ut >= rt) {
+            for (int ut = 0; ut < RT; ++ut) p[ut] = zf4();
+            mma_group(p, kf, [&](int ut, int kk) { return lk.row(qt, 16 * ut, kk); });
+            decay_tiles<false>(dc, p, rt, l16, g4);
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk) p[ut] = mma(lk.row(qt, 16 * ut, kk), kf[kk], p[ut]);
-                    p[ut] *= a.scale;
-                    f4 none = zf4();
-                    decayed_ts(dc, &p[ut], &none, ut, rt, l16, g4);
-                }
-            }
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
+            for (int kk = 0; kk < KS; ++kk) to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &pf[kk]);
         } else {
             Frag kf[NK], vf[NV];
-            f4 p[RT], d[RT];
+            f4 p[RT], d[RT], y[RT];
             float in = 0.f;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) vf[kk] = lv.row(vt, 16 * rt, kk);
 #pragma unroll
-            for (int ut = 0; ut < RT; ++ut) {
-                p[ut] = d[ut] = zf4();
-                GSCAN_STEP();
-                if (ut >= rt) {
-                    f4 y = zf4();
+            for (int ut = 0; ut < RT; ++ut) p[ut] = y[ut] = zf4();
+            mma_group(p, kf, [&](int ut, int kk) { return lk.row(qt, 16 * ut, kk); });
+            mma_group(y, vf, [&](int ut, int kk) { return lv.row(ot, 16 * ut, kk); });
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk) p[ut] = mma(lk.row(qt, 16 * ut, kk), kf[kk], p[ut]);
-#pragma unroll
-                    for (int kk = 0; kk < NV; ++kk) y = mma(lv.row(ot, 16 * ut, kk), vf[kk], y);
-                    p[ut] *= a.scale;
-                    d[ut] = a.scale * y;
-                    decayed_ts(dc, &p[ut], &d[ut], ut, rt, l16, g4);
-                    // W below the diagonal: sums over s < t of the tile's
-                    // columns, for u >= t
-                    if (ch == 0)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const bool low = ut > rt || g4 + j > l16;
-                            float v = low ? p[ut][j] * y[j] : 0.f;
-                            v += dpp<0x111>(v);
-                            v += dpp<0x112>(v);
-                            v += dpp<0x114>(v);
-                            v += dpp<0x118>(v);
-                            const float before = dpp<0x111>(v);
-                            in += ut > rt || g4 + j >= l16 ? before : 0.f;
-                            if (l16 == 15) rsum[16 * ut + g4 + j][rt] = v;
-                        }
-                }
-            }
+            for (int ut = 0; ut < RT; ++ut) d[ut] = y[ut];
+            decay_tiles<false>(dc, p, rt, l16, g4);
+            decay_tiles<false>(dc, d, rt, l16, g4);
+            // W below the diagonal: sums over s < t of the tile's columns, for u >= t
             if (ch == 0) {
+#pragma unroll
+                for (int ut = 0; ut < RT; ++ut)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool low = ut > rt || (ut == rt && g4 + j > l16);
+                        float v = low ? p[ut][j] * y[ut][j] : 0.f;
+                        v += dpp<0x111>(v);
+                        v += dpp<0x112>(v);
+                        v += dpp<0x114>(v);
+                        v += dpp<0x118>(v);
+                        const float before = dpp<0x111>(v);
+                        in += ut > rt || (ut == rt && g4 + j >= l16) ? before : 0.f;
+                        if (l16 == 15) rsum[16 * ut + g4 + j][rt] = a.scale * v;
+                    }
                 in += __shfl_xor(in, 16);
                 in += __shfl_xor(in, 32);
-                if (lane < 16) inner[16 * rt + lane] = in;
+                if (lane < 16) inner[16 * rt + lane] = a.scale * in;
             }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
-                to_frag(d[2 * kk], d[2 * kk + 1], &df[kk]);
+                to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &pf[kk]);
+                to_frag(a.scale * d[2 * kk], a.scale * d[2 * kk + 1], &df[kk]);
             }
         }
         __syncthreads();  // the states have been read
@@ -1546,20 +1557,22 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) vf[kk] = lv.row(vt, 16 * rt, kk);
 #pragma unroll
-            for (int i = 0; i < NTK; ++i) {
-                const int n = i * CH + ch;
-                f4 y = zf4();
-                GSCAN_STEP();
+            for (int i0 = 0; i0 < NTK; i0 += G) {
+                f4 y[G];
 #pragma unroll
-                for (int kk = 0; kk < NV; ++kk) y = mma(ST::get(state, n, kk, lane), vf[kk], y);
-                y *= ds;
-                const f4 kv = lk.quad(kt, 16 * rt, n);
+                for (int i = 0; i < G; ++i) y[i] = zf4();
+                mma_group(y, vf, [&](int i, int kk) { return ST::get(state, (i0 + i) * CH + ch, kk, lane); });
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bs += y[j] * kv[j];
-                acc[i] += y;
+                for (int i = 0; i < G; ++i) {
+                    y[i] *= ds;
+                    const f4 kv = lk.quad(kt, 16 * rt, (i0 + i) * CH + ch);
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk + 1 >= rt) acc[i] = mma(lk.col(qt, 32 * kk, n), df[kk], acc[i]);
+                    for (int j = 0; j < 4; ++j) bs += y[i][j] * kv[j];
+                    y[i] += acc[i0 + i];
+                }
+                mma_group(y, df, [&](int i, int kk) { return lk.col(qt, 32 * kk, (i0 + i) * CH + ch); });
+#pragma unroll
+                for (int i = 0; i < G; ++i) acc[i0 + i] = y[i];
             }
             if (nan)
 #pragma unroll
@@ -1577,17 +1590,23 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
-            for (int i = 0; i < NTV; ++i) {
-                const int m = (i * CH + ch) * 2 + keys;
-                f4 y = zf4();
-                GSCAN_STEP();
+            for (int i0 = 0; i0 < NTV; i0 += GV) {
+                f4 y[GV];
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) y = mma(ST::turned(state, m, kk, lane), kf[kk], y);
-                y *= ds;
+                for (int i = 0; i < GV; ++i) y[i] = zf4();
+                mma_group(y, kf, [&](int i, int kk) {
+                    return ST::turned(state, ((i0 + i) * CH + ch) * 2 + keys, kk, lane);
+                });
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk)
-                    if (2 * kk + 1 >= rt) y = mma(lv.col(ot, 32 * kk, m), pf[kk], y);
-                if (mine && 16 * m + g4 < a.Dv) put4(out + 16 * m, y);
+                for (int i = 0; i < GV; ++i) y[i] *= ds;
+                mma_group(y, pf, [&](int i, int kk) {
+                    return lv.at_col(ot, 32 * kk, lv.col_off(((i0 + i) * CH + ch) * 2 + keys));
+                });
+#pragma unroll
+                for (int i = 0; i < GV; ++i) {
+                    const int m = ((i0 + i) * CH + ch) * 2 + keys;
+                    if (mine && 16 * m + g4 < a.Dv) put4(out + 16 * m, y[i]);
+                }
             }
             if (nan && mine)
 #pragma unroll 1
