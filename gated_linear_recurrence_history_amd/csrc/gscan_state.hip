@@ -391,7 +391,10 @@ struct Unit {
     int seq, part, parts, len, slot0;
 };
 
-// Whether unit u exists.  Offsets are clamped to the tokens there are, so
+__device__ __forceinline__ int first_lane(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Whether unit u exists (the same answer, in scalar registers, for every
+// lane).  Offsets are clamped to the tokens there are, so
 // wrong ones read and write nothing out of range.  Called by whole wavefronts.
 __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t per, int C,
                                           int lane, Unit *w)
@@ -435,21 +438,21 @@ __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t
         const uint64_t hit = __ballot(u < ub + su);
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
-            const int64_t seq = i0 + l;
+            const int64_t seq = i0 + first_lane(l);
             if (seq >= a.B) return false;
             w->seq = (int)seq;
-            w->parts = __shfl(nu, l);
-            w->part = (int)(u - (ub + __shfl(su, l) - w->parts));
-            w->slot0 = (int)(cb + __shfl(sc, l) - __shfl(nc, l));
+            w->parts = first_lane(__shfl(nu, l));
+            w->part = first_lane((int)(u - (ub + __shfl(su, l) - w->parts)));
+            w->slot0 = first_lane((int)(cb + __shfl(sc, l) - __shfl(nc, l)));
             // offsets that overlap could ask for more chunks than there are
-            if (w->slot0 + __shfl(nc, l) > a.chunks) return false;
-            const int start = __shfl((int)s, l);
-            w->len = __shfl((int)(e - s), l);
+            if (w->slot0 + first_lane(__shfl(nc, l)) > a.chunks) return false;
+            const int start = first_lane(__shfl((int)s, l));
+            w->len = first_lane(__shfl((int)(e - s), l));
             w->tok0 = w->in0 = start;
             return true;
         }
-        ub += __shfl(su, 63);
-        cb += __shfl(sc, 63);
+        ub += first_lane(__shfl(su, 63));
+        cb += first_lane(__shfl(sc, 63));
     }
     return false;
 }
@@ -536,7 +539,7 @@ struct Stage {
         base += step;
     }
     template <class TL>
-    __device__ __forceinline__ void store(const Regs &r, char *tile, int tid) const
+    static __device__ __forceinline__ void store(const Regs &r, char *tile, int tid)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -550,7 +553,7 @@ struct Stage {
     // they do reach is not finite in any case (the whole column of the state
     // from that token on), so those results become NaN without being computed.
     template <class TL, class F>
-    __device__ __forceinline__ void scrub(const Regs &r, char *tile, int tid, F found) const
+    static __device__ __forceinline__ void scrub(const Regs &r, char *tile, int tid, F found)
     {
         uint32_t m = 0;
 #pragma unroll
@@ -588,7 +591,7 @@ struct __align__(16) Decay {
 
 // x of other lanes, zero where there is none: CTRL 0x110 + n, n lanes below in
 // the group of 16; 0x142 and 0x143, the last lane of the group (of the half)
-// before, taken by the groups of row mask RM.
+// before, taken by the groups of row mask RM; 0x150 + n, lane n of the group.
 template <int CTRL, int RM = 0xf>
 __device__ __forceinline__ float dpp(float x)
 {
@@ -1305,11 +1308,13 @@ __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
     return s;
 }
 
-// One workgroup per chunk and key head: its queries and keys stay in LDS
-// while it takes the value heads that share them one by one, so dQ and dK of
-// shared heads are summed in registers in a fixed order.  All of a head's
-// rows and state operands are requested at once, the next head's while this
-// one is computed.
+// Workgroups (one per CU, its registers full) take chunks of a key head in
+// turn: its queries and keys stay in LDS while the value heads that share
+// them are taken one by one, so dQ and dK of shared heads are summed in
+// registers in a fixed order.  The rows and state operands of the next head,
+// or of the next chunk's first, are requested while this one is computed
+// (one workgroup per chunk, which waits for its own, took 192 us where this
+// takes [measured below]).
 //
 // Eight wavefronts: `rt` owns token rows 16rt .. 16rt+15, half of them dQ and
 // half dK, each half of dV (and, fp32 with its two rows of tiles, each every
@@ -1319,10 +1324,11 @@ __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
 // (for dV and dK).  Gradients are formed transposed, four columns of a token
 // per lane.
 constexpr int kGThreads = 512;
+constexpr int kCus = 256;
 
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kGThreads, 2)
-gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
+gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
@@ -1349,38 +1355,60 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int rt = w % RT, ch = CH == 1 ? 0 : w / (2 * RT);
     const bool keys = (w / RT) & 1;
-    const int hk = blockIdx.x % a.Hk;
-    Unit un;
-    if (!find_unit(a, blockIdx.x / a.Hk, C, C, lane, &un)) return;
     const bool packed = a.off != nullptr;
-    const int t0 = un.part * C, reps = a.H / a.Hk, left = un.len - t0;
-    if (left <= 0) return;  // a sequence without tokens
-    const int64_t slot = un.slot0 + un.part;
+    const int reps = a.H / a.Hk;
     const char *ws = reinterpret_cast<const char *>(a.ws);
     const TK lk(lane);
     const TV lv(lane);
-    const bool mine = 16 * rt + l16 < left;  // this lane's token exists
 
-    Stage<T, NV, kGThreads> sv, so;
-    typename Stage<T, NV, kGThreads>::Regs rv, ro;
+    // what is computed: value head `h` of chunk `slot`, and where its tokens are
+    struct Item {
+        Unit un;
+        int64_t u, slot;  // unit of the grid (chunk and key head), chunk slot
+        int h, hk, t0, left;
+    };
+    // the first item from unit u on; u >= units when there is none
+    auto find = [&](int64_t u, Item *it) {
+        for (; u < units; u += gridDim.x) {
+            if (!find_unit(a, u / a.Hk, C, C, lane, &it->un)) continue;
+            it->t0 = it->un.part * C;
+            it->left = it->un.len - it->t0;
+            if (it->left <= 0) continue;  // a sequence without tokens
+            it->slot = it->un.slot0 + it->un.part;
+            it->hk = (int)(u % a.Hk);
+            it->h = it->hk * reps;
+            break;
+        }
+        it->u = u;
+    };
+    typedef Stage<T, NK, kGThreads> SK;
+    typedef Stage<T, NV, kGThreads> SV;
+    typename SK::Regs rq, rk;
+    typename SV::Regs rv, ro;
     u4 rs[NS], rd[NS];
-    float gx = 0.f;
-    auto request = [&](int h) {
-        sv.begin(rows_of<S>(a.v, a.vs, un, packed, h), a.vs.t, t0, a.Dv, tid);
-        so.begin(rows_of<S>(a.dout, a.ds, un, packed, h), a.ds.t, t0, a.Dv, tid);
-        sv.load(rv, left, 0, tid);
-        so.load(ro, left, 0, tid);
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + (slot * a.H + h) * kOps;
+    Gates::Raw gx;
+    auto request = [&](const Item &it, bool first) {
+        if (first) {
+            SK sq, sk;
+            sq.begin(rows_of<S>(a.q, a.qs, it.un, packed, it.hk), a.qs.t, it.t0, a.Dk, tid);
+            sk.begin(rows_of<S>(a.k, a.ks, it.un, packed, it.hk), a.ks.t, it.t0, a.Dk, tid);
+            sq.load(rq, it.left, 0, tid);
+            sk.load(rk, it.left, 0, tid);
+        }
+        SV sv, so;
+        sv.begin(rows_of<S>(a.v, a.vs, it.un, packed, it.h), a.vs.t, it.t0, a.Dv, tid);
+        so.begin(rows_of<S>(a.dout, a.ds, it.un, packed, it.h), a.ds.t, it.t0, a.Dv, tid);
+        sv.load(rv, it.left, 0, tid);
+        so.load(ro, it.left, 0, tid);
+        Gates gates;
+        gates.begin(a, it.un, it.h, it.t0, C, lane);
+        gx = gates.load(it.left, lane, 0);
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + (it.slot * a.H + it.h) * kOps;
 #pragma unroll
         for (int i = 0; i < NS; ++i) rs[i] = p[tid + kGThreads * i];
-        if (w == 0) {
-            const int64_t g0 = (packed ? un.in0 * a.gs.t : (int64_t)un.seq * a.gs.b) + (int64_t)h * a.gs.h;
-            if (lane < C && lane < left)
-                gx = load_scalar(a.gate, g0 + (int64_t)(t0 + lane) * a.gs.t, a.gate_dtype) + a.gate_shift;
-        }
     };
-    auto request_ds = [&](int h) {
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + (slot * a.H + h) * kOps;
+    auto request_ds = [&](const Item &it) {
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + (it.slot * a.H + it.h) * kOps;
 #pragma unroll
         for (int i = 0; i < NS; ++i) rd[i] = p[tid + kGThreads * i];
     };
@@ -1391,55 +1419,56 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
             state[(q & ~63) + place(q & 63)] = r[i];
         }
     };
-    for (int i = tid; i < NK * 32; i += kGThreads) {
-        first_k[i] = C;
-        last_q[i] = -1;
-    }
-    if (tid < NV * 32) last_o[tid] = -1;
-    if (tid < C) row_k[tid] = row_o[tid] = 0;
-    if (tid < 3) ends[tid] = tid < 2 ? -1 : C;
-    if (tid == 0) bad = 0;
-    {
-        Stage<T, NK, kGThreads> sq, sk;
-        typename Stage<T, NK, kGThreads>::Regs rq, rk;
-        sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, t0, a.Dk, tid);
-        sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, t0, a.Dk, tid);
-        sq.load(rq, left, 0, tid);
-        sk.load(rk, left, 0, tid);
-        request(hk * reps);
-        request_ds(hk * reps);
+    auto clear = [&] {
+        for (int i = tid; i < NK * 32; i += kGThreads) {
+            first_k[i] = C;
+            last_q[i] = -1;
+        }
+        if (tid < NV * 32) last_o[tid] = -1;
+        if (tid < C) row_k[tid] = row_o[tid] = 0;
+        if (tid < 3) ends[tid] = tid < 2 ? -1 : C;
+        if (tid == 0) bad = 0;
         __syncthreads();
-        sq.template store<TK>(rq, qt, tid);
-        sk.template store<TK>(rk, kt, tid);
-        sq.template scrub<TK>(rq, qt, tid, [&](int row, int c) {
-            atomicMax(&last_q[c], row);
-            atomicMax(&ends[0], row);
-            bad = 1;
-        });
-        sk.template scrub<TK>(rk, kt, tid, [&](int row, int c) {
-            atomicMin(&first_k[c], row);
-            atomicMin(&ends[2], row);
-            row_k[row] = 1;
-            bad = 1;
-        });
-    }
+    };
+    Item it;
+    find(blockIdx.x, &it);
+    if (it.u >= units) return;
+    request(it, true);
+    request_ds(it);
+    clear();
     f4 acc[NTK];  // dQ or dK of the wavefront's tokens
 #pragma unroll
     for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
-    for (int hr = 0; hr < reps; ++hr) {
-        const int h = hk * reps + hr;
-        sv.template store<TV>(rv, vt, tid);
-        so.template store<TV>(ro, ot, tid);
-        so.template scrub<TV>(ro, ot, tid, [&](int row, int c) {
+    while (true) {
+        const int h = it.h;
+        const bool mine = 16 * rt + l16 < it.left;  // this lane's token exists
+        if (h == it.hk * reps) {
+            SK::template store<TK>(rq, qt, tid);
+            SK::template store<TK>(rk, kt, tid);
+            SK::template scrub<TK>(rq, qt, tid, [&](int row, int c) {
+                atomicMax(&last_q[c], row);
+                atomicMax(&ends[0], row);
+                bad = 1;
+            });
+            SK::template scrub<TK>(rk, kt, tid, [&](int row, int c) {
+                atomicMin(&first_k[c], row);
+                atomicMin(&ends[2], row);
+                row_k[row] = 1;
+                bad = 1;
+            });
+        }
+        SV::template store<TV>(rv, vt, tid);
+        SV::template store<TV>(ro, ot, tid);
+        SV::template scrub<TV>(ro, ot, tid, [&](int row, int c) {
             atomicMax(&last_o[c], row);
             atomicMax(&ends[1], row);
             row_o[row] = 1;
             bad = 1;
         });
         keep(rs);
-        const float x = gx;
-        if (w == 0) gate_scan<C>(dc, x, lane < left, a.gate_form, lane);
+        const float x = Gates::value(gx, a);
+        if (w == 0) gate_scan<C>(dc, x, lane < it.left, a.gate_form, lane);
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
@@ -1448,9 +1477,14 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
             for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
             if (lane == 0) fsum[w] = f;
         }
+        Item next = it;
+        const bool same = h + 1 < (it.hk + 1) * reps;  // another head of this chunk
+        if (same) ++next.h;
+        else find(it.u + gridDim.x, &next);
+        const bool more = next.u < units;
         __syncthreads();
         const bool nan = bad != 0;
-        if (hr + 1 < reps) request(h + 1);
+        if (more) request(next, !same);
 
         Frag pf[KS], df[KS];
         if (!keys) {
@@ -1506,7 +1540,7 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
         } else {
             Frag kf[NK], vf[NV];
             f4 p[RT], d[RT], y[RT];
-            float in = 0.f;
+            float in = 0.f, row = 0.f;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
@@ -1531,10 +1565,11 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
                         v += dpp<0x112>(v);
                         v += dpp<0x114>(v);
                         v += dpp<0x118>(v);
-                        const float before = dpp<0x111>(v);
+                        const float before = dpp<0x111>(v), all = dpp<0x15f>(v);
                         in += ut > rt || (ut == rt && g4 + j >= l16) ? before : 0.f;
-                        if (l16 == 15) rsum[16 * ut + g4 + j][rt] = a.scale * v;
+                        row = l16 == 4 * ut + j ? all : row;
                     }
+                if (l16 < 4 * RT) rsum[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = a.scale * row;
                 in += __shfl_xor(in, 16);
                 in += __shfl_xor(in, 32);
                 if (lane < 16) inner[16 * rt + lane] = a.scale * in;
@@ -1548,7 +1583,7 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
         __syncthreads();  // the states have been read
         keep(rd);
         __syncthreads();
-        if (hr + 1 < reps) request_ds(h + 1);
+        if (more) request_ds(next);
         const float ds = dc.d[16 * rt + l16];
         if (keys) {
             // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
@@ -1586,7 +1621,7 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
         // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, half of the columns
         {
             Frag kf[NK];
-            S *out = reinterpret_cast<S *>(a.dv) + ((un.tok0 + t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
+            S *out = reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
@@ -1652,33 +1687,40 @@ gscan_state_grad_kernel(StateArgs a, size_t st_s, size_t st_ds)
             for (int i = 0; i < 8; ++i) F += fsum[i];
             F *= dc.g;
             const float before = __shfl_up(pb, 1);
-            if (lane < C && lane < left) {
+            if (lane < C && lane < it.left) {
                 float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
                 if (nan && (lane <= ends[0] || lane <= ends[1] || lane > ends[2])) r = __builtin_nanf("");
-                const int64_t at = (un.tok0 + t0 + lane) * a.H + h;
+                const int64_t at = (it.un.tok0 + it.t0 + lane) * a.H + h;
                 if (a.gate_dtype) reinterpret_cast<uint16_t *>(a.dgate)[at] = to_bf16(r);
                 else reinterpret_cast<float *>(a.dgate)[at] = r;
             }
         }
-        if (hr + 1 < reps) {
-            __syncthreads();
-            if (nan) {  // d_out's of this head (q's and k's stay)
+        if (!same) {  // the chunk's last head
+            if (mine) {
+                S *out = reinterpret_cast<S *>(keys ? a.dk : a.dq) +
+                         ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.Hk + it.hk) * a.Dk + g4;
+#pragma unroll
+                for (int i = 0; i < NTK; ++i) {
+                    const int n = i * CH + ch;
+                    if (16 * n + g4 < a.Dk) put4(out + 16 * n, acc[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NTK; ++i) acc[i] = zf4();
+        }
+        if (!more) break;
+        __syncthreads();
+        if (nan) {
+            if (!same) {
+                clear();
+            } else {  // d_out's of this head (q's and k's stay)
                 if (tid < NV * 32) last_o[tid] = -1;
                 if (tid < C) row_o[tid] = 0;
                 if (tid == 0) ends[1] = -1;
                 __syncthreads();
             }
         }
-    }
-
-    if (mine) {
-        S *out = reinterpret_cast<S *>(keys ? a.dk : a.dq) +
-                 ((un.tok0 + t0 + 16 * rt + l16) * a.Hk + hk) * a.Dk + g4;
-#pragma unroll
-        for (int i = 0; i < NTK; ++i) {
-            const int n = i * CH + ch;
-            if (16 * n + g4 < a.Dk) put4(out + 16 * n, acc[i]);
-        }
+        it = next;
     }
 }
 
@@ -1727,8 +1769,9 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
                        dim3(2 * kSThreads), 0, st, a, p.per, o);
     e = hipGetLastError();
     if (e != hipSuccess || a.T == 0) return e;
-    hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(p.chunks * a.Hk)),
-                       dim3(kGThreads), 0, st, a, p.st_s, p.st_ds);
+    const int64_t units = p.chunks * a.Hk;
+    hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(units < kCus ? units : kCus)),
+                       dim3(kGThreads), 0, st, a, units, p.st_s, p.st_ds);
     return hipGetLastError();
 }
 
