@@ -246,11 +246,16 @@ int check_state_desc(const gscan_state_scan_t *d, bool backward, gscan::StateArg
         !strides16(d->v_stride, 3, d->dtype) ||
         (backward && !strides16(d->d_out_stride, 3, d->dtype)))
         return fail(GSCAN_ERR_MISALIGNED, "strides of q, k, v, d_out must be multiples of 16 bytes");
-    auto far = [](const int64_t *s) { return s[1] < 0 || s[1] >= kMaxStride; };
-    if (d->T > 1 && (far(d->q_stride) || far(d->k_stride) || far(d->v_stride) ||
-                     (backward && far(d->d_out_stride))))
-        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "token strides of q, k, v, d_out must be 0 .. 2^23 - 1");
-    auto st = [](const int64_t *s) { return gscan::Strides{s[0], s[1], s[2]}; };
+    auto far = [](const int64_t *s) {
+        return s[0] < 0 || s[1] < 0 || s[1] >= kMaxStride || s[2] < 0 || s[2] > 2147483647;
+    };
+    if (far(d->q_stride) || far(d->k_stride) || far(d->v_stride) || far(d->gate_stride) ||
+        (backward && far(d->d_out_stride)))
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "strides must not be negative, token strides below 2^23, head strides below 2^31");
+    auto st = [&](const int64_t *s) {
+        return gscan::Strides{d->seq_offsets ? 0 : s[0], (uint32_t)s[1], (uint32_t)s[2]};
+    };
     a->qs = st(d->q_stride);
     a->ks = st(d->k_stride);
     a->vs = st(d->v_stride);

@@ -8,10 +8,11 @@
 
 namespace gscan {
 
-// Element strides of a [batch][token][head][width] operand; the width is
-// contiguous.
+// Element strides of a [batch][token][head][width] operand (packed: batch 0);
+// the width is contiguous.  Tokens and heads are less than 2^31 apart.
 struct Strides {
-    int64_t b = 0, t = 0, h = 0;
+    int64_t b = 0;
+    uint32_t t = 0, h = 0;
 };
 
 // What the scan's kernels take by value.

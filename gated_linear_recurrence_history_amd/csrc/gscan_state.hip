@@ -457,13 +457,13 @@ __device__ __forceinline__ bool find_unit(const StateArgs &a, int64_t u, int64_t
     return false;
 }
 
-// First element of a sequence's rows of head h.
+// The row of token t of a sequence and head h.
 template <class S>
-__device__ __forceinline__ const S *rows_of(const void *p, const Strides &s, const Unit &w,
-                                            bool packed, int h)
+__device__ __forceinline__ const S *row_at(const void *p, const Strides &s, const Unit &w, int h,
+                                           int64_t t)
 {
-    return reinterpret_cast<const S *>(p) + (packed ? w.in0 * s.t : (int64_t)w.seq * s.b) +
-           (int64_t)h * s.h;
+    return reinterpret_cast<const S *>(p) + (int64_t)w.seq * s.b +
+           ((uint64_t)s.h * (uint32_t)h + (uint64_t)s.t * (uint32_t)(w.in0 + t));
 }
 
 // Gate arguments of a chunk's tokens, one per lane (those from `left` on: zero),
@@ -476,12 +476,12 @@ struct Gates {
                                           int lane)
     {
         const int64_t e = a.gate_dtype ? 2 : 4;
-        base = reinterpret_cast<const char *>(a.gate) +
-               ((a.off ? w.in0 * a.gs.t : (int64_t)w.seq * a.gs.b) + (int64_t)h * a.gs.h + t0 * a.gs.t) * e;
-        const uint32_t at = (uint32_t)(lane * (int)a.gs.t) * (uint32_t)e;
+        base = a.gate_dtype ? reinterpret_cast<const char *>(row_at<uint16_t>(a.gate, a.gs, w, h, t0))
+                            : reinterpret_cast<const char *>(row_at<float>(a.gate, a.gs, w, h, t0));
+        const uint32_t at = (uint32_t)lane * a.gs.t * (uint32_t)e;
         o32 = lane < C && !a.gate_dtype ? at : kNowhere;
         o16 = lane < C && a.gate_dtype ? at : kNowhere;
-        step = C * a.gs.t * e;
+        step = (int64_t)(C * a.gs.t) * e;
     }
     struct Raw {
         uint32_t x32;
@@ -514,16 +514,15 @@ struct Stage {
     const typename T::S *base;  // that row
     static constexpr int kPpr = NKU * 32 / T::VE;  // pieces per row
 
-    // row 0 of the tile is row t0 of `rows` (stride st, below 2^23); columns
-    // before `cols` are read, the others are zero
-    __device__ __forceinline__ void begin(const typename T::S *rows, int64_t st, int64_t t0, int cols,
-                                          int tid)
+    // row 0 of the tile is at `row` (stride st, below 2^23); columns before
+    // `cols` are read, the others are zero
+    __device__ __forceinline__ void begin(const typename T::S *row0, uint32_t st, int cols, int tid)
     {
-        base = rows + t0 * st;
+        base = row0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int q = tid + TH * i, row = q / kPpr, col = q % kPpr * T::VE;
-            off[i] = col < cols ? (uint32_t)(row * (int)st + col) * (uint32_t)sizeof(typename T::S) : kNowhere;
+            off[i] = col < cols ? (uint32_t)(row * st + col) * (uint32_t)sizeof(typename T::S) : kNowhere;
         }
     }
     // the first `left` rows of the tile (the others zero), and on by `step`
@@ -612,8 +611,10 @@ __device__ __forceinline__ double of_lane(double x, int lane)
 }
 
 // x: the gate argument of token `lane` (ok: there is one).  One wavefront.
+// Factors of scores off the diagonal are multiplied by mul.
 template <int C>
-__device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane)
+__device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane,
+                                          float mul = 1.f)
 {
     double L = ok ? (double)log_gate(x, form) * 1.44269504088896340736 : 0.0;
     L += dpp<0x111>(L);
@@ -635,7 +636,7 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
         s.lo[lane] = (float)(L - (double)h);
         s.e[lane] = exp2_(h);
         s.d[lane] = exp2_((float)(end - L));
-        s.col[lane] = exp2_((float)(m - L));
+        s.col[lane] = mul * exp2_((float)(m - L));
 #pragma unroll
         for (int i = 0; i < C / 16 - 1; ++i)
             s.row[i][lane] = lane >= 16 * i + 16 ? exp2_((float)(L - mid[i])) : 0.f;
@@ -659,33 +660,46 @@ __device__ __forceinline__ f4 decayed_st(const Decay<C> &s, f4 x, int rt, int ct
         x[j] = g4 + j <= l16 ? x[j] * exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
     return x;
 }
-// The same for a wavefront that holds all tiles of its tokens `own` (16 of
-// them, known at run time only) without a branch: `ST` tokens t = 16own + l16
-// are the columns and s the rows of tiles p[0 ..], tiles behind the diagonal
-// zero; otherwise the columns are s = 16own + l16 and the rows t.
+// The same, times mul (Decay's own), for a wavefront that holds all tiles of
+// its 16 tokens `own`, known at run time only: ST, tokens t = 16own + l16 are
+// the columns and s the rows of tiles p[0 ..]; otherwise the columns are
+// s = 16own + l16 and the rows t.  Tiles behind the diagonal become zero.
 template <bool ST, int C>
-__device__ __forceinline__ void decay_tiles(const Decay<C> &s, f4 (&p)[C / 16], int own, int l16, int g4)
+__device__ __forceinline__ void decay_tiles(const Decay<C> &s, f4 (&p)[C / 16], int own, float mul,
+                                            int l16, int g4)
 {
     constexpr int RT = C / 16;
     const int me = 16 * own + l16;
-    f4 x = p[0];
-#pragma unroll
-    for (int i = 1; i < RT; ++i) x = own == i ? p[i] : x;
-    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * own + g4]);
-    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * own + g4]);
-    const float hm = s.hi[me], lm = s.lo[me];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float f = exp2_(ST ? (hm - hi[j]) + (lm - lo[j]) : (hi[j] - hm) + (lo[j] - lm));
-        x[j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? x[j] * f : 0.f;
-    }
-    const float c = s.col[me];
+    const float c = s.col[me], hm = s.hi[me], lm = s.lo[me];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const f4 f = ST ? *reinterpret_cast<const f4 *>(&s.col[16 * i + g4]) * s.row[i][me]
-                        : *reinterpret_cast<const f4 *>(&s.row[own][16 * i + g4]) * c;
-        p[i] = own == i ? x : (ST ? i < own : i > own) ? p[i] * f : zf4();
+        if (ST ? i < own : i > own) {
+            if (ST) p[i] *= *reinterpret_cast<const f4 *>(&s.col[16 * i + g4]) * s.row[i][me];
+            else p[i] *= *reinterpret_cast<const f4 *>(&s.row[own][16 * i + g4]) * c;
+        } else if (i == own) {
+            const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * i + g4]);
+            const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * i + g4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f = exp2_(ST ? (hm - hi[j]) + (lm - lo[j]) : (hi[j] - hm) + (lo[j] - lm));
+                p[i][j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? p[i][j] * (mul * f) : 0.f;
+            }
+        } else {
+            p[i] = zf4();
+        }
     }
+}
+
+// Running sum over the wavefront (the whole sum in its last lane).
+__device__ __forceinline__ float scan64(float x)
+{
+    x += dpp<0x111>(x);
+    x += dpp<0x112>(x);
+    x += dpp<0x114>(x);
+    x += dpp<0x118>(x);
+    x += dpp<0x142, 0xa>(x);
+    x += dpp<0x143, 0xc>(x);
+    return x;
 }
 
 // y[i] += A(i, k) b[k], the operands A of step k + 1 requested before the
@@ -779,7 +793,6 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     const int64_t unit = blockIdx.x / slices / a.H;
     Unit un;
     if (!find_unit(a, unit, per, C, lane, &un)) return;
-    const bool packed = a.off != nullptr;
     const int c0 = slice * kSlice, vcols = a.Dv - c0;
     const int tb = (int)(un.part * per);
     const int te = un.len - tb > per ? (int)(tb + per) : un.len;
@@ -798,14 +811,14 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
         Gates gates;
         Gates::Raw gx[2];
         gates.begin(a, un, h, tb, C, lane);
-        sq.begin(rows_of<S>(a.q, a.qs, un, packed, hk), a.qs.t, tb, a.Dk, tid);
-        sk.begin(rows_of<S>(a.k, a.ks, un, packed, hk), a.ks.t, tb, a.Dk, tid);
-        sv.begin(rows_of<S>(a.v, a.vs, un, packed, h) + c0, a.vs.t, tb, vcols, tid);
+        sq.begin(row_at<S>(a.q, a.qs, un, hk, tb), a.qs.t, a.Dk, tid);
+        sk.begin(row_at<S>(a.k, a.ks, un, hk, tb), a.ks.t, a.Dk, tid);
+        sv.begin(row_at<S>(a.v, a.vs, un, h, tb) + c0, a.vs.t, vcols, tid);
         auto request = [&](int t0, auto set) {
             constexpr int O = decltype(set)::value;
-            sq.load(rq[O], te - t0, C * a.qs.t, tid);
-            sk.load(rk[O], te - t0, C * a.ks.t, tid);
-            sv.load(rv[O], te - t0, C * a.vs.t, tid);
+            sq.load(rq[O], te - t0, (int64_t)(C * a.qs.t), tid);
+            sk.load(rk[O], te - t0, (int64_t)(C * a.ks.t), tid);
+            sv.load(rv[O], te - t0, (int64_t)(C * a.vs.t), tid);
             gx[O] = gates.load(te - t0, lane, 1);
         };
         request(tb, std::integral_constant<int, 0>());
@@ -1022,7 +1035,6 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool brings = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
-    const bool packed = a.off != nullptr;
     const int c0 = slice * kSlice, ycols = jb.yd - c0;
     const int cb = tb / C, nc = te > tb ? (te + C - 1) / C - cb : 1;  // chunks, at least one
     const int c1 = REV ? cb + nc - 1 : cb;                           // the first walked
@@ -1033,15 +1045,15 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
         Gates gates;
         u4 rx[2][NX], ry[2][2];
         Gates::Raw gx[2];
-        sx.begin(rows_of<S>(jb.x, jb.xs, un, packed, jb.xh), jb.xs.t, c1 * C, jb.xd, tid);
-        sy.begin(rows_of<S>(jb.y, jb.ys, un, packed, jb.yh) + c0, jb.ys.t, c1 * C, ycols, tid);
+        sx.begin(row_at<S>(jb.x, jb.xs, un, jb.xh, c1 * C), jb.xs.t, jb.xd, tid);
+        sy.begin(row_at<S>(jb.y, jb.ys, un, jb.yh, c1 * C) + c0, jb.ys.t, ycols, tid);
         gates.begin(a, un, h, c1 * C, C, lane);
         // chunks past the end (in either direction) have no rows
         auto request = [&](int n, auto set) {
             constexpr int O = decltype(set)::value;
             const int left = n < nc ? te - (c1 + step * n) * C : 0;
-            sx.load(rx[O], left, step * C * jb.xs.t, tid);
-            sy.load(ry[O], left, step * C * jb.ys.t, tid);
+            sx.load(rx[O], left, step * (int64_t)(C * jb.xs.t), tid);
+            sy.load(ry[O], left, step * (int64_t)(C * jb.ys.t), tid);
             gx[O] = gates.load(left, lane, step);
         };
         auto bring = [&](int n, auto set) {
@@ -1328,7 +1340,7 @@ constexpr int kCus = 256;
 
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kGThreads, 2)
-gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
+gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
@@ -1337,25 +1349,25 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
     typedef States<T, NV> ST;
     constexpr int C = T::C, RT = C / 16, KS = C / 32;
     constexpr int CH = 8 / (2 * RT);                // column halves
-    constexpr int NTK = 2 * NK / CH, NTV = NV / CH; // column tiles per wavefront
+    constexpr int NTK = 2 * NK / CH;                // column tiles of dQ, dK per wavefront
     constexpr int G = sizeof(Frag) == 16 && NK * NV < 16 ? 4 : 2;  // of them at a time
-    constexpr int GV = NTV < G ? NTV : G;
     constexpr int kOps = 2 * NK * NV * (int)sizeof(Frag) / 16 * 64;  // 16-byte pieces of a state
     constexpr int NS = kOps / kGThreads;
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
     __shared__ u4 state[kOps];
+    __shared__ Frag scores[RT][KS][64];  // P . D of a tile row's keys, for dV
     __shared__ Decay<C> dc;
-    __shared__ float rsum[C][RT], inner[C], asum[CH][C], bsum[CH][C], fsum[8];
+    __shared__ float rsum[C][RT], inner[C], asum[CH][C], bsum[CH][C], fsum[2][8];
     // what infinities and NaN reach: per column the first row of k and the last
     // of q and d_out that hold one, which rows of k and d_out do, and the last
     // row of q, of d_out, the first of k
     __shared__ int first_k[NK * 32], last_q[NK * 32], last_o[NV * 32], row_k[C], row_o[C], ends[3], bad;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tid = threadIdx.x;
+    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int rt = w % RT, ch = CH == 1 ? 0 : w / (2 * RT);
     const bool keys = (w / RT) & 1;
-    const bool packed = a.off != nullptr;
     const int reps = a.H / a.Hk;
     const char *ws = reinterpret_cast<const char *>(a.ws);
     const TK lk(lane);
@@ -1364,18 +1376,19 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
     // what is computed: value head `h` of chunk `slot`, and where its tokens are
     struct Item {
         Unit un;
-        int64_t u, slot;  // unit of the grid (chunk and key head), chunk slot
-        int h, hk, t0, left;
+        uint32_t u;  // unit of the grid (chunk and key head)
+        int slot, h, hk, t0, left;
     };
     // the first item from unit u on; u >= units when there is none
-    auto find = [&](int64_t u, Item *it) {
+    auto find = [&](uint32_t u, Item *it) {
         for (; u < units; u += gridDim.x) {
-            if (!find_unit(a, u / a.Hk, C, C, lane, &it->un)) continue;
+            const uint32_t c = u / (uint32_t)a.Hk;
+            if (!find_unit(a, c, C, C, lane, &it->un)) continue;
             it->t0 = it->un.part * C;
             it->left = it->un.len - it->t0;
             if (it->left <= 0) continue;  // a sequence without tokens
             it->slot = it->un.slot0 + it->un.part;
-            it->hk = (int)(u % a.Hk);
+            it->hk = (int)(u - c * (uint32_t)a.Hk);
             it->h = it->hk * reps;
             break;
         }
@@ -1390,25 +1403,25 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
     auto request = [&](const Item &it, bool first) {
         if (first) {
             SK sq, sk;
-            sq.begin(rows_of<S>(a.q, a.qs, it.un, packed, it.hk), a.qs.t, it.t0, a.Dk, tid);
-            sk.begin(rows_of<S>(a.k, a.ks, it.un, packed, it.hk), a.ks.t, it.t0, a.Dk, tid);
+            sq.begin(row_at<S>(a.q, a.qs, it.un, it.hk, it.t0), a.qs.t, a.Dk, tid);
+            sk.begin(row_at<S>(a.k, a.ks, it.un, it.hk, it.t0), a.ks.t, a.Dk, tid);
             sq.load(rq, it.left, 0, tid);
             sk.load(rk, it.left, 0, tid);
         }
         SV sv, so;
-        sv.begin(rows_of<S>(a.v, a.vs, it.un, packed, it.h), a.vs.t, it.t0, a.Dv, tid);
-        so.begin(rows_of<S>(a.dout, a.ds, it.un, packed, it.h), a.ds.t, it.t0, a.Dv, tid);
+        sv.begin(row_at<S>(a.v, a.vs, it.un, it.h, it.t0), a.vs.t, a.Dv, tid);
+        so.begin(row_at<S>(a.dout, a.ds, it.un, it.h, it.t0), a.ds.t, a.Dv, tid);
         sv.load(rv, it.left, 0, tid);
         so.load(ro, it.left, 0, tid);
         Gates gates;
         gates.begin(a, it.un, it.h, it.t0, C, lane);
         gx = gates.load(it.left, lane, 0);
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + (it.slot * a.H + it.h) * kOps;
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + ((int64_t)it.slot * a.H + it.h) * kOps;
 #pragma unroll
         for (int i = 0; i < NS; ++i) rs[i] = p[tid + kGThreads * i];
     };
     auto request_ds = [&](const Item &it) {
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + (it.slot * a.H + it.h) * kOps;
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + ((int64_t)it.slot * a.H + it.h) * kOps;
 #pragma unroll
         for (int i = 0; i < NS; ++i) rd[i] = p[tid + kGThreads * i];
     };
@@ -1440,7 +1453,8 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
 #pragma unroll
     for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
-    while (true) {
+    for (int odd = 0;; odd ^= 1) {
+        asm volatile("" : "+v"(tid));  // addresses from it are formed anew, not kept across the loop
         const int h = it.h;
         const bool mine = 16 * rt + l16 < it.left;  // this lane's token exists
         if (h == it.hk * reps) {
@@ -1468,14 +1482,13 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
         });
         keep(rs);
         const float x = Gates::value(gx, a);
-        if (w == 0) gate_scan<C>(dc, x, lane < it.left, a.gate_form, lane);
+        if (w == 0) gate_scan<C>(dc, x, lane < it.left, a.gate_form, lane, a.scale);
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) f += dot16(rs[i], rd[i], T());
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) f += __shfl_xor(f, d);
-            if (lane == 0) fsum[w] = f;
+            f = scan64(f);
+            if (lane == 63) fsum[odd][w] = f;
         }
         Item next = it;
         const bool same = h + 1 < (it.hk + 1) * reps;  // another head of this chunk
@@ -1496,9 +1509,9 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
 #pragma unroll
             for (int ct = 0; ct < RT; ++ct) p[ct] = zf4();
             mma_group(p, of, [&](int ct, int kk) { return lv.row(vt, 16 * ct, kk); });
-            decay_tiles<true>(dc, p, rt, l16, g4);
+            decay_tiles<true>(dc, p, rt, a.scale, l16, g4);
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &df[kk]);
+            for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &df[kk]);
             const float e = a.scale * dc.e[16 * rt + l16];
             float as = 0.f;
 #pragma unroll
@@ -1527,16 +1540,6 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
             as += __shfl_xor(as, 16);
             as += __shfl_xor(as, 32);
             if (lane < 16) asum[ch][16 * rt + lane] = as;
-            // P . D of its tokens (columns) with later ones, for dV
-            Frag kf[NK];
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
-#pragma unroll
-            for (int ut = 0; ut < RT; ++ut) p[ut] = zf4();
-            mma_group(p, kf, [&](int ut, int kk) { return lk.row(qt, 16 * ut, kk); });
-            decay_tiles<false>(dc, p, rt, l16, g4);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &pf[kk]);
         } else {
             Frag kf[NK], vf[NV];
             f4 p[RT], d[RT], y[RT];
@@ -1551,39 +1554,45 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
             mma_group(y, vf, [&](int ut, int kk) { return lv.row(ot, 16 * ut, kk); });
 #pragma unroll
             for (int ut = 0; ut < RT; ++ut) d[ut] = y[ut];
-            decay_tiles<false>(dc, p, rt, l16, g4);
-            decay_tiles<false>(dc, d, rt, l16, g4);
+            decay_tiles<false>(dc, p, rt, a.scale, l16, g4);
+            decay_tiles<false>(dc, d, rt, a.scale, l16, g4);
             // W below the diagonal: sums over s < t of the tile's columns, for u >= t
             if (ch == 0) {
 #pragma unroll
-                for (int ut = 0; ut < RT; ++ut)
+                for (int ut = 0; ut < RT; ++ut) {
+                    if (ut < rt) continue;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const bool low = ut > rt || (ut == rt && g4 + j > l16);
-                        float v = low ? p[ut][j] * y[ut][j] : 0.f;
+                        float v = p[ut][j] * y[ut][j];
+                        if (ut == rt) v = g4 + j > l16 ? v : 0.f;
                         v += dpp<0x111>(v);
                         v += dpp<0x112>(v);
                         v += dpp<0x114>(v);
                         v += dpp<0x118>(v);
                         const float before = dpp<0x111>(v), all = dpp<0x15f>(v);
-                        in += ut > rt || (ut == rt && g4 + j >= l16) ? before : 0.f;
+                        in += ut > rt || g4 + j >= l16 ? before : 0.f;
                         row = l16 == 4 * ut + j ? all : row;
                     }
-                if (l16 < 4 * RT) rsum[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = a.scale * row;
+                }
+                if (l16 < 4 * RT) rsum[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = row;
                 in += __shfl_xor(in, 16);
                 in += __shfl_xor(in, 32);
-                if (lane < 16) inner[16 * rt + lane] = a.scale * in;
+                if (lane < 16) inner[16 * rt + lane] = in;
             }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                to_frag(a.scale * p[2 * kk], a.scale * p[2 * kk + 1], &pf[kk]);
-                to_frag(a.scale * d[2 * kk], a.scale * d[2 * kk + 1], &df[kk]);
+                to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
+                to_frag(d[2 * kk], d[2 * kk + 1], &df[kk]);
+                if (ch == 0) scores[rt][kk][lane] = pf[kk];
             }
         }
         __syncthreads();  // the states have been read
         keep(rd);
         __syncthreads();
         if (more) request_ds(next);
+        if (!keys)
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) pf[kk] = scores[rt][kk][lane];
         const float ds = dc.d[16 * rt + l16];
         if (keys) {
             // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
@@ -1618,75 +1627,75 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
             bs += __shfl_xor(bs, 32);
             if (lane < 16) bsum[ch][16 * rt + lane] = bs;
         }
-        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, half of the columns
-        {
+        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, N column tiles from m0
+        auto values = [&](int m0, auto count) {
+            constexpr int N = decltype(count)::value;
             Frag kf[NK];
+            f4 y[N];
             S *out = reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
-            for (int i0 = 0; i0 < NTV; i0 += GV) {
-                f4 y[GV];
+            for (int i = 0; i < N; ++i) y[i] = zf4();
+            mma_group(y, kf, [&](int i, int kk) { return ST::turned(state, m0 + i, kk, lane); });
 #pragma unroll
-                for (int i = 0; i < GV; ++i) y[i] = zf4();
-                mma_group(y, kf, [&](int i, int kk) {
-                    return ST::turned(state, ((i0 + i) * CH + ch) * 2 + keys, kk, lane);
-                });
+            for (int i = 0; i < N; ++i) y[i] *= ds;
+            mma_group(y, pf, [&](int i, int kk) { return lv.at_col(ot, 32 * kk, lv.col_off(m0 + i)); });
 #pragma unroll
-                for (int i = 0; i < GV; ++i) y[i] *= ds;
-                mma_group(y, pf, [&](int i, int kk) {
-                    return lv.at_col(ot, 32 * kk, lv.col_off(((i0 + i) * CH + ch) * 2 + keys));
-                });
-#pragma unroll
-                for (int i = 0; i < GV; ++i) {
-                    const int m = ((i0 + i) * CH + ch) * 2 + keys;
-                    if (mine && 16 * m + g4 < a.Dv) put4(out + 16 * m, y[i]);
-                }
-            }
-            if (nan && mine)
+            for (int i = 0; i < N; ++i) {
+                const int c = 16 * (m0 + i) + g4;
+                if (mine && c < a.Dv) put4(out - g4 + c, y[i]);
+                if (nan && mine)
 #pragma unroll 1
-                for (int i = 0; i < 4 * NTV; ++i) {
-                    const int c = 16 * ((i / 4 * CH + ch) * 2 + keys) + g4 + i % 4;
-                    if (c < a.Dv && (16 * rt + l16 <= last_o[c] || 16 * rt + l16 <= ends[0] || row_k[16 * rt + l16]))
-                        put1(out - g4 + c, __builtin_nanf(""));
-                }
+                    for (int j = 0; j < 4; ++j)
+                        if (c + j < a.Dv && (16 * rt + l16 <= last_o[c + j] || 16 * rt + l16 <= ends[0] ||
+                                             row_k[16 * rt + l16]))
+                            put1(out - g4 + c + j, __builtin_nanf(""));
+            }
+        };
+        // the key wavefronts have dK to do: they take a quarter (fp32: half)
+        constexpr int MQ = CH == 1 ? 3 * NV / 2 : NV / 2, MK = CH == 1 ? NV / 2 : NV / 2;
+        if (!keys) {
+            if constexpr (MQ == 6) {
+                values(0, std::integral_constant<int, 3>());
+                values(3, std::integral_constant<int, 3>());
+            } else {
+                values(ch * 2 * MQ, std::integral_constant<int, MQ>());
+            }
+        } else {
+            values(CH == 1 ? MQ : ch * 2 * MQ + MQ, std::integral_constant<int, MK>());
         }
         __syncthreads();
         if (w == 0) {
-            float su = 0.f, pb = 0.f, in = 0.f, rw[RT];
+            // suffix sums run over the tokens backwards, lane i at token C - 1 - i
+            float su = 0.f, pb = 0.f, rw[RT];
+            const int t = C - 1 - lane;
 #pragma unroll
             for (int i = 0; i < RT; ++i) rw[i] = 0.f;
             if (lane < C) {
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
-                    su += asum[i][lane];
+                    su += asum[i][t];
                     pb += bsum[i][lane];
                 }
-                in = inner[lane];
 #pragma unroll
                 for (int i = 0; i + 1 < RT; ++i)
-                    rw[i] = lane >= 16 * i + 16 ? rsum[lane][i] : 0.f;  // rows below the tile
+                    rw[i] = t >= 16 * i + 16 ? rsum[t][i] : 0.f;  // rows below the tile
             }
+            su = scan64(su);
+            pb = scan64(pb);
 #pragma unroll
-            for (int d = 1; d < C; d *= 2) {
-                const float y = __shfl_down(su, d), z = __shfl_up(pb, d);
-                if (lane + d < 64) su += y;
-                if (lane >= d) pb += z;
-#pragma unroll
-                for (int i = 0; i + 1 < RT; ++i) {
-                    const float r = __shfl_down(rw[i], d);
-                    if (lane + d < 64) rw[i] += r;
-                }
+            for (int i = 0; i + 1 < RT; ++i) {
+                const float r = scan64(rw[i]);
+                if (t >= 16 * (i + 1)) su += r;
             }
-            su += in;
-#pragma unroll
-            for (int i = 0; i + 1 < RT; ++i)
-                if (lane >= 16 * (i + 1)) su += rw[i];
             float F = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) F += fsum[i];
+            for (int i = 0; i < 8; ++i) F += fsum[odd][i];
             F *= dc.g;
             const float before = __shfl_up(pb, 1);
+            su = __shfl(su, C - 1 - lane);
+            if (lane < C) su += inner[lane];
             if (lane < C && lane < it.left) {
                 float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
                 if (nan && (lane <= ends[0] || lane <= ends[1] || lane > ends[2])) r = __builtin_nanf("");
@@ -1709,8 +1718,8 @@ gscan_state_grad_kernel(StateArgs a, int64_t units, size_t st_s, size_t st_ds)
             for (int i = 0; i < NTK; ++i) acc[i] = zf4();
         }
         if (!more) break;
-        __syncthreads();
         if (nan) {
+            __syncthreads();
             if (!same) {
                 clear();
             } else {  // d_out's of this head (q's and k's stay)
@@ -1771,7 +1780,7 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
     if (e != hipSuccess || a.T == 0) return e;
     const int64_t units = p.chunks * a.Hk;
     hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(units < kCus ? units : kCus)),
-                       dim3(kGThreads), 0, st, a, units, p.st_s, p.st_ds);
+                       dim3(kGThreads), 0, st, a, (uint32_t)units, p.st_s, p.st_ds);
     return hipGetLastError();
 }
 

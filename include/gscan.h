@@ -323,7 +323,8 @@ size_t gscan_backward_workspace_bytes(int64_t B, int64_t K, int64_t SH2, int64_t
  * ([tokens][H][Dv], [tokens][Hk][Dk], [tokens][H]).
  *
  * Shapes: Dk and Dv multiples of 8 up to 128; 1 <= H <= 16384, Hk dividing H;
- * B >= 1, T >= 0, T < 2^31 - 128; token strides below 2^23 elements.  q, k, v, d_out pointers, and their strides in
+ * B >= 1, T >= 0, T < 2^31 - 128; no negative stride, token strides
+ * below 2^23 and head strides below 2^31 elements.  q, k, v, d_out pointers, and their strides in
  * bytes, are multiples of 16; states 16-byte aligned.
  *
  * Non-finite inputs reach what they reach in the recurrence and nothing else:
