@@ -1340,7 +1340,7 @@ constexpr int kCus = 256;
 
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kGThreads, 2)
-gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
+gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, size_t st_ds)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
@@ -1363,9 +1363,9 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
     // row of q, of d_out, the first of k
     __shared__ int first_k[NK * 32], last_q[NK * 32], last_o[NV * 32], row_k[C], row_o[C], ends[3], bad;
 
-    int tid = threadIdx.x;
-    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g4 = 4 * (lane >> 4);
+    int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int rt = w % RT, ch = CH == 1 ? 0 : w / (2 * RT);
     const bool keys = (w / RT) & 1;
     const int reps = a.H / a.Hk;
@@ -1373,15 +1373,17 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
     const TK lk(lane);
     const TV lv(lane);
 
+    const uint32_t last = (blockIdx.x + 1) * per < units ? (blockIdx.x + 1) * per : units;
+
     // what is computed: value head `h` of chunk `slot`, and where its tokens are
     struct Item {
         Unit un;
         uint32_t u;  // unit of the grid (chunk and key head)
         int slot, h, hk, t0, left;
     };
-    // the first item from unit u on; u >= units when there is none
+    // the first item from unit u on; u >= last when there is none
     auto find = [&](uint32_t u, Item *it) {
-        for (; u < units; u += gridDim.x) {
+        for (; u < last; ++u) {
             const uint32_t c = u / (uint32_t)a.Hk;
             if (!find_unit(a, c, C, C, lane, &it->un)) continue;
             it->t0 = it->un.part * C;
@@ -1393,6 +1395,18 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
             break;
         }
         it->u = u;
+    };
+    // the one after it: another head, the next chunk, or to be found
+    auto advance = [&](Item *it) {
+        if (++it->u >= last) return;
+        if (++it->hk == a.Hk) {
+            it->hk = 0;
+            it->t0 += C;
+            it->left -= C;
+            ++it->slot;
+            if (it->left <= 0) return find(it->u, it);
+        }
+        it->h = it->hk * reps;
     };
     typedef Stage<T, NK, kGThreads> SK;
     typedef Stage<T, NV, kGThreads> SV;
@@ -1444,8 +1458,8 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
         __syncthreads();
     };
     Item it;
-    find(blockIdx.x, &it);
-    if (it.u >= units) return;
+    find(blockIdx.x * per, &it);
+    if (it.u >= last) return;
     request(it, true);
     request_ds(it);
     clear();
@@ -1454,7 +1468,9 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
     for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
     for (int odd = 0;; odd ^= 1) {
-        asm volatile("" : "+v"(tid));  // addresses from it are formed anew, not kept across the loop
+        // addresses and comparisons are formed anew, not kept across the loop
+        // (there are more of them than registers)
+        asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(g4));
         const int h = it.h;
         const bool mine = 16 * rt + l16 < it.left;  // this lane's token exists
         if (h == it.hk * reps) {
@@ -1493,8 +1509,8 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
         Item next = it;
         const bool same = h + 1 < (it.hk + 1) * reps;  // another head of this chunk
         if (same) ++next.h;
-        else find(it.u + gridDim.x, &next);
-        const bool more = next.u < units;
+        else advance(&next);
+        const bool more = next.u < last;
         __syncthreads();
         const bool nan = bad != 0;
         if (more) request(next, !same);
@@ -1632,7 +1648,9 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
             constexpr int N = decltype(count)::value;
             Frag kf[NK];
             f4 y[N];
-            S *out = reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.H + h) * a.Dv + g4;
+            const __amdgpu_buffer_rsrc_t out = buffer(
+                reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0) * a.H + h) * a.Dv);
+            const uint32_t o = (uint32_t)((16 * rt + l16) * a.H * a.Dv + g4) * (uint32_t)sizeof(S);
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
@@ -1643,14 +1661,18 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, size_t st_s, size_t st_ds)
             mma_group(y, pf, [&](int i, int kk) { return lv.at_col(ot, 32 * kk, lv.col_off(m0 + i)); });
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = 16 * (m0 + i) + g4;
-                if (mine && c < a.Dv) put4(out - g4 + c, y[i]);
-                if (nan && mine)
+                const int c = 16 * (m0 + i);
+                store4(out, mine && c + g4 < a.Dv ? o + c * (uint32_t)sizeof(S) : kNowhere, y[i], T());
+            }
+            if (nan && mine) {
+                S *p = reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.H + h) * a.Dv;
 #pragma unroll 1
-                    for (int j = 0; j < 4; ++j)
-                        if (c + j < a.Dv && (16 * rt + l16 <= last_o[c + j] || 16 * rt + l16 <= ends[0] ||
-                                             row_k[16 * rt + l16]))
-                            put1(out - g4 + c + j, __builtin_nanf(""));
+                for (int i = 0; i < 4 * N; ++i) {
+                    const int c = 16 * (m0 + i / 4) + g4 + i % 4;
+                    if (c < a.Dv && (16 * rt + l16 <= last_o[c] || 16 * rt + l16 <= ends[0] ||
+                                     row_k[16 * rt + l16]))
+                        put1(p + c, __builtin_nanf(""));
+                }
             }
         };
         // the key wavefronts have dK to do: they take a quarter (fp32: half)
@@ -1779,8 +1801,9 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
     e = hipGetLastError();
     if (e != hipSuccess || a.T == 0) return e;
     const int64_t units = p.chunks * a.Hk;
-    hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)(units < kCus ? units : kCus)),
-                       dim3(kGThreads), 0, st, a, (uint32_t)units, p.st_s, p.st_ds);
+    const int64_t each = (units + kCus - 1) / kCus;
+    hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)((units + each - 1) / each)),
+                       dim3(kGThreads), 0, st, a, (uint32_t)units, (uint32_t)each, p.st_s, p.st_ds);
     return hipGetLastError();
 }
 
