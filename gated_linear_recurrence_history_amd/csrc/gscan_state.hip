@@ -660,30 +660,43 @@ __device__ __forceinline__ f4 decayed_st(const Decay<C> &s, f4 x, int rt, int ct
         x[j] = g4 + j <= l16 ? x[j] * exp2_((ht - hi[j]) + (lt - lo[j])) : 0.f;
     return x;
 }
-// The same, times mul (Decay's own), for a wavefront that holds all tiles of
-// its 16 tokens `own`, known at run time only: ST, tokens t = 16own + l16 are
-// the columns and s the rows of tiles p[0 ..]; otherwise the columns are
-// s = 16own + l16 and the rows t.  Tiles behind the diagonal become zero.
+// The factors, times mul (Decay's own), of all tiles of a wavefront's 16
+// tokens `own`, known at run time only: ST, tokens t = 16own + l16 are the
+// columns and s the rows; otherwise the columns are s = 16own + l16 and the
+// rows t.  Without a branch, to be read before the products they belong to.
 template <bool ST, int C>
-__device__ __forceinline__ void decay_tiles(const Decay<C> &s, f4 (&p)[C / 16], int own, float mul,
-                                            int l16, int g4)
+__device__ __forceinline__ void factors(const Decay<C> &s, f4 (&f)[C / 16], int own, float mul, int l16,
+                                        int g4)
 {
-    constexpr int RT = C / 16;
     const int me = 16 * own + l16;
     const float c = s.col[me], hm = s.hi[me], lm = s.lo[me];
+    const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * own + g4]);
+    const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * own + g4]);
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i)
+        f[i] = ST ? *reinterpret_cast<const f4 *>(&s.col[16 * i + g4]) * s.row[i][me]
+                  : *reinterpret_cast<const f4 *>(&s.row[own][16 * i + g4]) * c;
+    f4 d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float x = mul * exp2_(ST ? (hm - hi[j]) + (lm - lo[j]) : (hi[j] - hm) + (lo[j] - lm));
+        d[j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? x : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i) f[i] = i == own ? d : f[i];
+}
+// Scores times their factors; zero on the wrong side of the diagonal, whatever
+// the score.
+template <bool ST, int RT>
+__device__ __forceinline__ void apply(f4 (&p)[RT], const f4 (&f)[RT], int own, int l16, int g4)
+{
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        if (ST ? i < own : i > own) {
-            if (ST) p[i] *= *reinterpret_cast<const f4 *>(&s.col[16 * i + g4]) * s.row[i][me];
-            else p[i] *= *reinterpret_cast<const f4 *>(&s.row[own][16 * i + g4]) * c;
-        } else if (i == own) {
-            const f4 hi = *reinterpret_cast<const f4 *>(&s.hi[16 * i + g4]);
-            const f4 lo = *reinterpret_cast<const f4 *>(&s.lo[16 * i + g4]);
+        if (ST ? i <= own : i >= own) {
+            p[i] *= f[i];
+            if (i == own)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f = exp2_(ST ? (hm - hi[j]) + (lm - lo[j]) : (hi[j] - hm) + (lo[j] - lm));
-                p[i][j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? p[i][j] * (mul * f) : 0.f;
-            }
+                for (int j = 0; j < 4; ++j) p[i][j] = (ST ? g4 + j <= l16 : g4 + j >= l16) ? p[i][j] : 0.f;
         } else {
             p[i] = zf4();
         }
@@ -1356,8 +1369,12 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
     __shared__ u4 state[kOps];
     __shared__ Frag scores[RT][KS][64];  // P . D of a tile row's keys, for dV
-    __shared__ Decay<C> dc;
-    __shared__ float rsum[C][RT], inner[C], asum[CH][C], bsum[CH][C], fsum[2][8];
+    __shared__ Decay<C> dcs[2];
+    // sums for the gates' gradients, which are finished beside the next item
+    struct Sums {
+        float row[C][RT], inner[C], a[CH][C], b[CH][C], f[8];
+    };
+    __shared__ Sums sums[2];
     // what infinities and NaN reach: per column the first row of k and the last
     // of q and d_out that hold one, which rows of k and d_out do, and the last
     // row of q, of d_out, the first of k
@@ -1430,14 +1447,14 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         Gates gates;
         gates.begin(a, it.un, it.h, it.t0, C, lane);
         gx = gates.load(it.left, lane, 0);
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + ((int64_t)it.slot * a.H + it.h) * kOps;
+    };
+    auto request_states = [&](const Item &it) {
+        const int64_t at = ((int64_t)it.slot * a.H + it.h) * kOps;
+        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + at, *q = reinterpret_cast<const u4 *>(ws + st_ds) + at;
 #pragma unroll
         for (int i = 0; i < NS; ++i) rs[i] = p[tid + kGThreads * i];
-    };
-    auto request_ds = [&](const Item &it) {
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_ds) + ((int64_t)it.slot * a.H + it.h) * kOps;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) rd[i] = p[tid + kGThreads * i];
+        for (int i = 0; i < NS; ++i) rd[i] = q[tid + kGThreads * i];
     };
     auto keep = [&](const u4 (&r)[NS]) {
 #pragma unroll
@@ -1461,13 +1478,60 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     find(blockIdx.x * per, &it);
     if (it.u >= last) return;
     request(it, true);
-    request_ds(it);
+    request_states(it);
     clear();
     f4 acc[NTK];  // dQ or dK of the wavefront's tokens
 #pragma unroll
     for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
+    // dlog g of an item's tokens, by one wavefront: x its gate arguments, reach
+    // the tokens an infinity or NaN reaches (from the first, up to the last)
+    auto finish = [&](const Item &done, int was, float x, int up_to, int from) {
+        const Sums &q = sums[was];
+        // suffix sums run over the tokens backwards, lane i at token C - 1 - i
+        float su = 0.f, pb = 0.f, rw[RT];
+        const int t = C - 1 - lane;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) rw[i] = 0.f;
+        if (lane < C) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                su += q.a[i][t];
+                pb += q.b[i][lane];
+            }
+#pragma unroll
+            for (int i = 0; i + 1 < RT; ++i)
+                rw[i] = t >= 16 * i + 16 ? q.row[t][i] : 0.f;  // rows below the tile
+        }
+        su = scan64(su);
+        pb = scan64(pb);
+#pragma unroll
+        for (int i = 0; i + 1 < RT; ++i) {
+            const float r = scan64(rw[i]);
+            if (t >= 16 * (i + 1)) su += r;
+        }
+        float F = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) F += q.f[i];
+        F *= dcs[was].g;
+        const float before = __shfl_up(pb, 1);
+        su = __shfl(su, C - 1 - lane);
+        if (lane < C) su += q.inner[lane];
+        if (lane < C && lane < done.left) {
+            float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
+            if (lane <= up_to || lane > from) r = __builtin_nanf("");
+            const int64_t at = (done.un.tok0 + done.t0 + lane) * a.H + done.h;
+            if (a.gate_dtype) reinterpret_cast<uint16_t *>(a.dgate)[at] = to_bf16(r);
+            else reinterpret_cast<float *>(a.dgate)[at] = r;
+        }
+    };
+    Item done;
+    bool later = false;
+    float gdone = 0.f;
+    int up_to = -1, from = C;
     for (int odd = 0;; odd ^= 1) {
+        const Decay<C> &dc = dcs[odd];
+        Sums &sm = sums[odd];
         // addresses and comparisons are formed anew, not kept across the loop
         // (there are more of them than registers)
         asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(g4));
@@ -1498,13 +1562,13 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         });
         keep(rs);
         const float x = Gates::value(gx, a);
-        if (w == 0) gate_scan<C>(dc, x, lane < it.left, a.gate_form, lane, a.scale);
+        if (w == 1) gate_scan<C>(dcs[odd], x, lane < it.left, a.gate_form, lane, a.scale);
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) f += dot16(rs[i], rd[i], T());
             f = scan64(f);
-            if (lane == 63) fsum[odd][w] = f;
+            if (lane == 63) sm.f[w] = f;
         }
         Item next = it;
         const bool same = h + 1 < (it.hk + 1) * reps;  // another head of this chunk
@@ -1514,18 +1578,27 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         __syncthreads();
         const bool nan = bad != 0;
         if (more) request(next, !same);
+        if (w == 0) {
+            if (later) finish(done, odd ^ 1, gdone, up_to, from);
+            done = it;
+            gdone = x;
+            up_to = nan ? (ends[0] > ends[1] ? ends[0] : ends[1]) : -1;
+            from = nan ? ends[2] : C;
+        }
+        later = true;
 
         Frag pf[KS], df[KS];
         if (!keys) {
             // dQ^T = K^T (dP . D)^T + scale e^L S dO^T
             Frag of[NV];
-            f4 p[RT];
+            f4 p[RT], fac[RT];
+            factors<true>(dc, fac, rt, a.scale, l16, g4);
 #pragma unroll
             for (int kk = 0; kk < NV; ++kk) of[kk] = lv.row(ot, 16 * rt, kk);
 #pragma unroll
             for (int ct = 0; ct < RT; ++ct) p[ct] = zf4();
             mma_group(p, of, [&](int ct, int kk) { return lv.row(vt, 16 * ct, kk); });
-            decay_tiles<true>(dc, p, rt, a.scale, l16, g4);
+            apply<true>(p, fac, rt, l16, g4);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) to_frag(p[2 * kk], p[2 * kk + 1], &df[kk]);
             const float e = a.scale * dc.e[16 * rt + l16];
@@ -1555,11 +1628,12 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
                                            row_o[16 * rt + l16]);
             as += __shfl_xor(as, 16);
             as += __shfl_xor(as, 32);
-            if (lane < 16) asum[ch][16 * rt + lane] = as;
+            if (lane < 16) sm.a[ch][16 * rt + lane] = as;
         } else {
             Frag kf[NK], vf[NV];
-            f4 p[RT], d[RT], y[RT];
+            f4 p[RT], d[RT], y[RT], fac[RT];
             float in = 0.f, row = 0.f;
+            factors<false>(dc, fac, rt, a.scale, l16, g4);
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
 #pragma unroll
@@ -1570,8 +1644,8 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             mma_group(y, vf, [&](int ut, int kk) { return lv.row(ot, 16 * ut, kk); });
 #pragma unroll
             for (int ut = 0; ut < RT; ++ut) d[ut] = y[ut];
-            decay_tiles<false>(dc, p, rt, a.scale, l16, g4);
-            decay_tiles<false>(dc, d, rt, a.scale, l16, g4);
+            apply<false>(p, fac, rt, l16, g4);
+            apply<false>(d, fac, rt, l16, g4);
             // W below the diagonal: sums over s < t of the tile's columns, for u >= t
             if (ch == 0) {
 #pragma unroll
@@ -1590,10 +1664,10 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
                         row = l16 == 4 * ut + j ? all : row;
                     }
                 }
-                if (l16 < 4 * RT) rsum[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = row;
+                if (l16 < 4 * RT) sm.row[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = row;
                 in += __shfl_xor(in, 16);
                 in += __shfl_xor(in, 32);
-                if (lane < 16) inner[16 * rt + lane] = in;
+                if (lane < 16) sm.inner[16 * rt + lane] = in;
             }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
@@ -1605,7 +1679,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         __syncthreads();  // the states have been read
         keep(rd);
         __syncthreads();
-        if (more) request_ds(next);
+        if (more) request_states(next);
         if (!keys)
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) pf[kk] = scores[rt][kk][lane];
@@ -1641,7 +1715,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
                                           16 * rt + l16 <= ends[1]);
             bs += __shfl_xor(bs, 16);
             bs += __shfl_xor(bs, 32);
-            if (lane < 16) bsum[ch][16 * rt + lane] = bs;
+            if (lane < 16) sm.b[ch][16 * rt + lane] = bs;
         }
         // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, N column tiles from m0
         auto values = [&](int m0, auto count) {
@@ -1688,44 +1762,6 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             values(CH == 1 ? MQ : ch * 2 * MQ + MQ, std::integral_constant<int, MK>());
         }
         __syncthreads();
-        if (w == 0) {
-            // suffix sums run over the tokens backwards, lane i at token C - 1 - i
-            float su = 0.f, pb = 0.f, rw[RT];
-            const int t = C - 1 - lane;
-#pragma unroll
-            for (int i = 0; i < RT; ++i) rw[i] = 0.f;
-            if (lane < C) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    su += asum[i][t];
-                    pb += bsum[i][lane];
-                }
-#pragma unroll
-                for (int i = 0; i + 1 < RT; ++i)
-                    rw[i] = t >= 16 * i + 16 ? rsum[t][i] : 0.f;  // rows below the tile
-            }
-            su = scan64(su);
-            pb = scan64(pb);
-#pragma unroll
-            for (int i = 0; i + 1 < RT; ++i) {
-                const float r = scan64(rw[i]);
-                if (t >= 16 * (i + 1)) su += r;
-            }
-            float F = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) F += fsum[odd][i];
-            F *= dc.g;
-            const float before = __shfl_up(pb, 1);
-            su = __shfl(su, C - 1 - lane);
-            if (lane < C) su += inner[lane];
-            if (lane < C && lane < it.left) {
-                float r = (su + (lane ? before : 0.f) + F) * log_gate_slope(x, a.gate_form);
-                if (nan && (lane <= ends[0] || lane <= ends[1] || lane > ends[2])) r = __builtin_nanf("");
-                const int64_t at = (it.un.tok0 + it.t0 + lane) * a.H + h;
-                if (a.gate_dtype) reinterpret_cast<uint16_t *>(a.dgate)[at] = to_bf16(r);
-                else reinterpret_cast<float *>(a.dgate)[at] = r;
-            }
-        }
         if (!same) {  // the chunk's last head
             if (mine) {
                 S *out = reinterpret_cast<S *>(keys ? a.dk : a.dq) +
@@ -1739,7 +1775,10 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
 #pragma unroll
             for (int i = 0; i < NTK; ++i) acc[i] = zf4();
         }
-        if (!more) break;
+        if (!more) {
+            if (w == 0) finish(done, odd, gdone, up_to, from);
+            break;
+        }
         if (nan) {
             __syncthreads();
             if (!same) {
