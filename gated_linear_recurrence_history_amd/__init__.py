@@ -15,7 +15,7 @@ from .binding import (forward, forward_enrich, backward, backward_full,  # noqa:
                       batched_cifg_update, bias_grad_reduce, library_path, GScanError)
 from . import workloads  # noqa: F401
 from .autograd import GatedScanFunction, gated_scan  # noqa: F401
-from .state_scan import (StateScanFunction, state_scan, state_scan_backward,  # noqa: F401
+from .matrix_state import (StateScanFunction, state_scan, state_scan_backward,  # noqa: F401
                          state_scan_backward_workspace_bytes, state_scan_forward,
                          state_scan_forward_workspace_bytes, state_scan_step)
 from .qk_norm import (QkNormRopeFunction, qk_norm_rope, qk_norm_rope_backward,  # noqa: F401

@@ -24,6 +24,7 @@ multiple, such as a slice of a fused projection's output has.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -51,73 +52,93 @@ def _on_device(dev, **tensors):
             raise ValueError(f"{name} must be a tensor on {dev}")
 
 
-def _reads_rows(t):
+def _reads_rows(shape, stride):
     """Whether the last dimension is contiguous (or there is nothing to read)."""
-    return t.shape[-1] <= 1 or t.stride(-1) == 1 or t.numel() == 0
+    return shape[-1] <= 1 or stride[-1] == 1 or 0 in shape
 
 
-def _outer_strides(t):
-    """Strides of the dimensions before the last; one without a second element
-    has none."""
-    if t.numel() == 0:
-        return [0] * t.dim()
-    return [0 if n <= 1 else x for n, x in zip(t.shape, t.stride())]
+def _outer_strides(shape, stride):
+    """Strides of the dimensions; one without a second element has none."""
+    return [0] * len(shape) if 0 in shape else [0 if n <= 1 else x for n, x in zip(shape, stride)]
 
 
 def _strides(t, lead):
-    """(batch, token, head) strides of an operand."""
-    s = _outer_strides(t)
+    """(batch, token, head) strides of an operand, given as (shape, stride)."""
+    s = _outer_strides(*t)
     return _i64x3(s[0], s[1], s[2]) if lead == 2 else _i64x3(0, s[0], s[1])
 
 
-def _describe(q, k, v, gate, scale, gate_form, gate_shift, seq_offsets, single=False):
-    """Checks shapes, types and devices; returns the descriptor and the shape
-    before the heads.  `single`: one token per request ([N, heads, width])."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+def _layout(t):
+    return t.shape, t.stride()
+
+
+@functools.lru_cache(maxsize=256)
+def _template(q, k, v, gate, dtypes, devices, scale, gate_form, gate_shift, sequences, single):
+    """The descriptor of a call, as bytes, from what shapes, strides and types
+    say; refuses what does not fit.  q, k, v, gate are (shape, stride)."""
+    if devices[0].type != "cuda":
         raise TypeError("q, k, v and gate must be torch tensors on a GPU device")
-    dev = q.device
-    _on_device(dev, k=k, v=v, gate=gate)
-    if q.dtype not in _CODES or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError(f"q, k, v must share a type, float32 or bfloat16; got {q.dtype}, {k.dtype}, "
-                        f"{v.dtype}")
-    if gate.dtype not in _CODES:
-        raise TypeError(f"gate must be float32 or bfloat16, got {gate.dtype}")
+    for name, dev in zip(("k", "v", "gate"), devices[1:]):
+        if dev != devices[0]:
+            raise ValueError(f"{name} must be a tensor on {devices[0]}")
+    if dtypes[0] not in _CODES or dtypes[1] != dtypes[0] or dtypes[2] != dtypes[0]:
+        raise TypeError(f"q, k, v must share a type, float32 or bfloat16; got {dtypes[0]}, {dtypes[1]}, "
+                        f"{dtypes[2]}")
+    if dtypes[3] not in _CODES:
+        raise TypeError(f"gate must be float32 or bfloat16, got {dtypes[3]}")
     if gate_form not in GATE_FORMS:
         raise ValueError(f"gate_form must be one of {sorted(GATE_FORMS)}, got {gate_form!r}")
-    lead = 1 if single or seq_offsets is not None else 2
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
+    qs, ks, vs, gs = (tuple(x[0]) for x in (q, k, v, gate))
+    lead = 1 if single or sequences else 2
+    if len(qs) != lead + 2 or len(vs) != lead + 2:
         want = ("[requests, heads, width]" if single else "[tokens, heads, width] (packed)"
                 if lead == 1 else "[batch, tokens, heads, width]")
-        raise ValueError(f"q, k, v must be {want}; got {tuple(q.shape)}, {tuple(v.shape)}")
-    if k.shape != q.shape or v.shape[:lead] != q.shape[:lead] or gate.shape != v.shape[:-1]:
-        raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, "
-                         f"v {tuple(v.shape)}, gate {tuple(gate.shape)}")
+        raise ValueError(f"q, k, v must be {want}; got {qs}, {vs}")
+    if ks != qs or vs[:lead] != qs[:lead] or gs != vs[:-1]:
+        raise ValueError(f"shapes do not fit: q {qs}, k {ks}, v {vs}, gate {gs}")
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if not _reads_rows(t):
+        if not _reads_rows(*t):
             raise ValueError(f"the last dimension of {name} must be contiguous")
     d = _Desc()
     if single:
-        d.B, d.T = q.shape[0], 1
+        d.B, d.T = qs[0], 1
     elif lead == 2:
-        d.B, d.T = q.shape[0], q.shape[1]
+        d.B, d.T = qs[0], qs[1]
     else:
-        _on_device(dev, seq_offsets=seq_offsets)
-        if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or \
-                seq_offsets.numel() < 2 or not seq_offsets.is_contiguous():
-            raise ValueError("seq_offsets must be a contiguous int32 tensor [sequences + 1]; got "
-                             f"{seq_offsets.dtype} {tuple(seq_offsets.shape)}")
-        d.B, d.T = seq_offsets.numel() - 1, q.shape[0]
-        d.seq_offsets = seq_offsets.data_ptr()
-    d.H, d.Hk, d.Dk, d.Dv = v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1]
+        d.B, d.T = sequences, qs[0]
+    d.H, d.Hk, d.Dk, d.Dv = vs[-2], qs[-2], qs[-1], vs[-1]
     if single:  # requests are the batch dimension
         for name, t in (("q", q), ("k", k), ("v", v), ("gate", gate)):
-            s = _outer_strides(t)
+            s = _outer_strides(*t)
             setattr(d, name + "_stride", _i64x3(s[0], 0, s[1]))
     else:
         d.q_stride, d.k_stride = _strides(q, lead), _strides(k, lead)
         d.v_stride, d.gate_stride = _strides(v, lead), _strides(gate, lead)
-    d.dtype, d.gate_dtype = _CODES[q.dtype], _CODES[gate.dtype]
+    d.dtype, d.gate_dtype = _CODES[dtypes[0]], _CODES[dtypes[3]]
     d.gate_form, d.gate_shift, d.scale = GATE_FORMS[gate_form], gate_shift, scale
+    return bytes(d)
+
+
+def _describe(q, k, v, gate, scale, gate_form, gate_shift, seq_offsets, single=False):
+    """Checks shapes, types and devices; returns the descriptor.  `single`: one
+    token per request ([N, heads, width])."""
+    for t in (q, k, v, gate):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("q, k, v and gate must be torch tensors on a GPU device")
+    n = 0
+    if seq_offsets is not None:
+        _on_device(q.device, seq_offsets=seq_offsets)
+        if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or \
+                seq_offsets.numel() < 2 or not seq_offsets.is_contiguous():
+            raise ValueError("seq_offsets must be a contiguous int32 tensor [sequences + 1]; got "
+                             f"{seq_offsets.dtype} {tuple(seq_offsets.shape)}")
+        n = seq_offsets.numel() - 1
+    d = _Desc.from_buffer_copy(_template(
+        _layout(q), _layout(k), _layout(v), _layout(gate), (q.dtype, k.dtype, v.dtype, gate.dtype),
+        (q.device, k.device, v.device, gate.device), float(scale), gate_form, float(gate_shift), n,
+        single))
+    if n:
+        d.seq_offsets = seq_offsets.data_ptr()
     return d
 
 
@@ -145,15 +166,17 @@ class _On:
     it takes from torch's allocator then belongs to that stream."""
 
     def __init__(self, dev, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
         self.ctx = None
-        if stream is not None or torch.cuda.current_device() != dev.index:
-            self.ctx = torch.cuda.stream(self.stream)
+        if stream is None and torch.cuda.current_device() == dev.index:
+            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        else:
+            stream = torch.cuda.current_stream(dev) if stream is None else stream
+            self.ctx, self.handle = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return self.stream.cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -201,9 +224,9 @@ def state_scan_forward(q, k, v, gate, scale: float = 1.0, gate_form: str = "sigm
     need = int(L.gscan_state_scan_forward_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+            out = v.new_empty(v.shape)
         if final_state is True:
-            final_state = torch.empty(states, dtype=torch.float32, device=dev)
+            final_state = v.new_empty(states, dtype=torch.float32)
         wp, wn, _keep = _workspace(workspace, need, dev)
         binding._check(L.gscan_state_scan_forward(
             ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
@@ -229,18 +252,18 @@ def state_scan_backward(q, k, v, gate, d_out, scale: float = 1.0, gate_form: str
     if d_out.dtype != v.dtype or d_out.shape != v.shape:
         raise ValueError(f"d_out must be {v.dtype} {tuple(v.shape)}; got {d_out.dtype} "
                          f"{tuple(d_out.shape)}")
-    if not _reads_rows(d_out):
+    if not _reads_rows(*_layout(d_out)):
         raise ValueError("the last dimension of d_out must be contiguous")
     for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
         if t is not None:
             _check_dense(t, states, torch.float32, dev, name)
-    d.d_out_stride = _strides(d_out, d_out.dim() - 2)
+    d.d_out_stride = _strides(_layout(d_out), d_out.dim() - 2)
     need = int(L.gscan_state_scan_backward_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
-        dq, dk, dv, dgate = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v, gate))
+        dq, dk, dv, dgate = (t.new_empty(t.shape) for t in (q, k, v, gate))
         ds0 = None
         if initial_state is not None:
-            ds0 = torch.empty(states, dtype=torch.float32, device=dev)
+            ds0 = v.new_empty(states, dtype=torch.float32)
         wp, wn, _keep = _workspace(workspace, need, dev)
         binding._check(L.gscan_state_scan_backward(
             ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
@@ -268,7 +291,7 @@ def state_scan_step(q, k, v, gate, state, slots=None, scale: float = 1.0,
         _check_dense(out, v.shape, v.dtype, dev, "out")
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+            out = v.new_empty(v.shape)
         if d.B:
             binding._check(binding.lib().gscan_state_scan_step(
                 ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
@@ -279,8 +302,8 @@ def state_scan_step(q, k, v, gate, state, slots=None, scale: float = 1.0,
 def _readable(g, like):
     """An upstream gradient the library can read as it is, else a dense copy."""
     g = g.to(like.dtype)
-    fits = _reads_rows(g) and g.data_ptr() % 16 == 0 and all(
-        s * g.element_size() % 16 == 0 for s in _outer_strides(g)[:-1])
+    fits = _reads_rows(*_layout(g)) and g.data_ptr() % 16 == 0 and all(
+        s * g.element_size() % 16 == 0 for s in _outer_strides(*_layout(g))[:-1])
     return g if fits else g.contiguous()
 
 

@@ -10,14 +10,15 @@ gives freq for plain and lengthened contexts.  Argument marshalling only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .state_scan import (_CODES, _On, _check_dense, _on_device, _outer_strides, _ptr, _readable,
-                         _reads_rows, _workspace)
+from .matrix_state import (_CODES, _On, _check_dense, _layout, _on_device, _outer_strides, _ptr,
+                           _readable, _reads_rows, _workspace)
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 _i64x2 = ctypes.c_int64 * 2
@@ -74,36 +75,51 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
 
 
 def _stride2(t):
-    return _i64x2(*_outer_strides(t)[:2])
+    return _i64x2(*_outer_strides(*t)[:2])
+
+
+@functools.lru_cache(maxsize=256)
+def _template(q, k, qdt, kdt, qdev, kdev, eps, layout, magnitude):
+    """The descriptor of a call, as bytes, from what shapes, strides and types
+    say; refuses what does not fit.  q, k are (shape, stride), k may be None."""
+    if qdev.type != "cuda":
+        raise TypeError("q and k must be torch tensors on a GPU device")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+    if qdt not in _CODES:
+        raise TypeError(f"q and k must be float32 or bfloat16, got {qdt}")
+    d = _Desc()
+    for name, t, dt, dev in (("q", q, qdt, qdev), ("k", k, kdt, kdev)):
+        if t is None:
+            continue
+        if dev != qdev:
+            raise ValueError(f"{name} must be a tensor on {qdev}")
+        shape = tuple(t[0])
+        if len(shape) != 3 or dt != qdt or shape[0] != q[0][0] or shape[2] != q[0][2]:
+            raise ValueError(f"q and k must be [tokens, heads, D] of one type; got {name} {dt} {shape} "
+                             f"beside {qdt} {tuple(q[0])}")
+        if not _reads_rows(*t):
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        setattr(d, name + "_stride", _stride2(t))
+    d.tokens, d.Hq, d.D = q[0]
+    d.Hk = 0 if k is None else k[0][1]
+    if k is not None and d.Hk < 1:
+        raise ValueError("k has no heads; pass None")
+    d.dtype, d.layout = _CODES[qdt], LAYOUTS[layout]
+    d.eps, d.magnitude = eps, magnitude
+    return bytes(d)
 
 
 def _describe(q, k, weight_q, weight_k, positions, freq, eps, layout, magnitude):
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+    if not isinstance(q, torch.Tensor) or not (k is None or isinstance(k, torch.Tensor)):
         raise TypeError("q and k must be torch tensors on a GPU device")
     dev = q.device
-    if layout not in LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
-    if q.dtype not in _CODES:
-        raise TypeError(f"q and k must be float32 or bfloat16, got {q.dtype}")
-    d = _Desc()
-    for name, t in (("q", q), ("k", k)):
-        if t is None and name == "k":
-            continue
-        _on_device(dev, **{name: t})
-        if t.dim() != 3 or t.dtype != q.dtype or t.shape[0] != q.shape[0] or t.shape[2] != q.shape[2]:
-            raise ValueError(f"q and k must be [tokens, heads, D] of one type; got {name} "
-                             f"{t.dtype} {tuple(t.shape)} beside {q.dtype} {tuple(q.shape)}")
-        if not _reads_rows(t):
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-        setattr(d, name + "_stride", _stride2(t))
-    d.tokens, d.Hq, d.D = q.shape
-    d.Hk = 0 if k is None else k.shape[1]
-    if k is not None and k.shape[1] < 1:
-        raise ValueError("k has no heads; pass None")
+    d = _Desc.from_buffer_copy(_template(
+        _layout(q), None if k is None else _layout(k), q.dtype, None if k is None else k.dtype, dev,
+        None if k is None else k.device, float(eps), layout, float(magnitude)))
     for name, w in (("weight_q", weight_q), ("weight_k", weight_k)):
         if w is not None:
             _check_dense(w, (d.D,), torch.float32, dev, name)
-    d.rot = 0
     if freq is not None:
         if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
             raise ValueError("freq must be a float32 tensor [rot / 2]")
@@ -115,8 +131,6 @@ def _describe(q, k, weight_q, weight_k, positions, freq, eps, layout, magnitude)
             raise ValueError(f"positions must be a contiguous int32 or int64 tensor [{d.tokens}]; "
                              f"got {positions.dtype} {tuple(positions.shape)}")
         d.pos_int64 = int(positions.dtype == torch.int64)
-    d.dtype, d.layout = _CODES[q.dtype], LAYOUTS[layout]
-    d.eps, d.magnitude = eps, magnitude
     return d
 
 
@@ -138,8 +152,7 @@ def qk_norm_rope_forward(q, k, weight_q, weight_k, positions, freq, eps: float =
             _check_dense(out[1], k.shape, k.dtype, dev, "out[1]")
     with _On(dev, stream) as s:
         if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=dev),
-                   None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev))
+            out = (q.new_empty(q.shape), None if k is None else k.new_empty(k.shape))
         binding._check(binding.lib().gscan_qk_norm_rope_forward(
             ctypes.byref(d), q.data_ptr(), _ptr(k), _ptr(weight_q), _ptr(weight_k),
             _ptr(positions) if d.rot else None, _ptr(freq), out[0].data_ptr(),
@@ -158,15 +171,15 @@ def qk_norm_rope_backward(q, k, weight_q, weight_k, positions, freq, dy_q, dy_k,
         if like is None:
             continue
         _on_device(dev, **{name: t})
-        if t.dtype != like.dtype or t.shape != like.shape or not _reads_rows(t):
+        if t.dtype != like.dtype or t.shape != like.shape or not _reads_rows(*_layout(t)):
             raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, last dimension "
                              f"contiguous; got {t.dtype} {tuple(t.shape)}")
-        setattr(d, name + "_stride", _stride2(t))
+        setattr(d, name + "_stride", _stride2(_layout(t)))
     need = 0
     if weight_q is not None or weight_k is not None:
         need = int(L.gscan_qk_norm_rope_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
-        dq, dk, dwq, dwk = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+        dq, dk, dwq, dwk = (None if t is None else t.new_empty(t.shape)
                             for t in (q, k, weight_q, weight_k))
         wp, wn, _keep = _workspace(workspace, need, dev)
         binding._check(L.gscan_qk_norm_rope_backward(
