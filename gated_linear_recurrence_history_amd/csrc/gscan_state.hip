@@ -392,6 +392,14 @@ struct Unit {
 
 __device__ __forceinline__ int first_lane(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// Workgroups are dealt to the eight XCDs in turn.  The index this one takes so
+// that `share` neighbours, which read the same rows, meet in one XCD's L2.
+__device__ __forceinline__ uint32_t neighbours(uint32_t share)
+{
+    const uint32_t b = blockIdx.x, whole = gridDim.x / (8 * share) * (8 * share);
+    return b < whole ? ((b / 8 / share) * 8 + b % 8) * share + b / 8 % share : b;
+}
+
 // Whether unit u exists (the same answer, in scalar registers, for every
 // lane).  Offsets are clamped to the tokens there are, so
 // wrong ones read and write nothing out of range.  Called by whole wavefronts.
@@ -800,9 +808,9 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool brings = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int slice = blockIdx.x % slices;
-    const int h = blockIdx.x / slices % a.H;
-    const int64_t unit = blockIdx.x / slices / a.H;
+    const uint32_t block = neighbours(slices * (a.H / a.Hk));
+    const int slice = block % slices, h = block / slices % a.H;
+    const int64_t unit = block / slices / a.H;
     Unit un;
     if (!find_unit(a, unit, per, C, lane, &un)) return;
     const int c0 = slice * kSlice, vcols = a.Dv - c0;
@@ -1143,8 +1151,9 @@ gscan_state_part_kernel(StateArgs a, int slices, int ways, int64_t per, Parts2 o
 {
     __shared__ __align__(16) PassLds<T, NK> smem;
     __shared__ Decay<T::C> dcs[2];
-    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices, way = blockIdx.x / slices % ways;
-    const int64_t b = blockIdx.x / slices / ways;
+    const uint32_t block = neighbours(slices * ways * (a.H / a.Hk));
+    const int lane = threadIdx.x & 63, slice = block % slices, way = block / slices % ways;
+    const int64_t b = block / slices / ways;
     const int h = (int)(b % a.H), hk = h / (a.H / a.Hk);
     const int64_t unit = b / a.H;
     Unit un;
@@ -1241,8 +1250,9 @@ gscan_state_pass_kernel(StateArgs a, int64_t per, PassWs o)
     __shared__ __align__(16) PassLds<T, NV> smem;
     __shared__ Decay<T::C> dcs[2];
     constexpr int slices = NK / 2;
-    const int lane = threadIdx.x & 63, slice = blockIdx.x % slices, way = blockIdx.x / slices & 1;
-    const int64_t b = blockIdx.x / slices / 2;
+    const uint32_t block = neighbours(slices * 2 * (a.H / a.Hk));
+    const int lane = threadIdx.x & 63, slice = block % slices, way = block / slices & 1;
+    const int64_t b = block / slices / 2;
     const int h = (int)(b % a.H), hk = h / (a.H / a.Hk);
     const int64_t unit = b / a.H;
     Unit un;
@@ -1886,14 +1896,18 @@ StatePlan make_state_plan(const StateArgs &a, bool backward)
     auto rounds = [&](int64_t n) { return (n * walks + kCus - 1) / kCus; };
     int64_t best = 0, least = 4 * (a.off ? (nc * kCus > p.chunks * walks ? nc : p.chunks * walks / kCus)
                                          : nc * rounds(a.B));  // (all in quarters of a chunk)
-    for (int64_t c = 2; c < nc && c <= 4096; c = c & (c - 1) ? c / 3 * 4 : c + c / 2) {  // 2 3 4 6 8 12 ..
+    auto consider = [&](int64_t c) {
+        if (c < 2 || c >= nc) return;
         const int64_t run = a.off ? c / 2 + p.chunks * walks / kCus : c * rounds(units(c));
         const int64_t cost = ways * (5 * run + nc / c + (units(c) * state >> 18)) + 12;
         if (cost < least) {
             least = cost;
             best = c;
         }
-    }
+    };
+    for (int64_t c = 2; c <= 4096; c = c & (c - 1) ? c / 3 * 4 : c + c / 2) consider(c);  // 2 3 4 6 8 12 ..
+    for (int64_t r = 1; r <= 4 && !a.off; ++r)  // whole rounds
+        if (const int64_t u = r * kCus / (walks * a.B)) consider((nc + u - 1) / u);
     p.split = best != 0;
     p.per = (p.split ? best : nc) * p.chunk;
     p.units = p.split ? units(best) : a.B;
