@@ -617,11 +617,10 @@ __device__ __forceinline__ double of_lane(double x, int lane)
                                             (uint32_t)__builtin_amdgcn_readlane(u.y, lane)});
 }
 
-// x: the gate argument of token `lane` (ok: there is one).  One wavefront.
-// Factors of scores off the diagonal are multiplied by mul.
+// The running sum of log2 of the gates, of which token `lane` has the argument
+// x (ok: there is one).  One wavefront.
 template <int C>
-__device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane,
-                                          float mul = 1.f)
+__device__ __forceinline__ double gate_sum(float x, bool ok, int form)
 {
     double L = ok ? (double)log_gate(x, form) * 1.44269504088896340736 : 0.0;
     L += dpp<0x111>(L);
@@ -630,6 +629,12 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
     L += dpp<0x118>(L);
     L += dpp<0x142, 0xa>(L);
     if constexpr (C > 32) L += dpp<0x143, 0xc>(L);
+    return L;
+}
+// The decays from it.  Factors of scores off the diagonal are multiplied by mul.
+template <int C>
+__device__ __forceinline__ void gate_decays(Decay<C> &s, double L, int lane, float mul = 1.f)
+{
     const double end = of_lane(L, C - 1);
     double m = end, mid[C / 16 - 1];
 #pragma unroll
@@ -650,6 +655,12 @@ __device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int for
         s.row[C / 16 - 1][lane] = 0.f;
         if (lane == C - 1) s.g = exp2_((float)end);
     }
+}
+template <int C>
+__device__ __forceinline__ void gate_scan(Decay<C> &s, float x, bool ok, int form, int lane,
+                                          float mul = 1.f)
+{
+    gate_decays<C>(s, gate_sum<C>(x, ok, form), lane, mul);
 }
 
 // Scores of a tile times e^(L_t - L_s), zero where s > t.  Rows s = 16ct + 4g + j
@@ -1032,7 +1043,9 @@ struct PassJob {
 };
 
 // Wavefronts 4-7 bring the next chunk's rows and decays into LDS while
-// wavefronts 0-3 add this one's, one barrier a chunk.
+// wavefronts 0-3 add this one's, one barrier a chunk.  The decays, a long chain
+// of short steps, are formed by the last two in turn, each over two chunks: the
+// sum of log gates in one, the exponentials in the next.
 template <class T, int NX>
 struct PassLds {
     static constexpr int kX = T::C * Tile<T, NX * 32>::bytes, kBuf = kX + T::C * Tile<T, kSlice>::bytes;
@@ -1049,7 +1062,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
     typedef Tile<T, NX * 32> TX;
     typedef Tile<T, kSlice> TY;
     typedef PassLds<T, NX> Lds;
-    constexpr int C = T::C, KS = C / 32, step = REV ? -1 : 1, GW = 3;
+    constexpr int C = T::C, KS = C / 32, step = REV ? -1 : 1;
     Lds &lds = *reinterpret_cast<Lds *>(smem);
     const int tid = threadIdx.x & (kSThreads - 1), lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1076,18 +1089,23 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
             sy.load(ry[O], left, step * (int64_t)(C * jb.ys.t), tid);
             gx[O] = gates.load(left, lane, step);
         };
+        double sum = 0.0;
+        auto sum_gates = [&](int n, auto set) {
+            sum = gate_sum<C>(Gates::value(gx[decltype(set)::value], a), lane < te - (c1 + step * n) * C,
+                              a.gate_form);
+        };
         auto bring = [&](int n, auto set) {
             constexpr int odd = decltype(set)::value;
             sx.template store<TX>(rx[odd], lds.tile[odd], tid);
             sy.template store<TY>(ry[odd], lds.tile[odd] + Lds::kX, tid);
-            if (w == GW)
-                gate_scan<C>(dcs[odd], Gates::value(gx[odd], a), lane < te - (c1 + step * n) * C,
-                             a.gate_form, lane);
+            if (w == 2 + odd) gate_decays<C>(dcs[odd], sum, lane);
+            if (w == 3 - odd) sum_gates(n + 1, std::integral_constant<int, odd ^ 1>());
             request(n + 2, set);
             __syncthreads();
         };
         request(0, std::integral_constant<int, 0>());
         request(1, std::integral_constant<int, 1>());
+        if (w == 2) sum_gates(0, std::integral_constant<int, 0>());
         for (int n = 0; n < nc; n += 2) {
             bring(n, std::integral_constant<int, 0>());
             bring(n + 1, std::integral_constant<int, 1>());
