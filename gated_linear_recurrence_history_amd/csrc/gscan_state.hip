@@ -55,7 +55,6 @@ constexpr int kSlice = 64;  // columns of a state that one workgroup walks
 #define GSCAN_STEP() asm volatile("" ::: "memory")
 
 __device__ __forceinline__ f4 zf4() { return f4{0.f, 0.f, 0.f, 0.f}; }
-__device__ __forceinline__ u4 zu4() { return u4{0u, 0u, 0u, 0u}; }
 
 // ------------------------------------------------------- operand types
 
@@ -311,15 +310,6 @@ __device__ __forceinline__ void put_frag(void *base, int64_t i, int lane, const 
     reinterpret_cast<f4 *>(base)[i * 128 + lane] = f.a;
     reinterpret_cast<f4 *>(base)[i * 128 + 64 + lane] = f.b;
 }
-__device__ __forceinline__ void get_frag(const void *base, int64_t i, int lane, u4 *f)
-{
-    *f = reinterpret_cast<const u4 *>(base)[i * 64 + lane];
-}
-__device__ __forceinline__ void get_frag(const void *base, int64_t i, int lane, FP::Frag *f)
-{
-    f->a = reinterpret_cast<const f4 *>(base)[i * 128 + lane];
-    f->b = reinterpret_cast<const f4 *>(base)[i * 128 + 64 + lane];
-}
 
 // Whether sixteen bytes hold an infinity or NaN: the largest magnitude's bits.
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
@@ -356,13 +346,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p)
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), 0, 0x80000000, 0x00027000);
 }
 constexpr uint32_t kNowhere = 0xffffffffu;
-
-// Four consecutive elements.
-__device__ __forceinline__ void put4(uint16_t *p, f4 x)
-{
-    *reinterpret_cast<uint2 *>(p) = uint2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-}
-__device__ __forceinline__ void put4(float *p, f4 x) { *reinterpret_cast<f4 *>(p) = x; }
 
 __device__ __forceinline__ void put1(uint16_t *p, float x) { *p = to_bf16(x); }
 __device__ __forceinline__ void put1(float *p, float x) { *p = x; }
@@ -731,6 +714,44 @@ __device__ __forceinline__ float scan64(float x)
     x += dpp<0x142, 0xa>(x);
     x += dpp<0x143, 0xc>(x);
     return x;
+}
+
+// Running sum over groups of 16 lanes.
+__device__ __forceinline__ float scan16(float x)
+{
+    x += dpp<0x111>(x);
+    x += dpp<0x112>(x);
+    x += dpp<0x114>(x);
+    x += dpp<0x118>(x);
+    return x;
+}
+
+// The sums of v[i] over a group of 16 lanes, that of v[i] in lane i (eight
+// values: in i and i + 8): lanes eight apart exchange the halves they do not
+// keep, then mirrored ones of eight, then those two apart, then neighbours.
+template <int N>
+__device__ __forceinline__ float sums_to_lanes(float (&v)[N], int lane)
+{
+    auto halve = [&](auto ctrl, auto half, int bit) {
+        constexpr int M = decltype(half)::value;
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float keep = up ? v[i + M] : v[i], give = up ? v[i] : v[i + M];
+            v[i] = keep + dpp<decltype(ctrl)::value>(give);
+        }
+    };
+    if constexpr (N == 16) {
+        halve(std::integral_constant<int, 0x128>(), std::integral_constant<int, 8>(), 8);
+    } else {
+        static_assert(N == 8);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += dpp<0x128>(v[i]);
+    }
+    halve(std::integral_constant<int, 0x141>(), std::integral_constant<int, 4>(), 4);
+    halve(std::integral_constant<int, 0x4e>(), std::integral_constant<int, 2>(), 2);
+    halve(std::integral_constant<int, 0xb1>(), std::integral_constant<int, 1>(), 1);
+    return v[0];
 }
 
 // y[i] += A(i, k) b[k], the operands A of step k + 1 requested before the
@@ -1394,7 +1415,12 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     constexpr int kOps = 2 * NK * NV * (int)sizeof(Frag) / 16 * 64;  // 16-byte pieces of a state
     constexpr int NS = kOps / kGThreads;
     __shared__ __align__(16) char qt[C * TK::bytes], kt[C * TK::bytes], vt[C * TV::bytes], ot[C * TV::bytes];
-    __shared__ u4 state[kOps];
+    // the state before the chunk and the gradient of the one after it, side by
+    // side where LDS holds both (all but fp32 at the full widths, where the second
+    // takes the first one's place between the two steps)
+    constexpr bool both = sizeof(Frag) == 16 || NK * NV < 16;
+    __shared__ u4 state[kOps], second[both ? kOps : 1];
+    const u4 *after = both ? second : state;
     __shared__ Frag scores[RT][KS][64];  // P . D of a tile row's keys, for dV
     __shared__ Decay<C> dcs[2];
     // sums for the gates' gradients, which are finished beside the next item
@@ -1483,11 +1509,11 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
 #pragma unroll
         for (int i = 0; i < NS; ++i) rd[i] = q[tid + kGThreads * i];
     };
-    auto keep = [&](const u4 (&r)[NS]) {
+    auto keep = [&](const u4 (&r)[NS], u4 *to) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int q = tid + kGThreads * i;
-            state[(q & ~63) + place(q & 63)] = r[i];
+            to[(q & ~63) + place(q & 63)] = r[i];
         }
     };
     auto clear = [&] {
@@ -1507,13 +1533,18 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     request(it, true);
     request_states(it);
     clear();
+    // the decays of an item, beside the one before it
+    auto gates_of = [&](const Item &i, int which) {
+        gate_scan<C>(dcs[which], Gates::value(gx, a), lane < i.left, a.gate_form, lane, a.scale);
+    };
+    if (w == 1) gates_of(it, 0);
     f4 acc[NTK];  // dQ or dK of the wavefront's tokens
 #pragma unroll
     for (int i = 0; i < NTK; ++i) acc[i] = zf4();
 
     // dlog g of an item's tokens, by one wavefront: x its gate arguments, reach
     // the tokens an infinity or NaN reaches (from the first, up to the last)
-    auto finish = [&](const Item &done, int was, float x, int up_to, int from) {
+    auto finish = [&](const Item &done, int was, float x, float gall, int up_to, int from) {
         const Sums &q = sums[was];
         // suffix sums run over the tokens backwards, lane i at token C - 1 - i
         float su = 0.f, pb = 0.f, rw[RT];
@@ -1540,7 +1571,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         float F = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) F += q.f[i];
-        F *= dcs[was].g;
+        F *= gall;
         const float before = __shfl_up(pb, 1);
         su = __shfl(su, C - 1 - lane);
         if (lane < C) su += q.inner[lane];
@@ -1554,7 +1585,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     };
     Item done;
     bool later = false;
-    float gdone = 0.f;
+    float gdone = 0.f, gall = 0.f;
     int up_to = -1, from = C;
     for (int odd = 0;; odd ^= 1) {
         const Decay<C> &dc = dcs[odd];
@@ -1587,9 +1618,9 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             row_o[row] = 1;
             bad = 1;
         });
-        keep(rs);
+        keep(rs, state);
+        if constexpr (both) keep(rd, second);
         const float x = Gates::value(gx, a);
-        if (w == 1) gate_scan<C>(dcs[odd], x, lane < it.left, a.gate_form, lane, a.scale);
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
@@ -1606,9 +1637,10 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         const bool nan = bad != 0;
         if (more) request(next, !same);
         if (w == 0) {
-            if (later) finish(done, odd ^ 1, gdone, up_to, from);
+            if (later) finish(done, odd ^ 1, gdone, gall, up_to, from);
             done = it;
             gdone = x;
+            gall = dc.g;
             up_to = nan ? (ends[0] > ends[1] ? ends[0] : ends[1]) : -1;
             from = nan ? ends[2] : C;
         }
@@ -1658,8 +1690,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             if (lane < 16) sm.a[ch][16 * rt + lane] = as;
         } else {
             Frag kf[NK], vf[NV];
-            f4 p[RT], d[RT], y[RT], fac[RT];
-            float in = 0.f, row = 0.f;
+            f4 p[RT], y[RT], fac[RT];
             factors<false>(dc, fac, rt, a.scale, l16, g4);
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
@@ -1669,48 +1700,80 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             for (int ut = 0; ut < RT; ++ut) p[ut] = y[ut] = zf4();
             mma_group(p, kf, [&](int ut, int kk) { return lk.row(qt, 16 * ut, kk); });
             mma_group(y, vf, [&](int ut, int kk) { return lv.row(ot, 16 * ut, kk); });
-#pragma unroll
-            for (int ut = 0; ut < RT; ++ut) d[ut] = y[ut];
             apply<false>(p, fac, rt, l16, g4);
-            apply<false>(d, fac, rt, l16, g4);
             // W below the diagonal: sums over s < t of the tile's columns, for u >= t
             if (ch == 0) {
+                float v[4 * RT], below = 0.f, in = 0.f;
+                f4 own = zf4();
 #pragma unroll
                 for (int ut = 0; ut < RT; ++ut) {
-                    if (ut < rt) continue;
+                    f4 x = zf4();
+                    if (ut >= rt) x = p[ut] * y[ut];
+                    if (ut > rt) below += (x[0] + x[1]) + (x[2] + x[3]);
+                    if (ut == rt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v = p[ut][j] * y[ut][j];
-                        if (ut == rt) v = g4 + j > l16 ? v : 0.f;
-                        v += dpp<0x111>(v);
-                        v += dpp<0x112>(v);
-                        v += dpp<0x114>(v);
-                        v += dpp<0x118>(v);
-                        const float before = dpp<0x111>(v), all = dpp<0x15f>(v);
-                        in += ut > rt || g4 + j >= l16 ? before : 0.f;
-                        row = l16 == 4 * ut + j ? all : row;
+                        for (int j = 0; j < 4; ++j) x[j] = g4 + j > l16 ? x[j] : 0.f;
+                        own = x;
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * ut + j] = x[j];
                 }
+                const float row = sums_to_lanes(v, lane);
                 if (l16 < 4 * RT) sm.row[16 * (l16 >> 2) + g4 + (l16 & 3)][rt] = row;
+                in = dpp<0x111>(scan16(below));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float before = dpp<0x111>(scan16(own[j]));
+                    in += g4 + j >= l16 ? before : 0.f;
+                }
                 in += __shfl_xor(in, 16);
                 in += __shfl_xor(in, 32);
                 if (lane < 16) sm.inner[16 * rt + lane] = in;
             }
+            apply<false>(y, fac, rt, l16, g4);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 to_frag(p[2 * kk], p[2 * kk + 1], &pf[kk]);
-                to_frag(d[2 * kk], d[2 * kk + 1], &df[kk]);
+                to_frag(y[2 * kk], y[2 * kk + 1], &df[kk]);
                 if (ch == 0) scores[rt][kk][lane] = pf[kk];
             }
         }
-        __syncthreads();  // the states have been read
-        keep(rd);
-        __syncthreads();
-        if (more) request_states(next);
-        if (!keys)
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) pf[kk] = scores[rt][kk][lane];
+        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, MV column tiles: the states'
+        // part, without the scores of the key wavefronts, and the rest.  bf16: the
+        // query wavefronts' all, as the key wavefronts have more scores to form.
+        constexpr int MV = CH == 1 ? 2 * NV : NV / 2, GV = MV < 4 ? MV : 4;
+        const int m0 = CH == 1 ? 0 : (2 * ch + keys) * MV;
+        const bool has = CH > 1 || !keys;
         const float ds = dc.d[16 * rt + l16];
+        // the states' part before the barrier, where there are registers to hold it
+        constexpr bool early = NK * NV < 16;
+        f4 val[early ? MV : 1];
+        auto value_of_state = [&](int i0, f4 (&y)[GV]) {
+            Frag kf[NK];
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
+#pragma unroll
+            for (int i = 0; i < GV; ++i) y[i] = zf4();
+            mma_group(y, kf, [&](int i, int kk) { return ST::turned(after, m0 + i0 + i, kk, lane); });
+#pragma unroll
+            for (int i = 0; i < GV; ++i) y[i] *= ds;
+        };
+        if constexpr (early) {
+            if (has)
+#pragma unroll
+                for (int i0 = 0; i0 < MV; i0 += GV) value_of_state(i0, reinterpret_cast<f4 (&)[GV]>(val[i0]));
+        }
+        if constexpr (both) {
+            if (more) request_states(next);
+            if (more && w == 1) gates_of(next, odd ^ 1);
+            __syncthreads();  // the scores are there
+        } else {
+            __syncthreads();  // the states have been read
+            keep(rd, state);
+            __syncthreads();
+            if (more) request_states(next);
+            if (more && w == 1) gates_of(next, odd ^ 1);
+        }
         if (keys) {
             // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
             Frag vf[NV];
@@ -1722,7 +1785,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
                 f4 y[G];
 #pragma unroll
                 for (int i = 0; i < G; ++i) y[i] = zf4();
-                mma_group(y, vf, [&](int i, int kk) { return ST::get(state, (i0 + i) * CH + ch, kk, lane); });
+                mma_group(y, vf, [&](int i, int kk) { return ST::get(after, (i0 + i) * CH + ch, kk, lane); });
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
                     y[i] *= ds;
@@ -1744,66 +1807,55 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             bs += __shfl_xor(bs, 32);
             if (lane < 16) sm.b[ch][16 * rt + lane] = bs;
         }
-        // dV^T = dO^T (P . D) + e^(L_end - L) dS^T K^T, N column tiles from m0
-        auto values = [&](int m0, auto count) {
-            constexpr int N = decltype(count)::value;
-            Frag kf[NK];
-            f4 y[N];
+        if (has) {
             const __amdgpu_buffer_rsrc_t out = buffer(
                 reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0) * a.H + h) * a.Dv);
             const uint32_t o = (uint32_t)((16 * rt + l16) * a.H * a.Dv + g4) * (uint32_t)sizeof(S);
+            if (CH == 1 || !keys)
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) kf[kk] = lk.row(kt, 16 * rt, kk);
+                for (int kk = 0; kk < KS; ++kk) pf[kk] = scores[rt][kk][lane];
 #pragma unroll
-            for (int i = 0; i < N; ++i) y[i] = zf4();
-            mma_group(y, kf, [&](int i, int kk) { return ST::turned(state, m0 + i, kk, lane); });
+            for (int i0 = 0; i0 < MV; i0 += GV) {
+                f4 y[GV];
+                if constexpr (early) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) y[i] *= ds;
-            mma_group(y, pf, [&](int i, int kk) { return lv.at_col(ot, 32 * kk, lv.col_off(m0 + i)); });
+                    for (int i = 0; i < GV; ++i) y[i] = val[i0 + i];
+                } else {
+                    value_of_state(i0, y);
+                }
+                mma_group(y, pf, [&](int i, int kk) { return lv.at_col(ot, 32 * kk, lv.col_off(m0 + i0 + i)); });
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = 16 * (m0 + i);
-                store4(out, mine && c + g4 < a.Dv ? o + c * (uint32_t)sizeof(S) : kNowhere, y[i], T());
+                for (int i = 0; i < GV; ++i) {
+                    const int c = 16 * (m0 + i0 + i);
+                    store4(out, mine && c + g4 < a.Dv ? o + c * (uint32_t)sizeof(S) : kNowhere, y[i], T());
+                }
             }
             if (nan && mine) {
                 S *p = reinterpret_cast<S *>(a.dv) + ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.H + h) * a.Dv;
 #pragma unroll 1
-                for (int i = 0; i < 4 * N; ++i) {
+                for (int i = 0; i < 4 * MV; ++i) {
                     const int c = 16 * (m0 + i / 4) + g4 + i % 4;
                     if (c < a.Dv && (16 * rt + l16 <= last_o[c] || 16 * rt + l16 <= ends[0] ||
                                      row_k[16 * rt + l16]))
                         put1(p + c, __builtin_nanf(""));
                 }
             }
-        };
-        // the key wavefronts have dK to do: they take a quarter (fp32: half)
-        constexpr int MQ = CH == 1 ? 3 * NV / 2 : NV / 2, MK = CH == 1 ? NV / 2 : NV / 2;
-        if (!keys) {
-            if constexpr (MQ == 6) {
-                values(0, std::integral_constant<int, 3>());
-                values(3, std::integral_constant<int, 3>());
-            } else {
-                values(ch * 2 * MQ, std::integral_constant<int, MQ>());
-            }
-        } else {
-            values(CH == 1 ? MQ : ch * 2 * MQ + MQ, std::integral_constant<int, MK>());
         }
         __syncthreads();
         if (!same) {  // the chunk's last head
-            if (mine) {
-                S *out = reinterpret_cast<S *>(keys ? a.dk : a.dq) +
-                         ((it.un.tok0 + it.t0 + 16 * rt + l16) * a.Hk + it.hk) * a.Dk + g4;
+            const __amdgpu_buffer_rsrc_t out = buffer(reinterpret_cast<S *>(keys ? a.dk : a.dq) +
+                                                      ((it.un.tok0 + it.t0) * a.Hk + it.hk) * a.Dk);
+            const uint32_t o = (uint32_t)((16 * rt + l16) * a.Hk * a.Dk + g4) * (uint32_t)sizeof(S);
 #pragma unroll
-                for (int i = 0; i < NTK; ++i) {
-                    const int n = i * CH + ch;
-                    if (16 * n + g4 < a.Dk) put4(out + 16 * n, acc[i]);
-                }
+            for (int i = 0; i < NTK; ++i) {
+                const int c = 16 * (i * CH + ch);
+                store4(out, mine && c + g4 < a.Dk ? o + c * (uint32_t)sizeof(S) : kNowhere, acc[i], T());
             }
 #pragma unroll
             for (int i = 0; i < NTK; ++i) acc[i] = zf4();
         }
         if (!more) {
-            if (w == 0) finish(done, odd, gdone, up_to, from);
+            if (w == 0) finish(done, odd, gdone, gall, up_to, from);
             break;
         }
         if (nan) {
