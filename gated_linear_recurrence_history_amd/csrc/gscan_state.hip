@@ -1484,30 +1484,33 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     typename SV::Regs rv, ro;
     u4 rs[NS], rd[NS];
     Gates::Raw gx;
-    auto request = [&](const Item &it, bool first) {
-        if (first) {
-            SK sq, sk;
-            sq.begin(row_at<S>(a.q, a.qs, it.un, it.hk, it.t0), a.qs.t, a.Dk, tid);
-            sk.begin(row_at<S>(a.k, a.ks, it.un, it.hk, it.t0), a.ks.t, a.Dk, tid);
-            sq.load(rq, it.left, 0, tid);
-            sk.load(rk, it.left, 0, tid);
-        }
+    // requests of an item (`some`: there is one) without a branch, which would
+    // wait for what it loads where it ends; `first`: its chunk's queries and keys
+    auto request = [&](const Item &it, bool some, bool first) {
+        const int rows = some ? it.left : 0, shared = first ? rows : 0;
+        SK sq, sk;
+        sq.begin(row_at<S>(a.q, a.qs, it.un, it.hk, it.t0), a.qs.t, a.Dk, tid);
+        sk.begin(row_at<S>(a.k, a.ks, it.un, it.hk, it.t0), a.ks.t, a.Dk, tid);
+        sq.load(rq, shared, 0, tid);
+        sk.load(rk, shared, 0, tid);
         SV sv, so;
         sv.begin(row_at<S>(a.v, a.vs, it.un, it.h, it.t0), a.vs.t, a.Dv, tid);
         so.begin(row_at<S>(a.dout, a.ds, it.un, it.h, it.t0), a.ds.t, a.Dv, tid);
-        sv.load(rv, it.left, 0, tid);
-        so.load(ro, it.left, 0, tid);
+        sv.load(rv, rows, 0, tid);
+        so.load(ro, rows, 0, tid);
         Gates gates;
         gates.begin(a, it.un, it.h, it.t0, C, lane);
-        gx = gates.load(it.left, lane, 0);
+        gx = gates.load(rows, lane, 0);
     };
-    auto request_states = [&](const Item &it) {
-        const int64_t at = ((int64_t)it.slot * a.H + it.h) * kOps;
-        const u4 *p = reinterpret_cast<const u4 *>(ws + st_s) + at, *q = reinterpret_cast<const u4 *>(ws + st_ds) + at;
+    auto request_states = [&](const Item &it, bool some) {
+        const int64_t at = ((int64_t)it.slot * a.H + it.h) * kOps * 16;
+        const __amdgpu_buffer_rsrc_t p = buffer(ws + st_s + at), q = buffer(ws + st_ds + at);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) rs[i] = p[tid + kGThreads * i];
+        for (int i = 0; i < NS; ++i)
+            rs[i] = __builtin_amdgcn_raw_buffer_load_b128(p, some ? (tid + kGThreads * i) * 16 : kNowhere, 0, 0);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) rd[i] = q[tid + kGThreads * i];
+        for (int i = 0; i < NS; ++i)
+            rd[i] = __builtin_amdgcn_raw_buffer_load_b128(q, some ? (tid + kGThreads * i) * 16 : kNowhere, 0, 0);
     };
     auto keep = [&](const u4 (&r)[NS], u4 *to) {
 #pragma unroll
@@ -1530,8 +1533,8 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     Item it;
     find(blockIdx.x * per, &it);
     if (it.u >= last) return;
-    request(it, true);
-    request_states(it);
+    request(it, true, true);
+    request_states(it, true);
     clear();
     // the decays of an item, beside the one before it
     auto gates_of = [&](const Item &i, int which) {
@@ -1620,7 +1623,8 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         });
         keep(rs, state);
         if constexpr (both) keep(rd, second);
-        const float x = Gates::value(gx, a);
+        float x = Gates::value(gx, a);
+        asm volatile("" : "+v"(x));  // now: gx is about to be loaded again
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
@@ -1635,7 +1639,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         const bool more = next.u < last;
         __syncthreads();
         const bool nan = bad != 0;
-        if (more) request(next, !same);
+        request(next, more, !same);
         if (w == 0) {
             if (later) finish(done, odd ^ 1, gdone, gall, up_to, from);
             done = it;
@@ -1764,15 +1768,15 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
                 for (int i0 = 0; i0 < MV; i0 += GV) value_of_state(i0, reinterpret_cast<f4 (&)[GV]>(val[i0]));
         }
         if constexpr (both) {
-            if (more) request_states(next);
             if (more && w == 1) gates_of(next, odd ^ 1);
+            request_states(next, more);
             __syncthreads();  // the scores are there
         } else {
             __syncthreads();  // the states have been read
             keep(rd, state);
             __syncthreads();
-            if (more) request_states(next);
             if (more && w == 1) gates_of(next, odd ^ 1);
+            request_states(next, more);
         }
         if (keys) {
             // dK^T = Q^T (dP . D) + e^(L_end - L) dS V^T
