@@ -527,6 +527,17 @@ struct Stage {
         }
         base += step;
     }
+    // the same of a tile that is not followed by others
+    static __device__ __forceinline__ void fetch(Regs &r, __amdgpu_buffer_rsrc_t b, uint32_t st, int cols,
+                                                 int left, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int q = tid + TH * i, row = q / kPpr, col = q % kPpr * T::VE;
+            const uint32_t at = (__umul24(row, st) + col) * (uint32_t)sizeof(typename T::S);
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (row < left) & (col < cols) ? at : kNowhere, 0, 0);
+        }
+    }
     template <class TL>
     static __device__ __forceinline__ void store(const Regs &r, char *tile, int tid)
     {
@@ -1451,6 +1462,16 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
         uint32_t u;  // unit of the grid (chunk and key head)
         int slot, h, hk, t0, left;
     };
+    // Lanes 0 .. 4 hold the strides of q, k, v, d_out and the gate and where the
+    // sequence last found begins in each, so that an item's five addresses are
+    // one computation.
+    auto of_tensor = [&](auto q, auto k, auto v, auto o, auto g) {
+        return lane == 0 ? q : lane == 1 ? k : lane == 2 ? v : lane == 3 ? o : g;
+    };
+    const uint32_t ts = of_tensor(a.qs.t, a.ks.t, a.vs.t, a.ds.t, a.gs.t);
+    const uint32_t hs = of_tensor(a.qs.h, a.ks.h, a.vs.h, a.ds.h, a.gs.h);
+    const int se = sizeof(S) == 2 ? 1 : 2, ge = a.gate_dtype ? 1 : 2;  // element bytes, as shifts
+    uint64_t seq0 = 0;
     // the first item from unit u on; u >= last when there is none
     auto find = [&](uint32_t u, Item *it) {
         for (; u < last; ++u) {
@@ -1462,6 +1483,9 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             it->slot = it->un.slot0 + it->un.part;
             it->hk = (int)(u - c * (uint32_t)a.Hk);
             it->h = it->hk * reps;
+            const int64_t b = of_tensor(a.qs.b, a.ks.b, a.vs.b, a.ds.b, a.gs.b);
+            const uint64_t p = reinterpret_cast<uint64_t>(of_tensor(a.q, a.k, a.v, a.dout, a.gate));
+            seq0 = p + ((uint64_t)(it->un.seq * b + (int64_t)ts * it->un.in0) << (lane < 4 ? se : ge));
             break;
         }
         it->u = u;
@@ -1488,19 +1512,22 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     // wait for what it loads where it ends; `first`: its chunk's queries and keys
     auto request = [&](const Item &it, bool some, bool first) {
         const int rows = some ? it.left : 0, shared = first ? rows : 0;
-        SK sq, sk;
-        sq.begin(row_at<S>(a.q, a.qs, it.un, it.hk, it.t0), a.qs.t, a.Dk, tid);
-        sk.begin(row_at<S>(a.k, a.ks, it.un, it.hk, it.t0), a.ks.t, a.Dk, tid);
-        sq.load(rq, shared, 0, tid);
-        sk.load(rk, shared, 0, tid);
-        SV sv, so;
-        sv.begin(row_at<S>(a.v, a.vs, it.un, it.h, it.t0), a.vs.t, a.Dv, tid);
-        so.begin(row_at<S>(a.dout, a.ds, it.un, it.h, it.t0), a.ds.t, a.Dv, tid);
-        sv.load(rv, rows, 0, tid);
-        so.load(ro, rows, 0, tid);
-        Gates gates;
-        gates.begin(a, it.un, it.h, it.t0, C, lane);
-        gx = gates.load(rows, lane, 0);
+        const uint64_t at = seq0 + (((uint64_t)hs * (uint32_t)(lane < 2 ? it.hk : it.h) +
+                                     (uint64_t)ts * (uint32_t)it.t0) << (lane < 4 ? se : ge));
+        auto base = [&](int i) {
+            return buffer(reinterpret_cast<const void *>(
+                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(at >> 32), i) << 32 |
+                (uint32_t)__builtin_amdgcn_readlane((uint32_t)at, i)));
+        };
+        auto step = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane(ts, i); };
+        SK::fetch(rq, base(0), step(0), a.Dk, shared, tid);
+        SK::fetch(rk, base(1), step(1), a.Dk, shared, tid);
+        SV::fetch(rv, base(2), step(2), a.Dv, rows, tid);
+        SV::fetch(ro, base(3), step(3), a.Dv, rows, tid);
+        const __amdgpu_buffer_rsrc_t g = base(4);
+        const uint32_t og = __umul24(lane, step(4)) << ge;
+        gx.x32 = __builtin_amdgcn_raw_buffer_load_b32(g, lane < rows && lane < C && ge == 2 ? og : kNowhere, 0, 0);
+        gx.x16 = __builtin_amdgcn_raw_buffer_load_b16(g, lane < rows && lane < C && ge == 1 ? og : kNowhere, 0, 0);
     };
     auto request_states = [&](const Item &it, bool some) {
         const int64_t at = ((int64_t)it.slot * a.H + it.h) * kOps * 16;
