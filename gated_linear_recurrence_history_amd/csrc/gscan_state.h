@@ -45,6 +45,7 @@ struct StatePlan {
     size_t st_part_r = 0, st_dec_r = 0;  // backward: the same of the state's gradient
     int64_t chunks = 0;       // chunk slots over all sequences (an upper bound when packed)
     size_t st_s = 0, st_ds = 0;  // workspace: the backward's chunk states and their gradients
+    size_t down = 0;          // bf16: the powers of two of their column tiles
     size_t bytes = 0;
 };
 

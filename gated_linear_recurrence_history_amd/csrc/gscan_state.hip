@@ -299,17 +299,37 @@ struct PartsOf<FP> {
     typedef FP::Frag type;
 };
 
-// Operands kept in device memory: 16 bytes (bf16) or two planes of 16 bytes
-// (fp32) per lane.
-__device__ __forceinline__ void put_frag(void *base, int64_t i, int lane, const u4 &f)
+// Operands of states kept in device memory: 16 bytes (bf16) or two planes of
+// 16 bytes (fp32) per lane.  bf16: fp16 with a power of two per tile of 16
+// columns, whose 11 bits <S, dS> needs (with bf16's 8 its gradient of the gate
+// was off by 2.9e-3, more than the rounding of the result); they become bf16
+// where they are operands.
+__device__ __forceinline__ void put_state(void *base, int64_t i, int lane, f4 x, f4 y, float up, const BF &)
 {
-    reinterpret_cast<u4 *>(base)[i * 64 + lane] = f;
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    auto pk = [&](float u, float v) {
+        return __builtin_bit_cast(uint32_t, h2{(_Float16)(u * up), (_Float16)(v * up)});
+    };
+    reinterpret_cast<u4 *>(base)[i * 64 + lane] = u4{pk(x[0], x[1]), pk(x[2], x[3]), pk(y[0], y[1]), pk(y[2], y[3])};
 }
-__device__ __forceinline__ void put_frag(void *base, int64_t i, int lane, const FP::Frag &f)
+__device__ __forceinline__ void put_state(void *base, int64_t i, int lane, f4 x, f4 y, float, const FP &)
 {
-    reinterpret_cast<f4 *>(base)[i * 128 + lane] = f.a;
-    reinterpret_cast<f4 *>(base)[i * 128 + 64 + lane] = f.b;
+    reinterpret_cast<f4 *>(base)[i * 128 + lane] = x;
+    reinterpret_cast<f4 *>(base)[i * 128 + 64 + lane] = y;
 }
+__device__ __forceinline__ u4 get_state(const u4 &x, float down, const BF &)
+{
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    u4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = x[i];  // (a bit cast of the element itself takes the first one)
+        const h2 h = __builtin_bit_cast(h2, u);
+        r[i] = pack_bf16((float)h[0] * down, (float)h[1] * down);
+    }
+    return r;
+}
+__device__ __forceinline__ u4 get_state(const u4 &x, float, const FP &) { return x; }
 
 // Whether sixteen bytes hold an infinity or NaN: the largest magnitude's bits.
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
@@ -784,6 +804,29 @@ __device__ __forceinline__ void mma_group(f4 (&y)[N], const F (&b)[K], LD ld)
     }
 }
 
+// The exponent e of the wavefront's largest finite |st| (below 2^e), not below -100.
+template <int N>
+__device__ __forceinline__ int exponent_of(const f4 (&st)[N])
+{
+    auto largest = [&](auto part) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, part(fabsf(st[i][j])));  // (NaN is passed over)
+        m = fmaxf(m, dpp<0xb1>(m));
+        m = fmaxf(m, dpp<0x4e>(m));
+        m = fmaxf(m, dpp<0x141>(m));
+        m = fmaxf(m, dpp<0x140>(m));
+        auto row = [&](int i) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(m), i)); };
+        return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
+    };
+    float m = largest([](float x) { return x; });
+    if (m == __builtin_inff()) m = largest([](float x) { return x < __builtin_inff() ? x : 0.f; });
+    const int e = __builtin_amdgcn_frexp_expf(m);
+    return first_lane(e < -100 ? -100 : e);
+}
+
 // st = g st + mul X^T (m . y) of a staged tile X: y is an operand of 16 columns of
 // the chunk, m a factor per token.  Accumulators in turn, so that products
 // which follow each other do not wait for each other.
@@ -1072,6 +1115,8 @@ struct PassJob {
     int rstr, cstr;      // strides of a row and a column in init and fin
     void *dst;
     float mul;           // factor of what is added
+    float *down;         // bf16: what the operands of a column tile are to be multiplied by,
+                         // [chunk slot][H][2][2 NY], the state's and its gradient's
 };
 
 // Wavefronts 4-7 bring the next chunk's rows and decays into LDS while
@@ -1164,13 +1209,17 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
         const int odd = n & 1;
         const Decay<C> &dc = dcs[odd];
         if constexpr (STORE) {  // the operands of this chunk, before its own tokens enter
-#pragma unroll
-            for (int kk = 0; kk < NX; ++kk) {
-                Frag f;
-                to_frag(st[2 * kk], st[2 * kk + 1], &f);
-                put_frag(jb.dst, (((int64_t)(un.slot0 + c1 + step * n) * a.H + h) * 2 * ny +
-                                  slice * 4 + w) * NX + kk, lane, f);
+            const int64_t tile = ((int64_t)(un.slot0 + c1 + step * n) * a.H + h) * 2 * ny + slice * 4 + w;
+            float up = 1.f;
+            if constexpr (sizeof(S) == 2) {
+                const int e = exponent_of(st);
+                up = ldexpf(1.f, 14 - e);
+                const int64_t item = (int64_t)(un.slot0 + c1 + step * n) * a.H + h;
+                if (lane == 0) jb.down[(2 * item + REV) * 2 * ny + slice * 4 + w] = ldexpf(1.f, e - 14);
             }
+#pragma unroll
+            for (int kk = 0; kk < NX; ++kk)
+                put_state(jb.dst, tile * NX + kk, lane, st[2 * kk], st[2 * kk + 1], up, T());
         }
         Frag yf[KS];
 #pragma unroll
@@ -1215,11 +1264,12 @@ gscan_state_part_kernel(StateArgs a, int slices, int ways, int64_t per, Parts2 o
     float *fin = reinterpret_cast<float *>(ws + o.st[way]) + (unit * a.H + h) * a.Dk * a.Dv;
     float *dec = reinterpret_cast<float *>(ws + o.dec[way]) + unit * a.H + h;
     if (!way) {
-        const PassJob jb = {a.k, a.v, a.ks, a.vs, hk, h, a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr, 1.f};
+        const PassJob jb = {a.k, a.v, a.ks, a.vs, hk, h, a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr, 1.f,
+                            nullptr};
         pass_walk<T, NK, false, false>(a, jb, 0, slice, h, un, tb, te, &smem, dcs);
     } else {
         const PassJob jb = {a.q, a.dout, a.qs, a.ds, hk, h, a.Dk, a.Dv, nullptr, fin, dec, a.Dv, 1, nullptr,
-                            a.scale};
+                            a.scale, nullptr};
         pass_walk<T, NK, true, false>(a, jb, 0, slice, h, un, tb, te, &smem, dcs);
     }
 }
@@ -1290,6 +1340,7 @@ gscan_state_join_kernel(StateArgs a, int ways, int64_t per, Parts2 o)
 // S^T: operand (n, kk) holds columns (keys) 16n .. and rows (values) 32kk ...
 struct PassWs {
     size_t s, ds;  // operands
+    size_t down;   // bf16: the factors of their column tiles
     Parts2 parts;  // units' states and gradients of states (split sequences)
 };
 
@@ -1317,12 +1368,12 @@ gscan_state_pass_kernel(StateArgs a, int64_t per, PassWs o)
                                : from ? from + whole : nullptr;
     if (!way) {
         const PassJob jb = {a.v, a.k, a.vs, a.ks, h, hk, a.Dv, a.Dk, init, nullptr, nullptr, 1, a.Dv,
-                            ws + o.s, 1.f};
+                            ws + o.s, 1.f, reinterpret_cast<float *>(ws + o.down)};
         pass_walk<T, NV, false, true>(a, jb, NK, slice, h, un, tb, te, &smem, dcs);
     } else {
         const PassJob jb = {a.dout, a.q, a.ds, a.qs, h, hk, a.Dv, a.Dk, init,
                             a.ds0 && un.part == 0 ? a.ds0 + whole : nullptr, nullptr, 1, a.Dv,
-                            ws + o.ds, a.scale};
+                            ws + o.ds, a.scale, reinterpret_cast<float *>(ws + o.down)};
         pass_walk<T, NV, true, true>(a, jb, NK, slice, h, un, tb, te, &smem, dcs);
     }
 }
@@ -1377,11 +1428,16 @@ struct States<FP, NV> {
     }
 };
 
+// Of stored states (fp32 sums of exact products).
 __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const BF &)
 {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += bf_lo(x[i]) * bf_lo(y[i]) + bf_hi(x[i]) * bf_hi(y[i]);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = x[i], v = y[i];
+        s = __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, u), __builtin_bit_cast(h2, v), s, false);
+    }
     return s;
 }
 __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
@@ -1412,7 +1468,7 @@ constexpr int kCus = 256;
 
 template <class T, int NK, int NV>
 __global__ void __launch_bounds__(kGThreads, 2)
-gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, size_t st_ds)
+gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, PassWs o)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
@@ -1507,6 +1563,12 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     typename SK::Regs rq, rk;
     typename SV::Regs rv, ro;
     u4 rs[NS], rd[NS];
+    uint32_t down = 0;
+    // the factor of this thread's i-th piece of the state (of its gradient: from 2NK)
+    const int w0 = w;
+    auto factor = [&](int i, int from) {
+        return __uint_as_float(__builtin_amdgcn_readlane(down, from + (w0 + kGThreads / 64 * i) / NV));
+    };
     Gates::Raw gx;
     // requests of an item (`some`: there is one) without a branch, which would
     // wait for what it loads where it ends; `first`: its chunk's queries and keys
@@ -1531,19 +1593,23 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
     };
     auto request_states = [&](const Item &it, bool some) {
         const int64_t at = ((int64_t)it.slot * a.H + it.h) * kOps * 16;
-        const __amdgpu_buffer_rsrc_t p = buffer(ws + st_s + at), q = buffer(ws + st_ds + at);
+        const __amdgpu_buffer_rsrc_t p = buffer(ws + o.s + at), q = buffer(ws + o.ds + at);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             rs[i] = __builtin_amdgcn_raw_buffer_load_b128(p, some ? (tid + kGThreads * i) * 16 : kNowhere, 0, 0);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             rd[i] = __builtin_amdgcn_raw_buffer_load_b128(q, some ? (tid + kGThreads * i) * 16 : kNowhere, 0, 0);
+        if constexpr (sizeof(S) == 2) {  // lane n: of the state's tile n; 2NK + n: of its gradient's
+            const __amdgpu_buffer_rsrc_t u = buffer(ws + o.down + ((int64_t)it.slot * a.H + it.h) * 4 * NK * 4);
+            down = __builtin_amdgcn_raw_buffer_load_b32(u, some && lane < 4 * NK ? lane * 4 : kNowhere, 0, 0);
+        }
     };
-    auto keep = [&](const u4 (&r)[NS], u4 *to) {
+    auto keep = [&](const u4 (&r)[NS], u4 *to, int from) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int q = tid + kGThreads * i;
-            to[(q & ~63) + place(q & 63)] = r[i];
+            to[(q & ~63) + place(q & 63)] = get_state(r[i], factor(i, from), T());
         }
     };
     auto clear = [&] {
@@ -1648,14 +1714,17 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             row_o[row] = 1;
             bad = 1;
         });
-        keep(rs, state);
-        if constexpr (both) keep(rd, second);
+        keep(rs, state, 0);
+        if constexpr (both) keep(rd, second, 2 * NK);
         float x = Gates::value(gx, a);
         asm volatile("" : "+v"(x));  // now: gx is about to be loaded again
         {  // F = e^(L_end) <S, dS>
             float f = 0.f;
 #pragma unroll
-            for (int i = 0; i < NS; ++i) f += dot16(rs[i], rd[i], T());
+            for (int i = 0; i < NS; ++i) {
+                const float d = dot16(rs[i], rd[i], T());
+                f += sizeof(S) == 2 ? d * (factor(i, 0) * factor(i, 2 * NK)) : d;
+            }
             f = scan64(f);
             if (lane == 63) sm.f[w] = f;
         }
@@ -1800,7 +1869,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, size_t st_s, 
             __syncthreads();  // the scores are there
         } else {
             __syncthreads();  // the states have been read
-            keep(rd, state);
+            keep(rd, state, 2 * NK);
             __syncthreads();
             if (more && w == 1) gates_of(next, odd ^ 1);
             request_states(next, more);
@@ -1944,7 +2013,7 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
         e = part_launch<T, NK>(p, a, 2, st);
         if (e != hipSuccess) return e;
     }
-    const PassWs o = {p.st_s, p.st_ds, parts_of(p)};
+    const PassWs o = {p.st_s, p.st_ds, p.down, parts_of(p)};
     hipLaunchKernelGGL((gscan_state_pass_kernel<T, NK, NV>), dim3((unsigned)(p.units * a.H * NK)),
                        dim3(2 * kSThreads), 0, st, a, p.per, o);
     e = hipGetLastError();
@@ -1952,7 +2021,7 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
     const int64_t units = p.chunks * a.Hk;
     const int64_t each = (units + kCus - 1) / kCus;
     hipLaunchKernelGGL((gscan_state_grad_kernel<T, NK, NV>), dim3((unsigned)((units + each - 1) / each)),
-                       dim3(kGThreads), 0, st, a, (uint32_t)units, (uint32_t)each, p.st_s, p.st_ds);
+                       dim3(kGThreads), 0, st, a, (uint32_t)units, (uint32_t)each, o);
     return hipGetLastError();
 }
 
@@ -2033,6 +2102,7 @@ StatePlan make_state_plan(const StateArgs &a, bool backward)
                            (a.dtype ? 2u : 4u);
         p.st_s = take(one);
         p.st_ds = take(one);
+        if (a.dtype) p.down = take((size_t)p.chunks * (size_t)a.H * (size_t)(4 * p.nk) * 4u);
     }
     p.bytes = at;
     return p;

@@ -121,8 +121,9 @@ def test_scan_refuses_misaligned_states_and_offsets(lib):
 def test_scan_workspace(lib):
     d = scan_desc()
     need = lib.gscan_state_scan_backward_workspace_bytes(ctypes.byref(d))
-    # the states before and the gradients after each of 2 chunks of 64 tokens, bf16, widths 64 x 64
-    assert need == 2 * (2 * 2 * 8 * 64 * 64 * 2)
+    # the states before and the gradients after each of 2 chunks of 64 tokens, 16 bits, widths 64 x 64,
+    # and a factor for each of their tiles of 16 keys
+    assert need == 2 * (2 * 2 * 8 * (64 * 64 * 2 + 4 * 4))
     assert backward(lib, d, ws=P, n=need - 1) == WS_SMALL
     assert backward(lib, d, ws=P + 16, n=need) == MISALIGNED
     # short or many sequences are walked whole; one long one is divided
