@@ -19,6 +19,11 @@
 // accuracy.
 // dw: every workgroup keeps its sums in registers over its tokens and leaves
 // one partial, which a second kernel adds in a fixed order in fp64.
+// Rows are requested a few at a time as raw words, before the angles are formed
+// (one at a time: 88 us where this takes 78; four as fp32: 106, for fewer
+// wavefronts fit).  Measured: forward, 16384 tokens, 40 bf16 heads of 128: 336 MB
+// in 75 us, 4.5 TB/s (a large copy: 4.8); backward, 8191 tokens, 32 fp32 heads of
+// 80: 252 MB in 46 us and 7 us for the 1024 partials of dw; one token: 4 us.
 #include <type_traits>
 
 #include "gscan_state_dev.h"
