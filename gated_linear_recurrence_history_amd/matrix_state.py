@@ -145,9 +145,14 @@ def _describe(q, k, v, gate, scale, gate_form, gate_shift, seq_offsets, single=F
 def _check_dense(t, shape, dtype, dev, name):
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}; "
                          f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _empty(like):
+    """A dense tensor of the shape and type of `like`."""
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _workspace(workspace, need, dev):
@@ -224,7 +229,7 @@ def state_scan_forward(q, k, v, gate, scale: float = 1.0, gate_form: str = "sigm
     need = int(L.gscan_state_scan_forward_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
         if out is None:
-            out = v.new_empty(v.shape)
+            out = _empty(v)
         if final_state is True:
             final_state = v.new_empty(states, dtype=torch.float32)
         wp, wn, _keep = _workspace(workspace, need, dev)
@@ -260,7 +265,7 @@ def state_scan_backward(q, k, v, gate, d_out, scale: float = 1.0, gate_form: str
     d.d_out_stride = _strides(_layout(d_out), d_out.dim() - 2)
     need = int(L.gscan_state_scan_backward_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
-        dq, dk, dv, dgate = (t.new_empty(t.shape) for t in (q, k, v, gate))
+        dq, dk, dv, dgate = (_empty(t) for t in (q, k, v, gate))
         ds0 = None
         if initial_state is not None:
             ds0 = v.new_empty(states, dtype=torch.float32)
@@ -291,7 +296,7 @@ def state_scan_step(q, k, v, gate, state, slots=None, scale: float = 1.0,
         _check_dense(out, v.shape, v.dtype, dev, "out")
     with _On(dev, stream) as s:
         if out is None:
-            out = v.new_empty(v.shape)
+            out = _empty(v)
         if d.B:
             binding._check(binding.lib().gscan_state_scan_step(
                 ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),

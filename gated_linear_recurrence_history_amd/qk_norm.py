@@ -17,7 +17,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .matrix_state import (_CODES, _On, _check_dense, _layout, _on_device, _outer_strides, _ptr,
+from .matrix_state import (_CODES, _On, _check_dense, _empty, _layout, _on_device, _outer_strides, _ptr,
                            _readable, _reads_rows, _workspace)
 
 LAYOUTS = {"half": 0, "interleaved": 1}
@@ -125,9 +125,10 @@ def _describe(q, k, weight_q, weight_k, positions, freq, eps, layout, magnitude)
             raise ValueError("freq must be a float32 tensor [rot / 2]")
         _check_dense(freq, freq.shape, torch.float32, dev, "freq")
         d.rot = 2 * freq.shape[0]
-        _on_device(dev, positions=positions)
+        if not isinstance(positions, torch.Tensor) or positions.device != dev:
+            raise ValueError(f"positions must be a tensor on {dev}")
         if positions.dtype not in (torch.int32, torch.int64) or \
-                tuple(positions.shape) != (d.tokens,) or not positions.is_contiguous():
+                positions.shape != (d.tokens,) or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 or int64 tensor [{d.tokens}]; "
                              f"got {positions.dtype} {tuple(positions.shape)}")
         d.pos_int64 = int(positions.dtype == torch.int64)
@@ -152,7 +153,7 @@ def qk_norm_rope_forward(q, k, weight_q, weight_k, positions, freq, eps: float =
             _check_dense(out[1], k.shape, k.dtype, dev, "out[1]")
     with _On(dev, stream) as s:
         if out is None:
-            out = (q.new_empty(q.shape), None if k is None else k.new_empty(k.shape))
+            out = (_empty(q), None if k is None else _empty(k))
         binding._check(binding.lib().gscan_qk_norm_rope_forward(
             ctypes.byref(d), q.data_ptr(), _ptr(k), _ptr(weight_q), _ptr(weight_k),
             _ptr(positions) if d.rot else None, _ptr(freq), out[0].data_ptr(),
@@ -179,7 +180,7 @@ def qk_norm_rope_backward(q, k, weight_q, weight_k, positions, freq, dy_q, dy_k,
     if weight_q is not None or weight_k is not None:
         need = int(L.gscan_qk_norm_rope_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
-        dq, dk, dwq, dwk = (None if t is None else t.new_empty(t.shape)
+        dq, dk, dwq, dwk = (None if t is None else _empty(t)
                             for t in (q, k, weight_q, weight_k))
         wp, wn, _keep = _workspace(workspace, need, dev)
         binding._check(L.gscan_qk_norm_rope_backward(
