@@ -221,6 +221,10 @@ struct Tile<FP, W> {
     }
 };
 
+// Rows of N 32-wide units; three are in rows of four.
+template <class T, int N>
+using Rows = Tile<T, N == 3 ? 128 : N * 32>;
+
 // Two accumulators (rows 0..15 and 16..31 of a column) as an operand.
 __device__ __forceinline__ void to_frag(f4 x, f4 y, u4 *f)
 {
@@ -888,7 +892,7 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
-    typedef Tile<T, NK * 32> TK;
+    typedef Rows<T, NK> TK;
     typedef Tile<T, kSlice> TV;
     constexpr int C = T::C, RT = C / 16, KS = C / 32;
     constexpr int kQ = 0, kK = C * TK::bytes, kV = 2 * C * TK::bytes, kBuf = kV + C * TV::bytes;
@@ -1140,7 +1144,7 @@ struct PassJob {
 // sum of log gates in one, the exponentials in the next.
 template <class T, int NX>
 struct PassLds {
-    static constexpr int kX = T::C * Tile<T, NX * 32>::bytes, kBuf = kX + T::C * Tile<T, kSlice>::bytes;
+    static constexpr int kX = T::C * Rows<T, NX>::bytes, kBuf = kX + T::C * Tile<T, kSlice>::bytes;
     char tile[2][kBuf];
 };
 
@@ -1151,7 +1155,7 @@ __device__ __forceinline__ void pass_walk(const StateArgs &a, const PassJob &jb,
 {
     typedef typename T::S S;
     typedef typename T::Frag Frag;
-    typedef Tile<T, NX * 32> TX;
+    typedef Rows<T, NX> TX;
     typedef Tile<T, kSlice> TY;
     typedef PassLds<T, NX> Lds;
     constexpr int C = T::C, KS = C / 32, step = REV ? -1 : 1;
@@ -2003,11 +2007,16 @@ Parts2 parts_of(const StatePlan &p)
     return Parts2{{p.st_part, p.st_part_r}, {p.st_dec, p.st_dec_r}};
 }
 
-template <class T, int NK>
+// 32-wide units of the keys: three where they suffice (widths 72 to 96: 5100
+// packed fp32 tokens, 12 heads of 96 x 80: 98 us, with four units 108), in the
+// kernels whose states nobody else reads.
+template <class T>
 hipError_t part_launch(const StatePlan &p, const StateArgs &a, int ways, hipStream_t st)
 {
     const int slices = (a.Dv + kSlice - 1) / kSlice;
-    hipLaunchKernelGGL((gscan_state_part_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices * ways)),
+    auto *k = a.Dk <= 64 ? gscan_state_part_kernel<T, 2>
+                         : a.Dk <= 96 ? gscan_state_part_kernel<T, 3> : gscan_state_part_kernel<T, 4>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(p.units * a.H * slices * ways)),
                        dim3(2 * kSThreads), 0, st, a, slices, ways, p.per, parts_of(p));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -2017,15 +2026,17 @@ hipError_t part_launch(const StatePlan &p, const StateArgs &a, int ways, hipStre
     return hipGetLastError();
 }
 
-template <class T, int NK>
+template <class T>
 hipError_t fwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
     const int slices = (a.Dv + kSlice - 1) / kSlice;
     if (p.split) {
-        const hipError_t e = part_launch<T, NK>(p, a, 1, st);
+        const hipError_t e = part_launch<T>(p, a, 1, st);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((gscan_state_fwd_kernel<T, NK>), dim3((unsigned)(p.units * a.H * slices)),
+    auto *k = a.Dk <= 64 ? gscan_state_fwd_kernel<T, 2>
+                         : a.Dk <= 96 ? gscan_state_fwd_kernel<T, 3> : gscan_state_fwd_kernel<T, 4>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(p.units * a.H * slices)),
                        dim3(2 * kSThreads), 0, st, a, slices, p.per, p.st_part);
     return hipGetLastError();
 }
@@ -2035,7 +2046,7 @@ hipError_t bwd_launch(const StatePlan &p, const StateArgs &a, hipStream_t st)
 {
     hipError_t e;
     if (p.split) {
-        e = part_launch<T, NK>(p, a, 2, st);
+        e = part_launch<T>(p, a, 2, st);
         if (e != hipSuccess) return e;
     }
     const PassWs o = {p.st_s, p.st_ds, p.down, parts_of(p)};
@@ -2137,8 +2148,7 @@ hipError_t launch_state_forward(const StatePlan &p, const StateArgs &args, hipSt
 {
     StateArgs a = args;
     a.chunks = p.chunks;
-    if (a.dtype) return p.nk == 2 ? fwd_launch<BF, 2>(p, a, st) : fwd_launch<BF, 4>(p, a, st);
-    return p.nk == 2 ? fwd_launch<FP, 2>(p, a, st) : fwd_launch<FP, 4>(p, a, st);
+    return a.dtype ? fwd_launch<BF>(p, a, st) : fwd_launch<FP>(p, a, st);
 }
 
 hipError_t launch_state_backward(const StatePlan &p, const StateArgs &args, hipStream_t st)
