@@ -1478,7 +1478,7 @@ __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
 // takes 130).
 //
 // Measured (bf16): 8 x 2048 tokens, 16 heads of 64 x 128: 130 us for 534 MB,
-// 4.1 TB/s, near what the memory gives (a large copy: 4.8); 15060 tokens, 16
+// 4.1 TB/s, near what the memory gives (a large copy: 4.8); 15233 tokens, 16
 // heads of 128 x 64 on 4 key heads: 112 us for 285 MB.  An item (a chunk of a
 // head) takes about 13000 cycles: into LDS 1700, scores 6000 (key wavefronts;
 // the others form dQ and dV's part of the state meanwhile), requests 1000 to 2000
@@ -2007,7 +2007,7 @@ Parts2 parts_of(const StatePlan &p)
     return Parts2{{p.st_part, p.st_part_r}, {p.st_dec, p.st_dec_r}};
 }
 
-// 32-wide units of the keys: three where they suffice (widths 72 to 96: 5100
+// 32-wide units of the keys: three where they suffice (widths 72 to 96: 4206
 // packed fp32 tokens, 12 heads of 96 x 80: 98 us, with four units 108), in the
 // kernels whose states nobody else reads.
 template <class T>
