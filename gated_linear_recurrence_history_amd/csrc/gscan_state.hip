@@ -560,7 +560,7 @@ struct Stage {
         for (int i = 0; i < N; ++i) {
             const int q = tid + TH * i, row = q / kPpr, col = q % kPpr * T::VE;
             const uint32_t at = (__umul24(row, st) + col) * (uint32_t)sizeof(typename T::S);
-            r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (row < left) & (col < cols) ? at : kNowhere, 0, 0);
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, ((row < left) & (col < cols)) ? at : kNowhere, 0, 0);
         }
     }
     template <class TL>

@@ -337,8 +337,10 @@ size_t gscan_backward_workspace_bytes(int64_t B, int64_t K, int64_t SH2, int64_t
  * the products inside a chunk of tokens and of the state with q (backward:
  * with the upstream gradient, v and k) take bf16 roundings of the decayed
  * scores and of the state; the state itself, the final state and the
- * gradient of the initial state are accumulated to fp32 accuracy.  Results
- * are bitwise reproducible.
+ * gradient of the initial state are accumulated to fp32 accuracy, and the part
+ * of dgate that states bring from other chunks is formed from 11 bits of them.
+ * Results are bitwise reproducible.  No output may overlap an input, but
+ * final_state initial_state.
  */
 typedef enum {
     GSCAN_GATE_SIGMOID = 0,
