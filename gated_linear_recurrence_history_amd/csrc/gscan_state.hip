@@ -1416,27 +1416,24 @@ gscan_state_pass_kernel(StateArgs a, int64_t per, PassWs o)
 // ---------------------------------------------------- backward: gradients
 
 // The operands of a state in LDS: operand (n, kk) at 64 (n NV + kk) lanes of
-// sixteen bytes (fp32: two planes).  Within an operand lane l sits at
-// `place(l)`, so that reading four keys of a value (the transposed operand)
-// meets fewer banks twice.
+// sixteen bytes (fp32: two planes), read as they are or, four keys of a value,
+// transposed.
 template <class T, int NV>
 struct States;
-
-__device__ __forceinline__ uint32_t place(uint32_t lane) { return lane ^ ((lane >> 4 & 1) << 2); }
 
 template <int NV>
 struct States<BF, NV> {
     // keys 16n + l16, values 32kk + {4g.., 16 + 4g..}
     static __device__ __forceinline__ u4 get(const u4 *t, int n, int kk, int lane)
     {
-        return t[(n * NV + kk) * 64 + place(lane)];
+        return t[(n * NV + kk) * 64 + lane];
     }
     // value 16m + l16, keys 32kk + {4g.., 16 + 4g..}
     static __device__ __forceinline__ u4 turned(const u4 *t, int m, int kk, int lane)
     {
         const uint32_t l16 = lane & 15, g = lane >> 4;
         const char *p = reinterpret_cast<const char *>(t) + (2 * kk * NV + m / 2) * 1024 + (m & 1) * 8 +
-                        place((l16 & 3) * 16 + 4 * g + (l16 >> 2)) * 16;
+                        ((l16 & 3) * 16 + 4 * g + (l16 >> 2)) * 16;
         const uint2 x = Tile<BF, 64>::tr(p), y = Tile<BF, 64>::tr(p + NV * 1024);
         return u4{x.x, x.y, y.x, y.y};
     }
@@ -1445,7 +1442,7 @@ template <int NV>
 struct States<FP, NV> {
     static __device__ __forceinline__ FP::Frag get(const u4 *t, int n, int kk, int lane)
     {
-        const f4 *p = reinterpret_cast<const f4 *>(t) + (n * NV + kk) * 128 + place(lane);
+        const f4 *p = reinterpret_cast<const f4 *>(t) + (n * NV + kk) * 128 + lane;
         return FP::Frag{p[0], p[64]};
     }
     static __device__ __forceinline__ FP::Frag turned(const u4 *t, int m, int kk, int lane)
@@ -1455,7 +1452,7 @@ struct States<FP, NV> {
         FP::Frag f;
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t at = place((l16 >> 2) * 16 + 4 * g + j) * 4;
+            const uint32_t at = ((l16 >> 2) * 16 + 4 * g + j) * 4;
             f.a[j] = p[at];
             f.b[j] = p[at + NV * 512];
         }
@@ -1652,7 +1649,7 @@ gscan_state_grad_kernel(StateArgs a, uint32_t units, uint32_t per, PassWs o)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int q = tid + kGThreads * i;
-            to[(q & ~63) + place(q & 63)] = get_state(r[i], factor(i, from), T());
+            to[q] = get_state(r[i], factor(i, from), T());
         }
     };
     auto clear = [&] {
