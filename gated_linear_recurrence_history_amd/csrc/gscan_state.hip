@@ -883,15 +883,15 @@ __device__ __forceinline__ void add_decayed(f4 (&st)[2 * NX], const F (&y)[T::C 
 // two steps a chunk with a barrier after each; tiles and scores are kept
 // twice, decays three times.  (All of it in turn by the same four wavefronts took 3 us a
 // chunk, one workgroup per CU, most of it waiting.)  Workgroups that share
-// queries and keys sit in one XCD (neighbours): 65 -> 61 us in the case below.
+// queries and keys sit in one XCD (neighbours): 65 -> 61 us in the case below when it was added.
 //
 // Measured (bf16): 8 sequences of 2048 tokens, 16 heads of 64 x 128, one walk per
-// CU: 61 us, 3.3 TB/s of the 200 MB to be moved; a chunk takes 3200 cycles (keys
-// of 128: 4700), and 18000 pass before a walk's first (its loads, of all CUs at
+// CU: 57 us, 3.6 TB/s of the 206 MB to be moved; a chunk takes 3100 cycles (keys
+// of 128: 4500), and 18000 pass before a walk's first (its loads, of all CUs at
 // once, come at the memory's rate).  The two steps of a chunk are bound about
 // equally by the bringing side (rows into LDS 700 to 1100 cycles, requests 300 to
 // 1700, scores 1500 to 2400) and the finishing side (outputs 1250 to 2400, state
-// 1500 to 2000); LDS is busy about 45 per cent of the time, the matrix units 30.
+// 1500 to 2000); LDS is busy 38 per cent of the time, the matrix units 19.
 // fp32: 16x16x4 products are half of a chunk's time.
 //
 // Wavefront w < 4 keeps columns 16w .. 16w+15 of every row of the state in
@@ -1151,8 +1151,8 @@ struct PassJob {
 // Wavefronts 4-7 bring the next chunk's rows and decays into LDS while
 // wavefronts 0-3 add this one's, one barrier a chunk.  Measured (bf16): the two
 // walks of 8 x 2048 tokens, 16 heads of 64 x 128, move 334 MB (half of it the
-// stored states) in 60 us, 5.6 TB/s, which is all there is; without storing,
-// 32771 tokens of 16 heads of 128 x 64 in 256 walks take 42 us, 1.3 us a chunk,
+// stored states) in 61 us, 5.5 TB/s, which is all there is; without storing,
+// 32771 tokens of 16 heads of 128 x 64 in 256 walks take 40 us, 1.2 us a chunk,
 // bound by the products (three bf16 parts) and the chain of the decays.  The decays, a long chain
 // of short steps, are formed by the last two in turn, each over two chunks: the
 // sum of log gates in one, the exponentials in the next.
@@ -1486,15 +1486,15 @@ __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
 // registers in a fixed order.  The rows and state operands of the next head,
 // or of the next chunk's first, are requested while this one is computed
 // (one workgroup per chunk, which waits for its own, took 192 us where this
-// takes 130).
+// takes 125).
 //
-// Measured (bf16): 8 x 2048 tokens, 16 heads of 64 x 128: 130 us for 534 MB,
-// 4.1 TB/s, near what the memory gives (a large copy: 4.8); 15233 tokens, 16
-// heads of 128 x 64 on 4 key heads: 112 us for 285 MB.  An item (a chunk of a
+// Measured (bf16): 8 x 2048 tokens, 16 heads of 64 x 128: 125 us for 481 MB (by
+// the counters), 3.8 TB/s, near what the memory gives (a large copy: 4.8); 15233 tokens, 16
+// heads of 128 x 64 on 4 key heads: 110 us for 289 MB.  An item (a chunk of a
 // head) takes about 13000 cycles: into LDS 1700, scores 6000 (key wavefronts;
 // the others form dQ and dV's part of the state meanwhile), requests 1000 to 2000
-// (as fast as the memory takes them), dK or dV 2400.  LDS moves 620 KB in it, 37
-// per cent of its time.
+// (as fast as the memory takes them), dK or dV 2400.  LDS moves 620 KB in it and
+// is busy 36 to 39 per cent of the time, the matrix units 12.
 //
 // Eight wavefronts: `rt` owns token rows 16rt .. 16rt+15, half of them dQ and
 // half dK, each half of dV (and, fp32 with its two rows of tiles, each every
@@ -2094,7 +2094,7 @@ hipError_t bwd_widths(const StatePlan &p, const StateArgs &a, hipStream_t st)
 // division of least cost is 2 per cent off the fastest on average, 16 at most.
 // 24000 bf16 tokens, 8 heads of 64 x 64: unsplit 555 us, 4 chunks per unit 70,
 // 12 (chosen) 49, 48 123; 8 sequences of 2048, 16 heads of 64 x 128: unsplit
-// (chosen) 66 us, split 99 and more.
+// (chosen) 66 us, split 99 and more (all figures of one build).
 StatePlan make_state_plan(const StateArgs &a, bool backward)
 {
     StatePlan p;
