@@ -165,7 +165,9 @@ __device__ __forceinline__ Vec turn(const Vec &x, const float2 *cs, const Place 
 }
 
 // Rows of a workgroup: row r of its tokens is head r - t heads of token t =
-// r / heads (by the multiplier ceil(2^32 / heads), exact for r heads < 2^32).
+// r / heads = floor(2 r inv / 2^32) with inv = ceil(2^31 / heads), which fits 32
+// bits for one head too and is exact for r heads < 2^31 (r is below 2048 where a
+// workgroup has more than one token).  inv 0: one token.
 struct Row {
     int t, which, h;
     bool ok;
@@ -176,7 +178,7 @@ __device__ __forceinline__ Row row_of(const NormArgs &a, int row, int rows, int 
     Row r;
     r.ok = row < rows && in;
     row = row < rows ? row : 0;
-    r.t = inv ? (int)__umulhi((uint32_t)row, inv) : 0;
+    r.t = inv ? (int)__umulhi(2u * (uint32_t)row, inv) : 0;
     const int hh = row - r.t * heads;
     r.which = hh >= a.heads[0];
     r.h = hh - r.which * a.heads[0];
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(1024) gscan_norm_dw_kernel(const float *part, 
 
 struct NormGeom {
     int lpr, tpb;
-    uint32_t inv;  // ceil(2^32 / heads), 0 where a workgroup has one token
+    uint32_t inv;  // ceil(2^31 / heads), 0 where a workgroup has one token
     int64_t blocks;
 };
 
@@ -366,7 +368,7 @@ NormGeom geom(int64_t tokens, int heads, int D)
             g.tpb = t;
         }
     }
-    g.inv = g.tpb > 1 ? (uint32_t)((0x100000000ull + heads - 1) / heads) : 0u;
+    g.inv = g.tpb > 1 ? (uint32_t)((0x80000000ull + heads - 1) / heads) : 0u;
     g.blocks = (tokens + g.tpb - 1) / g.tpb;
     return g;
 }
