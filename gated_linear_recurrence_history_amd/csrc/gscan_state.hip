@@ -1032,7 +1032,10 @@ gscan_state_fwd_kernel(StateArgs a, int slices, int64_t per, size_t st_part)
     const int col = w * 16 + l16;
     const int64_t srow = ((int64_t)un.seq * a.H + h) * a.Dk;
     const float *init = a.s0 ? a.s0 + srow * a.Dv : nullptr;
-    if (un.part)
+    // A divided sequence begins from the workspace in its first part too, where the
+    // join has put the initial state: its last part, another workgroup of this
+    // launch, may write the final state over that one.
+    if (un.parts > 1)
         init = reinterpret_cast<const float *>(reinterpret_cast<const char *>(a.ws) + st_part) +
                (unit * a.H + h) * a.Dk * a.Dv;
     f4 st[2 * NK];
