@@ -46,7 +46,10 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
       "parts"   (YaRN, Peng et al. 2023) pairs that turn more than beta_fast
                 times over the original length keep their frequency, those
                 below beta_slow turns are divided by factor, a linear ramp
-                over the pair index between; magnitude 0.1 ln(factor) + 1.
+                over the pair index between, from whole pair indexes outwards
+                (the lower at least 0, the upper at most rot - 1 and so beyond
+                the last pair where that turns more than beta_slow times);
+                magnitude 0.1 ln(factor) + 1.
     """
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and at least 2, got {rot}")
@@ -65,7 +68,7 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
         def pair(turns):  # the (real) index of the pair with this many turns
             return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
         low = max(math.floor(pair(beta_fast)), 0)
-        high = min(math.ceil(pair(beta_slow)), rot // 2 - 1)
+        high = min(math.ceil(pair(beta_slow)), rot - 1)
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
         freq = freq / factor * ramp + freq * (1.0 - ramp)
         magnitude = 0.1 * math.log(factor) + 1.0
