@@ -309,7 +309,8 @@ def _readable(g, like):
     g = g.to(like.dtype)
     fits = _reads_rows(*_layout(g)) and g.data_ptr() % 16 == 0 and all(
         s * g.element_size() % 16 == 0 for s in _outer_strides(*_layout(g))[:-1])
-    return g if fits else g.contiguous()
+    # (contiguous() would return a dense tensor that begins on no 16 bytes)
+    return g if fits else g.clone(memory_format=torch.contiguous_format)
 
 
 class StateScanFunction(torch.autograd.Function):
