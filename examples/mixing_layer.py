@@ -41,7 +41,8 @@ class MixingLayer(torch.nn.Module):
 
     def _operands(self, x, positions):
         """x [tokens, width] -> q, k (normed, rotated), v, gate: the latter two
-        are slices of the projection's output, read in place."""
+        are slices of the projection's output, read in place (copied where its
+        rows, gates included, are no multiple of 16 bytes)."""
         heads, key_heads, dk, dv = self.shape
         q, k, v, gate = self.proj(x).split(self.parts, dim=-1)
         q, k = gs.qk_norm_rope(q.unflatten(-1, (key_heads, dk)), k.unflatten(-1, (key_heads, dk)),

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libgscan.so")
 
 GSCAN_F32 = 0
 GSCAN_BF16 = 1
+GSCAN_ERR_MISALIGNED = 3
 
 _lib = None
 

@@ -19,7 +19,9 @@ range).  Hk divides H: head h uses q and k of head h // (H // Hk).  Dk and Dv
 are multiples of 8 up to 128.  q, k, v share a type, float32 or bfloat16; the
 gate may have either; states are float32 [sequences, H, Dk, Dv].  The last
 dimension is contiguous, the others may have any stride of 16 bytes'
-multiple, such as a slice of a fused projection's output has.
+multiple, such as a slice of a fused projection's output has (the gate: any
+stride).  `state_scan` and `state_scan_step` copy q, k or v whose rows are not
+16-byte aligned; the two calls under `state_scan` refuse them.
 """
 from __future__ import annotations
 
@@ -283,7 +285,8 @@ def state_scan_step(q, k, v, gate, state, slots=None, scale: float = 1.0,
     updates state[slots[n]] (float32 [pool, H, Dk, Dv]) in place and returns
     the outputs [N, H, Dv] in the type of v.  `slots`: int32 [N], none twice;
     one outside the pool is padding (nothing is updated, its output is zero).
-    Without slots request n uses state n.
+    Without slots request n uses state n.  q, k, v whose rows are not 16-byte
+    aligned are copied.
     """
     d = _describe(q, k, v, gate, scale, gate_form, gate_shift, None, single=True)
     dev = q.device
@@ -298,9 +301,15 @@ def state_scan_step(q, k, v, gate, state, slots=None, scale: float = 1.0,
         if out is None:
             out = _empty(v)
         if d.B:
-            binding._check(binding.lib().gscan_state_scan_step(
+            status = binding.lib().gscan_state_scan_step(
                 ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
-                state.data_ptr(), state.shape[0], _ptr(slots), out.data_ptr(), s))
+                state.data_ptr(), state.shape[0], _ptr(slots), out.data_ptr(), s)
+            if status == binding.GSCAN_ERR_MISALIGNED:  # nothing was enqueued
+                rows = _readable_rows(q, k, v)
+                if any(x is not y for x, y in zip(rows, (q, k, v))):
+                    return state_scan_step(*rows, gate, state, slots, scale, gate_form, gate_shift, out,
+                                           stream)
+            binding._check(status)
     return out
 
 
@@ -313,6 +322,11 @@ def _readable(g, like):
     return g if fits else g.clone(memory_format=torch.contiguous_format)
 
 
+def _readable_rows(*operands):
+    """The same of inputs; what is no tensor is left to the checks."""
+    return [_readable(x, x) if isinstance(x, torch.Tensor) else x for x in operands]
+
+
 class StateScanFunction(torch.autograd.Function):
     """(out, final state) of the matrix-state scan; the backward replays the
     forward from the saved inputs, so nothing else is kept in between."""
@@ -320,6 +334,7 @@ class StateScanFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, gate, initial_state, scale, gate_form, gate_shift, seq_offsets):
         ctx.set_materialize_grads(False)
+        q, k, v = _readable_rows(q, k, v)
         ctx.save_for_backward(q, k, v, gate, initial_state, seq_offsets)
         ctx.args = (float(scale), gate_form, float(gate_shift))
         return state_scan_forward(q, k, v, gate, *ctx.args, seq_offsets, initial_state, True)
@@ -340,6 +355,7 @@ class StateScanFunction(torch.autograd.Function):
 
 def state_scan(q, k, v, gate, initial_state=None, scale: float = 1.0, gate_form: str = "sigmoid",
                gate_shift: float = 0.0, seq_offsets=None):
-    """Differentiable scan: (out, final state); see state_scan_forward."""
+    """Differentiable scan: (out, final state); see state_scan_forward.  q, k, v
+    that the library cannot read as they are, are copied."""
     return StateScanFunction.apply(q, k, v, gate, initial_state, scale, gate_form, gate_shift,
                                    seq_offsets)

@@ -18,7 +18,7 @@ from torch.autograd.function import once_differentiable
 
 from . import binding
 from .matrix_state import (_CODES, _On, _check_dense, _empty, _layout, _on_device, _outer_strides, _ptr,
-                           _readable, _reads_rows, _workspace)
+                           _readable, _readable_rows, _reads_rows, _workspace)
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 _i64x2 = ctypes.c_int64 * 2
@@ -200,6 +200,7 @@ class QkNormRopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, weight_q, weight_k, positions, freq, eps, layout, magnitude):
         ctx.set_materialize_grads(False)
+        q, k = _readable_rows(q, k)
         ctx.save_for_backward(q, k, weight_q, weight_k, positions, freq)
         ctx.args = (float(eps), layout, float(magnitude))
         return qk_norm_rope_forward(q, k, weight_q, weight_k, positions, freq, *ctx.args)
@@ -224,5 +225,6 @@ class QkNormRopeFunction(torch.autograd.Function):
 
 def qk_norm_rope(q, k, weight_q, weight_k, positions, freq, eps: float = 1e-6,
                  layout: str = "half", magnitude: float = 1.0):
-    """Differentiable (q', k'); see qk_norm_rope_forward."""
+    """Differentiable (q', k'); see qk_norm_rope_forward.  q and k whose rows are
+    not 16-byte aligned are copied."""
     return QkNormRopeFunction.apply(q, k, weight_q, weight_k, positions, freq, eps, layout, magnitude)
