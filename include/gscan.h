@@ -330,8 +330,11 @@ size_t gscan_backward_workspace_bytes(int64_t B, int64_t K, int64_t SH2, int64_t
  * Non-finite inputs reach what they reach in the recurrence and nothing else:
  * an Inf or NaN of v leaves NaN in its column of the outputs of its own and
  * later tokens of its sequence and head and of the state, not in earlier
- * ones (backward: likewise, in the other direction).  A gate of exactly zero (GSCAN_GATE_LOG: minus
- * infinity) forgets the state.  Log gates below -1000 count as -1000.
+ * ones (backward: likewise, in the other direction).  One exception: a NaN
+ * gate (GSCAN_GATE_LOG: or one of plus infinity) leaves NaN in the gradients of
+ * k and v of up to 63 later tokens too, which the recurrence would not reach.
+ * A gate of exactly zero (GSCAN_GATE_LOG: minus infinity) forgets the state.
+ * Log gates below -1000 count as -1000.
  *
  * Accuracy.  Sums, gates and states are fp32 or better.  With bf16 operands
  * the products inside a chunk of tokens and of the state with q (backward:
