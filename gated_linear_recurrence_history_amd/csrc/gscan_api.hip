@@ -218,6 +218,7 @@ bool strides16(const int64_t *s, int n, int dtype)
 constexpr int64_t kMaxTokens = 2147483647 - 128;
 constexpr int64_t kMaxGrid = 2147483647;
 constexpr int64_t kMaxHeads = 16384;        // a chunk's outputs stay below 2 GiB
+constexpr int64_t kMaxNormHeads = 1 << 20;
 constexpr int64_t kMaxStride = 1 << 23;     // and so do a chunk's rows of an operand
 
 // Sizes, types and strides of a scan (and of a step, which is a scan of one
@@ -343,8 +344,8 @@ int check_norm(const gscan_qk_norm_t *d, const void *q, const void *k, const flo
                     "need tokens, Hk, rot >= 0, Hq, D >= 1, eps > 0 (tokens=%lld Hq=%lld Hk=%lld "
                     "D=%lld rot=%lld eps=%g)", (long long)d->tokens, (long long)d->Hq,
                     (long long)d->Hk, (long long)d->D, (long long)d->rot, (double)d->eps);
-    if (d->D % 8 || d->D > 256 || d->rot % 8 || d->rot > d->D || d->Hq > (1 << 20) ||
-        d->Hk > (1 << 20) || d->tokens > kMaxTokens)
+    if (d->D % 8 || d->D > 256 || d->rot % 8 || d->rot > d->D || d->Hq > kMaxNormHeads ||
+        d->Hk > kMaxNormHeads || d->tokens > kMaxTokens)
         return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
                     "unsupported shape tokens=%lld Hq=%lld Hk=%lld D=%lld rot=%lld (need D a "
                     "multiple of 8 up to 256, rot a multiple of 8 up to D, at most 2^20 heads)",
@@ -937,7 +938,7 @@ int gscan_qk_norm_rope_backward(const gscan_qk_norm_t *desc, const void *q, cons
     a.dw[0] = d_weight_q;
     a.dw[1] = d_weight_k;
     const bool weights = d_weight_q || d_weight_k;
-    const size_t need = weights ? gscan::norm_workspace_bytes(a.tokens, a.D) : 0;
+    const size_t need = weights ? gscan::norm_workspace_bytes(a.tokens, a.heads[0] + a.heads[1], a.D) : 0;
     return with_workspace("query/key norm backward", weights ? workspace : nullptr, workspace_bytes,
                           need, stream, [&](void *ws) {
                               a.ws = ws;
@@ -947,8 +948,10 @@ int gscan_qk_norm_rope_backward(const gscan_qk_norm_t *desc, const void *q, cons
 
 size_t gscan_qk_norm_rope_workspace_bytes(const gscan_qk_norm_t *desc)
 {
-    if (!desc || desc->tokens < 0 || desc->D < 1 || desc->D > 256) return 0;
-    return gscan::norm_workspace_bytes(desc->tokens, (int)desc->D);
+    if (!desc || desc->tokens < 0 || desc->D < 1 || desc->D > 256 || desc->Hq < 1 || desc->Hk < 0 ||
+        desc->Hq > kMaxNormHeads || desc->Hk > kMaxNormHeads)
+        return 0;
+    return gscan::norm_workspace_bytes(desc->tokens, (int)(desc->Hq + desc->Hk), (int)desc->D);
 }
 
 const char *gscan_status_string(int status)

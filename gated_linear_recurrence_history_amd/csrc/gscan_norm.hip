@@ -349,8 +349,9 @@ struct NormGeom {
     int64_t blocks;
 };
 
-// Tokens per workgroup: as many as fill the lane groups' batches best, up to
-// two batches.
+// Tokens per workgroup: the fewest that come within 2 per cent of filling the
+// lane groups' batches best, up to two batches.  (Relative: few narrow heads fill
+// little of a workgroup even together.)
 NormGeom geom(int64_t tokens, int heads, int D)
 {
     NormGeom g;
@@ -363,7 +364,7 @@ NormGeom geom(int64_t tokens, int heads, int D)
         const int64_t rows = t * (int64_t)heads;
         const double use = (double)rows / (double)((rows + rpp - 1) / rpp * rpp) *
                            (rows < full ? (double)rows / full : 1.0);
-        if (use > best + 0.02) {
+        if (use > best * 1.02) {
             best = use;
             g.tpb = t;
         }
@@ -377,10 +378,11 @@ int64_t bwd_grid(int64_t blocks) { return blocks < kNMaxGrid ? blocks : kNMaxGri
 
 }  // namespace
 
-// Enough for either layout: the grid is at most kNMaxGrid and the tokens.
-size_t norm_workspace_bytes(int64_t tokens, int D)
+// A partial of both weights' gradients per workgroup.
+size_t norm_workspace_bytes(int64_t tokens, int heads, int D)
 {
-    return (size_t)(tokens > 0 ? bwd_grid(tokens) : 1) * 2u * (size_t)D * sizeof(float);
+    const int64_t n = bwd_grid(geom(tokens, heads, D).blocks);
+    return (size_t)(n > 0 ? n : 1) * 2u * (size_t)D * sizeof(float);
 }
 
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t st)

@@ -85,7 +85,7 @@ struct NormArgs {
     float eps = 0.f, magnitude = 1.f;
     void *ws = nullptr;
 };
-size_t norm_workspace_bytes(int64_t tokens, int D);
+size_t norm_workspace_bytes(int64_t tokens, int heads, int D);
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs &a, hipStream_t stream);
 
