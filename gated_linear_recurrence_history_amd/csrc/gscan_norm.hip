@@ -20,10 +20,13 @@
 // dw: every workgroup keeps its sums in registers over its tokens and leaves
 // one partial, which a second kernel adds in a fixed order in fp64.
 // Rows are requested a few at a time as raw words, before the angles are formed
-// (one at a time: 88 us where this takes 78; four as fp32: 106, for fewer
-// wavefronts fit).  Measured: forward, 16384 tokens, 40 bf16 heads of 128: 336 MB
-// in 75 us, 4.5 TB/s (a large copy: 4.8); backward, 8191 tokens, 32 fp32 heads of
-// 80: 252 MB in 46 us and 7 us for the 1024 partials of dw; one token: 4 us.
+// (one at a time: 88 us where this takes 81; four bf16 rows widened to fp32 as they
+// come: 106, for fewer wavefronts fit).  Measured (a profiler's means over 40 calls):
+// forward, 16384 tokens, 40 bf16 heads of 128: 336 MB in 81 us, 4.1 TB/s (a large
+// copy: 4.8; a whole call without the profiler, caches cold: 75 us); 8192 tokens in
+// fp32: 70; backward, 8191 tokens, 32 fp32 heads of 80: 252 MB in 46 us and 7 us for
+// the 1024 partials of dw; the 16384 tokens in bf16: 503 MB in 122 and 8; one token:
+// 4 us.
 #include <type_traits>
 
 #include "gscan_state_dev.h"
@@ -351,7 +354,8 @@ struct NormGeom {
 
 // Tokens per workgroup: the fewest that come within 2 per cent of filling the
 // lane groups' batches best, up to two batches.  (Relative: few narrow heads fill
-// little of a workgroup even together.)
+// little of a workgroup even together; 32768 tokens of 2 bf16 heads of 32 take 15
+// us, with a workgroup per token 82.)
 NormGeom geom(int64_t tokens, int heads, int D)
 {
     NormGeom g;

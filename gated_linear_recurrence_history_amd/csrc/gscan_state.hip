@@ -94,7 +94,7 @@ __device__ __forceinline__ f4 mma(const FP::Frag &a, const FP::Frag &b, f4 c)
 // touches, and the first (second) halves of eight 16-byte pieces each of two
 // neighbouring rows that are stored together on different banks (32 of 4
 // bytes; without the "^ r" such stores took each bank twice, and the
-// scan of 32771 tokens 125 us where it takes 120).  fp32 rows are 16 bytes
+// scan of 32771 tokens 125 us where it then took 120).  fp32 rows are 16 bytes
 // longer than their elements, which does the same for both reads.
 //
 // Per lane: byte offsets of the pieces it reads along a row (r[c]: elements
@@ -885,14 +885,18 @@ __device__ __forceinline__ void add_decayed(f4 (&st)[2 * NX], const F (&y)[T::C 
 // chunk, one workgroup per CU, most of it waiting.)  Workgroups that share
 // queries and keys sit in one XCD (neighbours): 65 -> 61 us in the case below when it was added.
 //
-// Measured (bf16): 8 sequences of 2048 tokens, 16 heads of 64 x 128, one walk per
+// Measured (bf16; times here and below are a profiler's means over 40 calls on
+// the same inputs): 8 sequences of 2048 tokens, 16 heads of 64 x 128, one walk per
 // CU: 57 us, 3.6 TB/s of the 206 MB to be moved; a chunk takes 3100 cycles (keys
 // of 128: 4500), and 18000 pass before a walk's first (its loads, of all CUs at
 // once, come at the memory's rate).  The two steps of a chunk are bound about
 // equally by the bringing side (rows into LDS 700 to 1100 cycles, requests 300 to
 // 1700, scores 1500 to 2400) and the finishing side (outputs 1250 to 2400, state
 // 1500 to 2000); LDS is busy 38 per cent of the time, the matrix units 19.
-// fp32: 16x16x4 products are half of a chunk's time.
+// One workgroup per CU fits: 154 registers at keys of 64 (73 KB of LDS would leave
+// room for two), 248 and 106 KB at keys of 128.  fp32: 16x16x4 products are half of
+// a chunk's time; every slice of 64 value columns stages queries and keys and forms
+// the scores again.
 //
 // Wavefront w < 4 keeps columns 16w .. 16w+15 of every row of the state in
 // accumulators, which are operands of S^T Q^T as they are.  The ten (three)
@@ -1153,9 +1157,9 @@ struct PassJob {
 
 // Wavefronts 4-7 bring the next chunk's rows and decays into LDS while
 // wavefronts 0-3 add this one's, one barrier a chunk.  Measured (bf16): the two
-// walks of 8 x 2048 tokens, 16 heads of 64 x 128, move 334 MB (half of it the
-// stored states) in 61 us, 5.5 TB/s, which is all there is; without storing,
-// 32771 tokens of 16 heads of 128 x 64 in 256 walks take 40 us, 1.2 us a chunk,
+// walks of 8 x 2048 tokens, 16 heads of 64 x 128, move 344 MB (134 of it the
+// stored states) in 67 us, 5.1 TB/s, which is all there is; without storing,
+// 32771 tokens of 16 heads of 128 x 64 in 256 walks take 43 us, 1.3 us a chunk,
 // bound by the products (three bf16 parts) and the chain of the decays.  The decays, a long chain
 // of short steps, are formed by the last two in turn, each over two chunks: the
 // sum of log gates in one, the exponentials in the next.
@@ -1313,7 +1317,7 @@ gscan_state_part_kernel(StateArgs a, int slices, int ways, int64_t per, Parts2 o
 // Joins the units of split sequences: in place, what each adds becomes the
 // state it begins with (backwards: the gradient of the state it ends with).
 // Four elements per thread, the units of a sequence in turn, eight requested at a
-// time: 5.7 us for 16 units of 16 heads of 128 x 64 (16 MB), most of it latency.
+// time: 5.8 us for 16 units of 16 heads of 128 x 64 (16 MB), most of it latency.
 __global__ void __launch_bounds__(kSThreads)
 gscan_state_join_kernel(StateArgs a, int ways, int64_t per, Parts2 o)
 {
@@ -1489,11 +1493,16 @@ __device__ __forceinline__ float dot16(const u4 &x, const u4 &y, const FP &)
 // registers in a fixed order.  The rows and state operands of the next head,
 // or of the next chunk's first, are requested while this one is computed
 // (one workgroup per chunk, which waits for its own, took 192 us where this
-// takes 125).
+// took 125 at its fastest).
 //
-// Measured (bf16): 8 x 2048 tokens, 16 heads of 64 x 128: 125 us for 481 MB (by
-// the counters), 3.8 TB/s, near what the memory gives (a large copy: 4.8); 15233 tokens, 16
-// heads of 128 x 64 on 4 key heads: 110 us for 289 MB.  An item (a chunk of a
+// Measured (bf16): 8 x 2048 tokens, 16 heads of 64 x 128: 144 us (the fastest call:
+// 125) for 481 MB (by the counters), 3.3 TB/s (a large copy: 4.8); 15233 tokens, 16
+// heads of 128 x 64 on 4 key heads: 116 us for 289 MB.  Where chunks times key heads
+// are few, CUs idle: one sequence of 2048, 16 heads of 64 x 64 takes 18 us on 16 key
+// heads, 24 on 4 and 72 on one, whose 32 workgroups take 16 heads in turn.  Of the
+// scores, dO V^T is formed by the query and by the key wavefronts, and all three
+// products in all 16 tiles of 16 x 16 (ten are on or below the diagonal).  100 to 114
+// scalar registers live in lanes of vector ones.  An item (a chunk of a
 // head) takes about 13000 cycles: into LDS 1700, scores 6000 (key wavefronts;
 // the others form dQ and dV's part of the state meanwhile), requests 1000 to 2000
 // (as fast as the memory takes them), dK or dV 2400.  LDS moves 620 KB in it and
@@ -2092,9 +2101,13 @@ hipError_t bwd_widths(const StatePlan &p, const StateArgs &a, hipStream_t st)
 // states, which are written and read; all of this once per direction; three for
 // the launches.  Unsplit there are only the rounds, a chunk each.  Of a packed
 // batch the host does not know the lengths: it counts as one sequence there, and
-// its rounds by their sum.  Over 229 measured cases (1 to 8 sequences of 300 to
-// 32771 tokens, 5 to 32 heads, both types and directions, 17 divisions each) the
-// division of least cost is 2 per cent off the fastest on average, 16 at most.
+// its rounds by their sum.  Over the 229 cases it was fitted to (1 to 8 sequences
+// of 300 to 32771 tokens, 5 to 32 heads, both types and directions, 17 divisions
+// each) the division of least cost was 2 per cent off the fastest on average, 16 at
+// most; the walks have become up to a tenth faster since and the rule was kept.
+// Many short packed sequences are planned like one long one: then the units' pass
+// finds nothing to do (72 sequences of 64 to 192 tokens, 8 heads of 64 x 64: 5 us and
+// 4 for the join, beside 29 for the scan).
 // 24000 bf16 tokens, 8 heads of 64 x 64: unsplit 555 us, 4 chunks per unit 70,
 // 12 (chosen) 49, 48 123; 8 sequences of 2048, 16 heads of 64 x 128: unsplit
 // (chosen) 66 us, split 99 and more (all figures of one build).

@@ -6,8 +6,9 @@
 // the kernel is a stream: one workgroup per request and head, sixteen bytes
 // per thread and row of S, up to eight rows of a thread in flight.  The sum
 // over Dk of o is kept per thread and joined in LDS in a fixed order.
-// Measured: 250 requests, 32 heads of 128 x 64: 524 MB in 112 us, 4.7 TB/s (a
-// large copy: 4.8); one request, 16 heads of 64 x 64: 5 us, launch and latency.
+// Measured: 250 requests, 32 heads of 128 x 64: 524 MB in 112 us a call with cold
+// caches, 4.7 TB/s (a large copy: 4.8), 85 us on the same states again; one
+// request, 16 heads of 64 x 64: 5 us, launch and latency.
 // Arithmetic is fp32; only o is rounded to the type of v.
 #include "gscan_state_dev.h"
 
