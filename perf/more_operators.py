@@ -9,7 +9,8 @@ A case is a dict with a "kind":
   dembed  embed_backward: the table's gradient
   gate    gated_projection_forward: act(x Wg^T) * (x Wu^T)
   dgate   gated_projection_backward: gradients of x and both weights
-  loss    linear_cross_entropy_forward: losses and log-sums of h W^T
+  loss    linear_cross_entropy_forward: losses and log-sums of h W^T, of the
+          tokens that count (zero for the others)
   dloss   linear_cross_entropy_backward: gradients of h and W
 """
 import math
@@ -224,7 +225,7 @@ def run(s):
     if kind == "loss":
         lse = _plain_lse(z)
         loss = torch.where(live, lse - torch.gather(z, 1, at)[:, 0], torch.zeros_like(lse))
-        return _plain_reduce(loss, live, case["reduction"]), lse
+        return _plain_reduce(loss, live, case["reduction"]), torch.where(live, lse, torch.zeros_like(lse))
     up = s["up"] / live.sum().clamp(min=1) if case["reduction"] == "mean" else s["up"]
     up = torch.where(live, up.expand(len(h)), torch.zeros_like(s["lse"]))[:, None]
     g = torch.exp(z - s["lse"][:, None])
@@ -269,7 +270,7 @@ def exact(case, seed):
         logp = torch.log_softmax(rows @ w.T, -1)
         if kind == "loss":
             losses.append(torch.nn.functional.nll_loss(logp, t, ignore_index=-100, reduction="none"))
-            lses.append(torch.logsumexp(rows @ w.T, -1))
+            lses.append(torch.logsumexp(rows @ w.T, -1).masked_fill(t == -100, 0.0))
             continue
         p = logp.exp()
         known = torch.nonzero(t != -100)[:, 0]
@@ -310,9 +311,8 @@ def work(case):
             return {"bytes": e * (n * D + 2 * F * D + n * F), "flops": 4 * n * D * F}
         # x, weights, upstream gradient read, three gradients written; two products replayed, four more
         return {"bytes": e * (2 * n * D + 4 * F * D + n * F), "flops": 12 * n * D * F}
-    V = case["vocabulary"]
+    V, live = case["vocabulary"], int(n * (1 - case["ignored"]))  # the tokens that count
     if kind == "loss":
-        return {"bytes": e * (n * D + V * D) + 16 * n, "flops": 2 * n * D * V}
-    # the logits again, and a product for each gradient, of the tokens that count
-    live = int(n * (1 - case["ignored"]))
+        return {"bytes": e * (live * D + V * D) + 16 * n, "flops": 2 * live * D * V}
+    # the logits again, and a product for each gradient
     return {"bytes": e * (live * D + n * D + 2 * V * D) + 16 * n, "flops": 6 * live * D * V}
