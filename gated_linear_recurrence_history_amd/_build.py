@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 
 HIP_SOURCES = ["gscan_kernels.hip", "gscan_generic.hip", "gscan_colsum.hip", "gscan_cifg.hip",
-               "gscan_state.hip", "gscan_step.hip", "gscan_norm.hip", "gscan_api.hip"]
+               "gscan_state.hip", "gscan_step.hip", "gscan_norm.hip", "gscan_embed.hip",
+               "gscan_gate.hip", "gscan_xent.hip", "gscan_api.hip"]
 
 
 def _hipcc() -> str:

@@ -94,6 +94,23 @@ def lib():
         L.gscan_qk_norm_rope_forward.restype = ctypes.c_int
         L.gscan_qk_norm_rope_backward.argtypes = [vp] * 14 + [sz, vp]
         L.gscan_qk_norm_rope_backward.restype = ctypes.c_int
+        L.gscan_embed_forward.argtypes = [vp] * 5
+        L.gscan_embed_forward.restype = ctypes.c_int
+        L.gscan_embed_backward.argtypes = [vp] * 5 + [sz, vp]
+        L.gscan_embed_backward.restype = ctypes.c_int
+        L.gscan_embed_workspace_bytes.argtypes = [vp]
+        L.gscan_embed_workspace_bytes.restype = sz
+        for f, n, ws in ((L.gscan_gated_projection_forward, 5, False),
+                         (L.gscan_gated_projection_backward, 8, True),
+                         (L.gscan_linear_cross_entropy_forward, 6, True),
+                         (L.gscan_linear_cross_entropy_backward, 8, True)):
+            f.argtypes = [vp] * n + ([vp, sz] if ws else []) + [vp]
+            f.restype = ctypes.c_int
+        for f in (L.gscan_gated_projection_workspace_bytes,
+                  L.gscan_linear_cross_entropy_forward_workspace_bytes,
+                  L.gscan_linear_cross_entropy_backward_workspace_bytes):
+            f.argtypes = [vp]
+            f.restype = sz
         L.gscan_status_string.argtypes = [ctypes.c_int]
         L.gscan_status_string.restype = ctypes.c_char_p
         L.gscan_last_error.argtypes = []

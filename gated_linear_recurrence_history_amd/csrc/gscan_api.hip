@@ -13,6 +13,7 @@
 #include "gscan.h"
 #include "gscan_internal.h"
 #include "gscan_state.h"
+#include "gscan_lm.h"
 
 namespace {
 
@@ -329,6 +330,126 @@ int with_workspace(const char *what, void *ws, size_t ws_bytes, size_t need, hip
     }
     if (e != hipSuccess) return fail(GSCAN_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
     g_last_error[0] = '\0';
+    return GSCAN_OK;
+}
+
+constexpr int64_t kMaxWidth = 65536;        // of the embedding and what follows
+constexpr int64_t kMaxRowStride = 1 << 21;  // 256 of its rows stay below 2 GiB
+
+int check_embed(const gscan_embed_t *d, const void *tokens, gscan::EmbedArgs *a, bool pointers = true)
+{
+    if (!d) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null descriptor");
+    if (!known(d->table_dtype) || !known(d->dtype))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d / %d", (int)d->table_dtype, (int)d->dtype);
+    if (d->tokens < 0 || d->vocabulary < 1 || d->width < 1 || d->stride < 0)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT,
+                    "need tokens, stride >= 0 and vocabulary, width >= 1 (tokens=%lld vocabulary=%lld "
+                    "width=%lld stride=%lld)", (long long)d->tokens, (long long)d->vocabulary,
+                    (long long)d->width, (long long)d->stride);
+    if (d->width % 8 || d->width > kMaxWidth || d->tokens > kMaxTokens || d->vocabulary > kMaxTokens ||
+        d->stride > (int64_t(1) << 31) || d->vocabulary > (int64_t(1) << 40) / d->width)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "unsupported shape tokens=%lld vocabulary=%lld width=%lld (need a width that is a "
+                    "multiple of 8 up to 65536, tokens and vocabulary below 2^31 - 128, a table of at most "
+                    "2^40 elements)", (long long)d->tokens, (long long)d->vocabulary, (long long)d->width);
+    if (pointers && d->tokens > 0 && !tokens) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null tokens");
+    if (mis(tokens, d->token_int64 ? 8 : 4)) return fail(GSCAN_ERR_MISALIGNED, "misaligned tokens");
+    a->tokens = tokens;
+    a->N = d->tokens;
+    a->V = d->vocabulary;
+    a->D = (int)d->width;
+    a->ld = d->stride;
+    a->tok64 = d->token_int64 != 0;
+    a->table_dtype = (int)d->table_dtype;
+    a->dtype = (int)d->dtype;
+    a->scale = d->scale;
+    return GSCAN_OK;
+}
+
+constexpr int64_t kMaxProducts = int64_t(1) << 43;  // rows times columns of an output: 2^30 tiles
+
+int check_gate(const gscan_gated_projection_t *d, const void *x, const void *wg, const void *wu,
+               gscan::GateArgs *a, bool pointers = true)
+{
+    if (!d) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null descriptor");
+    if (!known(d->dtype)) return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d", (int)d->dtype);
+    if (d->activation != GSCAN_ACT_SILU && d->activation != GSCAN_ACT_GELU &&
+        d->activation != GSCAN_ACT_GELU_TANH)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown activation %d", (int)d->activation);
+    if (d->tokens < 0 || d->width < 1 || d->inner < 1)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "need tokens >= 0 and width, inner >= 1 (tokens=%lld width=%lld "
+                    "inner=%lld)", (long long)d->tokens, (long long)d->width, (long long)d->inner);
+    if (d->width % 8 || d->inner % 8 || d->width > kMaxWidth || d->inner > kMaxWidth || d->tokens > kMaxTokens ||
+        d->tokens > kMaxProducts / (2 * (d->width > d->inner ? d->width : d->inner)))
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "unsupported shape tokens=%lld width=%lld inner=%lld (need widths that are multiples of 8 "
+                    "up to 65536, tokens below 2^31 - 128, tokens times the larger width at most 2^42)",
+                    (long long)d->tokens, (long long)d->width, (long long)d->inner);
+    for (int64_t s : {d->x_stride, d->gate_stride, d->up_stride}) {
+        if (s < 0 || s > kMaxRowStride)
+            return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "row strides must be 0 .. 2^21 elements");
+        if (!strides16(&s, 1, d->dtype))
+            return fail(GSCAN_ERR_MISALIGNED, "row strides must be multiples of 16 bytes");
+    }
+    if (pointers && (!wg || !wu || (d->tokens > 0 && !x)))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null x or weight");
+    if (mis(x, 16) || mis(wg, 16) || mis(wu, 16))
+        return fail(GSCAN_ERR_MISALIGNED, "x and the weights must be 16-byte aligned");
+    a->x = x;
+    a->wg = wg;
+    a->wu = wu;
+    a->N = d->tokens;
+    a->D = (int)d->width;
+    a->F = (int)d->inner;
+    a->ldx = d->x_stride;
+    a->ldg = d->gate_stride;
+    a->ldu = d->up_stride;
+    a->dtype = (int)d->dtype;
+    a->act = (int)d->activation;
+    return GSCAN_OK;
+}
+
+int check_xent(const gscan_linear_cross_entropy_t *d, const void *h, const void *w, const void *target,
+               gscan::XentArgs *a, bool pointers = true)
+{
+    if (!d) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null descriptor");
+    if (!known(d->dtype)) return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown dtype %d", (int)d->dtype);
+    if (d->reduction != GSCAN_LOSS_EACH && d->reduction != GSCAN_LOSS_SUM && d->reduction != GSCAN_LOSS_MEAN)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "unknown reduction %d", (int)d->reduction);
+    if (d->tokens < 0 || d->width < 1 || d->vocabulary < 1)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "need tokens >= 0 and width, vocabulary >= 1 (tokens=%lld "
+                    "width=%lld vocabulary=%lld)", (long long)d->tokens, (long long)d->width,
+                    (long long)d->vocabulary);
+    if (d->width % 8 || d->width > kMaxWidth || d->tokens > kMaxTokens || d->vocabulary > kMaxTokens ||
+        d->vocabulary > (int64_t(1) << 40) / d->width ||
+        d->tokens > kMaxProducts / (d->width > d->vocabulary ? d->width : d->vocabulary))
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE,
+                    "unsupported shape tokens=%lld width=%lld vocabulary=%lld (need a width that is a multiple of "
+                    "8 up to 65536, tokens and vocabulary below 2^31 - 128, vocabulary * width at most 2^40, "
+                    "tokens times the larger of both at most 2^43)", (long long)d->tokens, (long long)d->width,
+                    (long long)d->vocabulary);
+    for (int64_t s : {d->h_stride, d->weight_stride}) {
+        if (s < 0 || s > kMaxRowStride)
+            return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "row strides must be 0 .. 2^21 elements");
+        if (!strides16(&s, 1, d->dtype))
+            return fail(GSCAN_ERR_MISALIGNED, "row strides must be multiples of 16 bytes");
+    }
+    if (pointers && (!w || (d->tokens > 0 && (!h || !target))))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null h, weight or target");
+    if (mis(h, 16) || mis(w, 16) || mis(target, d->target_int64 ? 8 : 4))
+        return fail(GSCAN_ERR_MISALIGNED, "h and weight must be 16-byte aligned, targets to their elements");
+    a->h = h;
+    a->w = w;
+    a->target = target;
+    a->N = d->tokens;
+    a->V = d->vocabulary;
+    a->D = (int)d->width;
+    a->ldh = d->h_stride;
+    a->ldw = d->weight_stride;
+    a->dtype = (int)d->dtype;
+    a->target64 = d->target_int64 != 0;
+    a->reduction = (int)d->reduction;
+    a->scale = d->scale;
     return GSCAN_OK;
 }
 
@@ -952,6 +1073,150 @@ size_t gscan_qk_norm_rope_workspace_bytes(const gscan_qk_norm_t *desc)
         desc->Hq > kMaxNormHeads || desc->Hk > kMaxNormHeads)
         return 0;
     return gscan::norm_workspace_bytes(desc->tokens, (int)(desc->Hq + desc->Hk), (int)desc->D);
+}
+
+int gscan_embed_forward(const gscan_embed_t *desc, const void *table, const void *tokens, void *out,
+                        hipStream_t stream)
+{
+    gscan::EmbedArgs a;
+    int st = check_embed(desc, tokens, &a);
+    if (st != GSCAN_OK) return st;
+    if (a.N > 0 && (!table || !out)) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null table or out");
+    if (mis(table, 16) || mis(out, 16) || !strides16(&desc->stride, 1, a.table_dtype))
+        return fail(GSCAN_ERR_MISALIGNED, "table, its row stride and out must be multiples of 16 bytes");
+    a.table = table;
+    a.out = out;
+    return with_workspace("embedding", nullptr, 0, 0, stream,
+                          [&](void *) { return gscan::launch_embed_forward(a, stream); });
+}
+
+int gscan_embed_backward(const gscan_embed_t *desc, const void *d_out, const void *tokens, void *d_table,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    gscan::EmbedArgs a;
+    int st = check_embed(desc, tokens, &a);
+    if (st != GSCAN_OK) return st;
+    if (!d_table || (a.N > 0 && !d_out)) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null d_out or d_table");
+    if (mis(d_out, 16) || mis(d_table, 16) || !strides16(&desc->stride, 1, a.dtype))
+        return fail(GSCAN_ERR_MISALIGNED, "d_out, its row stride and d_table must be multiples of 16 bytes");
+    a.dout = d_out;
+    a.dtable = d_table;
+    return with_workspace("embedding backward", workspace, workspace_bytes,
+                          gscan::embed_workspace_bytes(a.N, a.V, a.D), stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_embed_backward(a, stream);
+                          });
+}
+
+size_t gscan_embed_workspace_bytes(const gscan_embed_t *desc)
+{
+    gscan::EmbedArgs a;
+    if (check_embed(desc, nullptr, &a, false) != GSCAN_OK) return 0;
+    return gscan::embed_workspace_bytes(a.N, a.V, a.D);
+}
+
+int gscan_gated_projection_forward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
+                                   const void *w_up, void *out, hipStream_t stream)
+{
+    gscan::GateArgs a;
+    int st = check_gate(desc, x, w_gate, w_up, &a);
+    if (st != GSCAN_OK) return st;
+    if (a.N > 0 && !out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null out");
+    if (mis(out, 16)) return fail(GSCAN_ERR_MISALIGNED, "out must be 16-byte aligned");
+    a.out = out;
+    return with_workspace("gated projection", nullptr, 0, 0, stream,
+                          [&](void *) { return gscan::launch_gate_forward(a, stream); });
+}
+
+int gscan_gated_projection_backward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
+                                    const void *w_up, const void *d_out, void *dx, void *d_w_gate,
+                                    void *d_w_up, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    gscan::GateArgs a;
+    int st = check_gate(desc, x, w_gate, w_up, &a);
+    if (st != GSCAN_OK) return st;
+    if (a.N > 0 && !d_out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null d_out");
+    if (!d_w_gate != !d_w_up)
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "d_w_gate and d_w_up go together");
+    if (mis(d_out, 16) || mis(dx, 16) || mis(d_w_gate, 16) || mis(d_w_up, 16) ||
+        !strides16(&desc->d_out_stride, 1, a.dtype))
+        return fail(GSCAN_ERR_MISALIGNED, "gradients and d_out's row stride must be multiples of 16 bytes");
+    if (desc->d_out_stride < 0 || desc->d_out_stride > kMaxRowStride)
+        return fail(GSCAN_ERR_UNSUPPORTED_SHAPE, "row strides must be 0 .. 2^21 elements");
+    a.dout = d_out;
+    a.ldd = desc->d_out_stride;
+    a.dx = dx;
+    a.dwg = d_w_gate;
+    a.dwu = d_w_up;
+    return with_workspace("gated projection backward", workspace, workspace_bytes,
+                          gscan::gate_workspace_bytes(a.N, a.F, a.dtype), stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_gate_backward(a, stream);
+                          });
+}
+
+size_t gscan_gated_projection_workspace_bytes(const gscan_gated_projection_t *desc)
+{
+    gscan::GateArgs a;
+    if (check_gate(desc, nullptr, nullptr, nullptr, &a, false) != GSCAN_OK) return 0;
+    return gscan::gate_workspace_bytes(a.N, a.F, a.dtype);
+}
+
+int gscan_linear_cross_entropy_forward(const gscan_linear_cross_entropy_t *desc, const void *h, const void *weight,
+                                       const void *target, float *loss, float *lse, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream)
+{
+    gscan::XentArgs a;
+    int st = check_xent(desc, h, weight, target, &a);
+    if (st != GSCAN_OK) return st;
+    if ((!loss && (a.N > 0 || a.reduction)) || (a.N > 0 && !lse))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null loss or lse");
+    if (mis(loss, 4) || mis(lse, 4)) return fail(GSCAN_ERR_MISALIGNED, "misaligned loss or lse");
+    if (!a.N && !a.reduction) return GSCAN_OK;
+    a.loss = loss;
+    a.lse = lse;
+    return with_workspace("cross entropy", workspace, workspace_bytes,
+                          gscan::xent_forward_workspace_bytes(a.N, a.V, a.D, a.dtype), stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_xent_forward(a, stream);
+                          });
+}
+
+int gscan_linear_cross_entropy_backward(const gscan_linear_cross_entropy_t *desc, const void *h, const void *weight,
+                                        const void *target, const float *lse, const float *d_loss, void *dh,
+                                        void *d_weight, void *workspace, size_t workspace_bytes,
+                                        hipStream_t stream)
+{
+    gscan::XentArgs a;
+    int st = check_xent(desc, h, weight, target, &a);
+    if (st != GSCAN_OK) return st;
+    if ((!d_loss && (a.N > 0 || a.reduction)) || (a.N > 0 && !lse))
+        return fail(GSCAN_ERR_INVALID_ARGUMENT, "null lse or d_loss");
+    if (mis(lse, 4) || mis(d_loss, 4) || mis(dh, 16) || mis(d_weight, 16))
+        return fail(GSCAN_ERR_MISALIGNED, "dh and d_weight must be 16-byte aligned, lse and d_loss to their elements");
+    a.lse = const_cast<float *>(lse);
+    a.dloss = d_loss;
+    a.dh = dh;
+    a.dw = d_weight;
+    return with_workspace("cross entropy backward", workspace, workspace_bytes,
+                          gscan::xent_backward_workspace_bytes(a.N, a.V, a.D, a.dtype), stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_xent_backward(a, stream);
+                          });
+}
+
+size_t gscan_linear_cross_entropy_forward_workspace_bytes(const gscan_linear_cross_entropy_t *desc)
+{
+    gscan::XentArgs a;
+    if (check_xent(desc, nullptr, nullptr, nullptr, &a, false) != GSCAN_OK) return 0;
+    return gscan::xent_forward_workspace_bytes(a.N, a.V, a.D, a.dtype);
+}
+
+size_t gscan_linear_cross_entropy_backward_workspace_bytes(const gscan_linear_cross_entropy_t *desc)
+{
+    gscan::XentArgs a;
+    if (check_xent(desc, nullptr, nullptr, nullptr, &a, false) != GSCAN_OK) return 0;
+    return gscan::xent_backward_workspace_bytes(a.N, a.V, a.D, a.dtype);
 }
 
 const char *gscan_status_string(int status)

@@ -1,0 +1,401 @@
+// Matrix products of the gated projection and the vocabulary's cross entropy:
+//
+//   C[m][n] = sum over k of A(m, k) B(n, k),
+//
+// where m is the index that the output has contiguous and n its row.  An
+// operand has k contiguous (its rows are m or n; KC below) or m or n contiguous
+// (its rows are k; RC):
+//   logits, both projections   A weights  KC   B tokens     KC
+//   gradient of the tokens     A weights  RC   B gradients  KC   (k: outputs)
+//   gradient of the weights    A tokens   RC   B gradients  RC   (k: tokens)
+// What a tile's sums become is the epilogue: the sums of a lane are those of
+// one n and of groups of four m that follow each other.
+#pragma once
+
+#include <type_traits>
+
+#include "gscan_lm_dev.h"
+
+namespace gscan {
+namespace {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+enum Epi {
+    EPI_STORE,   // out[n][m]
+    EPI_GATE,    // act(a) * b, of the halves a, b of the tile's m
+    EPI_DGATE,   // the gradients of a and b from dout
+    EPI_LSE,     // maximum and sum of exponentials of the tile's logits, for each n
+    EPI_DLOGIT,  // the gradient of the logits
+    EPI_ADD      // a sum over several calls: fp32 between them, the last into rows of out
+};
+enum Limit { LIMIT_NONE, LIMIT_N, LIMIT_K };
+
+struct MmArgs {
+    const void *a = nullptr, *a2 = nullptr;  // a2: of the second half (two weights); else null
+    const void *b = nullptr;
+    int64_t lda = 0, lda2 = 0, ldb = 0;
+    int64_t M = 0, N = 0, K = 0;
+    int64_t K1 = 0;                 // A RC with a2: the k at which it begins
+    // Rows that the device knows the number of: N or K is *count.  Where that
+    // is less than what the host knows, the tokens' operand (b, or a where K is
+    // limited) is alt, in which they follow each other.
+    const int32_t *count = nullptr;
+    const void *alt = nullptr;
+    int64_t ldalt = 0;
+    void *out = nullptr, *out2 = nullptr;
+    int64_t ldo = 0, N1 = 0;        // rows from N1 on are out2's
+    const void *dout = nullptr;
+    int64_t ldd = 0;
+    const int32_t *target = nullptr, *row = nullptr;  // by n: target, place in the caller's order
+    const float *up = nullptr, *lse = nullptr;        // by n (up null: one)
+    const float *factor = nullptr;  // EPI_STORE, EPI_ADD: of the whole output (null: one)
+    float2 *part = nullptr;         // [tile of m][N]
+    float *picked = nullptr;        // by n: the target's logit
+    int64_t v0 = 0;                 // the vocabulary's entry of m = 0
+    float *sum = nullptr;           // EPI_ADD between calls, [N][M]
+    int first = 1, last = 1;
+    float scale = 1.f;
+    int act = 0;
+};
+
+// -------------------------------------------------------------- activations
+
+// Hardware exponential and reciprocal (a few 2^-24 times |x|) where the result is
+// rounded to bf16.
+template <bool BF>
+__device__ __forceinline__ float sigmoid_(float x)
+{
+    return BF ? __builtin_amdgcn_rcpf(1.f + exp2_(-1.44269504f * x)) : 1.f / (1.f + expf(-x));
+}
+
+// act(a) and its derivative.  0: a sigmoid(a); 1: a Phi(a), Phi the normal
+// distribution's sum; 2: the same with the hyperbolic tangent's approximation
+// of Phi, 0.5 (1 + tanh(u)) = sigmoid(2 u).
+template <bool BF>
+__device__ __forceinline__ void activation(float a, int act, float &f, float &slope)
+{
+    if (act == 0) {
+        const float g = sigmoid_<BF>(a);
+        f = a * g;
+        slope = fmaf(f, 1.f - g, g);
+    } else if (act == 1) {
+        const float p = 0.5f * erfcf(-0.70710678118654752f * a);
+        f = a * p;
+        slope = fmaf(a * 0.39894228040143268f, BF ? exp2_(-0.72134752044448170f * a * a) : expf(-0.5f * a * a), p);
+    } else {
+        const float c = 0.79788456080286536f;
+        const float q = fminf(a * a, 1e6f), g = sigmoid_<BF>(2.f * c * a * fmaf(0.044715f, q, 1.f));
+        f = a * g;
+        slope = fmaf(2.f * f * (1.f - g), c * fmaf(0.134145f, q, 1.f), g);
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ f4 load4(const void *p, int64_t i)
+{
+    if constexpr (BF) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
+        return f4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
+    } else {
+        return *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(p) + i);
+    }
+}
+template <bool BF>
+__device__ __forceinline__ void store4(void *p, int64_t i, const f4 &x)
+{
+    if constexpr (BF)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
+            uint2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    else
+        *reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i) = x;
+}
+
+// (maximum, sum of exponentials relative to it) of two sets joined.  An empty
+// set is (-inf, 0).
+__device__ __forceinline__ void join_lse(float &m, float &s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2);
+    const float base = top == -INFINITY ? 0.f : top;
+    s = s * exp2_(1.44269504f * (m - base)) + s2 * exp2_(1.44269504f * (m2 - base));
+    m = top;
+}
+
+// ------------------------------------------------------------------ the tiles
+
+// Tile of a workgroup.  Workgroups go to the eight XCDs in turn: each takes
+// consecutive tiles, which walk eight tiles of n before the next tile of m, so
+// that what runs at the same time on an XCD shares its rows in that XCD's L2.
+__device__ __forceinline__ void tile_of(int64_t id, int64_t tm, int64_t tn, int64_t &im, int64_t &in)
+{
+    const int64_t all = tm * tn, q = all / 8, r = all % 8, x = id % 8;
+    const int64_t t = x * q + (x < r ? x : r) + id / 8;
+    const int64_t g = t / (8 * tm), left = tn - 8 * g, w = left < 8 ? left : 8, u = t - g * 8 * tm;
+    in = 8 * g + u % w;
+    im = u / w;
+}
+
+// What a workgroup's sums become.  acc[i][j]: the 32 x 32 sums of the rows
+// m0 + mat(i) .. + 31 and n0 + nat(j) .. + 31; element r of a lane is m = 8 (r / 4) + 4
+// (lane / 32) + r % 4, n = lane % 32.  Gated tiles hold the same m of both
+// weights in acc[i] and acc[i + MI / 2].  `red`: LDS of WM * 32 * NI * WN pairs.
+template <Epi E, bool BF, int MI, int NI, int WM, class MAt>
+__device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], int64_t im, int64_t m0,
+                                         int64_t n0, int64_t N, int wm, int nat, int TN, MAt mat, float2 *red)
+{
+    const int lane = threadIdx.x & 63, hi = lane >> 5, col = lane & 31;
+    float factor = 1.f;
+    if constexpr (E == EPI_STORE || E == EPI_ADD)
+        if (a.factor) factor = *a.factor;
+    if constexpr (E == EPI_LSE) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int64_t n = n0 + nat + 32 * j + col;
+            const int64_t t = n < N ? (int64_t)a.target[n] - a.v0 : -1;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t m = m0 + mat(i) + 8 * (r / 4) + 4 * hi + r % 4;
+                    float z = acc[i][j][r] * a.scale;
+                    if (m == t) a.picked[n] = z;
+                    z = m < a.M ? z : -INFINITY;
+                    acc[i][j][r] = z;
+                    top = fmaxf(top, z);
+                }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float base = top == -INFINITY ? 0.f : top;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s += exp2_(1.44269504f * (acc[i][j][r] - base));
+            s += __shfl_xor(s, 32);
+            if (hi == 0) red[wm * TN + nat + 32 * j + col] = float2{top, s};
+        }
+        __syncthreads();
+        for (int n = threadIdx.x; n < TN; n += blockDim.x) {
+            float2 x = red[n];
+#pragma unroll
+            for (int w = 1; w < WM; ++w) {
+                const float2 y = red[w * TN + n];
+                join_lse(x.x, x.y, y.x, y.y);
+            }
+            if (n0 + n < N) a.part[im * a.N + n0 + n] = x;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int64_t n = n0 + nat + 32 * j + col;
+            if (n >= N) continue;
+            int64_t t = 0, place = n;
+            float up = 0.f, lse = 0.f;
+            if constexpr (E == EPI_DLOGIT) {
+                t = (int64_t)a.target[n] - a.v0;
+                up = a.up ? a.up[n] : 1.f;
+                lse = a.lse[n];
+            }
+            if constexpr (E == EPI_ADD) place = a.last ? a.row[n] : n;
+            constexpr int HI = E == EPI_GATE || E == EPI_DGATE ? MI / 2 : MI;
+#pragma unroll
+            for (int i = 0; i < HI; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t m = m0 + mat(i) + 8 * g + 4 * hi;
+                    f4 v = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                    if constexpr (E == EPI_DLOGIT) {
+                        if (m >= a.ldo) continue;  // the piece's columns, padded to eight with zeros
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float z = v[e] * a.scale - lse;
+                            const float p = BF ? exp2_(1.44269504f * z) : expf(z);
+                            v[e] = m + e < a.M ? (p - (m + e == t ? 1.f : 0.f)) * up : 0.f;
+                        }
+                        store4<BF>(a.out, n * a.ldo + m, v);
+                        continue;
+                    }
+                    if (m >= a.M) continue;  // M is a multiple of eight from here on
+                    if constexpr (E == EPI_STORE) {
+                        v *= factor;
+                        if (n < a.N1)
+                            store4<BF>(a.out, n * a.ldo + m, v);
+                        else
+                            store4<BF>(a.out2, (n - a.N1) * a.ldo + m, v);
+                    } else if constexpr (E == EPI_ADD) {
+                        if (!a.first) {
+                            const f4 s = load4<false>(a.sum, n * a.M + m);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] += s[e];
+                        }
+                        if (a.last)
+                            store4<BF>(a.out, place * a.ldo + m, v * factor);
+                        else
+                            store4<false>(a.sum, n * a.M + m, v);
+                    } else {
+                        f4 o, o2, d = {};
+                        if constexpr (E == EPI_DGATE) d = load4<BF>(a.dout, n * a.ldd + m);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float f, slope;
+                            activation<BF>(v[e], a.act, f, slope);
+                            const float b = acc[HI + i][j][4 * g + e];
+                            if constexpr (E == EPI_GATE) {
+                                o[e] = f * b;
+                            } else {
+                                o[e] = d[e] * b * slope;
+                                o2[e] = d[e] * f;
+                            }
+                        }
+                        store4<BF>(a.out, n * a.ldo + m, o);
+                        if constexpr (E == EPI_DGATE) store4<BF>(a.out, n * a.ldo + a.M + m, o2);
+                    }
+                }
+        }
+    }
+}
+
+// --------------------------------------------------- products in fp32
+
+// Tiles of 128 x 128, four wavefronts of 64 x 64, 32 of k at a time through
+// registers into LDS, where k is the row.
+constexpr int kF32Tile = 128, kF32K = 32, kF32Pitch = 130, kF32Threads = 256;
+constexpr int kF32Part = 256;
+
+// Four elements of an operand's tile: of row r, from column c (KC: row m, column
+// k; RC: row k, column m).
+template <bool BF>
+__device__ __forceinline__ f4 piece(const void *p, int64_t ld, int64_t r, int64_t rows, int64_t c, int64_t cols)
+{
+    return r < rows && c < cols ? load4<BF>(p, r * ld + c) : f4{};
+}
+
+template <Epi E, bool RCA, bool RCB, Limit L, bool BF>
+__global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
+{
+    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;  // of m
+    __shared__ __align__(16) float lds[2][kF32K][kF32Pitch];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+    int64_t N = a.N, K = a.K;
+    const void *pa = a.a, *pb = a.b;
+    int64_t lda = a.lda, ldb = a.ldb;
+    if constexpr (L != LIMIT_NONE) {
+        const int64_t c = *a.count;
+        if (a.alt && c < (L == LIMIT_N ? a.N : a.K)) {
+            (L == LIMIT_N ? pb : pa) = a.alt;
+            (L == LIMIT_N ? ldb : lda) = a.ldalt;
+        }
+        (L == LIMIT_N ? N : K) = c;
+    }
+    const int64_t tm = (a.M + kTile - 1) / kTile, tn = (a.N + kF32Tile - 1) / kF32Tile;
+    int64_t im, in;
+    tile_of(blockIdx.x, tm, tn, im, in);
+    const int64_t m0 = im * kTile, n0 = in * kF32Tile;
+    if (n0 >= N) return;
+
+    auto load_a = [&](int64_t k0, int j) -> f4 {
+        const int q = tid + j * kF32Threads;
+        if constexpr (!RCA) {
+            const int r = q >> 3;
+            const int64_t c = k0 + 4 * (q & 7);
+            if (kGated && r >= kTile) return piece<BF>(a.a2, a.lda2, m0 + r - kTile, a.M, c, K);
+            return piece<BF>(pa, lda, m0 + r, a.M, c, K);
+        } else {
+            const int64_t k = k0 + (q >> 5), c = m0 + 4 * (q & 31);
+            if (a.a2 && k >= a.K1) return piece<BF>(a.a2, a.lda2, k - a.K1, K - a.K1, c, a.M);
+            return piece<BF>(pa, lda, k, K, c, a.M);
+        }
+    };
+    auto load_b = [&](int64_t k0, int j) -> f4 {
+        const int q = tid + j * kF32Threads;
+        if constexpr (!RCB) return piece<BF>(pb, ldb, n0 + (q >> 3), N, k0 + 4 * (q & 7), K);
+        else return piece<BF>(pb, ldb, k0 + (q >> 5), K, n0 + 4 * (q & 31), N);
+    };
+    auto put = [&](int which, bool rc, int j, const f4 &v) {
+        const int q = tid + j * kF32Threads;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (rc) lds[which][q >> 5][4 * (q & 31) + e] = v[e];
+            else lds[which][4 * (q & 7) + e][q >> 3] = v[e];
+        }
+    };
+    auto mat = [&](int i) { return kGated ? 32 * wm : 64 * wm + 32 * i; };
+    auto row_of = [&](int i) { return kGated ? kTile * i + 32 * wm : 64 * wm + 32 * i; };
+    f16v acc[2][2], all[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = all[i][j] = f16v{};
+    f4 ra[4], rb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        ra[j] = load_a(0, j);
+        rb[j] = load_b(0, j);
+    }
+    for (int64_t k0 = 0; k0 < K; k0 += kF32K) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            put(0, RCA, j, ra[j]);
+            put(1, RCB, j, rb[j]);
+        }
+        __syncthreads();
+        if (k0 + kF32K < K) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ra[j] = load_a(k0 + kF32K, j);
+                rb[j] = load_b(k0 + kF32K, j);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kF32K; k += 2) {
+            float x[2], y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[i] = lds[0][k + (lane >> 5)][row_of(i) + (lane & 31)];
+                y[i] = lds[1][k + (lane >> 5)][64 * wn + 32 * i + (lane & 31)];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[j], acc[i][j], 0, 0, 0);
+        }
+        // sums of 256 are joined, so that rounding grows with neither alone
+        if ((k0 + kF32K) % kF32Part == 0 || k0 + kF32K >= K) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    all[i][j] += acc[i][j];
+                    acc[i][j] = f16v{};
+                }
+        }
+    }
+    if (E == EPI_LSE) __syncthreads();  // the tiles become the epilogue's memory
+    epilogue<E, BF, 2, 2, 2>(a, all, im, m0, n0, N, wm, 64 * wn, kF32Tile, mat,
+                                    reinterpret_cast<float2 *>(&lds[0][0][0]));
+}
+
+template <Epi E, bool RCA, bool RCB, Limit L>
+hipError_t launch_mm(const MmArgs &a, int dtype, hipStream_t st)
+{
+    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;
+    const int64_t tiles = ((a.M + kTile - 1) / kTile) * ((a.N + kF32Tile - 1) / kF32Tile);
+    if (!tiles) return hipSuccess;
+    auto *k = dtype ? gscan_mm_f32_kernel<E, RCA, RCB, L, true> : gscan_mm_f32_kernel<E, RCA, RCB, L, false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(kF32Threads), 0, st, a);
+    return hipGetLastError();
+}
+
+// Tiles of m: the partial results of EPI_LSE for each n.
+int64_t tiles_of_m(int64_t M, int dtype)
+{
+    (void)dtype;
+    return (M + kF32Tile - 1) / kF32Tile;
+}
+
+}  // namespace
+}  // namespace gscan

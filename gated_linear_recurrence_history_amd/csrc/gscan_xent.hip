@@ -1,0 +1,296 @@
+// Cross entropy over a large vocabulary, forward and backward, for gfx950
+// (MI355X), without the logits in memory:
+//
+//   z = scale * h W^T,  lse_n = log sum over v of exp(z_nv),
+//   loss_n = lse_n - z_n,target
+//   G_nv = scale * u_n * (exp(z_nv - lse_n) - [v is the target]),
+//   dh = G W,  dW = G^T h         (u_n: the gradient that reaches loss_n)
+//
+// Where all u are one (a sum, a mean) they are left out of G and multiply the
+// outputs: most of G is the -1 at the targets, which is then exact, where the
+// rounding of -u would be the same for every token and move the whole gradient.
+//
+// Forward: every tile of the product leaves, for each token, the maximum of its
+// logits and the sum of their exponentials relative to it; a second kernel joins
+// a token's.  Backward: the vocabulary is taken in pieces.  Of a piece, G is
+// formed from the product again and rounded to the type of the operands once;
+// it adds to dh (fp32 between the pieces) and makes the piece's rows of dW
+// whole.
+//
+// Tokens that do not count (their target is outside the vocabulary) are left
+// out: a first kernel lists the others, and where some are missing their rows
+// are copied so that they follow each other.  What is in the rows left out, NaN
+// included, reaches nothing.
+#include "gscan_mm.h"
+
+namespace gscan {
+namespace {
+
+constexpr int kLThreads = 1024;
+constexpr int64_t kPieceBytes = 128ll << 20;  // G of a piece
+constexpr int kJoinRows = 16;
+
+// By place among the tokens that count.
+struct Listed {
+    int32_t *count = nullptr, *row = nullptr, *target = nullptr;
+    float *factor = nullptr, *up = nullptr, *lse = nullptr, *picked = nullptr, *loss = nullptr;
+    void *h = nullptr;          // their rows, where some do not count
+    float2 *part = nullptr;
+    void *g = nullptr;
+    float *sum = nullptr;
+    int64_t piece = 0;
+    size_t bytes = 0;
+};
+
+Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
+{
+    const size_t es = dtype ? 2 : 4;
+    Listed l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) -> void * {
+        void *p = reinterpret_cast<char *>(ws) + at;
+        at = (at + bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    l.count = (int32_t *)take(4);
+    l.row = (int32_t *)take((size_t)N * 4);
+    l.target = (int32_t *)take((size_t)N * 4);
+    l.h = take((size_t)N * D * es);
+    if (backward) {
+        l.factor = (float *)take(4);
+        l.up = (float *)take((size_t)N * 4);
+        l.lse = (float *)take((size_t)N * 4);
+        // whole tiles, at least 2048 columns
+        const int64_t fit = N > 0 ? kPieceBytes / (N * (int64_t)es) / 256 * 256 : V;
+        l.piece = fit < 2048 ? 2048 : fit;
+        if (l.piece > V) l.piece = V;
+        const int64_t ld = (l.piece + 7) / 8 * 8;
+        l.g = take((size_t)N * ld * es);
+        if (l.piece < V) l.sum = (float *)take((size_t)N * D * 4);
+    } else {
+        l.picked = (float *)take((size_t)N * 4);
+        l.loss = (float *)take((size_t)N * 4);
+        l.part = (float2 *)take((size_t)tiles_of_m(V, dtype) * N * sizeof(float2));
+    }
+    l.bytes = at;
+    return l;
+}
+
+// Lists the tokens that count, in order.  One workgroup, 1024 tokens at a time.
+template <bool BWD>
+__global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, Listed l)
+{
+    __shared__ int32_t n_of[kLThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t done = 0;
+    for (int64_t b = 0; b < a.N; b += kLThreads) {
+        const int64_t i = b + tid;
+        const int64_t t = i < a.N ? token_at(a.target, i, a.target64, a.V) : -1;
+        const uint64_t in = __ballot(t >= 0);
+        __syncthreads();
+        if (lane == 0) n_of[wave] = __popcll(in);
+        __syncthreads();
+        int64_t at = done + __popcll(in & ((1ull << lane) - 1));
+        for (int w = 0; w < kLThreads / 64; ++w) {
+            at += w < wave ? n_of[w] : 0;
+            done += n_of[w];
+        }
+        if (t >= 0) {
+            l.row[at] = (int32_t)i;
+            l.target[at] = (int32_t)t;
+            if (BWD) l.lse[at] = a.lse[i];
+        } else if (!BWD && i < a.N) {
+            a.lse[i] = 0.f;
+            (a.reduction ? l.loss : a.loss)[i] = 0.f;
+        }
+    }
+    if (tid == 0) *l.count = (int32_t)done;
+    if (!BWD) return;
+    if (a.reduction) {
+        if (tid == 0) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
+    } else {
+        __syncthreads();  // l.row is this workgroup's own
+        for (int64_t i = tid; i < done; i += kLThreads) l.up[i] = a.scale * a.dloss[l.row[i]];
+    }
+}
+
+// Rows that count, one after the other, where some do not; gradients of those
+// that do not are zero.
+template <bool BF>
+__global__ void __launch_bounds__(256) gscan_xent_rows_kernel(XentArgs a, Listed l)
+{
+    const int64_t n = blockIdx.x, count = *l.count;
+    if (count == a.N) return;
+    const bool copy = n < count, clear = a.dh && token_at(a.target, n, a.target64, a.V) < 0;
+    const int64_t from = copy ? l.row[n] : 0;
+    for (int c = 8 * threadIdx.x; c < a.D; c += 8 * 256) {
+        if (copy) {
+            const OctRaw<BF> x = load_oct<BF>(a.h, from * a.ldh + c);
+            *reinterpret_cast<OctRaw<BF> *>(reinterpret_cast<char *>(l.h) + (n * a.D + c) * (BF ? 2 : 4)) = x;
+        }
+        if (clear) store_oct<BF>(a.dh, n * a.D + c, Oct{});
+    }
+}
+
+// A token's partial results: 16 tokens, 16 lanes each.
+__global__ void __launch_bounds__(256) gscan_xent_join_kernel(XentArgs a, Listed l, int64_t parts)
+{
+    __shared__ float2 red[16][kJoinRows];
+    const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
+    const int64_t count = *l.count, n = (int64_t)blockIdx.x * kJoinRows + r;
+    float m = -INFINITY, s = 0.f;
+    if (n < count)
+        for (int64_t p = q; p < parts; p += 16) {
+            const float2 x = l.part[p * a.N + n];
+            join_lse(m, s, x.x, x.y);
+        }
+    red[q][r] = float2{m, s};
+    __syncthreads();
+    if (q == 0 && n < count) {
+        for (int i = 1; i < 16; ++i) join_lse(m, s, red[i][r].x, red[i][r].y);
+        const float lse = m + logf(s);
+        const int64_t i = l.row[n];
+        a.lse[i] = lse;
+        (a.reduction ? l.loss : a.loss)[i] = lse - l.picked[n];
+    }
+}
+
+__global__ void __launch_bounds__(kLThreads) gscan_xent_total_kernel(XentArgs a, Listed l)
+{
+    __shared__ double red[kLThreads];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < a.N; i += kLThreads) s += (double)l.loss[i];
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int h = kLThreads / 2; h > 0; h /= 2) {
+        if (threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const int32_t n = *l.count;
+        *a.loss = (float)(a.reduction == 2 && n ? red[0] / n : red[0]);
+    }
+}
+
+hipError_t launch_list(const XentArgs &x, const Listed &l, bool backward, hipStream_t st)
+{
+    if (backward)
+        hipLaunchKernelGGL(gscan_xent_list_kernel<true>, dim3(1), dim3(kLThreads), 0, st, x, l);
+    else
+        hipLaunchKernelGGL(gscan_xent_list_kernel<false>, dim3(1), dim3(kLThreads), 0, st, x, l);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !x.N) return e;
+    auto *k = x.dtype ? gscan_xent_rows_kernel<true> : gscan_xent_rows_kernel<false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)x.N), dim3(256), 0, st, x, l);
+    return hipGetLastError();
+}
+
+MmArgs logits_of(const XentArgs &x, const Listed &l, int64_t v0, int64_t v1)
+{
+    MmArgs a;
+    a.a = reinterpret_cast<const char *>(x.w) + v0 * x.ldw * (x.dtype ? 2 : 4);
+    a.lda = x.ldw;
+    a.b = x.h;
+    a.ldb = x.ldh;
+    a.M = v1 - v0;
+    a.N = x.N;
+    a.K = x.D;
+    a.count = l.count;
+    a.alt = l.h;
+    a.ldalt = x.D;
+    a.target = l.target;
+    a.v0 = v0;
+    a.scale = x.scale;
+    return a;
+}
+
+}  // namespace
+
+size_t xent_forward_workspace_bytes(int64_t N, int64_t V, int D, int dtype)
+{
+    return lay_out(nullptr, N, V, D, dtype, false).bytes;
+}
+
+size_t xent_backward_workspace_bytes(int64_t N, int64_t V, int D, int dtype)
+{
+    return lay_out(nullptr, N, V, D, dtype, true).bytes;
+}
+
+hipError_t launch_xent_forward(const XentArgs &x, hipStream_t st)
+{
+    const Listed l = lay_out(x.ws, x.N, x.V, x.D, x.dtype, false);
+    hipError_t e = launch_list(x, l, false, st);
+    if (e != hipSuccess) return e;
+    if (x.N) {
+        MmArgs a = logits_of(x, l, 0, x.V);
+        a.part = l.part;
+        a.picked = l.picked;
+        if ((e = launch_mm<EPI_LSE, false, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+        hipLaunchKernelGGL(gscan_xent_join_kernel, dim3((unsigned)((x.N + kJoinRows - 1) / kJoinRows)), dim3(256),
+                           0, st, x, l, tiles_of_m(x.V, x.dtype));
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!x.reduction) return hipSuccess;
+    hipLaunchKernelGGL(gscan_xent_total_kernel, dim3(1), dim3(kLThreads), 0, st, x, l);
+    return hipGetLastError();
+}
+
+hipError_t launch_xent_backward(const XentArgs &x, hipStream_t st)
+{
+    const Listed l = lay_out(x.ws, x.N, x.V, x.D, x.dtype, true);
+    const size_t es = x.dtype ? 2 : 4;
+    hipError_t e = launch_list(x, l, true, st);
+    if (e != hipSuccess) return e;
+    for (int64_t v0 = 0; v0 < x.V; v0 += l.piece) {
+        const int64_t v1 = v0 + l.piece < x.V ? v0 + l.piece : x.V;
+        const int64_t ld = (v1 - v0 + 7) / 8 * 8;
+        if (x.N) {
+            MmArgs a = logits_of(x, l, v0, v1);
+            a.up = x.reduction ? nullptr : l.up;
+            a.lse = l.lse;
+            a.out = l.g;
+            a.ldo = ld;
+            if ((e = launch_mm<EPI_DLOGIT, false, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+        }
+        if (x.dh && x.N) {
+            MmArgs a;
+            a.a = reinterpret_cast<const char *>(x.w) + (size_t)v0 * x.ldw * es;
+            a.lda = x.ldw;
+            a.b = l.g;
+            a.ldb = ld;
+            a.M = x.D;
+            a.N = x.N;
+            a.K = v1 - v0;
+            a.count = l.count;
+            a.row = l.row;
+            a.out = x.dh;
+            a.ldo = x.D;
+            a.sum = l.sum;
+            a.factor = x.reduction ? l.factor : nullptr;
+            a.first = v0 == 0;
+            a.last = v1 == x.V;
+            if ((e = launch_mm<EPI_ADD, true, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+        }
+        if (x.dw) {  // zeros without tokens
+            MmArgs a;
+            a.a = x.h;
+            a.lda = x.ldh;
+            a.b = l.g;
+            a.ldb = ld;
+            a.M = x.D;
+            a.N = v1 - v0;
+            a.N1 = a.N;
+            a.K = x.N;
+            a.count = l.count;
+            a.alt = l.h;
+            a.ldalt = x.D;
+            a.out = reinterpret_cast<char *>(x.dw) + (size_t)v0 * x.D * es;
+            a.ldo = x.D;
+            a.factor = x.reduction ? l.factor : nullptr;
+            if ((e = launch_mm<EPI_STORE, true, true, LIMIT_K>(a, x.dtype, st)) != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace gscan

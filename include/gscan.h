@@ -449,6 +449,138 @@ int gscan_qk_norm_rope_backward(const gscan_qk_norm_t *desc, const void *q, cons
 
 size_t gscan_qk_norm_rope_workspace_bytes(const gscan_qk_norm_t *desc);
 
+/*
+ * ----------------------------------------------------------------------
+ * A language model around the scans: its tokens' embedding, the gated
+ * projection of its feed-forward blocks, and the cross entropy over its
+ * vocabulary.
+ *
+ * Rows are read at a stride (in elements, at least 0): a slice of a wider
+ * matrix needs no copy.  Outputs are dense.  Widths are multiples of 8 up to
+ * 65536; row pointers and strides in bytes are multiples of 16.  Sums are
+ * fp32 or better and in a fixed order: results are bitwise reproducible.
+ * No output may overlap an input.
+ */
+
+/*
+ * Embedding: out[n] = scale * table[t_n] for the tokens t_n, and the table's
+ * gradient d_table[v] = scale * sum over n with t_n = v of d_out[n], summed in
+ * the order of n.  A token outside 0 .. vocabulary - 1 is padding: its output
+ * is zero and it adds to no gradient.  table and d_table have one type, out and
+ * d_out another (either).  d_table [vocabulary][width] is overwritten, zeros
+ * where no token is.  tokens: device int32 or int64 [tokens].
+ * Shapes: tokens >= 0 and vocabulary >= 1, both below 2^31 - 128; vocabulary *
+ * width at most 2^40.  An Inf or NaN stays in the rows of its token.
+ */
+typedef struct {
+    int64_t tokens, vocabulary, width;
+    int64_t stride;              /* of the rows of table (forward), of d_out (backward) */
+    gscan_dtype_t table_dtype, dtype;
+    int token_int64;             /* tokens are int64 (else int32) */
+    float scale;
+} gscan_embed_t;
+
+int gscan_embed_forward(const gscan_embed_t *desc, const void *table, const void *tokens, void *out,
+                        hipStream_t stream);
+
+/* workspace: at least gscan_embed_workspace_bytes() bytes, 256-byte aligned, or
+ * NULL to allocate stream-ordered. */
+int gscan_embed_backward(const gscan_embed_t *desc, const void *d_out, const void *tokens, void *d_table,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* 0 for an invalid descriptor and for no tokens. */
+size_t gscan_embed_workspace_bytes(const gscan_embed_t *desc);
+
+/*
+ * Gated projection, the first half of a feed-forward block:
+ *   a = x w_gate^T,  b = x w_up^T,  out = act(a) * b
+ * for x [tokens][width], weights [inner][width], out [tokens][inner], all of one
+ * type.  act: a sigmoid(a); a Phi(a) (Phi the sum of the normal distribution);
+ * or that with Phi = 0.5 (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))).
+ * Backward: the gradients of x and of both weights (overwritten; dx, or both
+ * d_w, may be NULL: not wanted) for d_out [tokens][inner]; a and b are formed
+ * again.  With bf16 operands the gradients of a and b are rounded to bf16
+ * before the products that take them.
+ * Shapes: width and inner multiples of 8 up to 65536, tokens >= 0, tokens * the
+ * larger width at most 2^42, row strides up to 2^21 elements.  An Inf or NaN of
+ * x reaches its token's row of out and dx and, as in the formulas, the weights'
+ * gradients.
+ */
+typedef enum {
+    GSCAN_ACT_SILU = 0,
+    GSCAN_ACT_GELU = 1,
+    GSCAN_ACT_GELU_TANH = 2
+} gscan_activation_t;
+
+typedef struct {
+    int64_t tokens, width, inner;
+    int64_t x_stride, gate_stride, up_stride;  /* of the rows of x, w_gate, w_up */
+    int64_t d_out_stride;                      /* backward only */
+    gscan_dtype_t dtype;
+    gscan_activation_t activation;
+} gscan_gated_projection_t;
+
+int gscan_gated_projection_forward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
+                                   const void *w_up, void *out, hipStream_t stream);
+
+/* workspace: at least gscan_gated_projection_workspace_bytes() bytes, 256-byte
+ * aligned, or NULL to allocate stream-ordered. */
+int gscan_gated_projection_backward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
+                                    const void *w_up, const void *d_out, void *dx, void *d_w_gate,
+                                    void *d_w_up, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t gscan_gated_projection_workspace_bytes(const gscan_gated_projection_t *desc);
+
+/*
+ * Cross entropy of softmax(scale * h weight^T) without the logits in memory,
+ * for h [tokens][width], weight [vocabulary][width] (one type) and targets
+ * (device int32 or int64 [tokens]):
+ *   lse[n] = log sum over v of exp(scale * <h_n, weight_v>)
+ *   loss[n] = lse[n] - scale * <h_n, weight_target[n]>
+ * A token whose target is outside 0 .. vocabulary - 1 does not count: its loss
+ * and lse are zero, it has no part in any gradient (its own is zero), and
+ * nothing that its row of h holds, NaN included, reaches anything.  loss is
+ * fp32: [tokens] (GSCAN_LOSS_EACH), or one value, the sum over the tokens that
+ * count or their mean (zero where none counts).
+ * Backward: dh [tokens][width] and d_weight [vocabulary][width] (overwritten;
+ * either may be NULL: not wanted) for d_loss, of loss's shape, from the lse that
+ * the forward left (not read for tokens that do not count).  The gradient of the
+ * logits exists for a piece of the vocabulary at a time; with bf16 operands it
+ * is rounded to bf16.
+ * Shapes: width a multiple of 8 up to 65536; any vocabulary >= 1 and tokens >=
+ * 0, both below 2^31 - 128; vocabulary * width at most 2^40; tokens times
+ * either at most 2^43; row strides up to 2^21 elements.
+ */
+typedef enum {
+    GSCAN_LOSS_EACH = 0,
+    GSCAN_LOSS_SUM = 1,
+    GSCAN_LOSS_MEAN = 2
+} gscan_reduction_t;
+
+typedef struct {
+    int64_t tokens, width, vocabulary;
+    int64_t h_stride, weight_stride;
+    gscan_dtype_t dtype;
+    gscan_reduction_t reduction;
+    int target_int64;            /* targets are int64 (else int32) */
+    float scale;
+} gscan_linear_cross_entropy_t;
+
+/* workspace: at least the matching query's bytes, 256-byte aligned, or NULL to
+ * allocate stream-ordered. */
+int gscan_linear_cross_entropy_forward(const gscan_linear_cross_entropy_t *desc, const void *h, const void *weight,
+                                       const void *target, float *loss, float *lse, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+int gscan_linear_cross_entropy_backward(const gscan_linear_cross_entropy_t *desc, const void *h, const void *weight,
+                                        const void *target, const float *lse, const float *d_loss, void *dh,
+                                        void *d_weight, void *workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+
+/* 0 for an invalid descriptor. */
+size_t gscan_linear_cross_entropy_forward_workspace_bytes(const gscan_linear_cross_entropy_t *desc);
+size_t gscan_linear_cross_entropy_backward_workspace_bytes(const gscan_linear_cross_entropy_t *desc);
+
 /* Static description of a status code. */
 const char *gscan_status_string(int status);
 
