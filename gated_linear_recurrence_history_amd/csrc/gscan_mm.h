@@ -148,19 +148,20 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
     if constexpr (E == EPI_STORE || E == EPI_ADD)
         if (a.factor) factor = *a.factor;
     if constexpr (E == EPI_LSE) {
+        const int end = (int)(a.M - m0 < 4096 ? a.M - m0 : 4096);  // of the tile's m
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             const int64_t n = n0 + nat + 32 * j + col;
-            const int64_t t = n < N ? (int64_t)a.target[n] - a.v0 : -1;
+            const int t = n < N ? (int)(a.target[n] - a.v0 - m0) : -1;
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int64_t m = m0 + mat(i) + 8 * (r / 4) + 4 * hi + r % 4;
+                    const int m = mat(i) + 8 * (r / 4) + 4 * hi + r % 4;
                     float z = acc[i][j][r] * a.scale;
                     if (m == t) a.picked[n] = z;
-                    z = m < a.M ? z : -INFINITY;
+                    z = m < end ? z : -INFINITY;
                     acc[i][j][r] = z;
                     top = fmaxf(top, z);
                 }
@@ -378,23 +379,269 @@ __global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
                                     reinterpret_cast<float2 *>(&lds[0][0][0]));
 }
 
+// --------------------------------------------------- products of bf16
+
+// Tiles of TM = 32 MI WM by TN = 64 WN, a wavefront's part 32 MI x 64 in registers.
+// Steps of 64 of k go from memory straight into LDS (16 bytes per lane, no
+// register in between), a step ahead, into the half that the step before has been
+// read from.  Rows of a KC tile hold eight pieces of 16 bytes; piece c of row r lies
+// at c ^ (r % 8), so that the 16-byte reads of eight rows meet no bank twice.  Rows
+// of an RC tile are k; their pieces lie at c ^ 2 (k % 4), so that the four rows of a
+// transposed read (four k of 16 columns) do not either.  Memory behind an operand's
+// last row is not touched: offsets past the end of its buffer read zeros, and what
+// of the last step lies past K is sent there.
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+template <class T>
+using lds_t = __attribute__((address_space(3))) T;
+template <class T>
+__device__ __forceinline__ lds_t<T> *in_lds(uint32_t address)
+{
+    return (lds_t<T> *)(uintptr_t)address;
+}
+
+constexpr int kBK = 64;
+constexpr uint32_t kNowhere = 0x7ffffff0u;  // past the end of every buffer
+
+// 64 lanes' 16 bytes at their offsets of the buffer, one after the other from the
+// LDS address on.  The wait for them is load_wait().
+__device__ __forceinline__ void load_to_lds(const u4 &buffer, uint32_t offset, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(offset), "s"(buffer), "s"(lds)
+                 : "memory");
+}
+__device__ __forceinline__ void load_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// An operand's buffer at a step: what there is from its first element on.
+__device__ __forceinline__ u4 buffer_at(uint64_t base, int64_t bytes)
+{
+    const uint32_t n = (uint32_t)(bytes < 0 ? 0 : bytes < 0x7fffffe0ll ? bytes : 0x7fffffe0ll);
+    return u4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
+              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) & 0xffffu,
+              (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
+}
+
+// A tile of T rows (KC) or columns (RC): offsets of a lane's loads, and where the
+// lane finds its elements.
+template <bool RC, int T, int W>
+struct Tile {
+    static constexpr int kLoads = T / 8 / W;      // of a wavefront
+    static constexpr int kPer = 1024 / (2 * T);   // RC: rows that one load covers
+    uint32_t off[kLoads];
+    uint32_t k[kLoads];    // the first k of the lane's 16 bytes
+    uint32_t at[RC ? 2 : 4];
+
+    __device__ __forceinline__ void set(int wave, int lane, uint32_t ld, int row)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = wave + W * i;
+            if constexpr (RC) {
+                const int r = q * kPer + lane / (64 / kPer), p = lane % (64 / kPer);
+                k[i] = (uint32_t)r;
+                off[i] = (uint32_t)r * ld * 2 + (uint32_t)(p ^ (2 * (r & 3))) * 16;
+            } else {
+                const int r = 8 * q + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+                k[i] = 8 * (uint32_t)c;
+                off[i] = (uint32_t)r * ld * 2 + (uint32_t)c * 16;
+            }
+        }
+        // row: the first of the wavefront's rows (KC) or columns (RC), a multiple of 32
+        if constexpr (RC) {
+            const int p = lane & 15, g = lane >> 4;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {  // even and odd groups of 32 columns
+                const int c = (4 * (row / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ (2 * (p >> 2));
+                at[o] = (uint32_t)((8 * (g >> 1) + (p >> 2)) * 2 * T + 16 * c + 8 * (p & 1));
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                at[s] = (uint32_t)((row + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7)));
+        }
+    }
+
+    // `half`: second halves of the loads come from another buffer (two weights)
+    template <bool TWO>
+    __device__ __forceinline__ void load(const u4 &b, const u4 &b2, uint32_t lds, int wave, int64_t left) const
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t o = off[i];
+            if (left < kBK && k[i] >= left) o = kNowhere;
+            load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, o, lds + (uint32_t)(wave + W * i) * 1024u);
+        }
+    }
+
+    // Elements of 16 k (the step's s-th 16) of the group `i` of 32 rows or columns
+    // from the wavefront's first: eight of a row per lane.
+    __device__ __forceinline__ bf8 get(uint32_t lds, int i, int s) const
+    {
+        if constexpr (RC) {
+            const uint32_t p = lds + at[i & 1] + (uint32_t)(s * 16 * 2 * T + 64 * (i & ~1));
+            const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p));
+            const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p + 4 * 2 * T));
+            const u4 v = {__builtin_bit_cast(uint2, x).x, __builtin_bit_cast(uint2, x).y,
+                          __builtin_bit_cast(uint2, y).x, __builtin_bit_cast(uint2, y).y};
+            return __builtin_bit_cast(bf8, v);
+        } else {
+            return *in_lds<bf8>(lds + at[s] + (uint32_t)(i * 4096));
+        }
+    }
+};
+
+template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a)
+{
+    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    constexpr int kW = WM * WN, kTA = 32 * MI * WM, kTN = 64 * WN;
+    constexpr int kTM = kGated ? kTA / 2 : kTA;  // of m
+    constexpr uint32_t kStage = (kTA + kTN) * 2 * kBK;
+    __shared__ __align__(1024) char lds[2 * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    int64_t N = a.N, K = a.K, lda = a.lda, ldb = a.ldb;
+    const void *pa = a.a, *pb = a.b;
+    if constexpr (L != LIMIT_NONE) {
+        const int64_t c = *a.count;
+        if (a.alt && c < (L == LIMIT_N ? a.N : a.K)) {
+            (L == LIMIT_N ? pb : pa) = a.alt;
+            (L == LIMIT_N ? ldb : lda) = a.ldalt;
+        }
+        (L == LIMIT_N ? N : K) = c;
+    }
+    int64_t im, in;
+    tile_of(blockIdx.x, (a.M + kTM - 1) / kTM, (a.N + kTN - 1) / kTN, im, in);
+    const int64_t m0 = im * kTM, n0 = in * kTN;
+    if (n0 >= N) return;
+
+    Tile<RCA, kTA, kW> ta;
+    Tile<RCB, kTN, kW> tb;
+    ta.set(wave, lane, (uint32_t)lda, kGated ? 16 * MI * wm : 32 * MI * wm);
+    tb.set(wave, lane, (uint32_t)ldb, 64 * wn);
+    if constexpr (kGated) {  // the second half of the tile's rows: the other weight's
+#pragma unroll
+        for (int i = ta.kLoads / 2; i < ta.kLoads; ++i)
+            ta.off[i] = (uint32_t)(8 * (wave + kW * (i - ta.kLoads / 2)) + (lane >> 3)) * (uint32_t)a.lda2 * 2 +
+                        2 * ta.k[i];
+    }
+    const bool two = RCA && a.a2;  // a second weight behind the first along k
+    const int64_t part = two ? a.K1 : K;
+    const int64_t steps = (part + kBK - 1) / kBK * (two ? 2 : 1);
+    // what there is of an operand from its first element of this tile on, in bytes
+    auto extent = [&](bool rc, int64_t ld, int64_t rows, int64_t tile, int64_t k) {
+        // (whole pieces: a gradient of the logits has zeros up to them)
+        if (rc) return ((k - 1) * ld + (rows + 7) / 8 * 8) * 2;
+        return (((rows < tile ? rows : tile) - 1) * ld + (k + 7) / 8 * 8) * 2;
+    };
+    auto first = [&](bool rc, const void *p, int64_t ld, int64_t r) {
+        return reinterpret_cast<uint64_t>(p) + (uint64_t)(rc ? r : r * ld) * 2u;
+    };
+    uint64_t ba = first(RCA, pa, lda, m0), ba2 = kGated ? first(false, a.a2, a.lda2, m0) : 0;
+    uint64_t bb = first(RCB, pb, ldb, n0);
+    int64_t na = extent(RCA, lda, a.M - m0, kTM, part), na2 = kGated ? extent(false, a.lda2, a.M - m0, kTM, part) : 0;
+    int64_t nb = extent(RCB, ldb, N - n0, kTN, part);
+    const int64_t ga = RCA ? lda * 2 * kBK : 2 * kBK, gb = RCB ? ldb * 2 * kBK : 2 * kBK;
+    int64_t left = part;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_t<char> *)lds;
+    auto request = [&](uint32_t stage) {
+        const u4 da = buffer_at(ba, na), da2 = kGated ? buffer_at(ba2, na2) : da;
+        ta.template load<kGated>(da, da2, stage, wave, left);
+        tb.template load<false>(buffer_at(bb, nb), da, stage + kTA * 2 * kBK, wave, left);
+        ba += (uint64_t)ga;
+        na -= ga;
+        if (kGated) {
+            ba2 += (uint64_t)ga;
+            na2 -= ga;
+        }
+        bb += (uint64_t)gb;
+        nb -= gb;
+        left -= kBK;
+        if (two && left <= 0) {
+            ba = first(true, a.a2, a.lda2, m0);
+            na = extent(true, a.lda2, a.M - m0, kTM, part);
+            bb = first(RCB, pb, ldb, n0) + (uint64_t)(RCB ? part * ldb : part) * 2u;
+            nb = extent(RCB, ldb, N - n0, kTN, part);
+            left = part;
+        }
+    };
+
+    f16v acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
+    auto group = [&](int i) { return kGated && i >= MI / 2 ? i - MI / 2 + kTM / 32 : i; };
+    if (steps > 0) {
+        request(base);
+        load_wait();
+        __syncthreads();
+    }
+    for (int64_t t = 0; t < steps; ++t) {
+        const uint32_t here = base + (uint32_t)(t & 1) * kStage;
+        if (t + 1 < steps) request(base + (uint32_t)((t + 1) & 1) * kStage);
+#pragma unroll
+        for (int s = 0; s < kBK / 16; ++s) {
+            bf8 x[MI], y[2];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) x[i] = ta.get(here, group(i), s);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) y[j] = tb.get(here + kTA * 2 * kBK, j, s);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+        }
+        load_wait();
+        __syncthreads();
+    }
+    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * i; };
+    epilogue<E, true, MI, 2, WM>(a, acc, im, m0, n0, N, wm, 64 * wn, kTN, mat, reinterpret_cast<float2 *>(lds));
+}
+
+struct MmGrid {
+    int64_t tiles;
+    bool big;
+};
+// Tiles of 256 x 256 where they fill the device, of 128 x 128 elsewhere.
+MmGrid mm_grid(int64_t M, int64_t N, bool gated)
+{
+    auto tiles = [&](int64_t t) { return ((M + (gated ? t / 2 : t) - 1) / (gated ? t / 2 : t)) * ((N + t - 1) / t); };
+    if (tiles(256) >= 192) return MmGrid{tiles(256), true};
+    return MmGrid{tiles(128), false};
+}
+
 template <Epi E, bool RCA, bool RCB, Limit L>
 hipError_t launch_mm(const MmArgs &a, int dtype, hipStream_t st)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    if (dtype) {
+        const MmGrid g = mm_grid(a.M, a.N, kGated);
+        if (!g.tiles) return hipSuccess;
+        if (g.big)
+            hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, 4, 2, 4>), dim3((unsigned)g.tiles), dim3(512), 0,
+                               st, a);
+        else
+            hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, 2, 2, 2>), dim3((unsigned)g.tiles), dim3(256), 0,
+                               st, a);
+        return hipGetLastError();
+    }
     constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;
     const int64_t tiles = ((a.M + kTile - 1) / kTile) * ((a.N + kF32Tile - 1) / kF32Tile);
     if (!tiles) return hipSuccess;
-    auto *k = dtype ? gscan_mm_f32_kernel<E, RCA, RCB, L, true> : gscan_mm_f32_kernel<E, RCA, RCB, L, false>;
-    hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(kF32Threads), 0, st, a);
+    hipLaunchKernelGGL((gscan_mm_f32_kernel<E, RCA, RCB, L, false>), dim3((unsigned)tiles), dim3(kF32Threads), 0, st,
+                       a);
     return hipGetLastError();
 }
 
 // Tiles of m: the partial results of EPI_LSE for each n.
-int64_t tiles_of_m(int64_t M, int dtype)
+int64_t tiles_of_m(int64_t M, int64_t N, int dtype)
 {
-    (void)dtype;
-    return (M + kF32Tile - 1) / kF32Tile;
+    const int t = dtype && mm_grid(M, N, false).big ? 256 : 128;
+    return (M + t - 1) / t;
 }
 
 }  // namespace

@@ -70,7 +70,7 @@ Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
     } else {
         l.picked = (float *)take((size_t)N * 4);
         l.loss = (float *)take((size_t)N * 4);
-        l.part = (float2 *)take((size_t)tiles_of_m(V, dtype) * N * sizeof(float2));
+        l.part = (float2 *)take((size_t)tiles_of_m(V, N, dtype) * N * sizeof(float2));
     }
     l.bytes = at;
     return l;
@@ -227,7 +227,7 @@ hipError_t launch_xent_forward(const XentArgs &x, hipStream_t st)
         a.picked = l.picked;
         if ((e = launch_mm<EPI_LSE, false, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
         hipLaunchKernelGGL(gscan_xent_join_kernel, dim3((unsigned)((x.N + kJoinRows - 1) / kJoinRows)), dim3(256),
-                           0, st, x, l, tiles_of_m(x.V, x.dtype));
+                           0, st, x, l, tiles_of_m(x.V, x.N, x.dtype));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!x.reduction) return hipSuccess;
