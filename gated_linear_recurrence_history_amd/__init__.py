@@ -21,7 +21,7 @@ from .embedding import (EmbedFunction, embed, embed_backward,  # noqa: F401
                         embed_backward_workspace_bytes, embed_forward)
 from .gated_projection import (GatedProjectionFunction, gated_projection,  # noqa: F401
                                gated_projection_backward, gated_projection_backward_workspace_bytes,
-                               gated_projection_forward)
+                               gated_projection_forward, gated_projection_forward_workspace_bytes)
 from .cross_entropy import (LinearCrossEntropyFunction, linear_cross_entropy,  # noqa: F401
                             linear_cross_entropy_backward,
                             linear_cross_entropy_backward_workspace_bytes, linear_cross_entropy_forward,
@@ -42,6 +42,7 @@ __all__ = ["forward", "forward_enrich", "backward", "backward_full", "backward_w
            "EmbedFunction", "embed", "embed_backward", "embed_backward_workspace_bytes",
            "embed_forward", "GatedProjectionFunction", "gated_projection", "gated_projection_backward",
            "gated_projection_backward_workspace_bytes", "gated_projection_forward",
+           "gated_projection_forward_workspace_bytes",
            "LinearCrossEntropyFunction", "linear_cross_entropy", "linear_cross_entropy_backward",
            "linear_cross_entropy_backward_workspace_bytes", "linear_cross_entropy_forward",
            "linear_cross_entropy_forward_workspace_bytes"]

@@ -100,13 +100,13 @@ def lib():
         L.gscan_embed_backward.restype = ctypes.c_int
         L.gscan_embed_workspace_bytes.argtypes = [vp]
         L.gscan_embed_workspace_bytes.restype = sz
-        for f, n, ws in ((L.gscan_gated_projection_forward, 5, False),
-                         (L.gscan_gated_projection_backward, 8, True),
-                         (L.gscan_linear_cross_entropy_forward, 6, True),
-                         (L.gscan_linear_cross_entropy_backward, 8, True)):
-            f.argtypes = [vp] * n + ([vp, sz] if ws else []) + [vp]
+        for f, n in ((L.gscan_gated_projection_forward, 5), (L.gscan_gated_projection_backward, 8),
+                     (L.gscan_linear_cross_entropy_forward, 6),
+                     (L.gscan_linear_cross_entropy_backward, 8)):
+            f.argtypes = [vp] * n + [vp, sz, vp]
             f.restype = ctypes.c_int
-        for f in (L.gscan_gated_projection_workspace_bytes,
+        for f in (L.gscan_gated_projection_forward_workspace_bytes,
+                  L.gscan_gated_projection_backward_workspace_bytes,
                   L.gscan_linear_cross_entropy_forward_workspace_bytes,
                   L.gscan_linear_cross_entropy_backward_workspace_bytes):
             f.argtypes = [vp]

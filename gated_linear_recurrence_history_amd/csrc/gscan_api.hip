@@ -1116,7 +1116,8 @@ size_t gscan_embed_workspace_bytes(const gscan_embed_t *desc)
 }
 
 int gscan_gated_projection_forward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
-                                   const void *w_up, void *out, hipStream_t stream)
+                                   const void *w_up, void *out, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream)
 {
     gscan::GateArgs a;
     int st = check_gate(desc, x, w_gate, w_up, &a);
@@ -1124,8 +1125,11 @@ int gscan_gated_projection_forward(const gscan_gated_projection_t *desc, const v
     if (a.N > 0 && !out) return fail(GSCAN_ERR_INVALID_ARGUMENT, "null out");
     if (mis(out, 16)) return fail(GSCAN_ERR_MISALIGNED, "out must be 16-byte aligned");
     a.out = out;
-    return with_workspace("gated projection", nullptr, 0, 0, stream,
-                          [&](void *) { return gscan::launch_gate_forward(a, stream); });
+    return with_workspace("gated projection", workspace, workspace_bytes, gscan::gate_workspace_bytes(a, false),
+                          stream, [&](void *ws) {
+                              a.ws = ws;
+                              return gscan::launch_gate_forward(a, stream);
+                          });
 }
 
 int gscan_gated_projection_backward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
@@ -1149,17 +1153,24 @@ int gscan_gated_projection_backward(const gscan_gated_projection_t *desc, const 
     a.dwg = d_w_gate;
     a.dwu = d_w_up;
     return with_workspace("gated projection backward", workspace, workspace_bytes,
-                          gscan::gate_workspace_bytes(a.N, a.F, a.dtype), stream, [&](void *ws) {
+                          gscan::gate_workspace_bytes(a, true), stream, [&](void *ws) {
                               a.ws = ws;
                               return gscan::launch_gate_backward(a, stream);
                           });
 }
 
-size_t gscan_gated_projection_workspace_bytes(const gscan_gated_projection_t *desc)
+size_t gscan_gated_projection_forward_workspace_bytes(const gscan_gated_projection_t *desc)
 {
     gscan::GateArgs a;
     if (check_gate(desc, nullptr, nullptr, nullptr, &a, false) != GSCAN_OK) return 0;
-    return gscan::gate_workspace_bytes(a.N, a.F, a.dtype);
+    return gscan::gate_workspace_bytes(a, false);
+}
+
+size_t gscan_gated_projection_backward_workspace_bytes(const gscan_gated_projection_t *desc)
+{
+    gscan::GateArgs a;
+    if (check_gate(desc, nullptr, nullptr, nullptr, &a, false) != GSCAN_OK) return 0;
+    return gscan::gate_workspace_bytes(a, true);
 }
 
 int gscan_linear_cross_entropy_forward(const gscan_linear_cross_entropy_t *desc, const void *h, const void *weight,

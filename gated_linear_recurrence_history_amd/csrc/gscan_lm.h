@@ -36,9 +36,9 @@ struct GateArgs {
     int64_t N = 0, ldx = 0, ldg = 0, ldu = 0, ldd = 0;
     int D = 0, F = 0;
     int dtype = 0, act = 0;
-    void *ws = nullptr;            // backward: gradients of both products, [N][2 F]
+    void *ws = nullptr;            // parts of tiles; backward: gradients of both products, [N][2 F]
 };
-size_t gate_workspace_bytes(int64_t N, int F, int dtype);
+size_t gate_workspace_bytes(const GateArgs &a, bool backward);
 hipError_t launch_gate_forward(const GateArgs &a, hipStream_t stream);
 hipError_t launch_gate_backward(const GateArgs &a, hipStream_t stream);
 

@@ -57,6 +57,7 @@ struct MmArgs {
     int first = 1, last = 1;
     float scale = 1.f;
     int act = 0;
+    float *partial = nullptr;       // sums of parts of tiles (Work)
 };
 
 // -------------------------------------------------------------- activations
@@ -123,16 +124,22 @@ __device__ __forceinline__ void join_lse(float &m, float &s, float m2, float s2)
 
 // ------------------------------------------------------------------ the tiles
 
-// Tile of a workgroup.  Workgroups go to the eight XCDs in turn: each takes
-// consecutive tiles, which walk eight tiles of n before the next tile of m, so
-// that what runs at the same time on an XCD shares its rows in that XCD's L2.
-__device__ __forceinline__ void tile_of(int64_t id, int64_t tm, int64_t tn, int64_t &im, int64_t &in)
+// Where tile t lies: eight tiles of n before the next tile of m, so that tiles that
+// run at the same time on an XCD share their rows in that XCD's L2.
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tm, uint32_t tn, int64_t &im, int64_t &in)
 {
-    const int64_t all = tm * tn, q = all / 8, r = all % 8, x = id % 8;
-    const int64_t t = x * q + (x < r ? x : r) + id / 8;
-    const int64_t g = t / (8 * tm), left = tn - 8 * g, w = left < 8 ? left : 8, u = t - g * 8 * tm;
-    in = 8 * g + u % w;
-    im = u / w;
+    const uint32_t g = t / (8 * tm), left = tn - 8 * g, w = left < 8 ? left : 8, u = t - g * 8 * tm;
+    const uint32_t q = left < 8 ? u / w : u / 8;
+    in = 8 * g + (u - q * w);
+    im = q;
+}
+
+// Workgroups go to the eight XCDs in turn; each XCD takes consecutive ones of n
+// places.  -1: none.
+__device__ __forceinline__ int place_of(int id, int n)
+{
+    const int q = n / 8, r = n % 8, x = id % 8, y = id / 8;
+    return y < q + (x < r ? 1 : 0) ? x * q + (x < r ? x : r) + y : -1;
 }
 
 // What a workgroup's sums become.  acc[i][j]: the 32 x 32 sums of the rows
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
     }
     const int64_t tm = (a.M + kTile - 1) / kTile, tn = (a.N + kF32Tile - 1) / kF32Tile;
     int64_t im, in;
-    tile_of(blockIdx.x, tm, tn, im, in);
+    tile_at((uint32_t)place_of((int)blockIdx.x, (int)(tm * tn)), (uint32_t)tm, (uint32_t)tn, im, in);
     const int64_t m0 = im * kTile, n0 = in * kF32Tile;
     if (n0 >= N) return;
 
@@ -492,6 +499,83 @@ struct Tile {
     }
 };
 
+// Who does what.  Every workgroup (as many as fit the device at once) does whole
+// tiles while there are enough for all; what is left, less than one for each, is
+// divided evenly by steps of k where that saves more than it costs: the parts of a
+// tile are sums in memory, which a second kernel adds in order.
+struct Work {
+    int tiles = 0, whole = 0;       // whole: tiles that one workgroup does alone
+    int steps = 0;                  // of a tile
+    int groups = 0;                 // workgroups
+    int parts = 0;                  // of them, those that share the divided tiles
+    int64_t share = 0;              // steps of such a workgroup,
+    int more = 0;                   // and how many of them take one more
+
+    __host__ __device__ int64_t first_step(int w) const { return w * share + (w < more ? w : more); }
+    __host__ __device__ int owner(int64_t step) const
+    {
+        const int64_t big = more * (share + 1);
+        return (int)(step < big ? step / (share + 1) : more + (step - big) / share);
+    }
+};
+
+constexpr int kPartSteps = 4;   // at least so many steps to a part
+// The parts' sums through memory and the second kernel, in steps: 64 kB (256 kB)
+// for each workgroup.
+constexpr int kPartCost = 14;
+
+__host__ __device__ __forceinline__ Work plan_work(int tiles, int steps, int groups)
+{
+    Work w;
+    w.tiles = w.whole = tiles;
+    w.steps = steps;
+    w.groups = groups;
+    const int left = (int)((uint32_t)tiles % (uint32_t)groups);
+    const int64_t total = (int64_t)left * steps;
+    const int parts = total / kPartSteps < groups ? (int)(total / kPartSteps) : groups;
+    if (left == 0 || parts <= left) return w;
+    const int64_t share = total >> 32 ? total / parts : (int64_t)((uint32_t)total / (uint32_t)parts);
+    if (steps - share - 1 <= kPartCost) return w;
+    w.whole = tiles - left;
+    w.parts = parts;
+    w.share = share;
+    w.more = (int)(total - share * parts);
+    return w;
+}
+
+__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Steps of k: of each of the two weights by itself where k runs over both.
+__host__ __device__ __forceinline__ int64_t steps_of(int64_t K, int64_t K1)
+{
+    return K1 ? 2 * ceil_div(K1, kBK) : ceil_div(K, kBK);
+}
+
+// What every kernel of a product knows of its operands.
+template <Limit L>
+struct Operands {
+    int64_t N, K, lda, ldb;
+    const void *pa, *pb;
+
+    __device__ __forceinline__ explicit Operands(const MmArgs &a)
+        : N(a.N), K(a.K), lda(a.lda), ldb(a.ldb), pa(a.a), pb(a.b)
+    {
+        if constexpr (L != LIMIT_NONE) {
+            const int64_t c = __builtin_amdgcn_readfirstlane(*a.count);
+            if (a.alt && c < (L == LIMIT_N ? N : K)) {
+                (L == LIMIT_N ? pb : pa) = a.alt;
+                (L == LIMIT_N ? ldb : lda) = a.ldalt;
+            }
+            (L == LIMIT_N ? N : K) = c;
+        }
+    }
+};
+
+// Workgroups that fit at once: one of 512 threads per CU (128 kB of LDS), two of
+// 256 (64 kB).
+template <int WM, int WN>
+constexpr int kGroups = WM * WN == 8 ? 256 : 512;
+
 template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a)
 {
@@ -500,22 +584,17 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     constexpr int kTM = kGated ? kTA / 2 : kTA;  // of m
     constexpr uint32_t kStage = (kTA + kTN) * 2 * kBK;
     __shared__ __align__(1024) char lds[2 * kStage];
+    __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    int64_t N = a.N, K = a.K, lda = a.lda, ldb = a.ldb;
-    const void *pa = a.a, *pb = a.b;
-    if constexpr (L != LIMIT_NONE) {
-        const int64_t c = *a.count;
-        if (a.alt && c < (L == LIMIT_N ? a.N : a.K)) {
-            (L == LIMIT_N ? pb : pa) = a.alt;
-            (L == LIMIT_N ? ldb : lda) = a.ldalt;
-        }
-        (L == LIMIT_N ? N : K) = c;
-    }
-    int64_t im, in;
-    tile_of(blockIdx.x, (a.M + kTM - 1) / kTM, (a.N + kTN - 1) / kTN, im, in);
-    const int64_t m0 = im * kTM, n0 = in * kTN;
-    if (n0 >= N) return;
+    const Operands<L> o(a);
+    const int64_t M = a.M, N = o.N, tm = ceil_div(M, kTM), lda = o.lda, ldb = o.ldb, lda2 = a.lda2;
+    const uint64_t pa = reinterpret_cast<uint64_t>(o.pa), pb = reinterpret_cast<uint64_t>(o.pb);
+    const uint64_t pa2 = reinterpret_cast<uint64_t>(a.a2);
+    const bool two = RCA && a.a2;  // a second weight behind the first along k
+    const int64_t part = two ? a.K1 : o.K, part_steps = ceil_div(part, kBK);
+    const int tn = (int)ceil_div(N, kTN);
+    const Work work = plan_work((int)tm * tn, (int)(two ? 2 * part_steps : part_steps), kGroups<WM, WN>);
 
     Tile<RCA, kTA, kW> ta;
     Tile<RCB, kTN, kW> tb;
@@ -524,29 +603,43 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     if constexpr (kGated) {  // the second half of the tile's rows: the other weight's
 #pragma unroll
         for (int i = ta.kLoads / 2; i < ta.kLoads; ++i)
-            ta.off[i] = (uint32_t)(8 * (wave + kW * (i - ta.kLoads / 2)) + (lane >> 3)) * (uint32_t)a.lda2 * 2 +
+            ta.off[i] = (uint32_t)(8 * (wave + kW * (i - ta.kLoads / 2)) + (lane >> 3)) * (uint32_t)lda2 * 2 +
                         2 * ta.k[i];
     }
-    const bool two = RCA && a.a2;  // a second weight behind the first along k
-    const int64_t part = two ? a.K1 : K;
-    const int64_t steps = (part + kBK - 1) / kBK * (two ? 2 : 1);
-    // what there is of an operand from its first element of this tile on, in bytes
-    auto extent = [&](bool rc, int64_t ld, int64_t rows, int64_t tile, int64_t k) {
+    // what there is of an operand from its first element of a tile on, in bytes
+    auto extent = [](bool rc, int64_t ld, int64_t rows, int64_t tile, int64_t k) {
         // (whole pieces: a gradient of the logits has zeros up to them)
         if (rc) return ((k - 1) * ld + (rows + 7) / 8 * 8) * 2;
         return (((rows < tile ? rows : tile) - 1) * ld + (k + 7) / 8 * 8) * 2;
     };
-    auto first = [&](bool rc, const void *p, int64_t ld, int64_t r) {
-        return reinterpret_cast<uint64_t>(p) + (uint64_t)(rc ? r : r * ld) * 2u;
+    auto first = [](bool rc, uint64_t p, int64_t ld, int64_t r) {
+        return p + (uint64_t)(rc ? r : r * ld) * 2u;
     };
-    uint64_t ba = first(RCA, pa, lda, m0), ba2 = kGated ? first(false, a.a2, a.lda2, m0) : 0;
-    uint64_t bb = first(RCB, pb, ldb, n0);
-    int64_t na = extent(RCA, lda, a.M - m0, kTM, part), na2 = kGated ? extent(false, a.lda2, a.M - m0, kTM, part) : 0;
-    int64_t nb = extent(RCB, ldb, N - n0, kTN, part);
-    const int64_t ga = RCA ? lda * 2 * kBK : 2 * kBK, gb = RCB ? ldb * 2 * kBK : 2 * kBK;
-    int64_t left = part;
+    const int64_t gb = RCB ? ldb * 2 * kBK : 2 * kBK;
+    uint64_t ba = 0, ba2 = 0, bb = 0;  // of the next step: where the operands begin,
+    int64_t na = 0, na2 = 0, nb = 0;   // what there is of them,
+    int64_t ga = 0, left = 0;                  // and of k
+    bool second = false;
+    int64_t m0 = 0, n0 = 0;
+    auto aim = [&](int64_t s) __attribute__((always_inline)) {
+        second = two && s >= part_steps;
+        const int64_t u = second ? s - part_steps : s;
+        const uint64_t p = second ? pa2 : pa;
+        const int64_t ld = second ? lda2 : lda;
+        ga = RCA ? ld * 2 * kBK : 2 * kBK;
+        ba = first(RCA, p, ld, m0) + (uint64_t)(u * ga);
+        na = extent(RCA, ld, M - m0, kTM, part) - u * ga;
+        if (kGated) {
+            ba2 = first(false, pa2, lda2, m0) + (uint64_t)(u * ga);
+            na2 = extent(false, lda2, M - m0, kTM, part) - u * ga;
+        }
+        bb = first(RCB, pb, ldb, n0) + (uint64_t)(second ? (RCB ? part * ldb : part) * 2 : 0) +
+             (uint64_t)(u * gb);
+        nb = extent(RCB, ldb, N - n0, kTN, part) - u * gb;
+        left = part - u * kBK;
+    };
     const uint32_t base = (uint32_t)(uintptr_t)(lds_t<char> *)lds;
-    auto request = [&](uint32_t stage) {
+    auto request = [&](uint32_t stage) __attribute__((always_inline)) {
         const u4 da = buffer_at(ba, na), da2 = kGated ? buffer_at(ba2, na2) : da;
         ta.template load<kGated>(da, da2, stage, wave, left);
         tb.template load<false>(buffer_at(bb, nb), da, stage + kTA * 2 * kBK, wave, left);
@@ -559,89 +652,222 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         bb += (uint64_t)gb;
         nb -= gb;
         left -= kBK;
-        if (two && left <= 0) {
-            ba = first(true, a.a2, a.lda2, m0);
-            na = extent(true, a.lda2, a.M - m0, kTM, part);
-            bb = first(RCB, pb, ldb, n0) + (uint64_t)(RCB ? part * ldb : part) * 2u;
-            nb = extent(RCB, ldb, N - n0, kTN, part);
-            left = part;
+        if (two && !second && left <= 0) aim(part_steps);
+    };
+
+    // this workgroup's tiles, whole ones and then its steps of the divided ones
+    const int id = (int)blockIdx.x, place = place_of(id, work.groups);
+    const int mine = work.parts ? place_of(id, work.parts) : -1;
+    int64_t step = mine >= 0 ? work.first_step(mine) : 0;
+    const int64_t end = mine >= 0 ? work.first_step(mine + 1) : 0;
+    int at = 0;  // the round's first tile
+    int64_t im = 0, in = 0;
+    int s0 = 0, s1 = 0, slot = -1;
+    auto next = [&]() __attribute__((always_inline)) -> bool {
+        int t = -1;
+        if (at < work.whole) {
+            const int last = work.whole - at;
+            const int p = last >= work.groups ? place : place_of(id, last);
+            if (p >= 0) t = at + p;
+            at += work.groups;
         }
+        s0 = 0;
+        s1 = work.steps;
+        slot = -1;
+        if (t < 0) {
+            if (step >= end) return false;
+            const int d = (int)(step >> 32 ? step / work.steps : (int64_t)((uint32_t)step / (uint32_t)work.steps));
+            const int64_t from = (int64_t)d * work.steps;
+            s0 = (int)(step - from);
+            s1 = (int)(end - from < work.steps ? end - from : work.steps);
+            step += s1 - s0;
+            if (s0 != 0 || s1 != work.steps) slot = mine + d;
+            t = work.whole + d;
+        }
+        tile_at((uint32_t)t, (uint32_t)tm, (uint32_t)tn, im, in);
+        m0 = im * kTM;
+        n0 = in * kTN;
+        return true;
     };
 
     f16v acc[MI][2];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
     auto group = [&](int i) { return kGated && i >= MI / 2 ? i - MI / 2 + kTM / 32 : i; };
-    if (steps > 0) {
-        request(base);
-        load_wait();
-        __syncthreads();
-    }
-    for (int64_t t = 0; t < steps; ++t) {
-        const uint32_t here = base + (uint32_t)(t & 1) * kStage;
-        if (t + 1 < steps) request(base + (uint32_t)((t + 1) & 1) * kStage);
+    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * i; };
+    uint32_t here = base, there = base + kStage;
+    bool more = next();
+    if (!more) return;
+    aim(s0);
+    if (s1 > s0) request(here);
+    load_wait();
+    __syncthreads();
+    while (more) {
+        const int64_t im_ = im, m0_ = m0, n0_ = n0;
+        const int slot_ = slot, count = s1 - s0;
 #pragma unroll
-        for (int s = 0; s < kBK / 16; ++s) {
-            bf8 x[MI], y[2];
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int i = 0; i < MI; ++i) x[i] = ta.get(here, group(i), s);
+            for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
+        for (int t = 0; t < count; ++t) {
+            // the next step's operands, or the next tile's first
+            if (t + 1 == count) {
+                more = next();
+                if (more) aim(s0);
+            }
+            if (more) request(there);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) y[j] = tb.get(here + kTA * 2 * kBK, j, s);
+            for (int s = 0; s < kBK / 16; ++s) {
+                bf8 x[MI], y[2];
+#pragma unroll
+                for (int i = 0; i < MI; ++i) x[i] = ta.get(here, group(i), s);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) y[j] = tb.get(here + kTA * 2 * kBK, j, s);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+            }
+            load_wait();
+            __syncthreads();
+            const uint32_t h = here;
+            here = there;
+            there = h;
+        }
+        if (count == 0) more = next();  // no k at all: sums of nothing
+        if (slot_ >= 0) {
+            f4 *p = reinterpret_cast<f4 *>(a.partial) + (int64_t)slot_ * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        p[((i * 2 + j) * 4 + g) * 64] = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                                           acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        } else {
+            epilogue<E, true, MI, 2, WM>(a, acc, im_, m0_, n0_, N, wm, 64 * wn, kTN, mat, red);
         }
-        load_wait();
-        __syncthreads();
     }
-    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * i; };
-    epilogue<E, true, MI, 2, WM>(a, acc, im, m0, n0, N, wm, 64 * wn, kTN, mat, reinterpret_cast<float2 *>(lds));
 }
 
-struct MmGrid {
-    int64_t tiles;
-    bool big;
-};
-// Tiles of 256 x 256 where they fill the device, of 128 x 128 elsewhere.
-MmGrid mm_grid(int64_t M, int64_t N, bool gated)
-{
-    auto tiles = [&](int64_t t) { return ((M + (gated ? t / 2 : t) - 1) / (gated ? t / 2 : t)) * ((N + t - 1) / t); };
-    if (tiles(256) >= 192) return MmGrid{tiles(256), true};
-    return MmGrid{tiles(128), false};
-}
-
-template <Epi E, bool RCA, bool RCB, Limit L>
-hipError_t launch_mm(const MmArgs &a, int dtype, hipStream_t st)
+// The divided tiles: a workgroup adds the parts of a tile in order (all of it for
+// EPI_LSE; else those of one of its groups of 32 rows per wavefront, or of the same
+// group of both weights) and finishes it.
+template <Epi E, Limit L, int MI, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    constexpr int kTA = 32 * MI * WM, kTN = 64 * WN, kTM = kGated ? kTA / 2 : kTA;
+    constexpr int kMine = E == EPI_LSE ? MI : kGated ? 2 : 1, kShares = MI / kMine;
+    __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM, mine = (int)(blockIdx.x % kShares);
+    const Operands<L> o(a);
+    const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kShares);
+    const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1), kGroups<WM, WN>);
+    if (d >= work.tiles - work.whole) return;
+    const int w0 = work.owner((int64_t)d * work.steps), w1 = work.owner((int64_t)(d + 1) * work.steps - 1);
+    if (w0 == w1) return;  // done whole
+    f16v acc[kMine][2];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
+    for (int w = w0; w <= w1; ++w) {
+        const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w + d) * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f4 v = p[(((mine + i * kShares) * 2 + j) * 4 + g) * 64];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] += v[e];
+                }
+    }
+    int64_t im, in;
+    tile_at((uint32_t)(work.whole + d), (uint32_t)tm, (uint32_t)tn, im, in);
+    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * (i + mine); };
+    epilogue<E, true, kMine, 2, WM>(a, acc, im, im * kTM, in * kTN, o.N, wm, 64 * wn, kTN, mat, red);
+}
+
+// The kernel of a product: tiles of 256 x 256 or of 128 x 128, by the steps that the
+// busiest workgroup has and what a step takes.
+struct MmPlan {
+    bool big = false;
+    Work work;
+    size_t bytes = 0;   // of parts of tiles
+    int64_t divided = 0;  // tiles, at most
+};
+MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited)
+{
+    auto of = [&](bool big) {
+        MmPlan p;
+        const int64_t t = big ? 256 : 128;
+        p.big = big;
+        p.work = plan_work((int)(ceil_div(M, gated ? t / 2 : t) * ceil_div(N, t)), (int)steps_of(K, K1), big ? 256 : 512);
+        p.divided = p.work.tiles - p.work.whole;
+        int64_t slots = p.work.parts + p.divided;
+        if (limited) {  // fewer tiles, or fewer steps, may be divided where these are not
+            p.divided = p.work.tiles < p.work.groups ? p.work.tiles : p.work.groups - 1;
+            slots = p.work.groups + p.divided;
+        }
+        p.bytes = (size_t)slots * (size_t)(t * t) * sizeof(float);
+        return p;
+    };
+    auto busiest = [](const Work &w) {
+        return ceil_div(w.whole, w.groups) * w.steps + (w.parts ? w.share + 1 + kPartCost : 0);
+    };
+    const MmPlan big = of(true), small = of(false);
+    return (double)busiest(big.work) * 1.25 <= (double)busiest(small.work) * 0.8 ? big : small;
+}
+
+size_t mm_bytes(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited, int dtype)
+{
+    return dtype ? plan_mm(M, N, K, K1, gated, limited).bytes : 0;
+}
+
+template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
+hipError_t launch_mm_bf16(const MmArgs &a, const MmPlan &p, hipStream_t st)
+{
+    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    constexpr int kShares = E == EPI_LSE ? 1 : kGated ? MI / 2 : MI;
+    const dim3 threads(64 * WM * WN);
+    const int64_t most = p.work.parts > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
+    const int64_t n = most < p.work.groups ? most : p.work.groups;
+    hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, MI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.divided) return e;
+    hipLaunchKernelGGL((gscan_mm_join_kernel<E, L, MI, WM, WN>), dim3((unsigned)(p.divided * kShares)), threads, 0, st,
+                       a);
+    return hipGetLastError();
+}
+
+// `partial`: mm_bytes() of memory.
+template <Epi E, bool RCA, bool RCB, Limit L>
+hipError_t launch_mm(MmArgs a, int dtype, void *partial, hipStream_t st)
+{
+    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
+    if (!a.M || !a.N) return hipSuccess;
     if (dtype) {
-        const MmGrid g = mm_grid(a.M, a.N, kGated);
-        if (!g.tiles) return hipSuccess;
-        if (g.big)
-            hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, 4, 2, 4>), dim3((unsigned)g.tiles), dim3(512), 0,
-                               st, a);
-        else
-            hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, 2, 2, 2>), dim3((unsigned)g.tiles), dim3(256), 0,
-                               st, a);
-        return hipGetLastError();
+        const MmPlan p = plan_mm(a.M, a.N, a.K, a.K1, kGated, L != LIMIT_NONE);
+        a.partial = reinterpret_cast<float *>(partial);
+        return p.big ? launch_mm_bf16<E, RCA, RCB, L, 4, 2, 4>(a, p, st)
+                     : launch_mm_bf16<E, RCA, RCB, L, 2, 2, 2>(a, p, st);
     }
     constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;
-    const int64_t tiles = ((a.M + kTile - 1) / kTile) * ((a.N + kF32Tile - 1) / kF32Tile);
-    if (!tiles) return hipSuccess;
+    const int64_t tiles = ceil_div(a.M, kTile) * ceil_div(a.N, kF32Tile);
     hipLaunchKernelGGL((gscan_mm_f32_kernel<E, RCA, RCB, L, false>), dim3((unsigned)tiles), dim3(kF32Threads), 0, st,
                        a);
     return hipGetLastError();
 }
 
 // Tiles of m: the partial results of EPI_LSE for each n.
-int64_t tiles_of_m(int64_t M, int64_t N, int dtype)
+int64_t tiles_of_m(int64_t M, int64_t N, int64_t K, int dtype)
 {
-    const int t = dtype && mm_grid(M, N, false).big ? 256 : 128;
-    return (M + t - 1) / t;
+    const int t = dtype && plan_mm(M, N, K, 0, false, true).big ? 256 : 128;
+    return ceil_div(M, t);
 }
 
 }  // namespace

@@ -38,6 +38,7 @@ struct Listed {
     float2 *part = nullptr;
     void *g = nullptr;
     float *sum = nullptr;
+    void *partial = nullptr;    // of tiles
     int64_t piece = 0;
     size_t bytes = 0;
 };
@@ -67,10 +68,19 @@ Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
         const int64_t ld = (l.piece + 7) / 8 * 8;
         l.g = take((size_t)N * ld * es);
         if (l.piece < V) l.sum = (float *)take((size_t)N * D * 4);
+        size_t parts = 0;
+        for (const int64_t v : {l.piece, V % l.piece}) {  // a last piece is smaller
+            if (!v) continue;
+            for (const size_t b : {mm_bytes(v, N, D, 0, false, true, dtype), mm_bytes(D, N, v, 0, false, true, dtype),
+                                   mm_bytes(D, v, N, 0, false, true, dtype)})
+                if (b > parts) parts = b;
+        }
+        l.partial = take(parts);
     } else {
         l.picked = (float *)take((size_t)N * 4);
         l.loss = (float *)take((size_t)N * 4);
-        l.part = (float2 *)take((size_t)tiles_of_m(V, N, dtype) * N * sizeof(float2));
+        l.part = (float2 *)take((size_t)tiles_of_m(V, N, D, dtype) * N * sizeof(float2));
+        l.partial = take(mm_bytes(V, N, D, 0, false, true, dtype));
     }
     l.bytes = at;
     return l;
@@ -225,9 +235,9 @@ hipError_t launch_xent_forward(const XentArgs &x, hipStream_t st)
         MmArgs a = logits_of(x, l, 0, x.V);
         a.part = l.part;
         a.picked = l.picked;
-        if ((e = launch_mm<EPI_LSE, false, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+        if ((e = launch_mm<EPI_LSE, false, false, LIMIT_N>(a, x.dtype, l.partial, st)) != hipSuccess) return e;
         hipLaunchKernelGGL(gscan_xent_join_kernel, dim3((unsigned)((x.N + kJoinRows - 1) / kJoinRows)), dim3(256),
-                           0, st, x, l, tiles_of_m(x.V, x.N, x.dtype));
+                           0, st, x, l, tiles_of_m(x.V, x.N, x.D, x.dtype));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!x.reduction) return hipSuccess;
@@ -250,7 +260,7 @@ hipError_t launch_xent_backward(const XentArgs &x, hipStream_t st)
             a.lse = l.lse;
             a.out = l.g;
             a.ldo = ld;
-            if ((e = launch_mm<EPI_DLOGIT, false, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+            if ((e = launch_mm<EPI_DLOGIT, false, false, LIMIT_N>(a, x.dtype, l.partial, st)) != hipSuccess) return e;
         }
         if (x.dh && x.N) {
             MmArgs a;
@@ -269,7 +279,7 @@ hipError_t launch_xent_backward(const XentArgs &x, hipStream_t st)
             a.factor = x.reduction ? l.factor : nullptr;
             a.first = v0 == 0;
             a.last = v1 == x.V;
-            if ((e = launch_mm<EPI_ADD, true, false, LIMIT_N>(a, x.dtype, st)) != hipSuccess) return e;
+            if ((e = launch_mm<EPI_ADD, true, false, LIMIT_N>(a, x.dtype, l.partial, st)) != hipSuccess) return e;
         }
         if (x.dw) {  // zeros without tokens
             MmArgs a;
@@ -287,7 +297,7 @@ hipError_t launch_xent_backward(const XentArgs &x, hipStream_t st)
             a.out = reinterpret_cast<char *>(x.dw) + (size_t)v0 * x.D * es;
             a.ldo = x.D;
             a.factor = x.reduction ? l.factor : nullptr;
-            if ((e = launch_mm<EPI_STORE, true, true, LIMIT_K>(a, x.dtype, st)) != hipSuccess) return e;
+            if ((e = launch_mm<EPI_STORE, true, true, LIMIT_K>(a, x.dtype, l.partial, st)) != hipSuccess) return e;
         }
     }
     return hipSuccess;

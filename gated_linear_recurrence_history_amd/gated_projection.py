@@ -48,25 +48,39 @@ def _describe(x, w_gate, w_up, activation):
                  _row_stride(w_up, "w_up"), 0, _type_code(x.dtype, "x"), ACTIVATIONS[activation])
 
 
-def gated_projection_forward(x, w_gate, w_up, activation: str = "silu", out=None, stream=None):
-    """act(x w_gate^T) * (x w_up^T), [..., inner] in the type of x.  `activation`:
-    "silu", "gelu" or "gelu_tanh"."""
-    d = _describe(x, w_gate, w_up, activation)
-    dev, shape = x.device, (*x.shape[:-1], w_gate.shape[0])
-    if out is not None:
-        _check_dense(out, shape, x.dtype, dev, "out")
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=dev)
-        binding._check(binding.lib().gscan_gated_projection_forward(
-            ctypes.byref(d), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), s))
-    return out
+def gated_projection_forward_workspace_bytes(x, w_gate, w_up) -> int:
+    """Workspace of gated_projection_forward for these operands (0: none needed)."""
+    d = _describe(x, w_gate, w_up, "silu")
+    return int(binding.lib().gscan_gated_projection_forward_workspace_bytes(ctypes.byref(d)))
 
 
 def gated_projection_backward_workspace_bytes(x, w_gate, w_up) -> int:
     """Workspace of gated_projection_backward for these operands."""
     d = _describe(x, w_gate, w_up, "silu")
-    return int(binding.lib().gscan_gated_projection_workspace_bytes(ctypes.byref(d)))
+    return int(binding.lib().gscan_gated_projection_backward_workspace_bytes(ctypes.byref(d)))
+
+
+def gated_projection_forward(x, w_gate, w_up, activation: str = "silu", out=None, workspace=None,
+                             stream=None):
+    """act(x w_gate^T) * (x w_up^T), [..., inner] in the type of x.  `activation`:
+    "silu", "gelu" or "gelu_tanh".
+
+    `workspace` may be a uint8 device tensor of at least
+    gated_projection_forward_workspace_bytes() bytes; otherwise one is taken from
+    torch's caching allocator where needed.
+    """
+    d = _describe(x, w_gate, w_up, activation)
+    dev, shape, L = x.device, (*x.shape[:-1], w_gate.shape[0]), binding.lib()
+    need = int(L.gscan_gated_projection_forward_workspace_bytes(ctypes.byref(d)))
+    if out is not None:
+        _check_dense(out, shape, x.dtype, dev, "out")
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=dev)
+        wp, wn, _keep = _workspace(workspace, need, dev)
+        binding._check(L.gscan_gated_projection_forward(
+            ctypes.byref(d), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), wp, wn, s))
+    return out
 
 
 def gated_projection_backward(x, w_gate, w_up, d_out, activation: str = "silu", wanted=(True, True),
@@ -85,7 +99,7 @@ def gated_projection_backward(x, w_gate, w_up, d_out, activation: str = "silu", 
         raise ValueError(f"d_out must be {x.dtype} {(*x.shape[:-1], w_gate.shape[0])}; got {d_out.dtype} "
                          f"{tuple(d_out.shape)}")
     d.d_out_stride = _row_stride(d_out, "d_out")
-    need = int(L.gscan_gated_projection_workspace_bytes(ctypes.byref(d)))
+    need = int(L.gscan_gated_projection_backward_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if wanted[0] else None
         dg, du = (torch.empty(w_gate.shape, dtype=x.dtype, device=dev) if wanted[1] else None for _ in range(2))

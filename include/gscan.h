@@ -520,16 +520,19 @@ typedef struct {
     gscan_activation_t activation;
 } gscan_gated_projection_t;
 
+/* workspace: at least the matching query's bytes, 256-byte aligned, or NULL to
+ * allocate stream-ordered (ignored where the query returns 0). */
 int gscan_gated_projection_forward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
-                                   const void *w_up, void *out, hipStream_t stream);
+                                   const void *w_up, void *out, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
 
-/* workspace: at least gscan_gated_projection_workspace_bytes() bytes, 256-byte
- * aligned, or NULL to allocate stream-ordered. */
 int gscan_gated_projection_backward(const gscan_gated_projection_t *desc, const void *x, const void *w_gate,
                                     const void *w_up, const void *d_out, void *dx, void *d_w_gate,
                                     void *d_w_up, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
-size_t gscan_gated_projection_workspace_bytes(const gscan_gated_projection_t *desc);
+/* 0 for an invalid descriptor, and where none is needed. */
+size_t gscan_gated_projection_forward_workspace_bytes(const gscan_gated_projection_t *desc);
+size_t gscan_gated_projection_backward_workspace_bytes(const gscan_gated_projection_t *desc);
 
 /*
  * Cross entropy of softmax(scale * h weight^T) without the logits in memory,
