@@ -51,7 +51,7 @@ struct MmArgs {
     const float *up = nullptr, *lse = nullptr;        // by n (up null: one)
     const float *factor = nullptr;  // EPI_STORE, EPI_ADD: of the whole output (null: one)
     float2 *part = nullptr;         // [tile of m][N]
-    float *picked = nullptr;        // by n: the target's logit
+    float *picked = nullptr;        // by n: the target's logit, in powers of two
     int64_t v0 = 0;                 // the vocabulary's entry of m = 0
     float *sum = nullptr;           // EPI_ADD between calls, [N][M]
     int first = 1, last = 1;
@@ -112,13 +112,13 @@ __device__ __forceinline__ void store4(void *p, int64_t i, const f4 &x)
         *reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i) = x;
 }
 
-// (maximum, sum of exponentials relative to it) of two sets joined.  An empty
-// set is (-inf, 0).
+// (maximum, sum of powers of two relative to it) of two sets joined, logits in
+// powers of two.  An empty set is (-inf, 0).
 __device__ __forceinline__ void join_lse(float &m, float &s, float m2, float s2)
 {
     const float top = fmaxf(m, m2);
     const float base = top == -INFINITY ? 0.f : top;
-    s = s * exp2_(1.44269504f * (m - base)) + s2 * exp2_(1.44269504f * (m2 - base));
+    s = s * exp2_(m - base) + s2 * exp2_(m2 - base);
     m = top;
 }
 
@@ -143,42 +143,61 @@ __device__ __forceinline__ int place_of(int id, int n)
 }
 
 // What a workgroup's sums become.  acc[i][j]: the 32 x 32 sums of the rows
-// m0 + mat(i) .. + 31 and n0 + nat(j) .. + 31; element r of a lane is m = 8 (r / 4) + 4
-// (lane / 32) + r % 4, n = lane % 32.  Gated tiles hold the same m of both
-// weights in acc[i] and acc[i + MI / 2].  `red`: LDS of WM * 32 * NI * WN pairs.
+// m0 + mat(i) .. + 31 and n0 + nat + 32 j .. + 31; element r of a lane is m = 8 (r / 4)
+// + 4 (lane / 32) + r % 4, n = lane % 32.  Gated tiles hold the same m of both
+// weights in acc[i] and acc[i + MI / 2].  TM, TN: the tile's m and n; red: LDS of WM *
+// TN pairs.
 template <Epi E, bool BF, int MI, int NI, int WM, class MAt>
 __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], int64_t im, int64_t m0,
-                                         int64_t n0, int64_t N, int wm, int nat, int TN, MAt mat, float2 *red)
+                                         int64_t n0, int64_t N, int wm, int nat, int TM, int TN, MAt mat,
+                                         float2 *red)
 {
     const int lane = threadIdx.x & 63, hi = lane >> 5, col = lane & 31;
-    float factor = 1.f;
-    if constexpr (E == EPI_STORE || E == EPI_ADD)
-        if (a.factor) factor = *a.factor;
+    const bool whole = m0 + TM <= a.M;
     if constexpr (E == EPI_LSE) {
-        const int end = (int)(a.M - m0 < 4096 ? a.M - m0 : 4096);  // of the tile's m
+        const int end = (int)(whole ? TM : a.M - m0);
+        const float unit = a.scale * 1.4426950408889634f;  // logits in powers of two
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             const int64_t n = n0 + nat + 32 * j + col;
             const int t = n < N ? (int)(a.target[n] - a.v0 - m0) : -1;
+            const int from = mat(0), to = mat(MI - 1) + 32;
+            if (__any(t >= from && t < to)) {
+                float z = 0.f;
+                bool has = false;
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (mat(i) + 8 * (r / 4) + 4 * hi + r % 4 == t) {
+                            z = acc[i][j][r];
+                            has = true;
+                        }
+                if (has) a.picked[n] = z * unit;
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int m = mat(i) + 8 * (r / 4) + 4 * hi + r % 4;
-                    float z = acc[i][j][r] * a.scale;
-                    if (m == t) a.picked[n] = z;
-                    z = m < end ? z : -INFINITY;
-                    acc[i][j][r] = z;
-                    top = fmaxf(top, z);
-                }
+                for (int r = 0; r < 16; ++r) acc[i][j][r] *= unit;
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (mat(i) + 8 * (r / 4) + 4 * hi + r % 4 >= end) acc[i][j][r] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
             top = fmaxf(top, __shfl_xor(top, 32));
             const float base = top == -INFINITY ? 0.f : top;
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s += exp2_(1.44269504f * (acc[i][j][r] - base));
+                for (int r = 0; r < 16; ++r) s += exp2_(acc[i][j][r] - base);
             s += __shfl_xor(s, 32);
             if (hi == 0) red[wm * TN + nat + 32 * j + col] = float2{top, s};
         }
@@ -193,73 +212,101 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
             if (n0 + n < N) a.part[im * a.N + n0 + n] = x;
         }
     } else {
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t n = n0 + nat + 32 * j + col;
-            if (n >= N) continue;
-            int64_t t = 0, place = n;
-            float up = 0.f, lse = 0.f;
-            if constexpr (E == EPI_DLOGIT) {
-                t = (int64_t)a.target[n] - a.v0;
-                up = a.up ? a.up[n] : 1.f;
-                lse = a.lse[n];
-            }
-            if constexpr (E == EPI_ADD) place = a.last ? a.row[n] : n;
+        float factor = 1.f;
+        if constexpr (E == EPI_STORE || E == EPI_ADD)
+            if (a.factor) factor = *a.factor;
+        // `all`: every m of the tile exists
+        auto finish = [&](auto all) __attribute__((always_inline)) {
             constexpr int HI = E == EPI_GATE || E == EPI_DGATE ? MI / 2 : MI;
 #pragma unroll
-            for (int i = 0; i < HI; ++i)
+            for (int j = 0; j < NI; ++j) {
+                const int64_t n = n0 + nat + 32 * j + col;
+                if (n >= N) continue;
+                const int64_t m1 = m0 + 4 * hi;
+                auto inside = [&](int m, int64_t end) { return all.value || m1 + m < end; };
+                if constexpr (E == EPI_DLOGIT) {
+                    const int t = (int)(a.target[n] - a.v0 - m1);
+                    const float up = a.up ? a.up[n] : 1.f, lse = a.lse[n];
+                    const int64_t at = n * a.ldo + m1;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int64_t m = m0 + mat(i) + 8 * g + 4 * hi;
-                    f4 v = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                    if constexpr (E == EPI_DLOGIT) {
-                        if (m >= a.ldo) continue;  // the piece's columns, padded to eight with zeros
+                    for (int i = 0; i < HI; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float z = v[e] * a.scale - lse;
-                            const float p = BF ? exp2_(1.44269504f * z) : expf(z);
-                            v[e] = m + e < a.M ? (p - (m + e == t ? 1.f : 0.f)) * up : 0.f;
+                        for (int g = 0; g < 4; ++g) {
+                            const int m = mat(i) + 8 * g;
+                            if (!inside(m, a.ldo)) continue;  // the piece's columns, padded to eight with zeros
+                            f4 v;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float z = acc[i][j][4 * g + e] * a.scale - lse;
+                                const float p = BF ? exp2_(1.44269504f * z) : expf(z);
+                                v[e] = inside(m + e, a.M) ? (p - (m + e == t ? 1.f : 0.f)) * up : 0.f;
+                            }
+                            store4<BF>(a.out, at + m, v);
                         }
-                        store4<BF>(a.out, n * a.ldo + m, v);
-                        continue;
+                } else if constexpr (E == EPI_STORE) {
+                    void *out = n < a.N1 ? a.out : a.out2;
+                    const int64_t at = (n < a.N1 ? n : n - a.N1) * a.ldo + m1;
+#pragma unroll
+                    for (int i = 0; i < HI; ++i)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (const int m = mat(i) + 8 * g; inside(m, a.M))
+                                store4<BF>(out, at + m, factor * f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                                                    acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
+                } else if constexpr (E == EPI_ADD) {
+                    const int64_t at = n * a.M + m1, to = a.last ? a.row[n] * a.ldo + m1 : 0;
+#pragma unroll
+                    for (int i = 0; i < HI; ++i) {
+                        f4 v[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            v[g] = f4{};
+                            if (!a.first && inside(mat(i) + 8 * g, a.M)) v[g] = load4<false>(a.sum, at + mat(i) + 8 * g);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int m = mat(i) + 8 * g;
+                            if (!inside(m, a.M)) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[g][e] += acc[i][j][4 * g + e];
+                            if (a.last) store4<BF>(a.out, to + m, v[g] * factor);
+                            else store4<false>(a.sum, at + m, v[g]);
+                        }
                     }
-                    if (m >= a.M) continue;  // M is a multiple of eight from here on
-                    if constexpr (E == EPI_STORE) {
-                        v *= factor;
-                        if (n < a.N1)
-                            store4<BF>(a.out, n * a.ldo + m, v);
-                        else
-                            store4<BF>(a.out2, (n - a.N1) * a.ldo + m, v);
-                    } else if constexpr (E == EPI_ADD) {
-                        if (!a.first) {
-                            const f4 s = load4<false>(a.sum, n * a.M + m);
+                } else {
+                    const int64_t at = n * a.ldo + m1;
+                    f4 d[HI * 4];
+                    if constexpr (E == EPI_DGATE) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] += s[e];
-                        }
-                        if (a.last)
-                            store4<BF>(a.out, place * a.ldo + m, v * factor);
-                        else
-                            store4<false>(a.sum, n * a.M + m, v);
-                    } else {
-                        f4 o, o2, d = {};
-                        if constexpr (E == EPI_DGATE) d = load4<BF>(a.dout, n * a.ldd + m);
+                        for (int q = 0; q < HI * 4; ++q)
+                            if (const int m = mat(q / 4) + 8 * (q % 4); inside(m, a.M))
+                                d[q] = load4<BF>(a.dout, n * a.ldd + m1 + m);
+                    }
+#pragma unroll
+                    for (int q = 0; q < HI * 4; ++q) {
+                        const int m = mat(q / 4) + 8 * (q % 4);
+                        if (!inside(m, a.M)) continue;
+                        f4 o, o2;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float f, slope;
-                            activation<BF>(v[e], a.act, f, slope);
-                            const float b = acc[HI + i][j][4 * g + e];
+                            activation<BF>(acc[q / 4][j][4 * (q % 4) + e], a.act, f, slope);
+                            const float b = acc[HI + q / 4][j][4 * (q % 4) + e];
                             if constexpr (E == EPI_GATE) {
                                 o[e] = f * b;
                             } else {
-                                o[e] = d[e] * b * slope;
-                                o2[e] = d[e] * f;
+                                o[e] = d[q][e] * b * slope;
+                                o2[e] = d[q][e] * f;
                             }
                         }
-                        store4<BF>(a.out, n * a.ldo + m, o);
-                        if constexpr (E == EPI_DGATE) store4<BF>(a.out, n * a.ldo + a.M + m, o2);
+                        store4<BF>(a.out, at + m, o);
+                        if constexpr (E == EPI_DGATE) store4<BF>(a.out, at + a.M + m, o2);
                     }
                 }
-        }
+            }
+        };
+        if (whole) finish(std::true_type{});
+        else finish(std::false_type{});
     }
 }
 
@@ -382,7 +429,7 @@ __global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
         }
     }
     if (E == EPI_LSE) __syncthreads();  // the tiles become the epilogue's memory
-    epilogue<E, BF, 2, 2, 2>(a, all, im, m0, n0, N, wm, 64 * wn, kF32Tile, mat,
+    epilogue<E, BF, 2, 2, 2>(a, all, im, m0, n0, N, wm, 64 * wn, kTile, kF32Tile, mat,
                                     reinterpret_cast<float2 *>(&lds[0][0][0]));
 }
 
@@ -394,9 +441,13 @@ __global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
 // read from.  Rows of a KC tile hold eight pieces of 16 bytes; piece c of row r lies
 // at c ^ (r % 8), so that the 16-byte reads of eight rows meet no bank twice.  Rows
 // of an RC tile are k; their pieces lie at c ^ 2 (k % 4), so that the four rows of a
-// transposed read (four k of 16 columns) do not either.  Memory behind an operand's
-// last row is not touched: offsets past the end of its buffer read zeros, and what
-// of the last step lies past K is sent there.
+// transposed read (four k of 16 columns) do not either.  Memory outside the operands
+// is not touched: what of a tile or of the last step lies outside is read from past
+// the end of the buffer, where the hardware finds zeros.
+//
+// The elements of 16 k are read from LDS while the products of the 16 before are
+// formed; for a step's first 16 that is behind the barrier that ends the step before
+// it, but before that step's last products.
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 template <class T>
@@ -410,24 +461,23 @@ __device__ __forceinline__ lds_t<T> *in_lds(uint32_t address)
 constexpr int kBK = 64;
 constexpr uint32_t kNowhere = 0x7ffffff0u;  // past the end of every buffer
 
-// 64 lanes' 16 bytes at their offsets of the buffer, one after the other from the
-// LDS address on.  The wait for them is load_wait().
-__device__ __forceinline__ void load_to_lds(const u4 &buffer, uint32_t offset, uint32_t lds)
+// 64 lanes' 16 bytes at their offsets (and `more`) of the buffer, one after the other
+// from the LDS address on.  The wait for them is load_wait().
+__device__ __forceinline__ void load_to_lds(const u4 &buffer, uint32_t offset, uint32_t more, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :
-                 : "v"(offset), "s"(buffer), "s"(lds)
+                 : "v"(offset), "s"(buffer), "s"(more), "s"(lds)
                  : "memory");
 }
 __device__ __forceinline__ void load_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// An operand's buffer at a step: what there is from its first element on.
-__device__ __forceinline__ u4 buffer_at(uint64_t base, int64_t bytes)
+// A buffer of an operand from `base` on.
+__device__ __forceinline__ u4 buffer_at(uint64_t base)
 {
-    const uint32_t n = (uint32_t)(bytes < 0 ? 0 : bytes < 0x7fffffe0ll ? bytes : 0x7fffffe0ll);
     return u4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
-              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) & 0xffffu,
-              (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
+              (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) & 0xffffu, 0x7fffffe0u,
+              0x00020000u};
 }
 
 // A tile of T rows (KC) or columns (RC): offsets of a lane's loads, and where the
@@ -437,48 +487,66 @@ struct Tile {
     static constexpr int kLoads = T / 8 / W;      // of a wavefront
     static constexpr int kPer = 1024 / (2 * T);   // RC: rows that one load covers
     uint32_t off[kLoads];
-    uint32_t k[kLoads];    // the first k of the lane's 16 bytes
     uint32_t at[RC ? 2 : 4];
 
-    __device__ __forceinline__ void set(int wave, int lane, uint32_t ld, int row)
+    // Load i of a lane: row (KC: of the tile, RC: k) and 16-byte piece (KC: of k, RC: of
+    // the tile's columns).
+    static __device__ __forceinline__ int row(int i, int wave, int lane)
     {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int q = wave + W * i;
-            if constexpr (RC) {
-                const int r = q * kPer + lane / (64 / kPer), p = lane % (64 / kPer);
-                k[i] = (uint32_t)r;
-                off[i] = (uint32_t)r * ld * 2 + (uint32_t)(p ^ (2 * (r & 3))) * 16;
-            } else {
-                const int r = 8 * q + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
-                k[i] = 8 * (uint32_t)c;
-                off[i] = (uint32_t)r * ld * 2 + (uint32_t)c * 16;
-            }
-        }
-        // row: the first of the wavefront's rows (KC) or columns (RC), a multiple of 32
+        const int q = wave + W * i;
+        return RC ? q * kPer + lane / (64 / kPer) : 8 * q + (lane >> 3);
+    }
+    static __device__ __forceinline__ int piece(int i, int wave, int lane)
+    {
+        if constexpr (RC) return (lane % (64 / kPer)) ^ (2 * (row(i, wave, lane) & 3));
+        else return (lane & 7) ^ (lane >> 3);
+    }
+
+    // `mine`: the first of the wavefront's rows (KC) or columns (RC), a multiple of 32
+    __device__ __forceinline__ void place(int lane, int mine)
+    {
         if constexpr (RC) {
             const int p = lane & 15, g = lane >> 4;
 #pragma unroll
             for (int o = 0; o < 2; ++o) {  // even and odd groups of 32 columns
-                const int c = (4 * (row / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ (2 * (p >> 2));
+                const int c = (4 * (mine / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ (2 * (p >> 2));
                 at[o] = (uint32_t)((8 * (g >> 1) + (p >> 2)) * 2 * T + 16 * c + 8 * (p & 1));
             }
         } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                at[s] = (uint32_t)((row + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7)));
+                at[s] = (uint32_t)((mine + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7)));
         }
     }
 
-    // `half`: second halves of the loads come from another buffer (two weights)
-    template <bool TWO>
-    __device__ __forceinline__ void load(const u4 &b, const u4 &b2, uint32_t lds, int wave, int64_t left) const
+    // The loads i0 .. i1 - 1 of a tile of which `there` rows (KC) or columns (RC) exist.
+    // KC: the tile's rows from `from` on are rows of another matrix (two weights).
+    __device__ __forceinline__ void aim(int i0, int i1, int wave, int lane, uint32_t ld, int there, int from = 0)
     {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t o = off[i];
-            if (left < kBK && k[i] >= left) o = kNowhere;
-            load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, o, lds + (uint32_t)(wave + W * i) * 1024u);
+        for (int i = 0; i < kLoads; ++i)
+            if (i >= i0 && i < i1) {
+                const int r = row(i, wave, lane) - from, c = piece(i, wave, lane);
+                off[i] = (RC ? 8 * c : r) < there ? (uint32_t)r * ld * 2 + (uint32_t)c * 16 : kNowhere;
+            }
+    }
+
+    // A step's loads; `left` of k are there, `k` is where the step begins (KC).
+    template <bool TWO>
+    __device__ __forceinline__ void load(const u4 &b, const u4 &b2, uint32_t k, uint32_t lds, int wave, int lane,
+                                         int left) const
+    {
+        if (left >= kBK) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, off[i], k, lds + (uint32_t)(wave + W * i) * 1024u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const bool in = (RC ? row(i, wave, lane) : 8 * piece(i, wave, lane)) < left;
+                load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, in ? off[i] : kNowhere, k,
+                            lds + (uint32_t)(wave + W * i) * 1024u);
+            }
         }
     }
 
@@ -576,166 +644,198 @@ struct Operands {
 template <int WM, int WN>
 constexpr int kGroups = WM * WN == 8 ? 256 : 512;
 
+// A workgroup's tiles in turn: whole ones, then its steps of the divided ones.
+struct Tiles {
+    int id, place, mine;   // workgroup; its place in a full round; among those that share the divided tiles
+    int at = 0;            // the round's first tile
+    int64_t step = 0, end = 0;  // of the divided tiles
+    // the present one: tile, steps s0 .. s1 - 1, slot of its sums (-1: it is whole)
+    int t = 0, s0 = 0, s1 = 0, slot = -1;
+
+    __device__ __forceinline__ Tiles(const Work &w, int id_) : id(id_)
+    {
+        place = place_of(id, w.groups);
+        mine = w.parts ? place_of(id, w.parts) : -1;
+        if (mine >= 0) {
+            step = w.first_step(mine);
+            end = w.first_step(mine + 1);
+        }
+    }
+    __device__ __forceinline__ bool next(const Work &w)
+    {
+        t = -1;
+        if (at < w.whole) {
+            const int last = w.whole - at;
+            const int p = last >= w.groups ? place : place_of(id, last);
+            if (p >= 0) t = at + p;
+            at += w.groups;
+        }
+        s0 = 0;
+        s1 = w.steps;
+        slot = -1;
+        if (t < 0) {
+            if (step >= end) return false;
+            const int d = (int)(step >> 32 ? step / w.steps : (int64_t)((uint32_t)step / (uint32_t)w.steps));
+            const int64_t from = (int64_t)d * w.steps;
+            s0 = (int)(step - from);
+            s1 = (int)(end - from < w.steps ? end - from : w.steps);
+            step += s1 - s0;
+            if (s0 != 0 || s1 != w.steps) slot = mine + d;
+            t = w.whole + d;
+        }
+        return true;
+    }
+};
+
 template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
     constexpr int kW = WM * WN, kTA = 32 * MI * WM, kTN = 64 * WN;
     constexpr int kTM = kGated ? kTA / 2 : kTA;  // of m
-    constexpr uint32_t kStage = (kTA + kTN) * 2 * kBK;
+    constexpr uint32_t kStage = (kTA + kTN) * 2 * kBK, kB = kTA * 2 * kBK;
     __shared__ __align__(1024) char lds[2 * kStage];
     __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const Operands<L> o(a);
-    const int64_t M = a.M, N = o.N, tm = ceil_div(M, kTM), lda = o.lda, ldb = o.ldb, lda2 = a.lda2;
+    const int64_t M = a.M, N = o.N, lda = o.lda, ldb = o.ldb, lda2 = a.lda2;
     const uint64_t pa = reinterpret_cast<uint64_t>(o.pa), pb = reinterpret_cast<uint64_t>(o.pb);
     const uint64_t pa2 = reinterpret_cast<uint64_t>(a.a2);
+    const int tm = (int)ceil_div(M, kTM), tn = (int)ceil_div(N, kTN);
     const bool two = RCA && a.a2;  // a second weight behind the first along k
-    const int64_t part = two ? a.K1 : o.K, part_steps = ceil_div(part, kBK);
-    const int tn = (int)ceil_div(N, kTN);
-    const Work work = plan_work((int)tm * tn, (int)(two ? 2 * part_steps : part_steps), kGroups<WM, WN>);
+    const int64_t part = two ? a.K1 : o.K;
+    const int part_steps = (int)ceil_div(part, kBK);
+    const Work work = plan_work(tm * tn, two ? 2 * part_steps : part_steps, kGroups<WM, WN>);
 
     Tile<RCA, kTA, kW> ta;
     Tile<RCB, kTN, kW> tb;
-    ta.set(wave, lane, (uint32_t)lda, kGated ? 16 * MI * wm : 32 * MI * wm);
-    tb.set(wave, lane, (uint32_t)ldb, 64 * wn);
-    if constexpr (kGated) {  // the second half of the tile's rows: the other weight's
-#pragma unroll
-        for (int i = ta.kLoads / 2; i < ta.kLoads; ++i)
-            ta.off[i] = (uint32_t)(8 * (wave + kW * (i - ta.kLoads / 2)) + (lane >> 3)) * (uint32_t)lda2 * 2 +
-                        2 * ta.k[i];
-    }
-    // what there is of an operand from its first element of a tile on, in bytes
-    auto extent = [](bool rc, int64_t ld, int64_t rows, int64_t tile, int64_t k) {
-        // (whole pieces: a gradient of the logits has zeros up to them)
-        if (rc) return ((k - 1) * ld + (rows + 7) / 8 * 8) * 2;
-        return (((rows < tile ? rows : tile) - 1) * ld + (k + 7) / 8 * 8) * 2;
-    };
-    auto first = [](bool rc, uint64_t p, int64_t ld, int64_t r) {
-        return p + (uint64_t)(rc ? r : r * ld) * 2u;
-    };
-    const int64_t gb = RCB ? ldb * 2 * kBK : 2 * kBK;
-    uint64_t ba = 0, ba2 = 0, bb = 0;  // of the next step: where the operands begin,
-    int64_t na = 0, na2 = 0, nb = 0;   // what there is of them,
-    int64_t ga = 0, left = 0;                  // and of k
-    bool second = false;
-    int64_t m0 = 0, n0 = 0;
-    auto aim = [&](int64_t s) __attribute__((always_inline)) {
-        second = two && s >= part_steps;
-        const int64_t u = second ? s - part_steps : s;
+    ta.place(lane, kGated ? 16 * MI * wm : 32 * MI * wm);
+    tb.place(lane, 64 * wn);
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_t<char> *)lds;
+
+    // Requests: two steps ahead of the products, so with tiles of their own.
+    Tiles ask(work, (int)blockIdx.x);
+    bool more = ask.next(work);
+    if (!more) return;
+    uint64_t ba = 0, ba2 = 0, bb = 0;   // the operands from the tile's first row (KC) or the step's (RC) on
+    int asked = 0, k0 = 0;              // the step, and its first k (of one weight)
+    int64_t am0 = 0, an0 = 0;
+    auto aim_k = [&]() __attribute__((always_inline)) {
+        const bool second = two && asked >= part_steps;
+        const int u = second ? asked - part_steps : asked;
+        k0 = u * kBK;
         const uint64_t p = second ? pa2 : pa;
         const int64_t ld = second ? lda2 : lda;
-        ga = RCA ? ld * 2 * kBK : 2 * kBK;
-        ba = first(RCA, p, ld, m0) + (uint64_t)(u * ga);
-        na = extent(RCA, ld, M - m0, kTM, part) - u * ga;
-        if (kGated) {
-            ba2 = first(false, pa2, lda2, m0) + (uint64_t)(u * ga);
-            na2 = extent(false, lda2, M - m0, kTM, part) - u * ga;
+        if constexpr (RCA) {
+            ta.aim(0, ta.kLoads, wave, lane, (uint32_t)ld, (int)(M - am0 < kTM ? M - am0 : kTM));
+            ba = p + (uint64_t)(am0 + k0 * ld) * 2u;
+        } else {
+            ba = p + (uint64_t)(am0 * ld) * 2u;
+            if (kGated) ba2 = pa2 + (uint64_t)(am0 * lda2) * 2u;
         }
-        bb = first(RCB, pb, ldb, n0) + (uint64_t)(second ? (RCB ? part * ldb : part) * 2 : 0) +
-             (uint64_t)(u * gb);
-        nb = extent(RCB, ldb, N - n0, kTN, part) - u * gb;
-        left = part - u * kBK;
+        if constexpr (RCB) bb = pb + (uint64_t)(an0 + k0 * ldb) * 2u;
+        else bb = pb + (uint64_t)(an0 * ldb + (second ? part : 0)) * 2u;
     };
-    const uint32_t base = (uint32_t)(uintptr_t)(lds_t<char> *)lds;
+    auto aim = [&]() __attribute__((always_inline)) {
+        int64_t im, in;
+        tile_at((uint32_t)ask.t, (uint32_t)tm, (uint32_t)tn, im, in);
+        am0 = im * kTM;
+        an0 = in * kTN;
+        asked = ask.s0;
+        const int rows = (int)(M - am0 < kTM ? M - am0 : kTM);
+        const int cols = (int)(N - an0 < kTN ? N - an0 : kTN);
+        if constexpr (kGated) {
+            ta.aim(0, ta.kLoads / 2, wave, lane, (uint32_t)lda, rows);
+            ta.aim(ta.kLoads / 2, ta.kLoads, wave, lane, (uint32_t)lda2, rows, kTM);
+        } else if constexpr (!RCA) {
+            ta.aim(0, ta.kLoads, wave, lane, (uint32_t)lda, rows);
+        }
+        tb.aim(0, tb.kLoads, wave, lane, (uint32_t)ldb, cols);
+        aim_k();
+    };
     auto request = [&](uint32_t stage) __attribute__((always_inline)) {
-        const u4 da = buffer_at(ba, na), da2 = kGated ? buffer_at(ba2, na2) : da;
-        ta.template load<kGated>(da, da2, stage, wave, left);
-        tb.template load<false>(buffer_at(bb, nb), da, stage + kTA * 2 * kBK, wave, left);
-        ba += (uint64_t)ga;
-        na -= ga;
-        if (kGated) {
-            ba2 += (uint64_t)ga;
-            na2 -= ga;
+        if (!more) return;
+        const int left = (int)(part - k0 < kBK ? part - k0 : kBK);
+        const u4 da = buffer_at(ba), da2 = kGated ? buffer_at(ba2) : da;
+        ta.template load<kGated>(da, da2, RCA ? 0u : 2u * k0, stage, wave, lane, left);
+        tb.template load<false>(buffer_at(bb), da, RCB ? 0u : 2u * k0, stage + kB, wave, lane, left);
+        if (++asked == ask.s1) {
+            more = ask.next(work);
+            if (more) aim();
+            return;
         }
-        bb += (uint64_t)gb;
-        nb -= gb;
-        left -= kBK;
-        if (two && !second && left <= 0) aim(part_steps);
+        if (RCA && two && asked == part_steps) {
+            aim_k();
+            return;
+        }
+        k0 += kBK;
+        if constexpr (RCA) ba += (uint64_t)((two && asked > part_steps ? lda2 : lda) * 2 * kBK);
+        if constexpr (RCB) bb += (uint64_t)(ldb * 2 * kBK);
     };
 
-    // this workgroup's tiles, whole ones and then its steps of the divided ones
-    const int id = (int)blockIdx.x, place = place_of(id, work.groups);
-    const int mine = work.parts ? place_of(id, work.parts) : -1;
-    int64_t step = mine >= 0 ? work.first_step(mine) : 0;
-    const int64_t end = mine >= 0 ? work.first_step(mine + 1) : 0;
-    int at = 0;  // the round's first tile
-    int64_t im = 0, in = 0;
-    int s0 = 0, s1 = 0, slot = -1;
-    auto next = [&]() __attribute__((always_inline)) -> bool {
-        int t = -1;
-        if (at < work.whole) {
-            const int last = work.whole - at;
-            const int p = last >= work.groups ? place : place_of(id, last);
-            if (p >= 0) t = at + p;
-            at += work.groups;
-        }
-        s0 = 0;
-        s1 = work.steps;
-        slot = -1;
-        if (t < 0) {
-            if (step >= end) return false;
-            const int d = (int)(step >> 32 ? step / work.steps : (int64_t)((uint32_t)step / (uint32_t)work.steps));
-            const int64_t from = (int64_t)d * work.steps;
-            s0 = (int)(step - from);
-            s1 = (int)(end - from < work.steps ? end - from : work.steps);
-            step += s1 - s0;
-            if (s0 != 0 || s1 != work.steps) slot = mine + d;
-            t = work.whole + d;
-        }
-        tile_at((uint32_t)t, (uint32_t)tm, (uint32_t)tn, im, in);
-        m0 = im * kTM;
-        n0 = in * kTN;
-        return true;
-    };
-
+    Tiles now(work, (int)blockIdx.x);
+    bool busy = now.next(work);
     f16v acc[MI][2];
+    bf8 x[2][MI], y[2][2];
     auto group = [&](int i) { return kGated && i >= MI / 2 ? i - MI / 2 + kTM / 32 : i; };
     auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * i; };
     uint32_t here = base, there = base + kStage;
-    bool more = next();
-    if (!more) return;
-    aim(s0);
-    if (s1 > s0) request(here);
-    load_wait();
-    __syncthreads();
-    while (more) {
-        const int64_t im_ = im, m0_ = m0, n0_ = n0;
-        const int slot_ = slot, count = s1 - s0;
+    if (work.steps > 0) {
+        aim();
+        request(here);
+        load_wait();
+        __syncthreads();
+        request(there);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[0][i] = ta.get(here, group(i), 0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) y[0][j] = tb.get(here + kB, j, 0);
+    }
+    while (busy) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
-        for (int t = 0; t < count; ++t) {
-            // the next step's operands, or the next tile's first
-            if (t + 1 == count) {
-                more = next();
-                if (more) aim(s0);
-            }
-            if (more) request(there);
+        for (int t = now.s0; t < now.s1; ++t) {
 #pragma unroll
             for (int s = 0; s < kBK / 16; ++s) {
-                bf8 x[MI], y[2];
+                const int u = s & 1, v = u ^ 1;
+                uint32_t from = here;
+                if (s == kBK / 16 - 1) {
+                    // everything of this step has been read and the next one's is there
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    load_wait();
+                    __syncthreads();
+                    from = there;
+                    request(here);
+                }
+                const int s1 = (s + 1) % (kBK / 16);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) x[i] = ta.get(here, group(i), s);
+                for (int j = 0; j < 2; ++j) y[v][j] = tb.get(from + kB, j, s1);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) y[j] = tb.get(here + kTA * 2 * kBK, j, s);
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
+                for (int i = 0; i < MI; ++i) {
+                    x[v][i] = ta.get(from, group(i), s1);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u][i], y[u][j], acc[i][j], 0, 0, 0);
+                }
+                // reads between the products
+                __builtin_amdgcn_sched_group_barrier(0x100, RCB ? 4 : 2, 0);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, RCA ? 2 : 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                }
             }
-            load_wait();
-            __syncthreads();
             const uint32_t h = here;
             here = there;
             there = h;
         }
-        if (count == 0) more = next();  // no k at all: sums of nothing
-        if (slot_ >= 0) {
-            f4 *p = reinterpret_cast<f4 *>(a.partial) + (int64_t)slot_ * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
+        int64_t im, in;
+        tile_at((uint32_t)now.t, (uint32_t)tm, (uint32_t)tn, im, in);
+        if (now.slot >= 0) {
+            f4 *p = reinterpret_cast<f4 *>(a.partial) + (int64_t)now.slot * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -745,51 +845,56 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
                         p[((i * 2 + j) * 4 + g) * 64] = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
                                                            acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
         } else {
-            epilogue<E, true, MI, 2, WM>(a, acc, im_, m0_, n0_, N, wm, 64 * wn, kTN, mat, red);
+            epilogue<E, true, MI, 2, WM>(a, acc, im, im * kTM, in * kTN, N, wm, 64 * wn, kTM, kTN, mat, red);
         }
+        busy = now.next(work);
     }
 }
 
 // The divided tiles: a workgroup adds the parts of a tile in order (all of it for
-// EPI_LSE; else those of one of its groups of 32 rows per wavefront, or of the same
+// EPI_LSE; else those of one of its groups of 32 x 32 per wavefront, or of the same
 // group of both weights) and finishes it.
+template <Epi E, int MI>
+constexpr int kShares = E == EPI_LSE ? 1 : (E == EPI_GATE || E == EPI_DGATE) ? MI : 2 * MI;
+
 template <Epi E, Limit L, int MI, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
     constexpr int kTA = 32 * MI * WM, kTN = 64 * WN, kTM = kGated ? kTA / 2 : kTA;
-    constexpr int kMine = E == EPI_LSE ? MI : kGated ? 2 : 1, kShares = MI / kMine;
+    constexpr int kN = kShares<E, MI>, kI = E == EPI_LSE ? MI : kGated ? 2 : 1, kJ = E == EPI_LSE ? 2 : 1;
     __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int wm = wave % WM, wn = wave / WM, mine = (int)(blockIdx.x % kShares);
+    const int wm = wave % WM, wn = wave / WM;
+    const int i0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) / 2, j0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) % 2;
     const Operands<L> o(a);
-    const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kShares);
+    const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kN);
     const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1), kGroups<WM, WN>);
     if (d >= work.tiles - work.whole) return;
     const int w0 = work.owner((int64_t)d * work.steps), w1 = work.owner((int64_t)(d + 1) * work.steps - 1);
     if (w0 == w1) return;  // done whole
-    f16v acc[kMine][2];
+    f16v acc[kI][kJ];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
+    for (int i = 0; i < kI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
+        for (int j = 0; j < kJ; ++j) acc[i][j] = f16v{};
     for (int w = w0; w <= w1; ++w) {
         const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w + d) * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
+        for (int i = 0; i < kI; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kJ; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const f4 v = p[(((mine + i * kShares) * 2 + j) * 4 + g) * 64];
+                    const f4 v = p[(((i0 + i * (MI / kI)) * 2 + j0 + j) * 4 + g) * 64];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] += v[e];
                 }
     }
     int64_t im, in;
     tile_at((uint32_t)(work.whole + d), (uint32_t)tm, (uint32_t)tn, im, in);
-    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * (i + mine); };
-    epilogue<E, true, kMine, 2, WM>(a, acc, im, im * kTM, in * kTN, o.N, wm, 64 * wn, kTN, mat, red);
+    auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * (i + i0); };
+    epilogue<E, true, kI, kJ, WM>(a, acc, im, im * kTM, in * kTN, o.N, wm, 64 * wn + 32 * j0, kTM, kTN, mat, red);
 }
 
 // The kernel of a product: tiles of 256 x 256 or of 128 x 128, by the steps that the
@@ -831,15 +936,13 @@ size_t mm_bytes(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool li
 template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
 hipError_t launch_mm_bf16(const MmArgs &a, const MmPlan &p, hipStream_t st)
 {
-    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
-    constexpr int kShares = E == EPI_LSE ? 1 : kGated ? MI / 2 : MI;
     const dim3 threads(64 * WM * WN);
     const int64_t most = p.work.parts > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
     const int64_t n = most < p.work.groups ? most : p.work.groups;
     hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, MI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.divided) return e;
-    hipLaunchKernelGGL((gscan_mm_join_kernel<E, L, MI, WM, WN>), dim3((unsigned)(p.divided * kShares)), threads, 0, st,
+    hipLaunchKernelGGL((gscan_mm_join_kernel<E, L, MI, WM, WN>), dim3((unsigned)(p.divided * kShares<E, MI>)), threads, 0, st,
                        a);
     return hipGetLastError();
 }

@@ -158,10 +158,10 @@ __global__ void __launch_bounds__(256) gscan_xent_join_kernel(XentArgs a, Listed
     __syncthreads();
     if (q == 0 && n < count) {
         for (int i = 1; i < 16; ++i) join_lse(m, s, red[i][r].x, red[i][r].y);
-        const float lse = m + logf(s);
+        const float tail = log2f(s), unit = 0.69314718055994531f;
         const int64_t i = l.row[n];
-        a.lse[i] = lse;
-        (a.reduction ? l.loss : a.loss)[i] = lse - l.picked[n];
+        a.lse[i] = (m + tail) * unit;
+        (a.reduction ? l.loss : a.loss)[i] = (m - l.picked[n] + tail) * unit;
     }
 }
 
