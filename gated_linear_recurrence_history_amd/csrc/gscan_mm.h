@@ -703,7 +703,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     const uint64_t pa = reinterpret_cast<uint64_t>(o.pa), pb = reinterpret_cast<uint64_t>(o.pb);
     const uint64_t pa2 = reinterpret_cast<uint64_t>(a.a2);
     const int tm = (int)ceil_div(M, kTM), tn = (int)ceil_div(N, kTN);
-    const bool two = RCA && a.a2;  // a second weight behind the first along k
+    constexpr bool kTwo = RCA && !RCB && E == EPI_STORE;
+    const bool two = kTwo && a.a2;  // a second weight behind the first along k
     const int64_t part = two ? a.K1 : o.K;
     const int part_steps = (int)ceil_div(part, kBK);
     const Work work = plan_work(tm * tn, two ? 2 * part_steps : part_steps, kGroups<WM, WN>);
@@ -725,8 +726,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         const bool second = two && asked >= part_steps;
         const int u = second ? asked - part_steps : asked;
         k0 = u * kBK;
-        const uint64_t p = second ? pa2 : pa;
-        const int64_t ld = second ? lda2 : lda;
+        uint64_t p = pa;
+        int64_t ld = lda;
+        if (kTwo && second) {
+            p = pa2;
+            ld = lda2;
+        }
         if constexpr (RCA) {
             ta.aim(0, ta.kLoads, wave, lane, (uint32_t)ld, (int)(M - am0 < kTM ? M - am0 : kTM));
             ba = p + (uint64_t)(am0 + k0 * ld) * 2u;
@@ -765,12 +770,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
             if (more) aim();
             return;
         }
-        if (RCA && two && asked == part_steps) {
+        if (kTwo && two && asked == part_steps) {
             aim_k();
             return;
         }
         k0 += kBK;
-        if constexpr (RCA) ba += (uint64_t)((two && asked > part_steps ? lda2 : lda) * 2 * kBK);
+        if constexpr (RCA) {
+            int64_t ld = lda;
+            if (kTwo && two && asked > part_steps) ld = lda2;
+            ba += (uint64_t)(ld * 2 * kBK);
+        }
         if constexpr (RCB) bb += (uint64_t)(ldb * 2 * kBK);
     };
 
@@ -847,6 +856,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         } else {
             epilogue<E, true, MI, 2, WM>(a, acc, im, im * kTM, in * kTN, N, wm, 64 * wn, kTM, kTN, mat, red);
         }
+        // Loads of the epilogue that some path leaves unused would make the compiler
+        // wait at the head of every step, for the requests too: wait for them here.
+        if constexpr (E != EPI_GATE) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         busy = now.next(work);
     }
 }
