@@ -531,23 +531,18 @@ struct Tile {
             }
     }
 
-    // A step's loads; `left` of k are there, `k` is where the step begins (KC).
-    template <bool TWO>
-    __device__ __forceinline__ void load(const u4 &b, const u4 &b2, uint32_t k, uint32_t lds, int wave, int lane,
-                                         int left) const
+    // Nothing from the `left`-th k of a step on.
+    __device__ __forceinline__ void cut(int wave, int lane, int left)
     {
-        if (left >= kBK) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, off[i], k, lds + (uint32_t)(wave + W * i) * 1024u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const bool in = (RC ? row(i, wave, lane) : 8 * piece(i, wave, lane)) < left;
-                load_to_lds(TWO && i >= kLoads / 2 ? b2 : b, in ? off[i] : kNowhere, k,
-                            lds + (uint32_t)(wave + W * i) * 1024u);
-            }
-        }
+        for (int i = 0; i < kLoads; ++i)
+            if ((RC ? row(i, wave, lane) : 8 * piece(i, wave, lane)) >= left) off[i] = kNowhere;
+    }
+
+    // Load i of a step; `k`: where the step begins (KC).
+    __device__ __forceinline__ void load(int i, const u4 &buffer, uint32_t k, uint32_t lds, int wave) const
+    {
+        load_to_lds(buffer, off[i], k, lds + (uint32_t)(wave + W * i) * 1024u);
     }
 
     // Elements of 16 k (the step's s-th 16) of the group `i` of 32 rows or columns
@@ -720,58 +715,60 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     bool more = ask.next(work);
     if (!more) return;
     uint64_t ba = 0, ba2 = 0, bb = 0;   // the operands from the tile's first row (KC) or the step's (RC) on
-    int asked = 0, k0 = 0;              // the step, and its first k (of one weight)
-    int64_t am0 = 0, an0 = 0;
-    auto aim_k = [&]() __attribute__((always_inline)) {
-        const bool second = two && asked >= part_steps;
-        const int u = second ? asked - part_steps : asked;
-        k0 = u * kBK;
-        uint64_t p = pa;
-        int64_t ld = lda;
-        if (kTwo && second) {
-            p = pa2;
-            ld = lda2;
-        }
-        if constexpr (RCA) {
-            ta.aim(0, ta.kLoads, wave, lane, (uint32_t)ld, (int)(M - am0 < kTM ? M - am0 : kTM));
-            ba = p + (uint64_t)(am0 + k0 * ld) * 2u;
-        } else {
-            ba = p + (uint64_t)(am0 * ld) * 2u;
-            if (kGated) ba2 = pa2 + (uint64_t)(am0 * lda2) * 2u;
-        }
-        if constexpr (RCB) bb = pb + (uint64_t)(an0 + k0 * ldb) * 2u;
-        else bb = pb + (uint64_t)(an0 * ldb + (second ? part : 0)) * 2u;
-    };
+    int asked = ask.s0, k0 = 0;         // the step, and its first k (of one weight)
     auto aim = [&]() __attribute__((always_inline)) {
         int64_t im, in;
         tile_at((uint32_t)ask.t, (uint32_t)tm, (uint32_t)tn, im, in);
-        am0 = im * kTM;
-        an0 = in * kTN;
-        asked = ask.s0;
-        const int rows = (int)(M - am0 < kTM ? M - am0 : kTM);
-        const int cols = (int)(N - an0 < kTN ? N - an0 : kTN);
+        const int64_t m0 = im * kTM, n0 = in * kTN;
+        const int rows = (int)(M - m0 < kTM ? M - m0 : kTM), cols = (int)(N - n0 < kTN ? N - n0 : kTN);
+        const bool second = kTwo && two && asked >= part_steps;
+        k0 = (second ? asked - part_steps : asked) * kBK;
+        uint64_t p = pa;
+        int64_t ld = lda;
+        if (second) {
+            p = pa2;
+            ld = lda2;
+        }
+        ta.aim(0, kGated ? ta.kLoads / 2 : ta.kLoads, wave, lane, (uint32_t)ld, rows);
+        ba = p + (uint64_t)(RCA ? m0 + k0 * ld : m0 * ld) * 2u;
         if constexpr (kGated) {
-            ta.aim(0, ta.kLoads / 2, wave, lane, (uint32_t)lda, rows);
             ta.aim(ta.kLoads / 2, ta.kLoads, wave, lane, (uint32_t)lda2, rows, kTM);
-        } else if constexpr (!RCA) {
-            ta.aim(0, ta.kLoads, wave, lane, (uint32_t)lda, rows);
+            ba2 = pa2 + (uint64_t)(m0 * lda2) * 2u;
         }
         tb.aim(0, tb.kLoads, wave, lane, (uint32_t)ldb, cols);
-        aim_k();
+        if constexpr (RCB) bb = pb + (uint64_t)(n0 + k0 * ldb) * 2u;
+        else bb = pb + (uint64_t)(n0 * ldb + (second ? part : 0)) * 2u;
     };
-    auto request = [&](uint32_t stage) __attribute__((always_inline)) {
+    u4 da = {}, da2 = {}, db = {};
+    uint32_t ka = 0, kb = 0;
+    // A step's loads: what they need, one after the other, and on to the next step.
+    // Behind the last one loads go nowhere.
+    auto begin = [&]() __attribute__((always_inline)) {
+        const int64_t left = more ? part - k0 : 0;
+        if (left < kBK) {
+            ta.cut(wave, lane, (int)left);
+            tb.cut(wave, lane, (int)left);
+        }
+        da = buffer_at(ba);
+        if (kGated) da2 = buffer_at(ba2);
+        db = buffer_at(bb);
+        ka = RCA ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(2 * k0);
+        kb = RCB ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(2 * k0);
+    };
+    auto load_a = [&](int i, uint32_t stage) __attribute__((always_inline)) {
+        ta.load(i, kGated && i >= ta.kLoads / 2 ? da2 : da, ka, stage, wave);
+    };
+    auto load_b = [&](int i, uint32_t stage) __attribute__((always_inline)) { tb.load(i, db, kb, stage + kB, wave); };
+    auto advance = [&]() __attribute__((always_inline)) {
         if (!more) return;
-        const int left = (int)(part - k0 < kBK ? part - k0 : kBK);
-        const u4 da = buffer_at(ba), da2 = kGated ? buffer_at(ba2) : da;
-        ta.template load<kGated>(da, da2, RCA ? 0u : 2u * k0, stage, wave, lane, left);
-        tb.template load<false>(buffer_at(bb), da, RCB ? 0u : 2u * k0, stage + kB, wave, lane, left);
         if (++asked == ask.s1) {
             more = ask.next(work);
+            asked = ask.s0;
             if (more) aim();
             return;
         }
         if (kTwo && two && asked == part_steps) {
-            aim_k();
+            aim();
             return;
         }
         k0 += kBK;
@@ -781,6 +778,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
             ba += (uint64_t)(ld * 2 * kBK);
         }
         if constexpr (RCB) bb += (uint64_t)(ldb * 2 * kBK);
+    };
+    auto request = [&](uint32_t stage) __attribute__((always_inline)) {
+        begin();
+#pragma unroll
+        for (int i = 0; i < ta.kLoads; ++i) load_a(i, stage);
+#pragma unroll
+        for (int i = 0; i < tb.kLoads; ++i) load_b(i, stage);
+        advance();
     };
 
     Tiles now(work, (int)blockIdx.x);
@@ -795,7 +800,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         request(here);
         load_wait();
         __syncthreads();
-        request(there);
+        begin();  // the second step's; the loop goes on with them
+#pragma unroll
+        for (int i = 0; i < ta.kLoads; ++i) load_a(i, there);
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[0][i] = ta.get(here, group(i), 0);
 #pragma unroll
@@ -817,7 +824,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
                     load_wait();
                     __syncthreads();
                     from = there;
-                    request(here);
+                    begin();
                 }
                 const int s1 = (s + 1) % (kBK / 16);
 #pragma unroll
@@ -825,10 +832,20 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     x[v][i] = ta.get(from, group(i), s1);
+                    // the loads of the step after the next, into what this step leaves, a few at
+                    // a time: all at once they hold the wavefront up for as long as the
+                    // memory's queue takes to accept those of all eight
+#pragma unroll
+                    for (int l = 0; l < ta.kLoads / MI; ++l)
+                        if (s == kBK / 16 - 1) load_a(i * (ta.kLoads / MI) + l, here);
+#pragma unroll
+                    for (int l = 0; l < tb.kLoads / MI; ++l)
+                        if (s == 0) load_b(i * (tb.kLoads / MI) + l, there);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u][i], y[u][j], acc[i][j], 0, 0, 0);
                 }
+                if (s == 0) advance();
                 // reads between the products
                 __builtin_amdgcn_sched_group_barrier(0x100, RCB ? 4 : 2, 0);
 #pragma unroll
@@ -861,6 +878,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         if constexpr (E != EPI_GATE) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         busy = now.next(work);
     }
+    load_wait();  // nothing may arrive in LDS that is another workgroup's
 }
 
 // The divided tiles: a workgroup adds the parts of a tile in order (all of it for
