@@ -310,144 +310,27 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
     }
 }
 
-// --------------------------------------------------- products in fp32
+// ------------------------------------------------------------------ products
 
-// Tiles of 128 x 128, four wavefronts of 64 x 64, 32 of k at a time through
-// registers into LDS, where k is the row.
-constexpr int kF32Tile = 128, kF32K = 32, kF32Pitch = 130, kF32Threads = 256;
-constexpr int kF32Part = 256;
-
-// Four elements of an operand's tile: of row r, from column c (KC: row m, column
-// k; RC: row k, column m).
-template <bool BF>
-__device__ __forceinline__ f4 piece(const void *p, int64_t ld, int64_t r, int64_t rows, int64_t c, int64_t cols)
-{
-    return r < rows && c < cols ? load4<BF>(p, r * ld + c) : f4{};
-}
-
-template <Epi E, bool RCA, bool RCB, Limit L, bool BF>
-__global__ void __launch_bounds__(kF32Threads) gscan_mm_f32_kernel(MmArgs a)
-{
-    constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
-    constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;  // of m
-    __shared__ __align__(16) float lds[2][kF32K][kF32Pitch];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
-    int64_t N = a.N, K = a.K;
-    const void *pa = a.a, *pb = a.b;
-    int64_t lda = a.lda, ldb = a.ldb;
-    if constexpr (L != LIMIT_NONE) {
-        const int64_t c = *a.count;
-        if (a.alt && c < (L == LIMIT_N ? a.N : a.K)) {
-            (L == LIMIT_N ? pb : pa) = a.alt;
-            (L == LIMIT_N ? ldb : lda) = a.ldalt;
-        }
-        (L == LIMIT_N ? N : K) = c;
-    }
-    const int64_t tm = (a.M + kTile - 1) / kTile, tn = (a.N + kF32Tile - 1) / kF32Tile;
-    int64_t im, in;
-    tile_at((uint32_t)place_of((int)blockIdx.x, (int)(tm * tn)), (uint32_t)tm, (uint32_t)tn, im, in);
-    const int64_t m0 = im * kTile, n0 = in * kF32Tile;
-    if (n0 >= N) return;
-
-    auto load_a = [&](int64_t k0, int j) -> f4 {
-        const int q = tid + j * kF32Threads;
-        if constexpr (!RCA) {
-            const int r = q >> 3;
-            const int64_t c = k0 + 4 * (q & 7);
-            if (kGated && r >= kTile) return piece<BF>(a.a2, a.lda2, m0 + r - kTile, a.M, c, K);
-            return piece<BF>(pa, lda, m0 + r, a.M, c, K);
-        } else {
-            const int64_t k = k0 + (q >> 5), c = m0 + 4 * (q & 31);
-            if (a.a2 && k >= a.K1) return piece<BF>(a.a2, a.lda2, k - a.K1, K - a.K1, c, a.M);
-            return piece<BF>(pa, lda, k, K, c, a.M);
-        }
-    };
-    auto load_b = [&](int64_t k0, int j) -> f4 {
-        const int q = tid + j * kF32Threads;
-        if constexpr (!RCB) return piece<BF>(pb, ldb, n0 + (q >> 3), N, k0 + 4 * (q & 7), K);
-        else return piece<BF>(pb, ldb, k0 + (q >> 5), K, n0 + 4 * (q & 31), N);
-    };
-    auto put = [&](int which, bool rc, int j, const f4 &v) {
-        const int q = tid + j * kF32Threads;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (rc) lds[which][q >> 5][4 * (q & 31) + e] = v[e];
-            else lds[which][4 * (q & 7) + e][q >> 3] = v[e];
-        }
-    };
-    auto mat = [&](int i) { return kGated ? 32 * wm : 64 * wm + 32 * i; };
-    auto row_of = [&](int i) { return kGated ? kTile * i + 32 * wm : 64 * wm + 32 * i; };
-    f16v acc[2][2], all[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = all[i][j] = f16v{};
-    f4 ra[4], rb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        ra[j] = load_a(0, j);
-        rb[j] = load_b(0, j);
-    }
-    for (int64_t k0 = 0; k0 < K; k0 += kF32K) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            put(0, RCA, j, ra[j]);
-            put(1, RCB, j, rb[j]);
-        }
-        __syncthreads();
-        if (k0 + kF32K < K) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ra[j] = load_a(k0 + kF32K, j);
-                rb[j] = load_b(k0 + kF32K, j);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kF32K; k += 2) {
-            float x[2], y[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                x[i] = lds[0][k + (lane >> 5)][row_of(i) + (lane & 31)];
-                y[i] = lds[1][k + (lane >> 5)][64 * wn + 32 * i + (lane & 31)];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[j], acc[i][j], 0, 0, 0);
-        }
-        // sums of 256 are joined, so that rounding grows with neither alone
-        if ((k0 + kF32K) % kF32Part == 0 || k0 + kF32K >= K) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    all[i][j] += acc[i][j];
-                    acc[i][j] = f16v{};
-                }
-        }
-    }
-    if (E == EPI_LSE) __syncthreads();  // the tiles become the epilogue's memory
-    epilogue<E, BF, 2, 2, 2>(a, all, im, m0, n0, N, wm, 64 * wn, kTile, kF32Tile, mat,
-                                    reinterpret_cast<float2 *>(&lds[0][0][0]));
-}
-
-// --------------------------------------------------- products of bf16
-
-// Tiles of TM = 32 MI WM by TN = 64 WN, a wavefront's part 32 MI x 64 in registers.
-// Steps of 64 of k go from memory straight into LDS (16 bytes per lane, no
-// register in between), a step ahead, into the half that the step before has been
-// read from.  Rows of a KC tile hold eight pieces of 16 bytes; piece c of row r lies
-// at c ^ (r % 8), so that the 16-byte reads of eight rows meet no bank twice.  Rows
-// of an RC tile are k; their pieces lie at c ^ 2 (k % 4), so that the four rows of a
-// transposed read (four k of 16 columns) do not either.  Memory outside the operands
-// is not touched: what of a tile or of the last step lies outside is read from past
-// the end of the buffer, where the hardware finds zeros.
+// Tiles of 32 MI WM by 32 NI WN, a wavefront's part 32 MI x 32 NI in registers.
+// Steps of 128 bytes of k (64 bf16, 32 fp32) go from memory straight into LDS (16
+// bytes per lane, no register in between), into the half that the step before has
+// been read from.  Rows of a KC tile hold eight pieces of 16 bytes; piece c of row r
+// lies at c ^ (r % 8), so that the 16-byte reads of eight rows meet no bank twice.
+// Rows of an RC tile are k; with bf16 their pieces lie at c ^ 2 (k % 4), so that the
+// four rows of a transposed read (four k of 16 columns) do not either.
+// Memory outside the operands is not touched: what of a tile or of the last step lies
+// outside is read from past the end of the buffer, where the hardware finds zeros.
 //
-// The elements of 16 k are read from LDS while the products of the 16 before are
-// formed; for a step's first 16 that is behind the barrier that ends the step before
+// A quarter of a step is read from LDS while the products of the quarter before are
+// formed; a step's first quarter is read behind the barrier that ends the step before
 // it, but before that step's last products.
+//
+// bf16 products run at what the card's power allows: 8192 tokens, 2048 x 2 x 5504,
+// at 1150 to 1200 TFLOP/s in the steps (zeros instead of random values: 1390; a
+// large library product: 1140 to 1320, 2250 on zeros).  Four stages of half a step,
+// three on their way, were slower where k is contiguous (64 bytes of a row at a time:
+// 403 -> 457 us) and no faster elsewhere.
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 template <class T>
@@ -458,7 +341,10 @@ __device__ __forceinline__ lds_t<T> *in_lds(uint32_t address)
     return (lds_t<T> *)(uintptr_t)address;
 }
 
-constexpr int kBK = 64;
+template <bool BF>
+constexpr int kSize = BF ? 2 : 4;
+template <bool BF>
+constexpr int kBK = 128 / kSize<BF>;  // k of a step
 constexpr uint32_t kNowhere = 0x7ffffff0u;  // past the end of every buffer
 
 // 64 lanes' 16 bytes at their offsets (and `more`) of the buffer, one after the other
@@ -480,17 +366,33 @@ __device__ __forceinline__ u4 buffer_at(uint64_t base)
               0x00020000u};
 }
 
+// What a lane gives to the products of a quarter of a step: eight bf16 of a row,
+// k = 8 (lane / 32) .. + 7 of 16, or four fp32, k = 4 (lane / 32) .. + 3 of 8.
+template <bool BF>
+using Piece = typename std::conditional<BF, bf8, f4>::type;
+
+__device__ __forceinline__ void multiply(const bf8 &x, const bf8 &y, f16v &acc)
+{
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void multiply(const f4 &x, const f4 &y, f16v &acc)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], acc, 0, 0, 0);
+}
+
 // A tile of T rows (KC) or columns (RC): offsets of a lane's loads, and where the
 // lane finds its elements.
-template <bool RC, int T, int W>
+template <bool BF, bool RC, int T, int W>
 struct Tile {
-    static constexpr int kLoads = T / 8 / W;      // of a wavefront
-    static constexpr int kPer = 1024 / (2 * T);   // RC: rows that one load covers
+    static constexpr int kSz = kSize<BF>, kIn = 16 / kSz;  // elements of a piece
+    static constexpr int kLoads = T / 8 / W;               // of a wavefront
+    static constexpr int kPer = 1024 / (kSz * T);          // RC: rows that one load covers
     uint32_t off[kLoads];
     uint32_t at[RC ? 2 : 4];
 
-    // Load i of a lane: row (KC: of the tile, RC: k) and 16-byte piece (KC: of k, RC: of
-    // the tile's columns).
+    // Load i of a lane: row (KC: of the tile, RC: k) and piece (KC: of k, RC: of the
+    // tile's columns).
     static __device__ __forceinline__ int row(int i, int wave, int lane)
     {
         const int q = wave + W * i;
@@ -498,20 +400,22 @@ struct Tile {
     }
     static __device__ __forceinline__ int piece(int i, int wave, int lane)
     {
-        if constexpr (RC) return (lane % (64 / kPer)) ^ (2 * (row(i, wave, lane) & 3));
+        if constexpr (RC) return (lane % (64 / kPer)) ^ (BF ? 2 * (row(i, wave, lane) & 3) : 0);
         else return (lane & 7) ^ (lane >> 3);
     }
 
     // `mine`: the first of the wavefront's rows (KC) or columns (RC), a multiple of 32
     __device__ __forceinline__ void place(int lane, int mine)
     {
-        if constexpr (RC) {
+        if constexpr (RC && BF) {
             const int p = lane & 15, g = lane >> 4;
 #pragma unroll
             for (int o = 0; o < 2; ++o) {  // even and odd groups of 32 columns
                 const int c = (4 * (mine / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ (2 * (p >> 2));
                 at[o] = (uint32_t)((8 * (g >> 1) + (p >> 2)) * 2 * T + 16 * c + 8 * (p & 1));
             }
+        } else if constexpr (RC) {
+            at[0] = at[1] = (uint32_t)((4 * (lane >> 5)) * 4 * T + 4 * (mine + (lane & 31)));
         } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
@@ -527,7 +431,7 @@ struct Tile {
         for (int i = 0; i < kLoads; ++i)
             if (i >= i0 && i < i1) {
                 const int r = row(i, wave, lane) - from, c = piece(i, wave, lane);
-                off[i] = (RC ? 8 * c : r) < there ? (uint32_t)r * ld * 2 + (uint32_t)c * 16 : kNowhere;
+                off[i] = (RC ? kIn * c : r) < there ? (uint32_t)r * ld * kSz + (uint32_t)c * 16 : kNowhere;
             }
     }
 
@@ -536,28 +440,33 @@ struct Tile {
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            if ((RC ? row(i, wave, lane) : 8 * piece(i, wave, lane)) >= left) off[i] = kNowhere;
+            if ((RC ? row(i, wave, lane) : kIn * piece(i, wave, lane)) >= left) off[i] = kNowhere;
     }
 
-    // Load i of a step; `k`: where the step begins (KC).
+    // Load i of a step; `k`: where the step begins (KC), in bytes.
     __device__ __forceinline__ void load(int i, const u4 &buffer, uint32_t k, uint32_t lds, int wave) const
     {
         load_to_lds(buffer, off[i], k, lds + (uint32_t)(wave + W * i) * 1024u);
     }
 
-    // Elements of 16 k (the step's s-th 16) of the group `i` of 32 rows or columns
-    // from the wavefront's first: eight of a row per lane.
-    __device__ __forceinline__ bf8 get(uint32_t lds, int i, int s) const
+    // The s-th quarter of a step, of the group `i` of 32 rows or columns from the
+    // wavefront's first.
+    static constexpr int kReads = !RC ? 1 : BF ? 2 : 4;
+    __device__ __forceinline__ Piece<BF> get(uint32_t lds, int i, int s) const
     {
-        if constexpr (RC) {
+        if constexpr (RC && BF) {
             const uint32_t p = lds + at[i & 1] + (uint32_t)(s * 16 * 2 * T + 64 * (i & ~1));
             const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p));
             const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p + 4 * 2 * T));
             const u4 v = {__builtin_bit_cast(uint2, x).x, __builtin_bit_cast(uint2, x).y,
                           __builtin_bit_cast(uint2, y).x, __builtin_bit_cast(uint2, y).y};
             return __builtin_bit_cast(bf8, v);
+        } else if constexpr (RC) {
+            const uint32_t p = lds + at[0] + (uint32_t)(s * 8 * 4 * T + 128 * i);
+            return f4{*in_lds<float>(p), *in_lds<float>(p + 4 * T), *in_lds<float>(p + 8 * T),
+                      *in_lds<float>(p + 12 * T)};
         } else {
-            return *in_lds<bf8>(lds + at[s] + (uint32_t)(i * 4096));
+            return *in_lds<Piece<BF>>(lds + at[s] + (uint32_t)(i * 4096));
         }
     }
 };
@@ -582,36 +491,58 @@ struct Work {
     }
 };
 
-constexpr int kPartSteps = 4;   // at least so many steps to a part
-// The parts' sums through memory and the second kernel, in steps: 64 kB (256 kB)
-// for each workgroup.
-constexpr int kPartCost = 14;
+// One of the kernels' tiles, and what it takes, in ns: a step with all workgroups at
+// work, and at least; a tile besides its steps; a part's sums through memory (3.5
+// TB/s); the second kernel.  Measured at 300 to 8192 rows.
+struct MmShape {
+    int m, n, groups, step, least, tile, part, join;
+};
+// 256 x 256, 128 x 128 or 128 (of m) x 64; fp32 has the latter two.
+constexpr MmShape kShapes[2][3] = {
+    {{256, 256, 256, 0, 0, 0, 0, 0}, {128, 128, 512, 4400, 2200, 3000, 37, 5000}, {128, 64, 768, 3300, 1100, 3000, 19, 5000}},
+    {{256, 256, 256, 1650, 1650, 5000, 150, 6000}, {128, 128, 512, 1050, 680, 2500, 37, 5000}, {128, 64, 768, 1170, 600, 2000, 19, 5000}},
+};
 
-__host__ __device__ __forceinline__ Work plan_work(int tiles, int steps, int groups)
+// ns of a step while n workgroups are at work, at most those that fit at once
+__host__ __device__ __forceinline__ int step_ns(const MmShape &c, int n)
+{
+    const int t = c.step * ((n + 255) / 256) / (c.groups / 256);
+    return t > c.least ? t : c.least;
+}
+
+constexpr int kPartSteps = 4;   // at least so many steps to a part
+
+__host__ __device__ __forceinline__ Work plan_work(int tiles, int steps, const MmShape &c)
 {
     Work w;
     w.tiles = w.whole = tiles;
     w.steps = steps;
-    w.groups = groups;
-    const int left = (int)((uint32_t)tiles % (uint32_t)groups);
+    w.groups = c.groups;
+    const int left = (int)((uint32_t)tiles % (uint32_t)c.groups);
+    if (!left) return w;
     const int64_t total = (int64_t)left * steps;
-    const int parts = total / kPartSteps < groups ? (int)(total / kPartSteps) : groups;
-    if (left == 0 || parts <= left) return w;
-    const int64_t share = total >> 32 ? total / parts : (int64_t)((uint32_t)total / (uint32_t)parts);
-    if (steps - share - 1 <= kPartCost) return w;
-    w.whole = tiles - left;
-    w.parts = parts;
-    w.share = share;
-    w.more = (int)(total - share * parts);
+    int64_t best = (int64_t)steps * step_ns(c, left);
+    for (int n = c.groups; n > left && n > c.groups / 16; n /= 2) {
+        const int parts = total / kPartSteps < n ? (int)(total / kPartSteps) : n;
+        if (parts <= left) continue;
+        const int64_t share = total >> 32 ? total / parts : (int64_t)((uint32_t)total / (uint32_t)parts);
+        const int64_t ns = (share + 1) * step_ns(c, parts) + (int64_t)(parts + left) * c.part + c.join;
+        if (ns >= best) continue;
+        best = ns;
+        w.whole = tiles - left;
+        w.parts = parts;
+        w.share = share;
+        w.more = (int)(total - share * parts);
+    }
     return w;
 }
 
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Steps of k: of each of the two weights by itself where k runs over both.
-__host__ __device__ __forceinline__ int64_t steps_of(int64_t K, int64_t K1)
+// Steps of bk of k: of each of the two weights by itself where k runs over both.
+__host__ __device__ __forceinline__ int64_t steps_of(int64_t K, int64_t K1, int bk)
 {
-    return K1 ? 2 * ceil_div(K1, kBK) : ceil_div(K, kBK);
+    return K1 ? 2 * ceil_div(K1, bk) : ceil_div(K, bk);
 }
 
 // What every kernel of a product knows of its operands.
@@ -634,10 +565,9 @@ struct Operands {
     }
 };
 
-// Workgroups that fit at once: one of 512 threads per CU (128 kB of LDS), two of
-// 256 (64 kB).
-template <int WM, int WN>
-constexpr int kGroups = WM * WN == 8 ? 256 : 512;
+// Workgroups per CU at once: one of 512 threads (128 kB of LDS); of 256 threads, two of
+// 128 x 128 (64 kB) or three of 128 x 64 (48 kB).
+constexpr int per_cu(int ni, int waves) { return waves == 8 ? 1 : ni == 2 ? 2 : 3; }
 
 // A workgroup's tiles in turn: whole ones, then its steps of the divided ones.
 struct Tiles {
@@ -682,13 +612,13 @@ struct Tiles {
     }
 };
 
-template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a)
+template <Epi E, bool BF, bool RCA, bool RCB, Limit L, int MI, int NI, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, per_cu(NI, WM *WN) == 3 ? 3 : 2) gscan_mm_kernel(MmArgs a)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
-    constexpr int kW = WM * WN, kTA = 32 * MI * WM, kTN = 64 * WN;
+    constexpr int kW = WM * WN, kTA = 32 * MI * WM, kTN = 32 * NI * WN, kSz = kSize<BF>, kStep = kBK<BF>;
     constexpr int kTM = kGated ? kTA / 2 : kTA;  // of m
-    constexpr uint32_t kStage = (kTA + kTN) * 2 * kBK, kB = kTA * 2 * kBK;
+    constexpr uint32_t kStage = (kTA + kTN) * 128, kB = kTA * 128;
     __shared__ __align__(1024) char lds[2 * kStage];
     __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -701,13 +631,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     constexpr bool kTwo = RCA && !RCB && E == EPI_STORE;
     const bool two = kTwo && a.a2;  // a second weight behind the first along k
     const int64_t part = two ? a.K1 : o.K;
-    const int part_steps = (int)ceil_div(part, kBK);
-    const Work work = plan_work(tm * tn, two ? 2 * part_steps : part_steps, kGroups<WM, WN>);
+    const int part_steps = (int)ceil_div(part, kStep);
+    constexpr MmShape kMine = kShapes[BF][kW == 8 ? 0 : NI == 2 ? 1 : 2];
+    const Work work = plan_work(tm * tn, two ? 2 * part_steps : part_steps, kMine);
 
-    Tile<RCA, kTA, kW> ta;
-    Tile<RCB, kTN, kW> tb;
+    Tile<BF, RCA, kTA, kW> ta;
+    Tile<BF, RCB, kTN, kW> tb;
     ta.place(lane, kGated ? 16 * MI * wm : 32 * MI * wm);
-    tb.place(lane, 64 * wn);
+    tb.place(lane, 32 * NI * wn);
     const uint32_t base = (uint32_t)(uintptr_t)(lds_t<char> *)lds;
 
     // Requests: two steps ahead of the products, so with tiles of their own.
@@ -722,7 +653,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
         const int64_t m0 = im * kTM, n0 = in * kTN;
         const int rows = (int)(M - m0 < kTM ? M - m0 : kTM), cols = (int)(N - n0 < kTN ? N - n0 : kTN);
         const bool second = kTwo && two && asked >= part_steps;
-        k0 = (second ? asked - part_steps : asked) * kBK;
+        k0 = (second ? asked - part_steps : asked) * kStep;
         uint64_t p = pa;
         int64_t ld = lda;
         if (second) {
@@ -730,14 +661,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
             ld = lda2;
         }
         ta.aim(0, kGated ? ta.kLoads / 2 : ta.kLoads, wave, lane, (uint32_t)ld, rows);
-        ba = p + (uint64_t)(RCA ? m0 + k0 * ld : m0 * ld) * 2u;
+        ba = p + (uint64_t)(RCA ? m0 + k0 * ld : m0 * ld) * (uint64_t)kSz;
         if constexpr (kGated) {
             ta.aim(ta.kLoads / 2, ta.kLoads, wave, lane, (uint32_t)lda2, rows, kTM);
-            ba2 = pa2 + (uint64_t)(m0 * lda2) * 2u;
+            ba2 = pa2 + (uint64_t)(m0 * lda2) * (uint64_t)kSz;
         }
         tb.aim(0, tb.kLoads, wave, lane, (uint32_t)ldb, cols);
-        if constexpr (RCB) bb = pb + (uint64_t)(n0 + k0 * ldb) * 2u;
-        else bb = pb + (uint64_t)(n0 * ldb + (second ? part : 0)) * 2u;
+        if constexpr (RCB) bb = pb + (uint64_t)(n0 + k0 * ldb) * (uint64_t)kSz;
+        else bb = pb + (uint64_t)(n0 * ldb + (second ? part : 0)) * (uint64_t)kSz;
     };
     u4 da = {}, da2 = {}, db = {};
     uint32_t ka = 0, kb = 0;
@@ -745,15 +676,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
     // Behind the last one loads go nowhere.
     auto begin = [&]() __attribute__((always_inline)) {
         const int64_t left = more ? part - k0 : 0;
-        if (left < kBK) {
+        if (left < kStep) {
             ta.cut(wave, lane, (int)left);
             tb.cut(wave, lane, (int)left);
         }
         da = buffer_at(ba);
         if (kGated) da2 = buffer_at(ba2);
         db = buffer_at(bb);
-        ka = RCA ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(2 * k0);
-        kb = RCB ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(2 * k0);
+        ka = RCA ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(kSz * k0);
+        kb = RCB ? 0u : (uint32_t)__builtin_amdgcn_readfirstlane(kSz * k0);
     };
     auto load_a = [&](int i, uint32_t stage) __attribute__((always_inline)) {
         ta.load(i, kGated && i >= ta.kLoads / 2 ? da2 : da, ka, stage, wave);
@@ -771,13 +702,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
             aim();
             return;
         }
-        k0 += kBK;
+        k0 += kStep;
         if constexpr (RCA) {
             int64_t ld = lda;
             if (kTwo && two && asked > part_steps) ld = lda2;
-            ba += (uint64_t)(ld * 2 * kBK);
+            ba += (uint64_t)(ld * 128);
         }
-        if constexpr (RCB) bb += (uint64_t)(ldb * 2 * kBK);
+        if constexpr (RCB) bb += (uint64_t)(ldb * 128);
     };
     auto request = [&](uint32_t stage) __attribute__((always_inline)) {
         begin();
@@ -790,8 +721,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
 
     Tiles now(work, (int)blockIdx.x);
     bool busy = now.next(work);
-    f16v acc[MI][2];
-    bf8 x[2][MI], y[2][2];
+    f16v acc[MI][NI], sum[BF ? 1 : MI][BF ? 1 : NI];  // fp32: sums of 256 k are joined in `sum`
+    Piece<BF> x[2][MI], y[2][NI];
     auto group = [&](int i) { return kGated && i >= MI / 2 ? i - MI / 2 + kTM / 32 : i; };
     auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * i; };
     uint32_t here = base, there = base + kStage;
@@ -806,19 +737,22 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[0][i] = ta.get(here, group(i), 0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) y[0][j] = tb.get(here + kB, j, 0);
+        for (int j = 0; j < NI; ++j) y[0][j] = tb.get(here + kB, j, 0);
     }
     while (busy) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = f16v{};
+            for (int j = 0; j < NI; ++j) {
+                acc[i][j] = f16v{};
+                if constexpr (!BF) sum[i][j] = f16v{};
+            }
         for (int t = now.s0; t < now.s1; ++t) {
 #pragma unroll
-            for (int s = 0; s < kBK / 16; ++s) {
+            for (int s = 0; s < 4; ++s) {  // quarters
                 const int u = s & 1, v = u ^ 1;
                 uint32_t from = here;
-                if (s == kBK / 16 - 1) {
+                if (s == 3) {
                     // everything of this step has been read and the next one's is there
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                     load_wait();
@@ -826,9 +760,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
                     from = there;
                     begin();
                 }
-                const int s1 = (s + 1) % (kBK / 16);
+                const int s1 = (s + 1) % 4;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) y[v][j] = tb.get(from + kB, j, s1);
+                for (int j = 0; j < NI; ++j) y[v][j] = tb.get(from + kB, j, s1);
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     x[v][i] = ta.get(from, group(i), s1);
@@ -836,42 +770,59 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
                     // a time: all at once they hold the wavefront up for as long as the
                     // memory's queue takes to accept those of all eight
 #pragma unroll
-                    for (int l = 0; l < ta.kLoads / MI; ++l)
-                        if (s == kBK / 16 - 1) load_a(i * (ta.kLoads / MI) + l, here);
+                    for (int l = i * ta.kLoads / MI; l < (i + 1) * ta.kLoads / MI; ++l)
+                        if (s == 3) load_a(l, here);
 #pragma unroll
-                    for (int l = 0; l < tb.kLoads / MI; ++l)
-                        if (s == 0) load_b(i * (tb.kLoads / MI) + l, there);
+                    for (int l = i * tb.kLoads / MI; l < (i + 1) * tb.kLoads / MI; ++l)
+                        if (s == 0) load_b(l, there);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u][i], y[u][j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < NI; ++j)
+                        multiply(x[u][i], y[u][j], acc[i][j]);
                 }
                 if (s == 0) advance();
                 // reads between the products
-                __builtin_amdgcn_sched_group_barrier(0x100, RCB ? 4 : 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, NI * tb.kReads, 0);
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x100, RCA ? 2 : 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, ta.kReads, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, BF ? NI : 4 * NI, 0);
                 }
             }
             const uint32_t h = here;
             here = there;
             there = h;
+            if constexpr (!BF) {
+                if ((t - now.s0) % 8 == 7 || t + 1 == now.s1) {
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            sum[i][j] += acc[i][j];
+                            acc[i][j] = f16v{};
+                        }
+                }
+            }
+        }
+        if constexpr (!BF) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) acc[i][j] = sum[i][j];
         }
         int64_t im, in;
         tile_at((uint32_t)now.t, (uint32_t)tm, (uint32_t)tn, im, in);
         if (now.slot >= 0) {
-            f4 *p = reinterpret_cast<f4 *>(a.partial) + (int64_t)now.slot * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
+            f4 *p = reinterpret_cast<f4 *>(a.partial) + (int64_t)now.slot * (kTA * kTN / 4) + wave * MI * NI * 256 + lane;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < NI; ++j)
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        p[((i * 2 + j) * 4 + g) * 64] = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                        p[((i * NI + j) * 4 + g) * 64] = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
                                                            acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
         } else {
-            epilogue<E, true, MI, 2, WM>(a, acc, im, im * kTM, in * kTN, N, wm, 64 * wn, kTM, kTN, mat, red);
+            epilogue<E, BF, MI, NI, WM>(a, acc, im, im * kTM, in * kTN, N, wm, 32 * NI * wn, kTM, kTN, mat, red);
         }
         // Loads of the epilogue that some path leaves unused would make the compiler
         // wait at the head of every step, for the requests too: wait for them here.
@@ -884,22 +835,23 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_bf16_kernel(MmArgs a
 // The divided tiles: a workgroup adds the parts of a tile in order (all of it for
 // EPI_LSE; else those of one of its groups of 32 x 32 per wavefront, or of the same
 // group of both weights) and finishes it.
-template <Epi E, int MI>
-constexpr int kShares = E == EPI_LSE ? 1 : (E == EPI_GATE || E == EPI_DGATE) ? MI : 2 * MI;
+template <Epi E, int MI, int NI>
+constexpr int kShares = E == EPI_LSE ? 1 : (E == EPI_GATE || E == EPI_DGATE) ? MI / 2 * NI : MI * NI;
 
-template <Epi E, Limit L, int MI, int WM, int WN>
+template <Epi E, bool BF, Limit L, int MI, int NI, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
-    constexpr int kTA = 32 * MI * WM, kTN = 64 * WN, kTM = kGated ? kTA / 2 : kTA;
-    constexpr int kN = kShares<E, MI>, kI = E == EPI_LSE ? MI : kGated ? 2 : 1, kJ = E == EPI_LSE ? 2 : 1;
+    constexpr int kTA = 32 * MI * WM, kTN = 32 * NI * WN, kTM = kGated ? kTA / 2 : kTA;
+    constexpr int kN = kShares<E, MI, NI>, kI = E == EPI_LSE ? MI : kGated ? 2 : 1, kJ = E == EPI_LSE ? NI : 1;
     __shared__ float2 red[E == EPI_LSE ? WM * kTN : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    const int i0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) / 2, j0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) % 2;
+    const int i0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) / NI, j0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) % NI;
     const Operands<L> o(a);
     const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kN);
-    const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1), kGroups<WM, WN>);
+    constexpr MmShape kMine = kShapes[BF][WM * WN == 8 ? 0 : NI == 2 ? 1 : 2];
+    const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1, kBK<BF>), kMine);
     if (d >= work.tiles - work.whole) return;
     const int w0 = work.owner((int64_t)d * work.steps), w1 = work.owner((int64_t)(d + 1) * work.steps - 1);
     if (w0 == w1) return;  // done whole
@@ -909,14 +861,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[i][j] = f16v{};
     for (int w = w0; w <= w1; ++w) {
-        const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w + d) * (kTA * kTN / 4) + wave * MI * 2 * 256 + lane;
+        const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w + d) * (kTA * kTN / 4) +
+                      wave * MI * NI * 256 + lane;
 #pragma unroll
         for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int j = 0; j < kJ; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const f4 v = p[(((i0 + i * (MI / kI)) * 2 + j0 + j) * 4 + g) * 64];
+                    const f4 v = p[(((i0 + i * (MI / kI)) * NI + j0 + j) * 4 + g) * 64];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] += v[e];
                 }
@@ -924,56 +877,60 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a
     int64_t im, in;
     tile_at((uint32_t)(work.whole + d), (uint32_t)tm, (uint32_t)tn, im, in);
     auto mat = [&](int i) { return (kGated ? 16 : 32) * MI * wm + 32 * (i + i0); };
-    epilogue<E, true, kI, kJ, WM>(a, acc, im, im * kTM, in * kTN, o.N, wm, 64 * wn + 32 * j0, kTM, kTN, mat, red);
+    epilogue<E, BF, kI, kJ, WM>(a, acc, im, im * kTM, in * kTN, o.N, wm, 32 * (NI * wn + j0), kTM, kTN, mat, red);
 }
 
-// The kernel of a product: tiles of 256 x 256 or of 128 x 128, by the steps that the
-// busiest workgroup has and what a step takes.
+// The kernel of a product: the one that the busiest workgroup is done with first.
 struct MmPlan {
-    bool big = false;
+    int shape = 0;
     Work work;
     size_t bytes = 0;   // of parts of tiles
-    int64_t divided = 0;  // tiles, at most
+    int divided = 0;    // tiles, at most
+    int64_t ns = 0;
 };
-MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited)
+MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited, int dtype)
 {
-    auto of = [&](bool big) {
+    MmPlan best;
+    for (int i = dtype ? 0 : 1; i < 3; ++i) {
+        const MmShape &c = kShapes[dtype ? 1 : 0][i];
         MmPlan p;
-        const int64_t t = big ? 256 : 128;
-        p.big = big;
-        p.work = plan_work((int)(ceil_div(M, gated ? t / 2 : t) * ceil_div(N, t)), (int)steps_of(K, K1), big ? 256 : 512);
-        p.divided = p.work.tiles - p.work.whole;
+        p.shape = i;
+        p.work = plan_work((int)(ceil_div(M, gated ? c.m / 2 : c.m) * ceil_div(N, c.n)),
+                           (int)steps_of(K, K1, dtype ? kBK<true> : kBK<false>), c);
+        const Work &w = p.work;
+        p.divided = w.tiles - w.whole;
+        const int full = w.whole / c.groups, last = w.whole % c.groups;
+        p.ns = (int64_t)full * ((int64_t)w.steps * c.step + c.tile);
+        if (last) p.ns += (int64_t)w.steps * step_ns(c, last) + c.tile;
+        if (w.parts)
+            p.ns += (w.share + 1) * step_ns(c, w.parts) + c.tile + (int64_t)(w.parts + p.divided) * c.part + c.join;
         int64_t slots = p.work.parts + p.divided;
         if (limited) {  // fewer tiles, or fewer steps, may be divided where these are not
-            p.divided = p.work.tiles < p.work.groups ? p.work.tiles : p.work.groups - 1;
-            slots = p.work.groups + p.divided;
+            p.divided = p.work.tiles < c.groups ? p.work.tiles : c.groups - 1;
+            slots = c.groups + p.divided;
         }
-        p.bytes = (size_t)slots * (size_t)(t * t) * sizeof(float);
-        return p;
-    };
-    auto busiest = [](const Work &w) {
-        return ceil_div(w.whole, w.groups) * w.steps + (w.parts ? w.share + 1 + kPartCost : 0);
-    };
-    const MmPlan big = of(true), small = of(false);
-    return (double)busiest(big.work) * 1.25 <= (double)busiest(small.work) * 0.8 ? big : small;
+        p.bytes = (size_t)slots * (size_t)(c.m * c.n) * sizeof(float);
+        if (!best.ns || p.ns < best.ns) best = p;
+    }
+    return best;
 }
 
 size_t mm_bytes(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited, int dtype)
 {
-    return dtype ? plan_mm(M, N, K, K1, gated, limited).bytes : 0;
+    return plan_mm(M, N, K, K1, gated, limited, dtype).bytes;
 }
 
-template <Epi E, bool RCA, bool RCB, Limit L, int MI, int WM, int WN>
-hipError_t launch_mm_bf16(const MmArgs &a, const MmPlan &p, hipStream_t st)
+template <Epi E, bool BF, bool RCA, bool RCB, Limit L, int MI, int NI, int WM, int WN>
+hipError_t launch_shape(const MmArgs &a, const MmPlan &p, hipStream_t st)
 {
     const dim3 threads(64 * WM * WN);
-    const int64_t most = p.work.parts > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
-    const int64_t n = most < p.work.groups ? most : p.work.groups;
-    hipLaunchKernelGGL((gscan_mm_bf16_kernel<E, RCA, RCB, L, MI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
+    const int most = p.work.parts > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
+    const int n = most < p.work.groups ? most : p.work.groups;
+    hipLaunchKernelGGL((gscan_mm_kernel<E, BF, RCA, RCB, L, MI, NI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.divided) return e;
-    hipLaunchKernelGGL((gscan_mm_join_kernel<E, L, MI, WM, WN>), dim3((unsigned)(p.divided * kShares<E, MI>)), threads, 0, st,
-                       a);
+    hipLaunchKernelGGL((gscan_mm_join_kernel<E, BF, L, MI, NI, WM, WN>),
+                       dim3((unsigned)(p.divided * kShares<E, MI, NI>)), threads, 0, st, a);
     return hipGetLastError();
 }
 
@@ -983,24 +940,20 @@ hipError_t launch_mm(MmArgs a, int dtype, void *partial, hipStream_t st)
 {
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
     if (!a.M || !a.N) return hipSuccess;
-    if (dtype) {
-        const MmPlan p = plan_mm(a.M, a.N, a.K, a.K1, kGated, L != LIMIT_NONE);
-        a.partial = reinterpret_cast<float *>(partial);
-        return p.big ? launch_mm_bf16<E, RCA, RCB, L, 4, 2, 4>(a, p, st)
-                     : launch_mm_bf16<E, RCA, RCB, L, 2, 2, 2>(a, p, st);
-    }
-    constexpr int kTile = kGated ? kF32Tile / 2 : kF32Tile;
-    const int64_t tiles = ceil_div(a.M, kTile) * ceil_div(a.N, kF32Tile);
-    hipLaunchKernelGGL((gscan_mm_f32_kernel<E, RCA, RCB, L, false>), dim3((unsigned)tiles), dim3(kF32Threads), 0, st,
-                       a);
-    return hipGetLastError();
+    const MmPlan p = plan_mm(a.M, a.N, a.K, a.K1, kGated, L != LIMIT_NONE, dtype);
+    a.partial = reinterpret_cast<float *>(partial);
+    if (!dtype)
+        return p.shape == 1 ? launch_shape<E, false, RCA, RCB, L, 2, 2, 2, 2>(a, p, st)
+                            : launch_shape<E, false, RCA, RCB, L, 2, 1, 2, 2>(a, p, st);
+    return p.shape == 0   ? launch_shape<E, true, RCA, RCB, L, 4, 2, 2, 4>(a, p, st)
+           : p.shape == 1 ? launch_shape<E, true, RCA, RCB, L, 2, 2, 2, 2>(a, p, st)
+                          : launch_shape<E, true, RCA, RCB, L, 2, 1, 2, 2>(a, p, st);
 }
 
 // Tiles of m: the partial results of EPI_LSE for each n.
 int64_t tiles_of_m(int64_t M, int64_t N, int64_t K, int dtype)
 {
-    const int t = dtype && plan_mm(M, N, K, 0, false, true).big ? 256 : 128;
-    return ceil_div(M, t);
+    return ceil_div(M, kShapes[dtype ? 1 : 0][plan_mm(M, N, K, 0, false, true, dtype).shape].m);
 }
 
 }  // namespace
