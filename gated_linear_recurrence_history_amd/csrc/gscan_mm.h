@@ -227,13 +227,13 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
                 if constexpr (E == EPI_DLOGIT) {
                     const int t = (int)(a.target[n] - a.v0 - m1);
                     const float up = a.up ? a.up[n] : 1.f, lse = a.lse[n];
-                    const int64_t at = n * a.ldo + m1;
+                    const int64_t at = n * a.ldo + m1, padded = (a.M + 7) / 8 * 8;
 #pragma unroll
                     for (int i = 0; i < HI; ++i)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const int m = mat(i) + 8 * g;
-                            if (!inside(m, a.ldo)) continue;  // the piece's columns, padded to eight with zeros
+                            if (!inside(m, padded)) continue;  // the piece's columns, padded to eight with zeros
                             f4 v;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -472,22 +472,25 @@ struct Tile {
 };
 
 // Who does what.  Every workgroup (as many as fit the device at once) does whole
-// tiles while there are enough for all; what is left, less than one for each, is
-// divided evenly by steps of k where that saves more than it costs: the parts of a
-// tile are sums in memory, which a second kernel adds in order.
+// tiles while there are enough for all.  Where what is left is for half of them or
+// fewer, and it saves more than it costs, every one of those tiles is divided along
+// k into as many parts as there are workgroups for: the parts are sums in memory,
+// which a second kernel adds in order.  All tiles are divided at the same k, so that
+// workgroups that run at the same time read the same rows of the operands.  (Divided
+// one behind the other, evenly over all workgroups, they read them at different times:
+// 84 tiles of 696 steps took 543 us, 7 TB/s.)
 struct Work {
-    int tiles = 0, whole = 0;       // whole: tiles that one workgroup does alone
-    int steps = 0;                  // of a tile
-    int groups = 0;                 // workgroups
-    int parts = 0;                  // of them, those that share the divided tiles
-    int64_t share = 0;              // steps of such a workgroup,
-    int more = 0;                   // and how many of them take one more
+    int tiles = 0, whole = 0;   // whole: tiles that one workgroup does alone
+    int steps = 0;              // of a tile
+    int groups = 0;             // workgroups
+    int splits = 0;             // parts of each tile that is left (0: none is)
 
-    __host__ __device__ int64_t first_step(int w) const { return w * share + (w < more ? w : more); }
-    __host__ __device__ int owner(int64_t step) const
+    __host__ __device__ int left() const { return tiles - whole; }
+    __host__ __device__ int parts() const { return left() * splits; }
+    __host__ __device__ int first_step(int split) const
     {
-        const int64_t big = more * (share + 1);
-        return (int)(step < big ? step / (share + 1) : more + (step - big) / share);
+        const int share = steps / splits, more = steps % splits;
+        return split * share + (split < more ? split : more);
     }
 };
 
@@ -520,19 +523,14 @@ __host__ __device__ __forceinline__ Work plan_work(int tiles, int steps, const M
     w.groups = c.groups;
     const int left = (int)((uint32_t)tiles % (uint32_t)c.groups);
     if (!left) return w;
-    const int64_t total = (int64_t)left * steps;
     int64_t best = (int64_t)steps * step_ns(c, left);
-    for (int n = c.groups; n > left && n > c.groups / 16; n /= 2) {
-        const int parts = total / kPartSteps < n ? (int)(total / kPartSteps) : n;
-        if (parts <= left) continue;
-        const int64_t share = total >> 32 ? total / parts : (int64_t)((uint32_t)total / (uint32_t)parts);
-        const int64_t ns = (share + 1) * step_ns(c, parts) + (int64_t)(parts + left) * c.part + c.join;
+    for (int n = (int)((uint32_t)c.groups / (uint32_t)left); n > 1; n = n > 3 ? n - n / 3 : n - 1) {
+        if (steps / n < kPartSteps) continue;
+        const int64_t ns = (int64_t)(steps / n + 1) * step_ns(c, left * n) + (int64_t)(left * n) * c.part + c.join;
         if (ns >= best) continue;
         best = ns;
         w.whole = tiles - left;
-        w.parts = parts;
-        w.share = share;
-        w.more = (int)(total - share * parts);
+        w.splits = n;
     }
     return w;
 }
@@ -569,22 +567,17 @@ struct Operands {
 // 128 x 128 (64 kB) or three of 128 x 64 (48 kB).
 constexpr int per_cu(int ni, int waves) { return waves == 8 ? 1 : ni == 2 ? 2 : 3; }
 
-// A workgroup's tiles in turn: whole ones, then its steps of the divided ones.
+// A workgroup's tiles in turn: whole ones, then a part of one.
 struct Tiles {
-    int id, place, mine;   // workgroup; its place in a full round; among those that share the divided tiles
+    int id, place, mine;   // workgroup; its place in a full round; its part (-1: none)
     int at = 0;            // the round's first tile
-    int64_t step = 0, end = 0;  // of the divided tiles
     // the present one: tile, steps s0 .. s1 - 1, slot of its sums (-1: it is whole)
     int t = 0, s0 = 0, s1 = 0, slot = -1;
 
     __device__ __forceinline__ Tiles(const Work &w, int id_) : id(id_)
     {
         place = place_of(id, w.groups);
-        mine = w.parts ? place_of(id, w.parts) : -1;
-        if (mine >= 0) {
-            step = w.first_step(mine);
-            end = w.first_step(mine + 1);
-        }
+        mine = w.splits ? place_of(id, w.parts()) : -1;
     }
     __device__ __forceinline__ bool next(const Work &w)
     {
@@ -599,14 +592,13 @@ struct Tiles {
         s1 = w.steps;
         slot = -1;
         if (t < 0) {
-            if (step >= end) return false;
-            const int d = (int)(step >> 32 ? step / w.steps : (int64_t)((uint32_t)step / (uint32_t)w.steps));
-            const int64_t from = (int64_t)d * w.steps;
-            s0 = (int)(step - from);
-            s1 = (int)(end - from < w.steps ? end - from : w.steps);
-            step += s1 - s0;
-            if (s0 != 0 || s1 != w.steps) slot = mine + d;
-            t = w.whole + d;
+            if (mine < 0) return false;
+            const int left = w.left(), split = (int)((uint32_t)mine / (uint32_t)left);
+            t = w.whole + mine - split * left;
+            s0 = w.first_step(split);
+            s1 = w.first_step(split + 1);
+            slot = mine;
+            mine = -1;
         }
         return true;
     }
@@ -852,16 +844,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a
     const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kN);
     constexpr MmShape kMine = kShapes[BF][WM * WN == 8 ? 0 : NI == 2 ? 1 : 2];
     const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1, kBK<BF>), kMine);
-    if (d >= work.tiles - work.whole) return;
-    const int w0 = work.owner((int64_t)d * work.steps), w1 = work.owner((int64_t)(d + 1) * work.steps - 1);
-    if (w0 == w1) return;  // done whole
+    if (d >= work.left()) return;
     f16v acc[kI][kJ];
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[i][j] = f16v{};
-    for (int w = w0; w <= w1; ++w) {
-        const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w + d) * (kTA * kTN / 4) +
+    for (int w = 0; w < work.splits; ++w) {
+        const f4 *p = reinterpret_cast<const f4 *>(a.partial) + (int64_t)(w * work.left() + d) * (kTA * kTN / 4) +
                       wave * MI * NI * 256 + lane;
 #pragma unroll
         for (int i = 0; i < kI; ++i)
@@ -898,16 +888,17 @@ MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool lim
         p.work = plan_work((int)(ceil_div(M, gated ? c.m / 2 : c.m) * ceil_div(N, c.n)),
                            (int)steps_of(K, K1, dtype ? kBK<true> : kBK<false>), c);
         const Work &w = p.work;
-        p.divided = w.tiles - w.whole;
+        p.divided = w.left();
         const int full = w.whole / c.groups, last = w.whole % c.groups;
         p.ns = (int64_t)full * ((int64_t)w.steps * c.step + c.tile);
         if (last) p.ns += (int64_t)w.steps * step_ns(c, last) + c.tile;
-        if (w.parts)
-            p.ns += (w.share + 1) * step_ns(c, w.parts) + c.tile + (int64_t)(w.parts + p.divided) * c.part + c.join;
-        int64_t slots = p.work.parts + p.divided;
+        if (w.splits)
+            p.ns += (int64_t)(w.steps / w.splits + 1) * step_ns(c, w.parts()) + c.tile +
+                    (int64_t)w.parts() * c.part + c.join;
+        int64_t slots = w.parts();
         if (limited) {  // fewer tiles, or fewer steps, may be divided where these are not
-            p.divided = p.work.tiles < c.groups ? p.work.tiles : c.groups - 1;
-            slots = c.groups + p.divided;
+            p.divided = w.tiles < c.groups / 2 ? w.tiles : c.groups / 2;
+            slots = c.groups;
         }
         p.bytes = (size_t)slots * (size_t)(c.m * c.n) * sizeof(float);
         if (!best.ns || p.ns < best.ns) best = p;
@@ -924,7 +915,7 @@ template <Epi E, bool BF, bool RCA, bool RCB, Limit L, int MI, int NI, int WM, i
 hipError_t launch_shape(const MmArgs &a, const MmPlan &p, hipStream_t st)
 {
     const dim3 threads(64 * WM * WN);
-    const int most = p.work.parts > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
+    const int most = p.work.parts() > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
     const int n = most < p.work.groups ? most : p.work.groups;
     hipLaunchKernelGGL((gscan_mm_kernel<E, BF, RCA, RCB, L, MI, NI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
     hipError_t e = hipGetLastError();
