@@ -491,7 +491,7 @@ EmbedPlan plan_embed(int64_t N, int64_t V, int D)
 {
     EmbedPlan p;
     while (p.passes < 4 && (V >> (8 * p.passes)) != 0) ++p.passes;  // keys are 0 .. V
-    while (p.chunk < 32 ? (int64_t)p.chunk * 1024 < N : (int64_t)p.chunk * p.chunk * 64 < N) p.chunk *= 2;
+    while (p.chunk < 32 ? (int64_t)p.chunk * 512 < N : (int64_t)p.chunk * p.chunk * 64 < N) p.chunk *= 2;
     p.small = N <= kSSmall && V < int64_t(1) << (32 - kPosBits);
     p.blocks = (N + kSBlock - 1) / kSBlock;
     p.chunks = (N + p.chunk - 1) / p.chunk;

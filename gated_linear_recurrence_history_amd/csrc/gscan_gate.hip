@@ -9,7 +9,7 @@
 // Backward: the same kernel again, whose epilogue leaves da | db (in the type of
 // the operands: the one rounding between the products), then a product for dx
 // over the columns of da and db in turn, and one for both weights' gradients.
-#include "gscan_mm.h"
+#include "gscan_few.h"
 
 namespace gscan {
 
@@ -57,7 +57,7 @@ MmArgs products(const GateArgs &g)
 
 size_t gate_workspace_bytes(const GateArgs &g, bool backward)
 {
-    return g.N ? lay_out(g, backward).bytes : 0;
+    return g.N && (backward || g.N > kFew) ? lay_out(g, backward).bytes : 0;
 }
 
 hipError_t launch_gate_forward(const GateArgs &g, hipStream_t st)
@@ -65,6 +65,8 @@ hipError_t launch_gate_forward(const GateArgs &g, hipStream_t st)
     MmArgs a = products(g);
     a.out = g.out;
     a.ldo = g.F;
+    if (!g.N) return hipSuccess;
+    if (g.N <= kFew) return launch_few<EPI_GATE>(a, g.dtype, st);
     return launch_mm<EPI_GATE, false, false, LIMIT_NONE>(a, g.dtype, g.ws, st);
 }
 

@@ -48,6 +48,8 @@ struct MmArgs {
     const void *dout = nullptr;
     int64_t ldd = 0;
     const int32_t *target = nullptr, *row = nullptr;  // by n: target, place in the caller's order
+    const void *tokens = nullptr;   // targets as the caller has them (few tokens)
+    int tok64 = 0;
     const float *up = nullptr, *lse = nullptr;        // by n (up null: one)
     const float *factor = nullptr;  // EPI_STORE, EPI_ADD: of the whole output (null: one)
     float2 *part = nullptr;         // [tile of m][N]

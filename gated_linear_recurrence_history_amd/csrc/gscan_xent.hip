@@ -21,7 +21,7 @@
 // out: a first kernel lists the others, and where some are missing their rows
 // are copied so that they follow each other.  What is in the rows left out, NaN
 // included, reaches nothing.
-#include "gscan_mm.h"
+#include "gscan_few.h"
 
 namespace gscan {
 namespace {
@@ -81,7 +81,9 @@ Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
     } else {
         l.picked = (float *)take((size_t)N * 4);
         l.loss = (float *)take((size_t)N * 4);
-        l.part = (float2 *)take((size_t)tiles_of_m(V, N, D, dtype) * N * sizeof(float2));
+        size_t parts = (size_t)tiles_of_m(V, N, D, dtype);
+        if (N <= kFew && parts < (size_t)kFewGrid) parts = (size_t)kFewGrid;
+        l.part = (float2 *)take(parts * N * sizeof(float2));
         l.partial = take(mm_bytes(V, N, D, 0, false, true, dtype));
     }
     l.bytes = at;
@@ -184,6 +186,41 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_total_kernel(XentArgs a,
     }
 }
 
+// Few tokens: a wavefront joins a token's partial results, and the last step of a sum or
+// a mean is the workgroup's.
+__global__ void __launch_bounds__(kLThreads) gscan_xent_few_join_kernel(XentArgs a, Listed l, int parts)
+{
+    __shared__ float losses[kFew];
+    __shared__ int counted[kFew];
+    const int lane = threadIdx.x & 63;
+    for (int n = threadIdx.x >> 6; n < a.N; n += kLThreads / 64) {
+        float m = -INFINITY, s = 0.f;
+        for (int p = lane; p < parts; p += 64) {
+            const float2 x = l.part[(int64_t)p * a.N + n];
+            join_lse(m, s, x.x, x.y);
+        }
+        for (int k = 32; k > 0; k /= 2) join_lse(m, s, __shfl_xor(m, k), __shfl_xor(s, k));
+        if (lane) continue;
+        const bool counts = token_at(a.target, n, a.target64, a.V) >= 0;
+        const float tail = log2f(s), unit = 0.69314718055994531f;
+        a.lse[n] = counts ? (m + tail) * unit : 0.f;
+        counted[n] = counts;
+        losses[n] = counts ? (m - l.picked[n] + tail) * unit : 0.f;
+        if (!a.reduction) a.loss[n] = losses[n];
+    }
+    if (!a.reduction) return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+        int count = 0;
+        for (int n = 0; n < a.N; ++n) {
+            all += (double)losses[n];
+            count += counted[n];
+        }
+        *a.loss = (float)(a.reduction == 2 && count ? all / count : all);
+    }
+}
+
 hipError_t launch_list(const XentArgs &x, const Listed &l, bool backward, hipStream_t st)
 {
     if (backward)
@@ -231,8 +268,18 @@ size_t xent_backward_workspace_bytes(int64_t N, int64_t V, int D, int dtype)
 hipError_t launch_xent_forward(const XentArgs &x, hipStream_t st)
 {
     const Listed l = lay_out(x.ws, x.N, x.V, x.D, x.dtype, false);
-    hipError_t e = launch_list(x, l, false, st);
-    if (e != hipSuccess) return e;
+    hipError_t e;
+    if (x.N && x.N <= kFew) {
+        MmArgs a = logits_of(x, l, 0, x.V);
+        a.part = l.part;
+        a.picked = l.picked;
+        a.tokens = x.target;
+        a.tok64 = x.target64;
+        if ((e = launch_few<EPI_LSE>(a, x.dtype, st)) != hipSuccess) return e;
+        hipLaunchKernelGGL(gscan_xent_few_join_kernel, dim3(1), dim3(kLThreads), 0, st, x, l, few_grid(few_groups<EPI_LSE>(a)));
+        return hipGetLastError();
+    }
+    if ((e = launch_list(x, l, false, st)) != hipSuccess) return e;
     if (x.N) {
         MmArgs a = logits_of(x, l, 0, x.V);
         a.part = l.part;
