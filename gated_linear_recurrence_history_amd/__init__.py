@@ -19,7 +19,7 @@ from . import workloads  # noqa: F401
 from .autograd import GatedScanFunction, gated_scan  # noqa: F401
 from .embedding import (EmbedFunction, embed, embed_backward,  # noqa: F401
                         embed_backward_workspace_bytes, embed_forward)
-from .gated_projection import (GatedProjectionFunction, gated_projection,  # noqa: F401
+from .gated import (GatedProjectionFunction, gated_projection,  # noqa: F401
                                gated_projection_backward, gated_projection_backward_workspace_bytes,
                                gated_projection_forward, gated_projection_forward_workspace_bytes)
 from .cross_entropy import (LinearCrossEntropyFunction, linear_cross_entropy,  # noqa: F401

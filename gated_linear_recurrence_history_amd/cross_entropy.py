@@ -17,14 +17,14 @@ lse are zero, and what its row of h holds reaches nothing.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .embedding import _check_tokens, _device_of, _row_stride, _type_code
-from .gated_projection import _rows
-from .matrix_state import _check_dense, _On, _on_device, _ptr, _workspace
+from .embedding import _check_tokens, _device_of, _row_stride, _rows, _type_code
+from .matrix_state import _check_dense, _layout, _On, _on_device, _ptr, _workspace
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
@@ -35,32 +35,44 @@ class _Desc(ctypes.Structure):
                 ("reduction", ctypes.c_int), ("target_int64", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+@functools.lru_cache(maxsize=256)
+def _template(h, weight, target, dtypes, scale, reduction):
+    """The descriptor of a call, as bytes; h and weight are (shape, stride)."""
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
+    if dtypes[1] != dtypes[0]:
+        raise TypeError(f"h and weight must share a type; got {dtypes[0]}, {dtypes[1]}")
+    hs, ws = h[0], weight[0]
+    if len(hs) < 1 or len(ws) != 2 or ws[1] != hs[-1] or target != hs[:-1]:
+        raise ValueError("h must be [..., width], weight [vocabulary, width], target [...]; got "
+                         f"{tuple(hs)}, {tuple(ws)}, {tuple(target)}")
+    return bytes(_Desc(target.numel(), hs[-1], ws[0], _row_stride(*h, "h"), _row_stride(*weight, "weight"),
+                       _type_code(dtypes[0], "h"), REDUCTIONS[reduction], dtypes[2] == torch.int64, scale))
+
+
+@functools.lru_cache(maxsize=256)
+def _need(desc, backward):
+    L = binding.lib()
+    return int((L.gscan_linear_cross_entropy_backward_workspace_bytes if backward else
+                L.gscan_linear_cross_entropy_forward_workspace_bytes)(desc))
+
+
 def _describe(h, weight, target, scale, reduction):
     dev = _device_of(h, "h")
     _on_device(dev, weight=weight)
     _check_tokens(target, dev, "target")
-    if reduction not in REDUCTIONS:
-        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
-    if weight.dtype != h.dtype:
-        raise TypeError(f"h and weight must share a type; got {h.dtype}, {weight.dtype}")
-    if h.dim() < 1 or weight.dim() != 2 or weight.shape[1] != h.shape[-1] or target.shape != h.shape[:-1]:
-        raise ValueError("h must be [..., width], weight [vocabulary, width], target [...]; got "
-                         f"{tuple(h.shape)}, {tuple(weight.shape)}, {tuple(target.shape)}")
-    return _Desc(target.numel(), h.shape[-1], weight.shape[0], _row_stride(h, "h"),
-                 _row_stride(weight, "weight"), _type_code(h.dtype, "h"), REDUCTIONS[reduction],
-                 target.dtype == torch.int64, float(scale))
+    return _template(_layout(h), _layout(weight), target.shape, (h.dtype, weight.dtype, target.dtype),
+                     float(scale), reduction)
 
 
 def linear_cross_entropy_forward_workspace_bytes(h, weight, target) -> int:
     """Workspace of linear_cross_entropy_forward for these operands."""
-    d = _describe(h, weight, target, 1.0, "none")
-    return int(binding.lib().gscan_linear_cross_entropy_forward_workspace_bytes(ctypes.byref(d)))
+    return _need(_describe(h, weight, target, 1.0, "none"), False)
 
 
 def linear_cross_entropy_backward_workspace_bytes(h, weight, target) -> int:
     """Workspace of linear_cross_entropy_backward for these operands."""
-    d = _describe(h, weight, target, 1.0, "none")
-    return int(binding.lib().gscan_linear_cross_entropy_backward_workspace_bytes(ctypes.byref(d)))
+    return _need(_describe(h, weight, target, 1.0, "none"), True)
 
 
 def linear_cross_entropy_forward(h, weight, target, scale: float = 1.0, reduction: str = "mean",
@@ -74,14 +86,13 @@ def linear_cross_entropy_forward(h, weight, target, scale: float = 1.0, reductio
     from torch's caching allocator.
     """
     d = _describe(h, weight, target, scale, reduction)
-    dev, L = h.device, binding.lib()
-    need = int(L.gscan_linear_cross_entropy_forward_workspace_bytes(ctypes.byref(d)))
+    dev, need = h.device, _need(d, False)
     with _On(dev, stream) as s:
         lse = torch.empty(target.shape, dtype=torch.float32, device=dev)
-        loss = torch.empty(() if d.reduction else target.shape, dtype=torch.float32, device=dev)
+        loss = torch.empty(target.shape if reduction == "none" else (), dtype=torch.float32, device=dev)
         wp, wn, _keep = _workspace(workspace, need, dev)
-        binding._check(L.gscan_linear_cross_entropy_forward(
-            ctypes.byref(d), h.data_ptr(), weight.data_ptr(), target.data_ptr(), loss.data_ptr(),
+        binding._check(binding.lib().gscan_linear_cross_entropy_forward(
+            d, h.data_ptr(), weight.data_ptr(), target.data_ptr(), loss.data_ptr(),
             lse.data_ptr(), wp, wn, s))
     return loss, lse
 
@@ -97,16 +108,15 @@ def linear_cross_entropy_backward(h, weight, target, lse, d_loss, scale: float =
     from torch's caching allocator.
     """
     d = _describe(h, weight, target, scale, reduction)
-    dev, L = h.device, binding.lib()
+    dev, need = h.device, _need(d, True)
     _check_dense(lse, target.shape, torch.float32, dev, "lse")
-    _check_dense(d_loss, torch.Size() if d.reduction else target.shape, torch.float32, dev, "d_loss")
-    need = int(L.gscan_linear_cross_entropy_backward_workspace_bytes(ctypes.byref(d)))
+    _check_dense(d_loss, target.shape if reduction == "none" else torch.Size(), torch.float32, dev, "d_loss")
     with _On(dev, stream) as s:
         dh = torch.empty(h.shape, dtype=h.dtype, device=dev) if wanted[0] else None
         dw = torch.empty(weight.shape, dtype=h.dtype, device=dev) if wanted[1] else None
         wp, wn, _keep = _workspace(workspace, need, dev)
-        binding._check(L.gscan_linear_cross_entropy_backward(
-            ctypes.byref(d), h.data_ptr(), weight.data_ptr(), target.data_ptr(), lse.data_ptr(),
+        binding._check(binding.lib().gscan_linear_cross_entropy_backward(
+            d, h.data_ptr(), weight.data_ptr(), target.data_ptr(), lse.data_ptr(),
             d_loss.data_ptr(), _ptr(dh), _ptr(dw), wp, wn, s))
     return dh, dw
 

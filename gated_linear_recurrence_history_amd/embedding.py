@@ -15,12 +15,13 @@ float32 table gives bfloat16 activations without a copy of its own.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .matrix_state import (_CODES, _On, _check_dense, _layout, _on_device, _outer_strides, _ptr, _readable,
+from .matrix_state import (_CODES, _On, _check_dense, _layout, _on_device, _outer_strides, _readable,
                            _reads_rows, _workspace)
 
 
@@ -30,15 +31,18 @@ class _Desc(ctypes.Structure):
                 ("token_int64", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
-def _row_stride(t, name):
+def _row_stride(shape, stride, name):
     """The one stride between the rows of a tensor [..., width]."""
-    if not _reads_rows(*_layout(t)):
+    if not _reads_rows(shape, stride):
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    if t.dim() == 2:
-        return _outer_strides(*_layout(t))[0]
-    if not t.is_contiguous():
-        raise ValueError(f"{name} of more than two dimensions must be contiguous")
-    return t.shape[-1]
+    if len(shape) == 2:
+        return _outer_strides(shape, stride)[0]
+    dense = 1
+    for n, x in zip(reversed(shape), reversed(stride)):
+        if n > 1 and x != dense and 0 not in shape:
+            raise ValueError(f"{name} of more than two dimensions must be contiguous")
+        dense *= n
+    return shape[-1]
 
 
 def _check_tokens(tokens, dev, name="tokens"):
@@ -60,42 +64,65 @@ def _device_of(t, name):
     return t.device
 
 
+def _rows(t):
+    """t as the library reads it: copied where its rows lie on no multiple of 16
+    bytes or at no single stride; what is no tensor is left to the checks."""
+    if not isinstance(t, torch.Tensor):
+        return t
+    return _readable(t if t.dim() == 2 else t.contiguous(), t)
+
+
+@functools.lru_cache(maxsize=256)
+def _template(rows, dtype, other, tokens, token_dtype, vocabulary, scale):
+    """The descriptor of a call, as bytes; rows: (shape, stride) of the table
+    (vocabulary None) or of the gradients of the output."""
+    if vocabulary is None:
+        if len(rows[0]) != 2:
+            raise ValueError(f"table must be [vocabulary, width], got {tuple(rows[0])}")
+        d = _Desc(tokens.numel(), *rows[0], _row_stride(*rows, "table"), _type_code(dtype, "table"),
+                  _type_code(other, "dtype"))
+    else:
+        if len(rows[0]) < 1 or rows[0][:-1] != tokens:
+            raise ValueError(f"d_out must be [*tokens.shape, width]; got {tuple(rows[0])} beside {tuple(tokens)}")
+        d = _Desc(tokens.numel(), vocabulary, rows[0][-1], _row_stride(*rows, "d_out"),
+                  _type_code(other, "dtype"), _type_code(dtype, "d_out"))
+    d.token_int64, d.scale = token_dtype == torch.int64, scale
+    return bytes(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _need(desc):
+    return int(binding.lib().gscan_embed_workspace_bytes(desc))
+
+
 def embed_forward(table, tokens, scale: float = 1.0, dtype=None, out=None, stream=None):
     """scale * table[tokens], of shape [*tokens.shape, width] and type `dtype`
     (float32 or bfloat16; the table's own by default)."""
     dev = _device_of(table, "table")
-    if table.dim() != 2:
-        raise ValueError(f"table must be [vocabulary, width], got {tuple(table.shape)}")
     _check_tokens(tokens, dev)
     dtype = table.dtype if dtype is None else dtype
+    d = _template(_layout(table), table.dtype, dtype, tokens.shape, tokens.dtype, None, float(scale))
     shape = (*tokens.shape, table.shape[1])
-    d = _Desc(tokens.numel(), *table.shape, _row_stride(table, "table"), _type_code(table.dtype, "table"),
-              _type_code(dtype, "dtype"), tokens.dtype == torch.int64, float(scale))
     if out is not None:
         _check_dense(out, shape, dtype, dev, "out")
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=dev)
-        binding._check(binding.lib().gscan_embed_forward(
-            ctypes.byref(d), table.data_ptr(), tokens.data_ptr(), out.data_ptr(), s))
+        binding._check(binding.lib().gscan_embed_forward(d, table.data_ptr(), tokens.data_ptr(),
+                                                         out.data_ptr(), s))
     return out
 
 
 def _describe_backward(d_out, tokens, vocabulary, scale, dtype):
     dev = _device_of(d_out, "d_out")
     _check_tokens(tokens, dev)
-    if d_out.dim() < 1 or d_out.shape[:-1] != tokens.shape:
-        raise ValueError(f"d_out must be [*tokens.shape, width]; got {tuple(d_out.shape)} beside "
-                         f"{tuple(tokens.shape)}")
-    return _Desc(tokens.numel(), int(vocabulary), d_out.shape[-1], _row_stride(d_out, "d_out"),
-                 _type_code(dtype, "dtype"), _type_code(d_out.dtype, "d_out"), tokens.dtype == torch.int64,
-                 float(scale))
+    return _template(_layout(d_out), d_out.dtype, d_out.dtype if dtype is None else dtype, tokens.shape,
+                     tokens.dtype, int(vocabulary), float(scale))
 
 
 def embed_backward_workspace_bytes(d_out, tokens, vocabulary) -> int:
     """Workspace of embed_backward for these operands."""
-    d = _describe_backward(d_out, tokens, vocabulary, 1.0, d_out.dtype)
-    return int(binding.lib().gscan_embed_workspace_bytes(ctypes.byref(d)))
+    return _need(_describe_backward(d_out, tokens, vocabulary, 1.0, None))
 
 
 def embed_backward(d_out, tokens, vocabulary: int, scale: float = 1.0, dtype=None, out=None,
@@ -107,19 +134,18 @@ def embed_backward(d_out, tokens, vocabulary: int, scale: float = 1.0, dtype=Non
     embed_backward_workspace_bytes() bytes; otherwise one is taken from torch's
     caching allocator.
     """
-    dtype = d_out.dtype if dtype is None and isinstance(d_out, torch.Tensor) else dtype
     d = _describe_backward(d_out, tokens, vocabulary, scale, dtype)
-    dev, L = d_out.device, binding.lib()
-    shape = (d.vocabulary, d.width)
+    dev = d_out.device
+    dtype = d_out.dtype if dtype is None else dtype
+    shape, need = (int(vocabulary), d_out.shape[-1]), _need(d)
     if out is not None:
         _check_dense(out, shape, dtype, dev, "out")
-    need = int(L.gscan_embed_workspace_bytes(ctypes.byref(d)))
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape if d.vocabulary > 0 else (0, 0), dtype=dtype, device=dev)
+            out = torch.empty(shape if shape[0] > 0 else (0, 0), dtype=dtype, device=dev)
         wp, wn, _keep = _workspace(workspace, need, dev)
-        binding._check(L.gscan_embed_backward(ctypes.byref(d), _ptr(d_out), tokens.data_ptr(),
-                                              out.data_ptr(), wp, wn, s))
+        binding._check(binding.lib().gscan_embed_backward(d, d_out.data_ptr(), tokens.data_ptr(),
+                                                          out.data_ptr(), wp, wn, s))
     return out
 
 
@@ -128,19 +154,17 @@ class EmbedFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, table, tokens, scale, dtype):
+        out = embed_forward(_rows(table), tokens, scale, dtype)
         ctx.save_for_backward(tokens)
-        ctx.args = (table.shape, table.dtype, float(scale))
-        return embed_forward(_readable(table, table), tokens, scale, dtype)
+        ctx.args = (table.shape[0], float(scale), table.dtype)
+        return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_out):
         if not ctx.needs_input_grad[0]:
             return (None,) * 4
-        (tokens,), (shape, dtype, scale) = ctx.saved_tensors, ctx.args
-        if d_out.dim() != 2:
-            d_out = d_out.contiguous()
-        return embed_backward(_readable(d_out, d_out), tokens, shape[0], scale, dtype), None, None, None
+        return embed_backward(_rows(d_out), ctx.saved_tensors[0], *ctx.args), None, None, None
 
 
 def embed(table, tokens, scale: float = 1.0, dtype=None):

@@ -15,13 +15,14 @@ are multiples of 8 up to 65536.  Rows may lie any multiple of 16 bytes up to
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .embedding import _device_of, _row_stride, _type_code
-from .matrix_state import _check_dense, _On, _on_device, _ptr, _readable, _workspace
+from .embedding import _device_of, _row_stride, _rows, _type_code
+from .matrix_state import _check_dense, _layout, _On, _on_device, _ptr, _workspace
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
@@ -33,31 +34,53 @@ class _Desc(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("activation", ctypes.c_int)]
 
 
-def _describe(x, w_gate, w_up, activation):
-    dev = _device_of(x, "x")
-    _on_device(dev, w_gate=w_gate, w_up=w_up)
+@functools.lru_cache(maxsize=256)
+def _template(x, w_gate, w_up, dtypes, activation, d_out):
+    """The descriptor of a call, as bytes; operands are (shape, stride), d_out None
+    in the forward."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
-        raise TypeError(f"x and the weights must share a type; got {x.dtype}, {w_gate.dtype}, {w_up.dtype}")
-    if x.dim() < 1 or w_gate.dim() != 2 or w_up.shape != w_gate.shape or w_gate.shape[1] != x.shape[-1]:
+    if dtypes[1] != dtypes[0] or dtypes[2] != dtypes[0]:
+        raise TypeError(f"x and the weights must share a type; got {dtypes[0]}, {dtypes[1]}, {dtypes[2]}")
+    xs, gs, us = x[0], w_gate[0], w_up[0]
+    if len(xs) < 1 or len(gs) != 2 or us != gs or gs[1] != xs[-1]:
         raise ValueError("x must be [..., width], the weights [inner, width]; got "
-                         f"{tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)}")
-    tokens = x.numel() // x.shape[-1] if x.shape[-1] else 0
-    return _Desc(tokens, x.shape[-1], w_gate.shape[0], _row_stride(x, "x"), _row_stride(w_gate, "w_gate"),
-                 _row_stride(w_up, "w_up"), 0, _type_code(x.dtype, "x"), ACTIVATIONS[activation])
+                         f"{tuple(xs)}, {tuple(gs)}, {tuple(us)}")
+    d = _Desc(xs[:-1].numel(), xs[-1], gs[0], _row_stride(*x, "x"), _row_stride(*w_gate, "w_gate"),
+              _row_stride(*w_up, "w_up"), 0, _type_code(dtypes[0], "x"), ACTIVATIONS[activation])
+    if d_out is not None:
+        if dtypes[3] != dtypes[0] or d_out[0] != (*xs[:-1], gs[0]):
+            raise ValueError(f"d_out must be {dtypes[0]} {(*xs[:-1], gs[0])}; got {dtypes[3]} {tuple(d_out[0])}")
+        d.d_out_stride = _row_stride(*d_out, "d_out")
+    return bytes(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _need(desc, backward):
+    L = binding.lib()
+    return int((L.gscan_gated_projection_backward_workspace_bytes if backward else
+                L.gscan_gated_projection_forward_workspace_bytes)(desc))
+
+
+def _describe(x, w_gate, w_up, activation, d_out=None):
+    dev = _device_of(x, "x")
+    _on_device(dev, w_gate=w_gate, w_up=w_up)
+    if d_out is None:
+        return _template(_layout(x), _layout(w_gate), _layout(w_up), (x.dtype, w_gate.dtype, w_up.dtype),
+                         activation, None)
+    _on_device(dev, d_out=d_out)
+    return _template(_layout(x), _layout(w_gate), _layout(w_up),
+                     (x.dtype, w_gate.dtype, w_up.dtype, d_out.dtype), activation, _layout(d_out))
 
 
 def gated_projection_forward_workspace_bytes(x, w_gate, w_up) -> int:
     """Workspace of gated_projection_forward for these operands (0: none needed)."""
-    d = _describe(x, w_gate, w_up, "silu")
-    return int(binding.lib().gscan_gated_projection_forward_workspace_bytes(ctypes.byref(d)))
+    return _need(_describe(x, w_gate, w_up, "silu"), False)
 
 
 def gated_projection_backward_workspace_bytes(x, w_gate, w_up) -> int:
     """Workspace of gated_projection_backward for these operands."""
-    d = _describe(x, w_gate, w_up, "silu")
-    return int(binding.lib().gscan_gated_projection_backward_workspace_bytes(ctypes.byref(d)))
+    return _need(_describe(x, w_gate, w_up, "silu"), True)
 
 
 def gated_projection_forward(x, w_gate, w_up, activation: str = "silu", out=None, workspace=None,
@@ -70,16 +93,15 @@ def gated_projection_forward(x, w_gate, w_up, activation: str = "silu", out=None
     torch's caching allocator where needed.
     """
     d = _describe(x, w_gate, w_up, activation)
-    dev, shape, L = x.device, (*x.shape[:-1], w_gate.shape[0]), binding.lib()
-    need = int(L.gscan_gated_projection_forward_workspace_bytes(ctypes.byref(d)))
+    dev, shape, need = x.device, (*x.shape[:-1], w_gate.shape[0]), _need(d, False)
     if out is not None:
         _check_dense(out, shape, x.dtype, dev, "out")
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty(shape, dtype=x.dtype, device=dev)
         wp, wn, _keep = _workspace(workspace, need, dev)
-        binding._check(L.gscan_gated_projection_forward(
-            ctypes.byref(d), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), wp, wn, s))
+        binding._check(binding.lib().gscan_gated_projection_forward(
+            d, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), wp, wn, s))
     return out
 
 
@@ -92,28 +114,18 @@ def gated_projection_backward(x, w_gate, w_up, d_out, activation: str = "silu", 
     gated_projection_backward_workspace_bytes() bytes; otherwise one is taken
     from torch's caching allocator.
     """
-    d = _describe(x, w_gate, w_up, activation)
-    dev, L = x.device, binding.lib()
-    _on_device(dev, d_out=d_out)
-    if d_out.dtype != x.dtype or d_out.shape != (*x.shape[:-1], w_gate.shape[0]):
-        raise ValueError(f"d_out must be {x.dtype} {(*x.shape[:-1], w_gate.shape[0])}; got {d_out.dtype} "
-                         f"{tuple(d_out.shape)}")
-    d.d_out_stride = _row_stride(d_out, "d_out")
-    need = int(L.gscan_gated_projection_backward_workspace_bytes(ctypes.byref(d)))
+    if d_out is None:
+        raise ValueError("d_out must be a tensor")
+    d = _describe(x, w_gate, w_up, activation, d_out)
+    dev, need = x.device, _need(d, True)
     with _On(dev, stream) as s:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if wanted[0] else None
         dg, du = (torch.empty(w_gate.shape, dtype=x.dtype, device=dev) if wanted[1] else None for _ in range(2))
         wp, wn, _keep = _workspace(workspace, need, dev)
-        binding._check(L.gscan_gated_projection_backward(
-            ctypes.byref(d), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), d_out.data_ptr(), _ptr(dx),
-            _ptr(dg), _ptr(du), wp, wn, s))
+        binding._check(binding.lib().gscan_gated_projection_backward(
+            d, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), d_out.data_ptr(), _ptr(dx), _ptr(dg),
+            _ptr(du), wp, wn, s))
     return dx, dg, du
-
-
-def _rows(t):
-    """t as the library reads it: copied where its rows lie on no multiple of 16
-    bytes or at no single stride."""
-    return _readable(t, t) if t.dim() == 2 else _readable(t.contiguous(), t)
 
 
 class GatedProjectionFunction(torch.autograd.Function):
@@ -123,9 +135,10 @@ class GatedProjectionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, activation):
         x, w_gate, w_up = _rows(x), _rows(w_gate), _rows(w_up)
+        out = gated_projection_forward(x, w_gate, w_up, activation)
         ctx.save_for_backward(x, w_gate, w_up)
         ctx.activation = activation
-        return gated_projection_forward(x, w_gate, w_up, activation)
+        return out
 
     @staticmethod
     @once_differentiable
