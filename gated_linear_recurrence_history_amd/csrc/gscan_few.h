@@ -31,7 +31,7 @@ __device__ __forceinline__ f4 multiply16(const u4 &x, const u4 &y, f4 acc)
     }
 }
 
-// EPI_GATE: out[n][m].  EPI_LSE: part[workgroup][n], the maximum and the sum of
+// EPI_GATE: out[n][m].  EPI_LSE: part[n][workgroup], the maximum and the sum of
 // powers of two of the workgroup's logits, and the targets' logits.  R: groups of 16 rows of a weight taken together.
 template <Epi E, int NT>
 constexpr int kFewRows = E == EPI_GATE || NT == 1 ? NT : 4;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kFewThreads, 4) gscan_few_kernel(MmArgs a, int
             if (tid < 16 && 16 * t + tid < a.N) {
                 float m = -INFINITY, s = 0.f;
                 for (int i = 0; i < 16; ++i) join_lse(m, s, ends[16 * tid + i].x, ends[16 * tid + i].y);
-                a.part[(int64_t)blockIdx.x * a.N + 16 * t + tid] = float2{m, s};
+                a.part[(int64_t)(16 * t + tid) * gridDim.x + blockIdx.x] = float2{m, s};
             }
         }
     }

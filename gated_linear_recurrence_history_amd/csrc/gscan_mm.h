@@ -59,7 +59,8 @@ struct MmArgs {
     int first = 1, last = 1;
     float scale = 1.f;
     int act = 0;
-    float *partial = nullptr;       // sums of parts of tiles (Work)
+    int parts = 0;                  // of the tiles that are left, at most (Work)
+    float *partial = nullptr;       // their sums
 };
 
 // -------------------------------------------------------------- activations
@@ -144,6 +145,65 @@ __device__ __forceinline__ int place_of(int id, int n)
     return y < q + (x < r ? 1 : 0) ? x * q + (x < r ? x : r) + y : -1;
 }
 
+// The 16 elements of a lane among 32 m (groups of four at 8 g + 4 (lane / 32)) to or from
+// row[m ..]; in(x) says whether the eight m from x on exist.  bf16: the halves of the
+// wavefront exchange theirs, so that a lane has eight that follow each other: 16
+// bytes instead of 8, half as many accesses.
+template <bool BF, class In>
+__device__ __forceinline__ void store16(void *out, int64_t row, int m, const f4 (&v)[4], int hi, In in)
+{
+    if constexpr (BF) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto s = __builtin_amdgcn_permlane32_swap(pack_bf16(v[g][2 * e], v[g][2 * e + 1]),
+                                                                pack_bf16(v[g + 1][2 * e], v[g + 1][2 * e + 1]),
+                                                                false, false);
+                x[e] = s[0];
+                x[2 + e] = s[1];
+            }
+            const int to = m + 8 * (g + hi);
+            if (in(to)) *reinterpret_cast<u4 *>(reinterpret_cast<uint16_t *>(out) + row + to) = u4{x[0], x[1], x[2], x[3]};
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (in(m + 8 * g)) store4<false>(out, row + m + 8 * g + 4 * hi, v[g]);
+    }
+}
+
+template <bool BF, class In>
+__device__ __forceinline__ void load16(const void *from, int64_t row, int m, f4 (&v)[4], int hi, In in)
+{
+    if constexpr (BF) {
+        u4 x[2];
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            const int at = m + 8 * (g + hi);
+            x[g / 2] = u4{};
+            if (in(at)) x[g / 2] = *reinterpret_cast<const u4 *>(reinterpret_cast<const uint16_t *>(from) + row + at);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; g += 2)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto s = __builtin_amdgcn_permlane32_swap(x[g / 2][e], x[g / 2][2 + e], false, false);
+                v[g][2 * e] = bf_lo(s[0]);
+                v[g][2 * e + 1] = bf_hi(s[0]);
+                v[g + 1][2 * e] = bf_lo(s[1]);
+                v[g + 1][2 * e + 1] = bf_hi(s[1]);
+            }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            v[g] = f4{};
+            if (in(m + 8 * g)) v[g] = load4<false>(from, row + m + 8 * g + 4 * hi);
+        }
+    }
+}
+
 // What a workgroup's sums become.  acc[i][j]: the 32 x 32 sums of the rows
 // m0 + mat(i) .. + 31 and n0 + nat + 32 j .. + 31; element r of a lane is m = 8 (r / 4)
 // + 4 (lane / 32) + r % 4, n = lane % 32.  Gated tiles hold the same m of both
@@ -217,92 +277,104 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
         float factor = 1.f;
         if constexpr (E == EPI_STORE || E == EPI_ADD)
             if (a.factor) factor = *a.factor;
-        // `all`: every m of the tile exists
+        // `all`: every m of the tile exists.  Else M is a multiple of eight (the gradients of the
+        // logits are padded to it with zeros).
         auto finish = [&](auto all) __attribute__((always_inline)) {
             constexpr int HI = E == EPI_GATE || E == EPI_DGATE ? MI / 2 : MI;
+            auto inside = [&](int m) { return all.value || m0 + m < a.M; };
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int64_t n = n0 + nat + 32 * j + col;
-                if (n >= N) continue;
-                const int64_t m1 = m0 + 4 * hi;
-                auto inside = [&](int m, int64_t end) { return all.value || m1 + m < end; };
+                if (n >= N) continue;  // (the halves of a wavefront have the same n: both are there or neither)
+                const int64_t at = n * a.ldo + m0;
+                auto sums = [&](int i, f4 (&v)[4]) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        v[g] = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                };
                 if constexpr (E == EPI_DLOGIT) {
-                    const int t = (int)(a.target[n] - a.v0 - m1);
+                    const int t = (int)(a.target[n] - a.v0 - m0) - 4 * hi;
                     const float up = a.up ? a.up[n] : 1.f, lse = a.lse[n];
-                    const int64_t at = n * a.ldo + m1, padded = (a.M + 7) / 8 * 8;
-#pragma unroll
-                    for (int i = 0; i < HI; ++i)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int m = mat(i) + 8 * g;
-                            if (!inside(m, padded)) continue;  // the piece's columns, padded to eight with zeros
-                            f4 v;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float z = acc[i][j][4 * g + e] * a.scale - lse;
-                                const float p = BF ? exp2_(1.44269504f * z) : expf(z);
-                                v[e] = inside(m + e, a.M) ? (p - (m + e == t ? 1.f : 0.f)) * up : 0.f;
-                            }
-                            store4<BF>(a.out, at + m, v);
-                        }
-                } else if constexpr (E == EPI_STORE) {
-                    void *out = n < a.N1 ? a.out : a.out2;
-                    const int64_t at = (n < a.N1 ? n : n - a.N1) * a.ldo + m1;
-#pragma unroll
-                    for (int i = 0; i < HI; ++i)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (const int m = mat(i) + 8 * g; inside(m, a.M))
-                                store4<BF>(out, at + m, factor * f4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
-                                                                    acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
-                } else if constexpr (E == EPI_ADD) {
-                    const int64_t at = n * a.M + m1, to = a.last ? a.row[n] * a.ldo + m1 : 0;
+                    const float unit = a.scale * 1.4426950408889634f, base = -1.4426950408889634f * lse;
+                    const int64_t padded = (a.M + 7) / 8 * 8;
 #pragma unroll
                     for (int i = 0; i < HI; ++i) {
                         f4 v[4];
+                        sums(i, v);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            v[g] = f4{};
-                            if (!a.first && inside(mat(i) + 8 * g, a.M)) v[g] = load4<false>(a.sum, at + mat(i) + 8 * g);
+                        for (int g = 0; g < 4; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[g][e] = BF ? exp2_(fmaf(v[g][e], unit, base)) : expf(v[g][e] * a.scale - lse);
+                        if (__any(t >= mat(i) - 4 && t < mat(i) + 32)) {  // someone's target is here
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[g][e] -= mat(i) + 8 * g + e == t ? 1.f : 0.f;
                         }
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int m = mat(i) + 8 * g;
-                            if (!inside(m, a.M)) continue;
+                        for (int g = 0; g < 4; ++g)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) v[g][e] += acc[i][j][4 * g + e];
-                            if (a.last) store4<BF>(a.out, to + m, v[g] * factor);
-                            else store4<false>(a.sum, at + m, v[g]);
+                            for (int e = 0; e < 4; ++e)
+                                v[g][e] = inside(mat(i) + 8 * g + 4 * hi + e) ? v[g][e] * up : 0.f;
+                        store16<BF>(a.out, at, mat(i), v, hi, [&](int m) { return all.value || m0 + m < padded; });
+                    }
+                } else if constexpr (E == EPI_STORE) {
+                    void *out = n < a.N1 ? a.out : a.out2;
+                    const int64_t to = n < a.N1 ? at : at - a.N1 * a.ldo;
+#pragma unroll
+                    for (int i = 0; i < HI; ++i) {
+                        f4 v[4];
+                        sums(i, v);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) v[g] *= factor;
+                        store16<BF>(out, to, mat(i), v, hi, inside);
+                    }
+                } else if constexpr (E == EPI_ADD) {
+                    const int64_t between = n * a.M + m0, to = a.last ? a.row[n] * a.ldo + m0 : 0;
+#pragma unroll
+                    for (int i = 0; i < HI; ++i) {
+                        f4 v[4], s[4];
+                        sums(i, v);
+                        if (!a.first) {
+                            load16<false>(a.sum, between, mat(i), s, hi, inside);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) v[g] += s[g];
+                        }
+                        if (a.last) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) v[g] *= factor;
+                            store16<BF>(a.out, to, mat(i), v, hi, inside);
+                        } else {
+                            store16<false>(a.sum, between, mat(i), v, hi, inside);
                         }
                     }
                 } else {
-                    const int64_t at = n * a.ldo + m1;
-                    f4 d[HI * 4];
+                    f4 d[HI][4];
                     if constexpr (E == EPI_DGATE) {
 #pragma unroll
-                        for (int q = 0; q < HI * 4; ++q)
-                            if (const int m = mat(q / 4) + 8 * (q % 4); inside(m, a.M))
-                                d[q] = load4<BF>(a.dout, n * a.ldd + m1 + m);
+                        for (int i = 0; i < HI; ++i)
+                            load16<BF>(a.dout, n * a.ldd + m0, mat(i), d[i], hi, inside);
                     }
 #pragma unroll
-                    for (int q = 0; q < HI * 4; ++q) {
-                        const int m = mat(q / 4) + 8 * (q % 4);
-                        if (!inside(m, a.M)) continue;
-                        f4 o, o2;
+                    for (int i = 0; i < HI; ++i) {
+                        f4 o[4], o2[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float f, slope;
-                            activation<BF>(acc[q / 4][j][4 * (q % 4) + e], a.act, f, slope);
-                            const float b = acc[HI + q / 4][j][4 * (q % 4) + e];
-                            if constexpr (E == EPI_GATE) {
-                                o[e] = f * b;
-                            } else {
-                                o[e] = d[q][e] * b * slope;
-                                o2[e] = d[q][e] * f;
+                        for (int g = 0; g < 4; ++g)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float f, slope;
+                                activation<BF>(acc[i][j][4 * g + e], a.act, f, slope);
+                                const float b = acc[HI + i][j][4 * g + e];
+                                if constexpr (E == EPI_GATE) {
+                                    o[g][e] = f * b;
+                                } else {
+                                    o[g][e] = d[i][g][e] * b * slope;
+                                    o2[g][e] = d[i][g][e] * f;
+                                }
                             }
-                        }
-                        store4<BF>(a.out, at + m, o);
-                        if constexpr (E == EPI_DGATE) store4<BF>(a.out, at + a.M + m, o2);
+                        store16<BF>(a.out, at, mat(i), o, hi, inside);
+                        if constexpr (E == EPI_DGATE) store16<BF>(a.out, at + a.M, mat(i), o2, hi, inside);
                     }
                 }
             }
@@ -517,24 +589,37 @@ __host__ __device__ __forceinline__ int step_ns(const MmShape &c, int n)
 
 constexpr int kPartSteps = 4;   // at least so many steps to a part
 
-__host__ __device__ __forceinline__ Work plan_work(int tiles, int steps, const MmShape &c)
+// The work with the tiles that are left divided into `parts` parts at most (tokens that
+// the host does not know of leave fewer tiles, or steps).
+__host__ __device__ __forceinline__ Work divide_work(int tiles, int steps, const MmShape &c, int parts)
 {
     Work w;
     w.tiles = w.whole = tiles;
     w.steps = steps;
     w.groups = c.groups;
     const int left = (int)((uint32_t)tiles % (uint32_t)c.groups);
-    if (!left) return w;
-    int64_t best = (int64_t)steps * step_ns(c, left);
-    for (int n = (int)((uint32_t)c.groups / (uint32_t)left); n > 1; n = n > 3 ? n - n / 3 : n - 1) {
-        if (steps / n < kPartSteps) continue;
-        const int64_t ns = (int64_t)(steps / n + 1) * step_ns(c, left * n) + (int64_t)(left * n) * c.part + c.join;
-        if (ns >= best) continue;
-        best = ns;
-        w.whole = tiles - left;
-        w.splits = n;
+    if (left && 2 * left <= parts) {
+        const int most = steps / kPartSteps, n = (int)((uint32_t)parts / (uint32_t)left);
+        w.splits = n < most ? n : most;
+        if (w.splits > 1) w.whole = tiles - left;
+        else w.splits = 0;
     }
     return w;
+}
+
+Work plan_work(int tiles, int steps, const MmShape &c)
+{
+    Work best = divide_work(tiles, steps, c, 0);
+    const int left = tiles % c.groups;
+    if (!left) return best;
+    int64_t least = (int64_t)steps * step_ns(c, left);
+    for (int n = 2; left * n <= c.groups && steps / n >= kPartSteps; ++n) {
+        const int64_t ns = (int64_t)(steps / n + 1) * step_ns(c, left * n) + (int64_t)(left * n) * c.part + c.join;
+        if (ns >= least) continue;
+        least = ns;
+        best = divide_work(tiles, steps, c, left * n);
+    }
+    return best;
 }
 
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -627,7 +712,7 @@ __global__ void __launch_bounds__(64 * WM * WN, per_cu(NI, WM *WN) == 3 ? 3 : 2)
     const int64_t part = two ? a.K1 : o.K;
     const int part_steps = (int)ceil_div(part, kStep);
     constexpr MmShape kMine = kShapes[BF][kW == 8 ? 0 : NI == 2 ? 1 : 2];
-    const Work work = plan_work(tm * tn, two ? 2 * part_steps : part_steps, kMine);
+    const Work work = divide_work(tm * tn, two ? 2 * part_steps : part_steps, kMine, a.parts);
 
     Tile<BF, RCA, kTA, kW> ta;
     Tile<BF, RCB, kTN, kW> tb;
@@ -845,7 +930,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a
     const Operands<L> o(a);
     const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kN);
     constexpr MmShape kMine = kShapes[BF][WM * WN == 8 ? 0 : NI == 2 ? 1 : 2];
-    const Work work = plan_work(tm * tn, (int)steps_of(o.K, a.K1, kBK<BF>), kMine);
+    const Work work = divide_work(tm * tn, (int)steps_of(o.K, a.K1, kBK<BF>), kMine, a.parts);
     if (d >= work.left()) return;
     f16v acc[kI][kJ];
 #pragma unroll
@@ -877,7 +962,7 @@ struct MmPlan {
     int shape = 0;
     Work work;
     size_t bytes = 0;   // of parts of tiles
-    int divided = 0;    // tiles, at most
+    int parts = 0, divided = 0;  // parts, and tiles that have any, at most
     int64_t ns = 0;
 };
 MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited, int dtype)
@@ -897,12 +982,12 @@ MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool lim
         if (w.splits)
             p.ns += (int64_t)(w.steps / w.splits + 1) * step_ns(c, w.parts()) + c.tile +
                     (int64_t)w.parts() * c.part + c.join;
-        int64_t slots = w.parts();
-        if (limited) {  // fewer tiles, or fewer steps, may be divided where these are not
-            p.divided = w.tiles < c.groups / 2 ? w.tiles : c.groups / 2;
-            slots = c.groups;
+        p.parts = w.parts();
+        if (limited && w.splits) {  // fewer tokens may leave other tiles
+            if (w.splits == c.groups / w.left()) p.parts = c.groups;
+            p.divided = w.tiles < p.parts / 2 ? w.tiles : p.parts / 2;
         }
-        p.bytes = (size_t)slots * (size_t)(c.m * c.n) * sizeof(float);
+        p.bytes = (size_t)p.parts * (size_t)(c.m * c.n) * sizeof(float);
         if (!best.ns || p.ns < best.ns) best = p;
     }
     return best;
@@ -917,7 +1002,7 @@ template <Epi E, bool BF, bool RCA, bool RCB, Limit L, int MI, int NI, int WM, i
 hipError_t launch_shape(const MmArgs &a, const MmPlan &p, hipStream_t st)
 {
     const dim3 threads(64 * WM * WN);
-    const int most = p.work.parts() > p.work.tiles || L != LIMIT_NONE ? p.work.groups : p.work.tiles;
+    const int most = p.parts > p.work.tiles ? p.parts : p.work.tiles;
     const int n = most < p.work.groups ? most : p.work.groups;
     hipLaunchKernelGGL((gscan_mm_kernel<E, BF, RCA, RCB, L, MI, NI, WM, WN>), dim3((unsigned)n), threads, 0, st, a);
     hipError_t e = hipGetLastError();
@@ -934,6 +1019,7 @@ hipError_t launch_mm(MmArgs a, int dtype, void *partial, hipStream_t st)
     constexpr bool kGated = E == EPI_GATE || E == EPI_DGATE;
     if (!a.M || !a.N) return hipSuccess;
     const MmPlan p = plan_mm(a.M, a.N, a.K, a.K1, kGated, L != LIMIT_NONE, dtype);
+    a.parts = p.parts;
     a.partial = reinterpret_cast<float *>(partial);
     if (!dtype)
         return p.shape == 1 ? launch_shape<E, false, RCA, RCB, L, 2, 2, 2, 2>(a, p, st)

@@ -195,10 +195,14 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_few_join_kernel(XentArgs
     const int lane = threadIdx.x & 63;
     for (int n = threadIdx.x >> 6; n < a.N; n += kLThreads / 64) {
         float m = -INFINITY, s = 0.f;
-        for (int p = lane; p < parts; p += 64) {
-            const float2 x = l.part[(int64_t)p * a.N + n];
-            join_lse(m, s, x.x, x.y);
+        float2 x[kFewGrid / 64];
+#pragma unroll
+        for (int i = 0; i < kFewGrid / 64; ++i) {
+            x[i] = float2{-INFINITY, 0.f};
+            if (lane + 64 * i < parts) x[i] = l.part[(int64_t)n * parts + lane + 64 * i];
         }
+#pragma unroll
+        for (int i = 0; i < kFewGrid / 64; ++i) join_lse(m, s, x[i].x, x[i].y);
         for (int k = 32; k > 0; k /= 2) join_lse(m, s, __shfl_xor(m, k), __shfl_xor(s, k));
         if (lane) continue;
         const bool counts = token_at(a.target, n, a.target64, a.V) >= 0;
