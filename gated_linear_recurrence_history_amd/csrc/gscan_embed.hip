@@ -13,17 +13,23 @@
 // writes a row of the table's gradient where the whole run lies in its chunk.  Of a
 // run that crosses chunks every chunk leaves a partial sum, which a second kernel
 // adds in order: no token, however frequent, is walked by one wavefront alone.
-// Sums are fp32.  Rows without a token are zeros, which other workgroups write
-// meanwhile: beside the one that sorts few tokens, whose tokens they mark in a bit per
-// row of theirs, or beside the sums of many, looking their rows up among the sorted
-// tokens.  Every row is written once.
+// Sums are fp32.  Rows without a token are zeros.  Every row is written once.
 //
-// Sort: counting by digits of eight bits, from the lowest.  A wavefront takes
-// 64 keys at a time; the lanes with the same digit find each other by one
-// ballot per bit, which gives every key its rank among those before it.  Up to
-// 16384 tokens (of a vocabulary below 2^18: token and position share a word) one
-// workgroup does all digits with the keys in LDS; else each digit takes a launch that
-// counts and one that moves.
+// Sort, up to 65536 tokens (and 2^20 rows): every workgroup has up to 256 rows of the
+// table, goes through all tokens, counts those of the rows before its own and sorts its
+// own by their row; it also writes its rows' zeros.  One launch for any number of
+// rows, and hardly any work for most wavefronts: they skip 64 tokens of which none is
+// theirs after a comparison (16384 tokens of 32000 rows: 16 us; one workgroup that sorts
+// them all by two digits took 30).  Up to 2048 tokens (rows of more than 512: 64) the
+// workgroup adds them up as well, and nothing else is launched: 777 tokens, 1003 rows
+// of 200 fp32, 7.5 us, with the sums and their join in launches of their own 15; rows
+// of 2048 are the other way round from there on (777 tokens, 32000 rows: 58 to 70 us
+// against 56), as the workgroups with frequent tokens add up slice after slice.
+// More tokens are sorted by digits of eight bits, from the lowest, with a launch that
+// counts and one that moves for each; zeros are then written beside the sums, by
+// workgroups that look their rows up among the sorted tokens.
+// Ranks: a wavefront takes 64 keys at a time; the lanes with the same digit find each
+// other by one ballot per bit, which gives every key its rank among those before it.
 #include <type_traits>
 
 #include "gscan_lm_dev.h"
@@ -37,13 +43,18 @@ constexpr int kSThreads = 1024;        // the sort's workgroup,
 constexpr int kSWaves = kSThreads / 64;
 constexpr int kSItems = 8;             // keys per lane of many workgroups
 constexpr int64_t kSBlock = kSThreads * kSItems;
-constexpr int64_t kSSmall = 16384;     // tokens that one workgroup sorts
-constexpr int kPosBits = 14;           // of their positions
+constexpr int64_t kSFew = 2048;        // tokens that are sorted and added up at once,
+constexpr int64_t kSWide = 64;         // of wide rows these,
+constexpr int kFewItems = (int)kSFew / kSThreads;
+constexpr int64_t kSSome = 65536;      // and that are sorted by one launch,
+constexpr int64_t kSRows = int64_t(1) << 20;  // of a table of fewer rows
+constexpr int kLoadItems = 16;         // tokens that a lane requests together
+constexpr int kAlone = 32;             // few tokens: so many of a row are one wavefront's,
+constexpr int kFewAhead = 8;           // which requests so many of them together
 constexpr int kDigits = 256;
 constexpr int kAhead = 16;             // rows a lane requests together
 constexpr int64_t kFewBlocks = 64;     // so many histograms every workgroup adds up by itself
-constexpr int kZeroRows = 64;          // rows of the table that a workgroup looks up,
-constexpr int kMarkRows = 1024;        // or marks, at most
+constexpr int kZeroRows = 64;          // rows of the table that a workgroup looks up
 
 template <bool BFI, bool BFO>
 __global__ void __launch_bounds__(kEThreads) gscan_embed_fwd_kernel(EmbedArgs a, int lpr)
@@ -79,43 +90,75 @@ __global__ void __launch_bounds__(kEThreads) gscan_embed_fwd_kernel(EmbedArgs a,
 
 struct SortLds {
     uint32_t hist[kSWaves][kDigits];
-    uint32_t total[kDigits], lead[4];
+    uint32_t total[kDigits + 1], lead[4];
 };
 
-// Lanes (of those in `in`) with the same digit.
-__device__ __forceinline__ uint64_t peers_of(uint32_t digit, uint64_t in)
+// Keys (tokens; V for padding, which comes after everything) of the tokens i0 + 64 j,
+// the lanes' behind each other; none behind the last of the n tokens: ~0.
+template <int ITEMS>
+__device__ __forceinline__ void token_keys(const EmbedArgs &a, int64_t i0, int64_t n, uint32_t (&key)[ITEMS])
+{
+    if (a.tok64) {  // (not by token: the loads of one lane are to be under way together)
+        int64_t t[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            t[j] = -1;
+            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int64_t *>(a.tokens)[i0 + 64 * j];
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < a.V ? (uint32_t)t[j] : (uint32_t)a.V;
+    } else {
+        int32_t t[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            t[j] = -1;
+            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int32_t *>(a.tokens)[i0 + 64 * j];
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < a.V ? (uint32_t)t[j] : (uint32_t)a.V;
+    }
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (i0 + 64 * j >= n) key[j] = ~0u;
+}
+
+// Lanes (of those in `in`) with the same digit, of so many bits.
+__device__ __forceinline__ uint64_t peers_of(uint32_t digit, uint64_t in, int bits)
 {
     uint64_t m = in;
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
+        if (b >= bits) break;
         const uint64_t s = __ballot((digit >> b) & 1u);
         m &= ((digit >> b) & 1u) ? s : ~s;
     }
     return m;
 }
 
-// Ranks of the workgroup's n keys by their digit: item (wave, j, lane) is key
-// (wave * ITEMS + j) * 64 + lane.  rank[j] counts the equal digits before it
-// in its wavefront; the histograms then become, per wavefront and digit, where
-// its first key goes among the workgroup's own.
+// Ranks of the workgroup's items by their digit (kDigits: not one of them): item
+// (wave, j, lane) comes before (wave, j, lane + 1), (wave, j + 1, ..) and (wave + 1, ..).
+// item[j] becomes digit << 16 | the equal digits before it in its wavefront; the
+// histograms then become, per wavefront and digit, those of the wavefronts before.
 template <int ITEMS>
-__device__ __forceinline__ void rank_keys(SortLds &s, const uint32_t (&key)[ITEMS], uint32_t (&rank)[ITEMS], int n,
-                                          int shift)
+__device__ __forceinline__ void rank_items(SortLds &s, uint32_t (&item)[ITEMS], int bits)
 {
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = tid >> 6;
     for (int i = tid; i < kSWaves * kDigits; i += kSThreads) s.hist[i / kDigits][i % kDigits] = 0;
     __syncthreads();
     volatile uint32_t *h = s.hist[wave];  // read by lanes that others of the wavefront write for
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
-        const bool in = (wave * ITEMS + j) * 64 + lane < n;
-        const uint32_t d = (key[j] >> shift) & (kDigits - 1);
-        const uint64_t peers = peers_of(d, __ballot(in));
+        const uint32_t d = item[j];
+        const bool in = d < (uint32_t)kDigits;
+        const uint64_t some = __ballot(in);
+        item[j] = d << 16;
+        if (!some) continue;
+        const uint64_t peers = peers_of(d, some, bits);
         const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(peers >> 32),
                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)peers, 0u));
         uint32_t seen = 0;
         if (in) seen = h[d];
-        rank[j] = seen + before;
+        item[j] |= seen + before;
         if (in && before == 0) h[d] = seen + (uint32_t)__popcll(peers);
     }
     __syncthreads();
@@ -133,7 +176,14 @@ __device__ __forceinline__ void rank_keys(SortLds &s, const uint32_t (&key)[ITEM
     __syncthreads();
 }
 
-// Exclusive sums of x over the first 256 threads, into s.total.
+// Of a ranked item: its digit, and where it goes among the equal ones.
+__device__ __forceinline__ uint32_t digit_of(uint32_t item) { return item >> 16; }
+__device__ __forceinline__ uint32_t rank_of(const SortLds &s, uint32_t item)
+{
+    return s.hist[threadIdx.x >> 6][item >> 16] + (item & 0xffffu);
+}
+
+// Exclusive sums of x over the first 256 threads, into s.total; all of it behind them.
 __device__ void scan_digits(SortLds &s, uint32_t x)
 {
     const int tid = threadIdx.x, lane = tid & 63;
@@ -147,81 +197,148 @@ __device__ void scan_digits(SortLds &s, uint32_t x)
     if (tid < kDigits) {
         for (int w = 0; w < (tid >> 6); ++w) y += s.lead[w];
         s.total[tid] = y - x;
+        if (tid == kDigits - 1) s.total[kDigits] = y;
     }
     __syncthreads();
 }
 
-__device__ __forceinline__ uint32_t key_of(const EmbedArgs &a, int64_t i)
-{
-    const int64_t t = token_at(a.tokens, i, a.tok64, a.V);
-    return t >= 0 ? (uint32_t)t : (uint32_t)a.V;  // padding after everything
-}
-
-// Zeros for the rows first .. first + rows - 1 that no token has.
-template <bool BFT>
-__device__ __forceinline__ void zero_unmarked(const EmbedArgs &a, int64_t first, int rows)
-{
-    __shared__ uint32_t marks[kMarkRows / 32];
-    if (threadIdx.x < kMarkRows / 32) marks[threadIdx.x] = 0;
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < a.N; i += kSThreads) {
-        const int64_t r = token_at(a.tokens, i, a.tok64, a.V) - first;
-        if (r >= 0 && r < rows) atomicOr(&marks[r >> 5], 1u << (r & 31));
-    }
-    __syncthreads();
-    const int octs = a.D / 8;
-    for (int r = threadIdx.x >> 6; r < rows; r += kSWaves) {
-        if (marks[r >> 5] >> (r & 31) & 1u) continue;
-        for (int c = threadIdx.x & 63; c < octs; c += 64) store_oct<BFT>(a.dtable, (first + r) * a.D + 8 * c, Oct{});
-    }
-}
-
-// All digits at once, up to 1024 ITEMS tokens, by the first workgroup; the others
-// take `rows` rows of the table each and write zeros.
+// The tokens of the rows first .. first + rows - 1 (row V: padding), ranked by their row:
+// their digit is the row's number here.  Returns how many there are of the rows before.
 template <int ITEMS>
-__global__ void __launch_bounds__(kSThreads) gscan_sort_small_kernel(EmbedArgs a, int passes, int rows, uint32_t *keys,
-                                                                    uint32_t *order)
+__device__ __forceinline__ uint32_t rank_rows(const EmbedArgs &a, uint32_t first, uint32_t rows, SortLds &s,
+                                              uint32_t (&item)[ITEMS])
 {
-    if (blockIdx.x > 0) {
-        const int64_t first = (int64_t)(blockIdx.x - 1) * rows;
-        const int n = (int)(a.V - first < rows ? a.V - first : rows);
-        if (a.table_dtype) zero_unmarked<true>(a, first, n);
-        else zero_unmarked<false>(a, first, n);
-        return;
+    __shared__ uint32_t below;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x == 0) below = 0;
+    __syncthreads();
+    uint32_t before = 0;
+    constexpr int kBatch = ITEMS < kLoadItems ? ITEMS : kLoadItems;
+#pragma unroll
+    for (int b = 0; b < ITEMS; b += kBatch) {
+        uint32_t key[kBatch];
+        token_keys<kBatch>(a, (int64_t)(wave * ITEMS + b) * 64 + lane, a.N, key);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            before += (uint32_t)__popcll(__ballot(key[j] < first));
+            item[b + j] = key[j] - first < rows ? key[j] - first : (uint32_t)kDigits;
+        }
     }
+    if (lane == 0) atomicAdd(&below, before);  // whole numbers: any order
+    rank_items<ITEMS>(s, item, 32 - __builtin_clz(rows | 1u));
+    scan_digits(s, threadIdx.x < kDigits ? s.total[threadIdx.x] : 0u);
+    return below;
+}
+
+// Up to 1024 ITEMS tokens: sorted, and zeros for the rows without one.
+template <int ITEMS>
+__global__ void __launch_bounds__(kSThreads) gscan_sort_rows_kernel(EmbedArgs a, int rows, uint32_t *keys,
+                                                                   uint32_t *order)
+{
     __shared__ SortLds s;
-    __shared__ uint32_t moved[kSThreads * ITEMS];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = (int)a.N;
-    uint32_t item[ITEMS], rank[ITEMS];  // token and position
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t first = (int64_t)blockIdx.x * rows;
+    uint32_t item[ITEMS];
+    const uint32_t below = rank_rows<ITEMS>(a, (uint32_t)first, (uint32_t)rows, s, item);
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
-        const int i = (wave * ITEMS + j) * 64 + lane;
-        item[j] = i < n ? key_of(a, i) << kPosBits | (uint32_t)i : 0u;
+        const uint32_t d = digit_of(item[j]);
+        if (d < (uint32_t)kDigits) {
+            const uint32_t at = below + s.total[d] + rank_of(s, item[j]);
+            keys[at] = (uint32_t)first + d;
+            order[at] = (uint32_t)((wave * ITEMS + j) * 64 + lane);
+        }
     }
-    for (int p = 0; p < passes; ++p) {
-        const int shift = kPosBits + 8 * p;
-        rank_keys<ITEMS>(s, item, rank, n, shift);
-        scan_digits(s, tid < kDigits ? s.total[tid] : 0u);
+    const int octs = a.D / 8;
+    for (int r = wave; r < rows && first + r < a.V; r += kSWaves) {
+        if (s.total[r] != s.total[r + 1]) continue;
+        for (int c = lane; c < octs; c += 64) {
+            if (a.table_dtype) store_oct<true>(a.dtable, (first + r) * a.D + 8 * c, Oct{});
+            else store_oct<false>(a.dtable, (first + r) * a.D + 8 * c, Oct{});
+        }
+    }
+}
+
+// The rows of dout at list[b .. e - 1], eight columns from c on, in order.
+template <bool BF>
+__device__ __forceinline__ Oct add_rows(const EmbedArgs &a, const uint32_t *list, uint32_t b, uint32_t e, int c)
+{
+    Oct sum = {};
+    const bool in = c < a.D;
+    for (; b < e; b += kFewAhead) {
+        OctRaw<BF> x[kFewAhead];
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            if ((wave * ITEMS + j) * 64 + lane < n) {
-                const uint32_t d = (item[j] >> shift) & (kDigits - 1);
-                moved[s.total[d] + s.hist[wave][d] + rank[j]] = item[j];
+        for (int k = 0; k < kFewAhead; ++k) {
+            x[k] = OctRaw<BF>{};
+            if (in && b + k < e) x[k] = load_oct<BF>(a.dout, (int64_t)list[b + k] * a.ld + c);
+        }
+#pragma unroll
+        for (int k = 0; k < kFewAhead; ++k) {
+            if (b + k >= e) break;
+            const Oct v = widen(x[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum.v[i] += v.v[i];
+        }
+    }
+    return sum;
+}
+
+// Few tokens: sorted and added up, `rows` rows of the table for a workgroup.  A row
+// of up to 32 tokens is one wavefront's; of more every wavefront takes its share, and
+// the shares are added in order.
+template <bool BF, bool BFT>
+__global__ void __launch_bounds__(kSThreads) gscan_embed_few_kernel(EmbedArgs a, int rows)
+{
+    __shared__ SortLds s;
+    __shared__ uint32_t list[kSFew], many[kSFew / kAlone], count;
+    __shared__ __align__(16) float share[kSWaves][512];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t first = (int64_t)blockIdx.x * rows;
+    uint32_t item[kFewItems];
+    if (threadIdx.x == 0) count = 0;
+    rank_rows<kFewItems>(a, (uint32_t)first, (uint32_t)rows, s, item);
+#pragma unroll
+    for (int j = 0; j < kFewItems; ++j) {
+        const uint32_t d = digit_of(item[j]);
+        if (d < (uint32_t)kDigits)
+            list[s.total[d] + rank_of(s, item[j])] = (uint32_t)((wave * kFewItems + j) * 64 + lane);
+    }
+    if (threadIdx.x < rows && first + threadIdx.x < a.V && s.total[threadIdx.x + 1] - s.total[threadIdx.x] > kAlone)
+        many[atomicAdd(&count, 1u)] = threadIdx.x;  // each by itself: any order
+    __syncthreads();
+    auto put = [&](Oct sum, int64_t r, int c) {
+        if (c >= a.D) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum.v[i] *= a.scale;
+        store_oct<BFT>(a.dtable, (first + r) * a.D + c, sum);
+    };
+    for (int c0 = 512 * (int)blockIdx.y; c0 < a.D; c0 += 512 * (int)gridDim.y) {
+        const int c = c0 + 8 * lane;
+        for (int r = wave; r < rows && first + r < a.V; r += kSWaves) {
+            const uint32_t b = __builtin_amdgcn_readfirstlane(s.total[r]),
+                           e = __builtin_amdgcn_readfirstlane(s.total[r + 1]);
+            if (b == e) {
+                if (c < a.D) store_oct<BFT>(a.dtable, (first + r) * a.D + c, Oct{});
+            } else if (e - b <= kAlone) {
+                put(add_rows<BF>(a, list, b, e, c), r, c);
             }
         }
-        __syncthreads();
+        for (uint32_t m = 0; m < count; ++m) {
+            const uint32_t r = many[m], b = s.total[r], e = s.total[r + 1], each = (e - b + kSWaves - 1) / kSWaves;
+            const uint32_t b1 = b + wave * each, e1 = b1 + each < e ? b1 + each : e;
+            const Oct x = add_rows<BF>(a, list, b1, e1, c);
+            store_oct<false>(share[wave], 8 * lane, x);
+            __syncthreads();
+            if (wave == 0) {
+                Oct sum = x;
+                for (int w = 1; w < kSWaves; ++w) {
+                    const Oct y = widen(load_oct<false>(share[w], 8 * lane));
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            const int i = (wave * ITEMS + j) * 64 + lane;
-            if (i < n) item[j] = moved[i];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        const int i = (wave * ITEMS + j) * 64 + lane;
-        if (i < n) {
-            keys[i] = item[j] >> kPosBits;
-            order[i] = item[j] & ((1u << kPosBits) - 1);
+                    for (int i = 0; i < 8; ++i) sum.v[i] += y.v[i];
+                }
+                put(sum, r, c);
+            }
+            __syncthreads();
         }
     }
 }
@@ -230,17 +347,23 @@ __global__ void __launch_bounds__(kSThreads) gscan_sort_small_kernel(EmbedArgs a
 // first pass.  count[block][digit].
 template <bool FIRST>
 __device__ __forceinline__ void load_keys(const EmbedArgs &a, const uint32_t *keys, const uint32_t *order,
-                                          int64_t base, int n, uint32_t (&key)[kSItems],
+                                          int64_t base, int64_t end, uint32_t (&key)[kSItems],
                                           uint32_t (&pos)[kSItems])
 {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t i0 = base + (threadIdx.x >> 6) * kSItems * 64 + (threadIdx.x & 63);
+    if constexpr (FIRST) {
+        token_keys<kSItems>(a, i0, end, key);
 #pragma unroll
-    for (int j = 0; j < kSItems; ++j) {
-        const int i = (wave * kSItems + j) * 64 + lane;
-        key[j] = pos[j] = 0;
-        if (i < n) {
-            key[j] = FIRST ? key_of(a, base + i) : keys[base + i];
-            pos[j] = FIRST ? (uint32_t)(base + i) : order[base + i];
+        for (int j = 0; j < kSItems; ++j) pos[j] = (uint32_t)(i0 + 64 * j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kSItems; ++j) {
+            key[j] = ~0u;
+            pos[j] = 0;
+            if (i0 + 64 * j < end) {
+                key[j] = keys[i0 + 64 * j];
+                pos[j] = order[i0 + 64 * j];
+            }
         }
     }
 }
@@ -251,13 +374,14 @@ __global__ void __launch_bounds__(kSThreads) gscan_sort_count_kernel(EmbedArgs a
 {
     __shared__ uint32_t h[kDigits];
     const int64_t base = (int64_t)blockIdx.x * kSBlock;
-    const int n = (int)(a.N - base < kSBlock ? a.N - base : kSBlock);
+    const int64_t end = a.N - base < kSBlock ? a.N : base + kSBlock;
     if (threadIdx.x < kDigits) h[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSThreads) {
-        const uint32_t k = FIRST ? key_of(a, base + i) : keys[base + i];
-        atomicAdd(&h[(k >> shift) & (kDigits - 1)], 1u);  // whole numbers: any order
-    }
+    uint32_t key[kSItems], pos[kSItems];
+    load_keys<FIRST>(a, keys, keys, base, end, key, pos);
+#pragma unroll
+    for (int j = 0; j < kSItems; ++j)
+        if (key[j] != ~0u) atomicAdd(&h[(key[j] >> shift) & (kDigits - 1)], 1u);  // whole numbers: any order
     __syncthreads();
     if (threadIdx.x < kDigits) count[(int64_t)blockIdx.x * kDigits + threadIdx.x] = h[threadIdx.x];
 }
@@ -299,12 +423,13 @@ __global__ void __launch_bounds__(kSThreads) gscan_sort_move_kernel(EmbedArgs a,
 {
     __shared__ SortLds s;
     __shared__ uint32_t first[kDigits];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int64_t base = (int64_t)blockIdx.x * kSBlock;
-    const int n = (int)(a.N - base < kSBlock ? a.N - base : kSBlock);
-    uint32_t key[kSItems], pos[kSItems], rank[kSItems];
-    load_keys<FIRST>(a, keys, order, base, n, key, pos);
-    rank_keys<kSItems>(s, key, rank, n, shift);
+    const int tid = threadIdx.x;
+    const int64_t base = (int64_t)blockIdx.x * kSBlock, end = a.N - base < kSBlock ? a.N : base + kSBlock;
+    uint32_t key[kSItems], pos[kSItems], item[kSItems];
+    load_keys<FIRST>(a, keys, order, base, end, key, pos);
+#pragma unroll
+    for (int j = 0; j < kSItems; ++j) item[j] = key[j] != ~0u ? (key[j] >> shift) & (kDigits - 1) : (uint32_t)kDigits;
+    rank_items<kSItems>(s, item, 8);
     uint32_t mine = 0, all = 0;  // of this digit: in workgroups before, in all
     if (tid < kDigits) {
         if (blocks > kFewBlocks) {
@@ -323,9 +448,8 @@ __global__ void __launch_bounds__(kSThreads) gscan_sort_move_kernel(EmbedArgs a,
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kSItems; ++j) {
-        if ((wave * kSItems + j) * 64 + lane < n) {
-            const uint32_t d = (key[j] >> shift) & (kDigits - 1);
-            const uint32_t at = first[d] + s.hist[wave][d] + rank[j];
+        if (key[j] != ~0u) {
+            const uint32_t at = first[digit_of(item[j])] + rank_of(s, item[j]);
             keys_out[at] = key[j];
             order_out[at] = pos[j];
         }
@@ -478,7 +602,8 @@ int lanes_per_row(int D)
 
 struct EmbedPlan {
     int passes = 1, chunk = 8;
-    bool small = false;         // one workgroup sorts
+    bool few = false, some = false;  // one launch does it all, sorts
+    int rows = 0;               // of a workgroup of that
     int64_t blocks = 0, chunks = 0;
     size_t keys[2], order[2], count = 0, part = 0, bytes = 0;
 };
@@ -492,7 +617,12 @@ EmbedPlan plan_embed(int64_t N, int64_t V, int D)
     EmbedPlan p;
     while (p.passes < 4 && (V >> (8 * p.passes)) != 0) ++p.passes;  // keys are 0 .. V
     while (p.chunk < 32 ? (int64_t)p.chunk * 512 < N : (int64_t)p.chunk * p.chunk * 64 < N) p.chunk *= 2;
-    p.small = N <= kSSmall && V < int64_t(1) << (32 - kPosBits);
+    p.some = N <= kSSome && V < kSRows;
+    p.few = p.some && (D <= 512 ? N <= kSFew : D <= 4096 && N <= kSWide);
+    // a workgroup per CU (two: 16384 tokens 38 -> 43 us); padding is row V
+    const int64_t rows = (V + 256) / 256;
+    p.rows = (int)(rows < kDigits ? rows : kDigits);
+    if (p.few) return p;
     p.blocks = (N + kSBlock - 1) / kSBlock;
     p.chunks = (N + p.chunk - 1) / p.chunk;
     size_t at = 0;
@@ -501,14 +631,14 @@ EmbedPlan plan_embed(int64_t N, int64_t V, int D)
         at = round_up(at + (size_t)N * 4);
         p.order[i] = at;
         at = round_up(at + (size_t)N * 4);
-        if (p.small) {  // no second copy
+        if (p.some) {  // no second copy
             p.keys[1] = p.keys[0];
             p.order[1] = p.order[0];
             break;
         }
     }
     p.count = at;
-    if (!p.small) at = round_up(at + (size_t)(p.blocks + 1) * kDigits * 4);
+    if (!p.some) at = round_up(at + (size_t)(p.blocks + 1) * kDigits * 4);
     p.part = at;
     p.bytes = at + (size_t)p.chunks * 2 * (size_t)D * sizeof(float);
     return p;
@@ -544,17 +674,23 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t st)
     int at = 0;
     if (!a.N) {
         // only zeros
-    } else if (p.small) {
+    } else if (p.few) {
+        auto *k = a.dtype ? (a.table_dtype ? gscan_embed_few_kernel<true, true> : gscan_embed_few_kernel<true, false>)
+                          : (a.table_dtype ? gscan_embed_few_kernel<false, true> : gscan_embed_few_kernel<false, false>);
+        const int64_t groups = (a.V + p.rows) / p.rows, slices = (a.D + 511) / 512;
+        int64_t apart = 256 / groups;  // few rows: their columns are divided too
+        apart = apart < 1 ? 1 : apart > slices ? slices : apart;
+        hipLaunchKernelGGL(k, dim3((unsigned)groups, (unsigned)apart), dim3(kSThreads), 0, st, a, p.rows);
+        return hipGetLastError();
+    } else if (p.some) {
         const int items = (int)((a.N + kSThreads - 1) / kSThreads);
-        auto *k = items <= 1   ? gscan_sort_small_kernel<1>
-                  : items <= 2 ? gscan_sort_small_kernel<2>
-                  : items <= 4 ? gscan_sort_small_kernel<4>
-                  : items <= 8 ? gscan_sort_small_kernel<8>
-                               : gscan_sort_small_kernel<16>;
-        int64_t rows = (a.V + 254) / 255;  // a workgroup per CU, of which one sorts
-        if (rows > kMarkRows) rows = kMarkRows;
-        hipLaunchKernelGGL(k, dim3((unsigned)(1 + (a.V + rows - 1) / rows)), dim3(kSThreads), 0, st, a, p.passes,
-                           (int)rows, keys[0], order[0]);
+        auto *k = items <= 4    ? gscan_sort_rows_kernel<4>
+                  : items <= 8  ? gscan_sort_rows_kernel<8>
+                  : items <= 16 ? gscan_sort_rows_kernel<16>
+                  : items <= 32 ? gscan_sort_rows_kernel<32>
+                                : gscan_sort_rows_kernel<64>;
+        hipLaunchKernelGGL(k, dim3((unsigned)((a.V + p.rows) / p.rows)), dim3(kSThreads), 0, st, a, p.rows, keys[0],
+                           order[0]);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     } else {
         uint32_t *count = reinterpret_cast<uint32_t *>(ws + p.count);
@@ -583,7 +719,7 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t st)
     float *part = reinterpret_cast<float *>(ws + p.part);
     const int slices = (a.D + 511) / 512;
     const int64_t waves = p.chunks * slices, groups = (waves + 3) / 4;
-    const int64_t zeros = p.small && a.N ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
+    const int64_t zeros = p.some && a.N ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
     const dim3 blk(kEThreads);
     auto *sum = a.dtype ? (a.table_dtype ? gscan_embed_sum_kernel<true, true> : gscan_embed_sum_kernel<true, false>)
                         : (a.table_dtype ? gscan_embed_sum_kernel<false, true> : gscan_embed_sum_kernel<false, false>);

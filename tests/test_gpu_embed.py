@@ -38,6 +38,19 @@ CASES = {  # tokens, vocabulary, width
     "three digits": (20000, 2 ** 17, 8),
     "a frequent token": (70001, 3, 24),
     "many workgroups": (600001, 256, 8),
+    # up to 2048 tokens (wide rows: 64) at once, up to 65536 of fewer than 2^20 rows sorted by one launch
+    "a wavefront's own row": (32, 1, 24),
+    "a shared row": (33, 1, 24),
+    "most at once": (2048, 5, 512),
+    "one more": (2049, 5, 512),
+    "most at once, 256 rows a workgroup": (2048, 65535, 8),
+    "most wide rows at once": (64, 300, 4096),
+    "one more wide row": (65, 300, 520),
+    "wider rows": (64, 7, 4104),
+    "most in one sort": (65536, 1003, 8),
+    "one more than one sort": (65537, 1003, 8),
+    "most rows of one sort": (3000, 2 ** 20 - 1, 8),
+    "one more row": (50, 2 ** 20, 8),
 }
 
 
@@ -185,5 +198,6 @@ def test_refusals():
     for V in (0, -1):
         with pytest.raises(gs.GScanError):
             gs.embed_backward(d, t, V)
+    many, dmany = t.repeat(1000), d.repeat(1000, 1)  # few tokens need no workspace
     with pytest.raises((ValueError, gs.GScanError)):
-        gs.embed_backward(d, t, 5, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        gs.embed_backward(dmany, many, 5, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
