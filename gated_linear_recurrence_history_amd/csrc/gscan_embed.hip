@@ -60,28 +60,30 @@ template <bool BFI, bool BFO>
 __global__ void __launch_bounds__(kEThreads) gscan_embed_fwd_kernel(EmbedArgs a, int lpr)
 {
     const int sub = threadIdx.x & (lpr - 1), rpp = kEThreads / lpr;
-    const int64_t r0 = (int64_t)blockIdx.x * rpp * kERows + threadIdx.x / lpr;
-    int64_t t[kERows];
-#pragma unroll
-    for (int i = 0; i < kERows; ++i) {
-        const int64_t r = r0 + (int64_t)i * rpp;
-        t[i] = r < a.N ? token_at(a.tokens, r, a.tok64, a.V) : -1;
-    }
-    for (int c = 8 * sub; c < a.D; c += 8 * lpr) {
-        OctRaw<BFI> x[kERows];
-#pragma unroll
-        for (int i = 0; i < kERows; ++i) {
-            x[i] = OctRaw<BFI>{};
-            if (t[i] >= 0) x[i] = load_oct<BFI>(a.table, t[i] * a.ld + c);
-        }
+    const int64_t step = (int64_t)rpp * kERows;
+    for (int64_t r0 = blockIdx.x * step + threadIdx.x / lpr; r0 < a.N; r0 += gridDim.x * step) {
+        int64_t t[kERows];
 #pragma unroll
         for (int i = 0; i < kERows; ++i) {
             const int64_t r = r0 + (int64_t)i * rpp;
-            if (r >= a.N) continue;
-            Oct y = widen(x[i]);
+            t[i] = r < a.N ? token_at(a.tokens, r, a.tok64, a.V) : -1;
+        }
+        for (int c = 8 * sub; c < a.D; c += 8 * lpr) {
+            OctRaw<BFI> x[kERows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y.v[e] = t[i] >= 0 ? y.v[e] * a.scale : 0.f;
-            store_oct<BFO>(a.out, r * a.D + c, y);
+            for (int i = 0; i < kERows; ++i) {
+                x[i] = OctRaw<BFI>{};
+                if (t[i] >= 0) x[i] = load_oct<BFI>(a.table, t[i] * a.ld + c);
+            }
+#pragma unroll
+            for (int i = 0; i < kERows; ++i) {
+                const int64_t r = r0 + (int64_t)i * rpp;
+                if (r >= a.N) continue;
+                Oct y = widen(x[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y.v[e] = t[i] >= 0 ? y.v[e] * a.scale : 0.f;
+                store_oct<BFO>(a.out, r * a.D + c, y);
+            }
         }
     }
 }
@@ -463,6 +465,7 @@ template <bool BFT>
 __device__ __forceinline__ void zero_rows(const EmbedArgs &a, const uint32_t *keys, int64_t first)
 {
     __shared__ uint32_t absent[kZeroRows], count;
+    __syncthreads();
     if (threadIdx.x == 0) count = 0;
     __syncthreads();
     const int64_t row = first + threadIdx.x;
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(kEThreads) gscan_embed_sum_kernel(EmbedArgs a,
     const bool zero = id < both ? id % 2 == 1 : zeros > groups;
     id = id < both ? id / 2 : id - both / 2;
     if (zero) {
-        zero_rows<BFT>(a, keys, id * kZeroRows);
+        for (; id * kZeroRows < a.V; id += zeros) zero_rows<BFT>(a, keys, id * kZeroRows);
         return;
     }
     const int64_t w = id * 4 + (threadIdx.x >> 6);
@@ -657,7 +660,7 @@ hipError_t launch_embed_forward(const EmbedArgs &a, hipStream_t st)
     const int lpr = lanes_per_row(a.D), rows = kEThreads / lpr * kERows;
     auto *k = a.table_dtype ? (a.dtype ? gscan_embed_fwd_kernel<true, true> : gscan_embed_fwd_kernel<true, false>)
                             : (a.dtype ? gscan_embed_fwd_kernel<false, true> : gscan_embed_fwd_kernel<false, false>);
-    hipLaunchKernelGGL(k, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kEThreads), 0, st, a, lpr);
+    hipLaunchKernelGGL(k, groups_of((a.N + rows - 1) / rows), dim3(kEThreads), 0, st, a, lpr);
     return hipGetLastError();
 }
 
@@ -719,7 +722,7 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t st)
     float *part = reinterpret_cast<float *>(ws + p.part);
     const int slices = (a.D + 511) / 512;
     const int64_t waves = p.chunks * slices, groups = (waves + 3) / 4;
-    const int64_t zeros = p.some && a.N ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
+    const int64_t zeros = p.some && a.N ? 0 : groups_of((a.V + kZeroRows - 1) / kZeroRows).x;
     const dim3 blk(kEThreads);
     auto *sum = a.dtype ? (a.table_dtype ? gscan_embed_sum_kernel<true, true> : gscan_embed_sum_kernel<true, false>)
                         : (a.table_dtype ? gscan_embed_sum_kernel<false, true> : gscan_embed_sum_kernel<false, false>);

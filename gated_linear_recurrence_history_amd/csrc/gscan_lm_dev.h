@@ -8,6 +8,10 @@
 namespace gscan {
 namespace {
 
+// A launch has fewer than 2^32 threads: workgroups of what may be more go on in strides.
+constexpr int64_t kMaxGroups = int64_t(1) << 20;
+inline dim3 groups_of(int64_t n) { return dim3((unsigned)(n < kMaxGroups ? n : kMaxGroups)); }
+
 // Eight elements of a row (fp32 or bf16, 16-byte aligned), widened.
 struct Oct {
     float v[8];

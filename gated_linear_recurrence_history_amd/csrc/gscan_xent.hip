@@ -133,16 +133,18 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, 
 template <bool BF>
 __global__ void __launch_bounds__(256) gscan_xent_rows_kernel(XentArgs a, Listed l)
 {
-    const int64_t n = blockIdx.x, count = *l.count;
+    const int64_t count = *l.count;
     if (count == a.N) return;
-    const bool copy = n < count, clear = a.dh && token_at(a.target, n, a.target64, a.V) < 0;
-    const int64_t from = copy ? l.row[n] : 0;
-    for (int c = 8 * threadIdx.x; c < a.D; c += 8 * 256) {
-        if (copy) {
-            const OctRaw<BF> x = load_oct<BF>(a.h, from * a.ldh + c);
-            *reinterpret_cast<OctRaw<BF> *>(reinterpret_cast<char *>(l.h) + (n * a.D + c) * (BF ? 2 : 4)) = x;
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+        const bool copy = n < count, clear = a.dh && token_at(a.target, n, a.target64, a.V) < 0;
+        const int64_t from = copy ? l.row[n] : 0;
+        for (int c = 8 * threadIdx.x; c < a.D; c += 8 * 256) {
+            if (copy) {
+                const OctRaw<BF> x = load_oct<BF>(a.h, from * a.ldh + c);
+                *reinterpret_cast<OctRaw<BF> *>(reinterpret_cast<char *>(l.h) + (n * a.D + c) * (BF ? 2 : 4)) = x;
+            }
+            if (clear) store_oct<BF>(a.dh, n * a.D + c, Oct{});
         }
-        if (clear) store_oct<BF>(a.dh, n * a.D + c, Oct{});
     }
 }
 
@@ -151,21 +153,25 @@ __global__ void __launch_bounds__(256) gscan_xent_join_kernel(XentArgs a, Listed
 {
     __shared__ float2 red[16][kJoinRows];
     const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
-    const int64_t count = *l.count, n = (int64_t)blockIdx.x * kJoinRows + r;
-    float m = -INFINITY, s = 0.f;
-    if (n < count)
-        for (int64_t p = q; p < parts; p += 16) {
-            const float2 x = l.part[p * a.N + n];
-            join_lse(m, s, x.x, x.y);
+    const int64_t count = *l.count;
+    for (int64_t n0 = (int64_t)blockIdx.x * kJoinRows; n0 < count; n0 += (int64_t)gridDim.x * kJoinRows) {
+        const int64_t n = n0 + r;
+        float m = -INFINITY, s = 0.f;
+        if (n < count)
+            for (int64_t p = q; p < parts; p += 16) {
+                const float2 x = l.part[p * a.N + n];
+                join_lse(m, s, x.x, x.y);
+            }
+        __syncthreads();
+        red[q][r] = float2{m, s};
+        __syncthreads();
+        if (q == 0 && n < count) {
+            for (int i = 1; i < 16; ++i) join_lse(m, s, red[i][r].x, red[i][r].y);
+            const float tail = log2f(s), unit = 0.69314718055994531f;
+            const int64_t i = l.row[n];
+            a.lse[i] = (m + tail) * unit;
+            (a.reduction ? l.loss : a.loss)[i] = (m - l.picked[n] + tail) * unit;
         }
-    red[q][r] = float2{m, s};
-    __syncthreads();
-    if (q == 0 && n < count) {
-        for (int i = 1; i < 16; ++i) join_lse(m, s, red[i][r].x, red[i][r].y);
-        const float tail = log2f(s), unit = 0.69314718055994531f;
-        const int64_t i = l.row[n];
-        a.lse[i] = (m + tail) * unit;
-        (a.reduction ? l.loss : a.loss)[i] = (m - l.picked[n] + tail) * unit;
     }
 }
 
@@ -234,7 +240,7 @@ hipError_t launch_list(const XentArgs &x, const Listed &l, bool backward, hipStr
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !x.N) return e;
     auto *k = x.dtype ? gscan_xent_rows_kernel<true> : gscan_xent_rows_kernel<false>;
-    hipLaunchKernelGGL(k, dim3((unsigned)x.N), dim3(256), 0, st, x, l);
+    hipLaunchKernelGGL(k, groups_of(x.N), dim3(256), 0, st, x, l);
     return hipGetLastError();
 }
 
@@ -289,8 +295,7 @@ hipError_t launch_xent_forward(const XentArgs &x, hipStream_t st)
         a.part = l.part;
         a.picked = l.picked;
         if ((e = launch_mm<EPI_LSE, false, false, LIMIT_N>(a, x.dtype, l.partial, st)) != hipSuccess) return e;
-        hipLaunchKernelGGL(gscan_xent_join_kernel, dim3((unsigned)((x.N + kJoinRows - 1) / kJoinRows)), dim3(256),
-                           0, st, x, l, tiles_of_m(x.V, x.N, x.D, x.dtype));
+        hipLaunchKernelGGL(gscan_xent_join_kernel, groups_of((x.N + kJoinRows - 1) / kJoinRows), dim3(256), 0, st, x, l, tiles_of_m(x.V, x.N, x.D, x.dtype));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!x.reduction) return hipSuccess;

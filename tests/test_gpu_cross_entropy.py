@@ -191,6 +191,31 @@ def test_weights_past_32_bits():
     assert abs(float(dh[0, 3]) - 4 * (p - 1)) <= 2.0 ** -7 * 4
 
 
+def test_more_tokens_than_a_launch_has_groups():
+    n, D, V = 2 ** 24 + 1000, 8, 5  # 16 tokens a workgroup, or one
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    h = torch.randn(n, D, generator=gen, device=DEV)
+    w = torch.randn(V, D, generator=gen, device=DEV)
+    target = torch.randint(-1, V, (n,), generator=gen, device=DEV)
+    ok = target >= 0
+    z = h.double() @ w.double().T
+    lse = torch.where(ok, torch.logsumexp(z, -1), 0.0)
+    picked = torch.gather(z, 1, target.clamp(min=0)[:, None])[:, 0]
+    loss, got = gs.linear_cross_entropy_forward(h, w, target, reduction="none")
+    top = float(z.abs().max())
+    tol = (top + 1) * (ref.product(D) + 12 * ref.U) + 80 * ref.U
+    assert float((got.double() - lse).abs().max()) <= tol
+    assert float((loss.double() - torch.where(ok, lse - picked, 0.0)).abs().max()) <= tol
+    dh, dw = gs.linear_cross_entropy_backward(h, w, target, got, torch.ones(n, device=DEV), reduction="none")
+    g = torch.softmax(z, -1)
+    g[torch.arange(n, device=DEV), target.clamp(min=0)] -= 1.0
+    g[~ok] = 0.0
+    assert bool((dh[~ok] == 0).all())
+    # a gradient of a logit: its exponential's argument is off by tol; then products of V and n terms
+    ref.close(dh, g @ w.double(), 2 * tol + ref.product(V), "dh")
+    ref.close(dw, g.T @ h.double(), 2 * tol + ref.product(n), "dW")
+
+
 def test_directional_difference():
     """Step 2^-5 along directions that move logits by about one standard deviation: the
     cubic term is 2^-10 / 6 of the third derivative, of the size of the loss."""

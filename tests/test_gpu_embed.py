@@ -130,6 +130,31 @@ def test_table_past_32_bits():
     assert float(g[1:-2].abs().amax()) == 0.0
 
 
+def test_gradient_of_more_rows_than_a_launch_has_threads():
+    V, D = 2 ** 30 + 65, 8
+    t = torch.tensor([0, V - 1, 2 ** 30, V - 1], device=DEV)
+    d = torch.ones(4, D, dtype=BF, device=DEV)
+    out = torch.full((V, D), float("nan"), dtype=BF, device=DEV)
+    gs.embed_backward(d, t, V, out=out)
+    assert out[0, 0] == 1 and out[2 ** 30, 0] == 1 and out[V - 1, 0] == 2
+    out[t] = 0
+    step = 2 ** 27
+    assert all(bool((out[i:i + step] == 0).all()) for i in range(0, V, step))
+
+
+def test_more_tokens_than_a_launch_has_groups():
+    n, D = 2 ** 30 + 1025, 8  # 1024 tokens a workgroup
+    table = torch.randn(3, D, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    t = (torch.arange(n, device=DEV, dtype=torch.int32) % 4) - 1
+    y = gs.embed_forward(table, t)
+    want = torch.cat([torch.zeros(1, D, dtype=BF, device=DEV), table])
+    step = 2 ** 26
+    for i in range(0, n, step):
+        part = y[i:i + step]
+        assert torch.equal(part[:len(part) // 4 * 4].view(-1, 4, D), want.expand(len(part) // 4, 4, D))
+    assert torch.equal(y[-1], want[(n - 1) % 4])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_autograd(dtype):
     gen = torch.Generator().manual_seed(6)
