@@ -95,35 +95,6 @@ struct SortLds {
     uint32_t total[kDigits + 1], lead[4];
 };
 
-// Keys (tokens; V for padding, which comes after everything) of the tokens i0 + 64 j,
-// the lanes' behind each other; none behind the last of the n tokens: ~0.
-template <int ITEMS>
-__device__ __forceinline__ void token_keys(const EmbedArgs &a, int64_t i0, int64_t n, uint32_t (&key)[ITEMS])
-{
-    if (a.tok64) {  // (not by token: the loads of one lane are to be under way together)
-        int64_t t[ITEMS];
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            t[j] = -1;
-            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int64_t *>(a.tokens)[i0 + 64 * j];
-        }
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < a.V ? (uint32_t)t[j] : (uint32_t)a.V;
-    } else {
-        int32_t t[ITEMS];
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            t[j] = -1;
-            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int32_t *>(a.tokens)[i0 + 64 * j];
-        }
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < a.V ? (uint32_t)t[j] : (uint32_t)a.V;
-    }
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j)
-        if (i0 + 64 * j >= n) key[j] = ~0u;
-}
-
 // Lanes (of those in `in`) with the same digit, of so many bits.
 __device__ __forceinline__ uint64_t peers_of(uint32_t digit, uint64_t in, int bits)
 {
@@ -219,7 +190,7 @@ __device__ __forceinline__ uint32_t rank_rows(const EmbedArgs &a, uint32_t first
 #pragma unroll
     for (int b = 0; b < ITEMS; b += kBatch) {
         uint32_t key[kBatch];
-        token_keys<kBatch>(a, (int64_t)(wave * ITEMS + b) * 64 + lane, a.N, key);
+        token_keys<kBatch>(a.tokens, a.tok64, a.V, (int64_t)(wave * ITEMS + b) * 64 + lane, a.N, key);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             before += (uint32_t)__popcll(__ballot(key[j] < first));
@@ -354,7 +325,7 @@ __device__ __forceinline__ void load_keys(const EmbedArgs &a, const uint32_t *ke
 {
     const int64_t i0 = base + (threadIdx.x >> 6) * kSItems * 64 + (threadIdx.x & 63);
     if constexpr (FIRST) {
-        token_keys<kSItems>(a, i0, end, key);
+        token_keys<kSItems>(a.tokens, a.tok64, a.V, i0, end, key);
 #pragma unroll
         for (int j = 0; j < kSItems; ++j) pos[j] = (uint32_t)(i0 + 64 * j);
     } else {

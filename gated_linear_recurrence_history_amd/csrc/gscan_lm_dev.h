@@ -71,5 +71,35 @@ __device__ __forceinline__ int64_t token_at(const void *tokens, int64_t i, int t
     return t >= 0 && t < V ? t : -1;
 }
 
+// Tokens i0 + 64 j, the lanes' behind each other, as keys: anything outside 0 .. V - 1
+// is V, what lies behind the last of the n tokens ~0.
+template <int ITEMS>
+__device__ __forceinline__ void token_keys(const void *tokens, int tok64, int64_t V, int64_t i0, int64_t n,
+                                           uint32_t (&key)[ITEMS])
+{
+    if (tok64) {  // (not by token: the loads of one lane are to be under way together)
+        int64_t t[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            t[j] = -1;
+            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int64_t *>(tokens)[i0 + 64 * j];
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < V ? (uint32_t)t[j] : (uint32_t)V;
+    } else {
+        int32_t t[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            t[j] = -1;
+            if (i0 + 64 * j < n) t[j] = reinterpret_cast<const int32_t *>(tokens)[i0 + 64 * j];
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) key[j] = t[j] >= 0 && t[j] < V ? (uint32_t)t[j] : (uint32_t)V;
+    }
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (i0 + 64 * j >= n) key[j] = ~0u;
+}
+
 }  // namespace
 }  // namespace gscan

@@ -31,6 +31,7 @@ constexpr int kLThreads = 1024;
 // 512; 6007 tokens, 1024 x 50021: 2207, 2109, 2015; 16384, 512 x 65000: 4455, 4526, 4082.
 constexpr int64_t kPieceBytes = 512ll << 20;
 constexpr int kJoinRows = 16;
+constexpr int64_t kRowGroups = 2048;  // all that are at work at once
 
 // By place among the tokens that count.
 struct Listed {
@@ -90,42 +91,54 @@ Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
     return l;
 }
 
-// Lists the tokens that count, in order.  One workgroup, 1024 tokens at a time.
-template <bool BWD>
+// Lists the tokens that count, in order.  One workgroup, 1024 ITEMS tokens at a time.
+template <bool BWD, int ITEMS>
 __global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, Listed l)
 {
     __shared__ int32_t n_of[kLThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int64_t done = 0;
-    for (int64_t b = 0; b < a.N; b += kLThreads) {
-        const int64_t i = b + tid;
-        const int64_t t = i < a.N ? token_at(a.target, i, a.target64, a.V) : -1;
-        const uint64_t in = __ballot(t >= 0);
+    for (int64_t b = 0; b < a.N; b += kLThreads * ITEMS) {
+        const int64_t i0 = b + wave * (64 * ITEMS) + lane;
+        uint32_t key[ITEMS];
+        float lse[ITEMS], up[ITEMS];
+        token_keys<ITEMS>(a.target, a.target64, a.V, i0, a.N, key);
+        int own = 0;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const bool in = key[j] < (uint32_t)a.V;
+            lse[j] = BWD && in ? a.lse[i0 + 64 * j] : 0.f;
+            up[j] = BWD && in && !a.reduction ? a.dloss[i0 + 64 * j] : 0.f;
+            own += __popcll(__ballot(in));
+        }
         __syncthreads();
-        if (lane == 0) n_of[wave] = __popcll(in);
+        if (lane == 0) n_of[wave] = own;
         __syncthreads();
-        int64_t at = done + __popcll(in & ((1ull << lane) - 1));
+        int64_t first = done;
         for (int w = 0; w < kLThreads / 64; ++w) {
-            at += w < wave ? n_of[w] : 0;
+            first += w < wave ? n_of[w] : 0;
             done += n_of[w];
         }
-        if (t >= 0) {
-            l.row[at] = (int32_t)i;
-            l.target[at] = (int32_t)t;
-            if (BWD) l.lse[at] = a.lse[i];
-        } else if (!BWD && i < a.N) {
-            a.lse[i] = 0.f;
-            (a.reduction ? l.loss : a.loss)[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const int64_t i = i0 + 64 * j;
+            const uint64_t in = __ballot(key[j] < (uint32_t)a.V);
+            const int64_t at = first + __popcll(in & ((1ull << lane) - 1));
+            first += __popcll(in);
+            if (key[j] < (uint32_t)a.V) {
+                l.row[at] = (int32_t)i;
+                l.target[at] = (int32_t)key[j];
+                if (BWD) l.lse[at] = lse[j];
+                if (BWD && !a.reduction) l.up[at] = a.scale * up[j];
+            } else if (!BWD && i < a.N) {
+                a.lse[i] = 0.f;
+                (a.reduction ? l.loss : a.loss)[i] = 0.f;
+            }
         }
     }
-    if (tid == 0) *l.count = (int32_t)done;
-    if (!BWD) return;
-    if (a.reduction) {
-        if (tid == 0) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
-    } else {
-        __syncthreads();  // l.row is this workgroup's own
-        for (int64_t i = tid; i < done; i += kLThreads) l.up[i] = a.scale * a.dloss[l.row[i]];
-    }
+    if (tid) return;
+    *l.count = (int32_t)done;
+    if (BWD && a.reduction) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
 }
 
 // Rows that count, one after the other, where some do not; gradients of those
@@ -233,14 +246,13 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_few_join_kernel(XentArgs
 
 hipError_t launch_list(const XentArgs &x, const Listed &l, bool backward, hipStream_t st)
 {
-    if (backward)
-        hipLaunchKernelGGL(gscan_xent_list_kernel<true>, dim3(1), dim3(kLThreads), 0, st, x, l);
-    else
-        hipLaunchKernelGGL(gscan_xent_list_kernel<false>, dim3(1), dim3(kLThreads), 0, st, x, l);
+    auto *list = x.N <= kLThreads ? (backward ? gscan_xent_list_kernel<true, 1> : gscan_xent_list_kernel<false, 1>)
+                                  : (backward ? gscan_xent_list_kernel<true, 8> : gscan_xent_list_kernel<false, 8>);
+    hipLaunchKernelGGL(list, dim3(1), dim3(kLThreads), 0, st, x, l);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !x.N) return e;
     auto *k = x.dtype ? gscan_xent_rows_kernel<true> : gscan_xent_rows_kernel<false>;
-    hipLaunchKernelGGL(k, groups_of(x.N), dim3(256), 0, st, x, l);
+    hipLaunchKernelGGL(k, dim3((unsigned)(x.N < kRowGroups ? x.N : kRowGroups)), dim3(256), 0, st, x, l);
     return hipGetLastError();
 }
 
