@@ -588,6 +588,10 @@ __host__ __device__ __forceinline__ int step_ns(const MmShape &c, int n)
 }
 
 constexpr int kPartSteps = 4;   // at least so many steps to a part
+// Parts that the device may make where the host sees no reason to, as tokens that do not count
+// leave few tiles: a workgroup per CU (fp32 gradients of 1141 tokens, half of which count,
+// 1248 x 1134: SPARE).
+constexpr int kSpare = 256;
 
 // The work with the tiles that are left divided into `parts` parts at most (tokens that
 // the host does not know of leave fewer tiles, or steps).
@@ -983,8 +987,9 @@ MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool lim
             p.ns += (int64_t)(w.steps / w.splits + 1) * step_ns(c, w.parts()) + c.tile +
                     (int64_t)w.parts() * c.part + c.join;
         p.parts = w.parts();
-        if (limited && w.splits) {  // fewer tokens may leave other tiles
-            if (w.splits == c.groups / w.left()) p.parts = c.groups;
+        if (limited) {  // fewer tokens may leave other tiles
+            if (!w.splits && (int64_t)w.steps * c.least / 2 > c.join + kSpare * (int64_t)c.part) p.parts = kSpare;
+            if (w.splits && w.splits == c.groups / w.left()) p.parts = c.groups;
             p.divided = w.tiles < p.parts / 2 ? w.tiles : p.parts / 2;
         }
         p.bytes = (size_t)p.parts * (size_t)(c.m * c.n) * sizeof(float);
