@@ -988,7 +988,9 @@ MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool lim
                     (int64_t)w.parts() * c.part + c.join;
         p.parts = w.parts();
         if (limited) {  // fewer tokens may leave other tiles
-            if (!w.splits && (int64_t)w.steps * c.least / 2 > c.join + kSpare * (int64_t)c.part) p.parts = kSpare;
+            if (!w.splits && w.tiles <= kSpare &&
+                (int64_t)w.steps * c.least / 2 > c.join + kSpare * (int64_t)c.part)
+                p.parts = kSpare;
             if (w.splits && w.splits == c.groups / w.left()) p.parts = c.groups;
             p.divided = w.tiles < p.parts / 2 ? w.tiles : p.parts / 2;
         }

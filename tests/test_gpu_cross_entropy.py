@@ -50,6 +50,7 @@ CASES = {  # tokens, width, vocabulary, ignored, reduction, scale
     "odd": (515, 200, 1003, 0.125, "mean", 0.7),
     "tiles divided along k": (130, 2048, 136, 0, "none", 1.0),
     "large tiles": (2100, 64, 6011, 0.05, "mean", 1.0),
+    "tiles divided as many do not count": (1141, 1248, 1134, 0.6, "none", 1.0),
 }
 
 
