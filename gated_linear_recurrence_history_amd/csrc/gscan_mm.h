@@ -389,10 +389,14 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
 // Tiles of 32 MI WM by 32 NI WN, a wavefront's part 32 MI x 32 NI in registers.
 // Steps of 128 bytes of k (64 bf16, 32 fp32) go from memory straight into LDS (16
 // bytes per lane, no register in between), into the half that the step before has
-// been read from.  Rows of a KC tile hold eight pieces of 16 bytes; piece c of row r
-// lies at c ^ (r % 8), so that the 16-byte reads of eight rows meet no bank twice.
-// Rows of an RC tile are k; with bf16 their pieces lie at c ^ 2 (k % 4), so that the
-// four rows of a transposed read (four k of 16 columns) do not either.
+// been read from.  The 64 banks of LDS take 16 lanes' pieces of 16 bytes at once, 32 of
+// 8 or 64 of 4.  Rows of a KC tile hold eight pieces; piece c of row r lies at c ^ (r / 2 %
+// 8), so that no two of 16 rows meet at a bank.  Rows of an RC tile are k; bf16: their
+// pieces lie at c ^ 4 (k % 4) (64 columns: 4 (k / 2 % 2)), so that the four rows of a
+// transposed read (32 lanes, 64 bytes of each) do not meet either; fp32: at c ^ 8 (k / 4 %
+// 2), as half of the wavefront reads four rows on.  No conflicts are counted, and LDS is
+// busy for a quarter of the cycles of 8192 tokens' gated products (half of them with the
+// banks taken for 32; the time, which power sets, is the same within 1 per cent).
 // Memory outside the operands is not touched: what of a tile or of the last step lies
 // outside is read from past the end of the buffer, where the hardware finds zeros.
 //
@@ -463,7 +467,7 @@ struct Tile {
     static constexpr int kLoads = T / 8 / W;               // of a wavefront
     static constexpr int kPer = 1024 / (kSz * T);          // RC: rows that one load covers
     uint32_t off[kLoads];
-    uint32_t at[RC ? 2 : 4];
+    uint32_t at[4];  // RC: of its groups of 32 columns; KC: of the quarters of a step
 
     // Load i of a lane: row (KC: of the tile, RC: k) and piece (KC: of k, RC: of the
     // tile's columns).
@@ -472,10 +476,14 @@ struct Tile {
         const int q = wave + W * i;
         return RC ? q * kPer + lane / (64 / kPer) : 8 * q + (lane >> 3);
     }
+    static __device__ __forceinline__ int swizzle(int k)
+    {
+        return !BF ? 8 * ((k >> 2) & 1) : T == 64 ? 4 * ((k >> 1) & 1) : 4 * (k & 3);
+    }
     static __device__ __forceinline__ int piece(int i, int wave, int lane)
     {
-        if constexpr (RC) return (lane % (64 / kPer)) ^ (BF ? 2 * (row(i, wave, lane) & 3) : 0);
-        else return (lane & 7) ^ (lane >> 3);
+        if constexpr (RC) return (lane % (64 / kPer)) ^ swizzle(row(i, wave, lane));
+        else return (lane & 7) ^ ((row(i, wave, lane) >> 1) & 7);
     }
 
     // `mine`: the first of the wavefront's rows (KC) or columns (RC), a multiple of 32
@@ -484,16 +492,18 @@ struct Tile {
         if constexpr (RC && BF) {
             const int p = lane & 15, g = lane >> 4;
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {  // even and odd groups of 32 columns
-                const int c = (4 * (mine / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ (2 * (p >> 2));
+            for (int o = 0; o < 4; ++o) {
+                const int c = (4 * (mine / 32 + o) + 2 * (g & 1) + ((p & 3) >> 1)) ^ swizzle(p >> 2);
                 at[o] = (uint32_t)((8 * (g >> 1) + (p >> 2)) * 2 * T + 16 * c + 8 * (p & 1));
             }
         } else if constexpr (RC) {
-            at[0] = at[1] = (uint32_t)((4 * (lane >> 5)) * 4 * T + 4 * (mine + (lane & 31)));
+#pragma unroll
+            for (int o = 0; o < 4; ++o)
+                at[o] = (uint32_t)((4 * (lane >> 5)) * 4 * T + 128 * ((mine / 32 + o) ^ (lane >> 5)) + 4 * (lane & 31));
         } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                at[s] = (uint32_t)((mine + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7)));
+                at[s] = (uint32_t)((mine + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)));
         }
     }
 
@@ -529,14 +539,14 @@ struct Tile {
     __device__ __forceinline__ Piece<BF> get(uint32_t lds, int i, int s) const
     {
         if constexpr (RC && BF) {
-            const uint32_t p = lds + at[i & 1] + (uint32_t)(s * 16 * 2 * T + 64 * (i & ~1));
+            const uint32_t p = lds + at[i] + (uint32_t)(s * 16 * 2 * T);
             const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p));
             const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(in_lds<s4v>(p + 4 * 2 * T));
             const u4 v = {__builtin_bit_cast(uint2, x).x, __builtin_bit_cast(uint2, x).y,
                           __builtin_bit_cast(uint2, y).x, __builtin_bit_cast(uint2, y).y};
             return __builtin_bit_cast(bf8, v);
         } else if constexpr (RC) {
-            const uint32_t p = lds + at[0] + (uint32_t)(s * 8 * 4 * T + 128 * i);
+            const uint32_t p = lds + at[i] + (uint32_t)(s * 8 * 4 * T);
             return f4{*in_lds<float>(p), *in_lds<float>(p + 4 * T), *in_lds<float>(p + 8 * T),
                       *in_lds<float>(p + 12 * T)};
         } else {
