@@ -6,7 +6,8 @@
 // registers in the layout of the 16 x 16 products, a good part of it requested before the
 // first product (1 kB a load; the tokens' rows come from L2 the same way, lanes past the
 // last token load nothing: R rows of the weight share them), and the eight partial sums
-// meet in LDS.
+// meet in LDS.  One token, 2048 x 2 x 5504: 11.6 us, 3.9 TB/s; 19 tokens, 2048 x 32000: 30 us, 4.4
+// TB/s (both as tiles of 128 x 64: 22 and 50, which take as long for one token as for 64).
 #pragma once
 
 #include "gscan_mm.h"

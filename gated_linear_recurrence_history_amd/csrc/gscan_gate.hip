@@ -9,6 +9,8 @@
 // Backward: the same kernel again, whose epilogue leaves da | db (in the type of
 // the operands: the one rounding between the products), then a product for dx
 // over the columns of da and db in turn, and one for both weights' gradients.
+// 8192 tokens, 2048 x 2 x 5504: forward 328 us (1128 TFLOP/s); 4109 tokens, backward: 564 us
+// (985 TFLOP/s).
 #include "gscan_few.h"
 
 namespace gscan {

@@ -21,14 +21,18 @@
 // out: a first kernel lists the others, and where some are missing their rows
 // are copied so that they follow each other.  What is in the rows left out, NaN
 // included, reaches nothing.
+//
+// The products bound all of it: 8192 tokens, 2048 x 32000, forward 916 us (1172 TFLOP/s), of
+// which the lists and joins are 21.
 #include "gscan_few.h"
 
 namespace gscan {
 namespace {
 
 constexpr int kLThreads = 1024;
-// G of a piece: 8192 tokens, 2048 x 32000: 2742 us with 128 MiB, 2667 with 256, 2677 with
-// 512; 6007 tokens, 1024 x 50021: 2207, 2109, 2015; 16384, 512 x 65000: 4455, 4526, 4082.
+// G of a piece.  Gradients of 16384 tokens with 256, 512 and 1023 MiB: 512 x 65000, 3730, 3430
+// and 3330 us; 2048 x 65000, 10830, 10580 and 10930; of 6007 tokens, 1024 x 50021, 1600, 1560
+// and 1590.
 constexpr int64_t kPieceBytes = 512ll << 20;
 constexpr int kJoinRows = 16;
 constexpr int64_t kRowGroups = 2048;  // all that are at work at once
