@@ -64,8 +64,10 @@ def test_embed_pointers(lib, table, tokens, out, code):
 
 
 def test_embed_workspace(lib):
-    for n, v, w in [(1, 10, 8), (777, 1003, 200), (16384, 32000, 2048), (16385, 32000, 64), (100, 2 ** 18, 8),
-                    (2 ** 20, 50000, 128)]:
+    for n, v, w in [(1, 10, 8), (777, 1003, 200), (2048, 2 ** 20 - 1, 512), (64, 32000, 4096)]:  # added up at once
+        assert lib.gscan_embed_workspace_bytes(ctypes.byref(embed_desc(tokens=n, vocabulary=v, width=w))) == 0
+    for n, v, w in [(1, 2 ** 20, 8), (777, 1003, 520), (16384, 32000, 2048), (16385, 32000, 64), (2049, 2 ** 18, 8),
+                    (65537, 300, 24), (2 ** 20, 50000, 128)]:
         d = embed_desc(tokens=n, vocabulary=v, width=w)
         need = lib.gscan_embed_workspace_bytes(ctypes.byref(d))
         # keys and positions, and two partial sums a chunk of at least eight tokens
