@@ -35,7 +35,7 @@ constexpr int kLThreads = 1024;
 // and 1590.
 constexpr int64_t kPieceBytes = 512ll << 20;
 constexpr int kJoinRows = 16;
-constexpr int64_t kRowGroups = 2048;  // all that are at work at once
+constexpr int kListGroups = 256;
 
 // By place among the tokens that count.
 struct Listed {
@@ -95,41 +95,71 @@ Listed lay_out(void *ws, int64_t N, int64_t V, int D, int dtype, bool backward)
     return l;
 }
 
-// Lists the tokens that count, in order.  One workgroup, 1024 ITEMS tokens at a time.
+// The workgroup's sum of a number per wavefront, and of the wavefronts before this one.
+__device__ __forceinline__ int sum_before(int32_t (&n_of)[kLThreads / 64], int own, int &all)
+{
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) n_of[wave] = own;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+    for (int w = 0; w < kLThreads / 64; ++w) {
+        before += w < wave ? n_of[w] : 0;
+        all += n_of[w];
+    }
+    return before;
+}
+
+// Lists the tokens that count, in order, 1024 ITEMS at a time; where some do not, copies
+// of the others' rows, one after the other, and zeros for the gradients of those that do
+// not.  Every workgroup goes through all targets (which costs less than a launch of its
+// own for the rows); the first one writes the list, each some of the rows.
 template <bool BWD, int ITEMS>
 __global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, Listed l)
 {
+    constexpr int kChunk = kLThreads * ITEMS, kOwn = kChunk / kListGroups;
     __shared__ int32_t n_of[kLThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int64_t done = 0;
-    for (int64_t b = 0; b < a.N; b += kLThreads * ITEMS) {
-        const int64_t i0 = b + wave * (64 * ITEMS) + lane;
+    __shared__ int32_t place[kOwn];  // of the workgroup's tokens among those that count, or -1
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, o0 = wave * (64 * ITEMS) + lane;
+    const bool first_group = blockIdx.x == 0;
+    int64_t count = 0, done = 0;
+    if (a.N > kChunk) {
+        for (int64_t b = 0; b < a.N; b += kChunk) {
+            uint32_t key[ITEMS];
+            token_keys<ITEMS>(a.target, a.target64, a.V, b + o0, a.N, key);
+            int own = 0, all;
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) own += __popcll(__ballot(key[j] < (uint32_t)a.V));
+            sum_before(n_of, own, all);
+            count += all;
+        }
+    }
+    for (int64_t b = 0; b < a.N; b += kChunk) {
         uint32_t key[ITEMS];
         float lse[ITEMS], up[ITEMS];
-        token_keys<ITEMS>(a.target, a.target64, a.V, i0, a.N, key);
-        int own = 0;
+        token_keys<ITEMS>(a.target, a.target64, a.V, b + o0, a.N, key);
+        int own = 0, all;
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
             const bool in = key[j] < (uint32_t)a.V;
-            lse[j] = BWD && in ? a.lse[i0 + 64 * j] : 0.f;
-            up[j] = BWD && in && !a.reduction ? a.dloss[i0 + 64 * j] : 0.f;
+            lse[j] = BWD && in && first_group ? a.lse[b + o0 + 64 * j] : 0.f;
+            up[j] = BWD && in && first_group && !a.reduction ? a.dloss[b + o0 + 64 * j] : 0.f;
             own += __popcll(__ballot(in));
         }
-        __syncthreads();
-        if (lane == 0) n_of[wave] = own;
-        __syncthreads();
-        int64_t first = done;
-        for (int w = 0; w < kLThreads / 64; ++w) {
-            first += w < wave ? n_of[w] : 0;
-            done += n_of[w];
-        }
+        int64_t first = done + sum_before(n_of, own, all);
+        done += all;
+        if (a.N <= kChunk) count = done;
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            const int64_t i = i0 + 64 * j;
-            const uint64_t in = __ballot(key[j] < (uint32_t)a.V);
-            const int64_t at = first + __popcll(in & ((1ull << lane) - 1));
-            first += __popcll(in);
-            if (key[j] < (uint32_t)a.V) {
+            const int64_t i = b + o0 + 64 * j;
+            const uint64_t some = __ballot(key[j] < (uint32_t)a.V);
+            const bool in = key[j] < (uint32_t)a.V;
+            const int64_t at = first + __popcll(some & ((1ull << lane) - 1));
+            first += __popcll(some);
+            if ((o0 + 64 * j) / kOwn == (int)blockIdx.x) place[(o0 + 64 * j) % kOwn] = in ? (int32_t)at : -1;
+            if (!first_group) continue;
+            if (in) {
                 l.row[at] = (int32_t)i;
                 l.target[at] = (int32_t)key[j];
                 if (BWD) l.lse[at] = lse[j];
@@ -139,30 +169,30 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, 
                 (a.reduction ? l.loss : a.loss)[i] = 0.f;
             }
         }
-    }
-    if (tid) return;
-    *l.count = (int32_t)done;
-    if (BWD && a.reduction) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
-}
-
-// Rows that count, one after the other, where some do not; gradients of those
-// that do not are zero.
-template <bool BF>
-__global__ void __launch_bounds__(256) gscan_xent_rows_kernel(XentArgs a, Listed l)
-{
-    const int64_t count = *l.count;
-    if (count == a.N) return;
-    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-        const bool copy = n < count, clear = a.dh && token_at(a.target, n, a.target64, a.V) < 0;
-        const int64_t from = copy ? l.row[n] : 0;
-        for (int c = 8 * threadIdx.x; c < a.D; c += 8 * 256) {
-            if (copy) {
-                const OctRaw<BF> x = load_oct<BF>(a.h, from * a.ldh + c);
-                *reinterpret_cast<OctRaw<BF> *>(reinterpret_cast<char *>(l.h) + (n * a.D + c) * (BF ? 2 : 4)) = x;
+        if (count == a.N) continue;
+        __syncthreads();
+        for (int r = wave; r < kOwn; r += kLThreads / 64) {
+            const int64_t i = b + (int64_t)blockIdx.x * kOwn + r;
+            if (i >= a.N) break;
+            const int64_t at = place[r];
+            for (int c = 8 * lane; c < a.D; c += 8 * 64) {
+                if (at < 0) {
+                    if (!BWD || !a.dh) break;
+                    if (a.dtype) store_oct<true>(a.dh, i * a.D + c, Oct{});
+                    else store_oct<false>(a.dh, i * a.D + c, Oct{});
+                } else if (a.dtype) {
+                    reinterpret_cast<u4 *>(l.h)[(at * a.D + c) / 8] = load_oct<true>(a.h, i * a.ldh + c).a;
+                } else {
+                    const OctRaw<false> x = load_oct<false>(a.h, i * a.ldh + c);
+                    reinterpret_cast<f4 *>(l.h)[(at * a.D + c) / 4] = x.a;
+                    reinterpret_cast<f4 *>(l.h)[(at * a.D + c) / 4 + 1] = x.b;
+                }
             }
-            if (clear) store_oct<BF>(a.dh, n * a.D + c, Oct{});
         }
     }
+    if (!first_group || tid) return;
+    *l.count = (int32_t)done;
+    if (BWD && a.reduction) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
 }
 
 // A token's partial results: 16 tokens, 16 lanes each.
@@ -252,11 +282,9 @@ hipError_t launch_list(const XentArgs &x, const Listed &l, bool backward, hipStr
 {
     auto *list = x.N <= kLThreads ? (backward ? gscan_xent_list_kernel<true, 1> : gscan_xent_list_kernel<false, 1>)
                                   : (backward ? gscan_xent_list_kernel<true, 8> : gscan_xent_list_kernel<false, 8>);
-    hipLaunchKernelGGL(list, dim3(1), dim3(kLThreads), 0, st, x, l);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !x.N) return e;
-    auto *k = x.dtype ? gscan_xent_rows_kernel<true> : gscan_xent_rows_kernel<false>;
-    hipLaunchKernelGGL(k, dim3((unsigned)(x.N < kRowGroups ? x.N : kRowGroups)), dim3(256), 0, st, x, l);
+    const int64_t own = (x.N <= kLThreads ? 1 : 8) * kLThreads / kListGroups, n = (x.N + own - 1) / own;
+    hipLaunchKernelGGL(list, dim3((unsigned)(n < 1 ? 1 : n < kListGroups ? n : kListGroups)), dim3(kLThreads), 0, st, x,
+                       l);
     return hipGetLastError();
 }
 
