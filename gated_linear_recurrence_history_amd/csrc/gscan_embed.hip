@@ -15,7 +15,7 @@
 // adds in order: no token, however frequent, is walked by one wavefront alone.
 // Sums are fp32.  Rows without a token are zeros.  Every row is written once.
 //
-// Sort, up to 65536 tokens (and 2^20 rows): every workgroup has up to 256 rows of the
+// Sort, up to 32768 tokens (and 2^20 rows): every workgroup has up to 256 rows of the
 // table, goes through all tokens, counts those of the rows before its own and sorts its
 // own by their row; it also writes its rows' zeros.  One launch for any number of
 // rows, and hardly any work for most wavefronts: they skip 64 tokens of which none is
@@ -46,8 +46,10 @@ constexpr int64_t kSBlock = kSThreads * kSItems;
 constexpr int64_t kSFew = 2048;        // tokens that are sorted and added up at once,
 constexpr int64_t kSWide = 64;         // of wide rows these,
 constexpr int kFewItems = (int)kSFew / kSThreads;
-constexpr int64_t kSSome = 65536;      // and that are sorted by one launch,
-constexpr int64_t kSRows = int64_t(1) << 20;  // of a table of fewer rows
+// and that are sorted by one launch, of a table of fewer rows, and tokens times rows: 65536 of
+// 32000 rows took 86 us (77 by digits), 32768 of 2^19 146 (139), 32768 of 2^18 95 (100), 16384
+// of 2^20 144 (163).
+constexpr int64_t kSSome = 32768, kSRows = int64_t(1) << 20, kSProduct = int64_t(1) << 34;
 constexpr int kLoadItems = 16;         // tokens that a lane requests together
 constexpr int kAlone = 32;             // few tokens: so many of a row are one wavefront's,
 constexpr int kFewAhead = 8;           // which requests so many of them together
@@ -591,7 +593,7 @@ EmbedPlan plan_embed(int64_t N, int64_t V, int D)
     EmbedPlan p;
     while (p.passes < 4 && (V >> (8 * p.passes)) != 0) ++p.passes;  // keys are 0 .. V
     while (p.chunk < 32 ? (int64_t)p.chunk * 512 < N : (int64_t)p.chunk * p.chunk * 64 < N) p.chunk *= 2;
-    p.some = N <= kSSome && V < kSRows;
+    p.some = N <= kSSome && V < kSRows && N * V < kSProduct;
     p.few = p.some && (D <= 512 ? N <= kSFew : D <= 4096 && N <= kSWide);
     // a workgroup per CU (two: 16384 tokens 38 -> 43 us); padding is row V
     const int64_t rows = (V + 256) / 256;
@@ -661,8 +663,7 @@ hipError_t launch_embed_backward(const EmbedArgs &a, hipStream_t st)
         auto *k = items <= 4    ? gscan_sort_rows_kernel<4>
                   : items <= 8  ? gscan_sort_rows_kernel<8>
                   : items <= 16 ? gscan_sort_rows_kernel<16>
-                  : items <= 32 ? gscan_sort_rows_kernel<32>
-                                : gscan_sort_rows_kernel<64>;
+                                : gscan_sort_rows_kernel<32>;
         hipLaunchKernelGGL(k, dim3((unsigned)((a.V + p.rows) / p.rows)), dim3(kSThreads), 0, st, a, p.rows, keys[0],
                            order[0]);
         if ((e = hipGetLastError()) != hipSuccess) return e;

@@ -38,7 +38,7 @@ CASES = {  # tokens, vocabulary, width
     "three digits": (20000, 2 ** 17, 8),
     "a frequent token": (70001, 3, 24),
     "many workgroups": (600001, 256, 8),
-    # up to 2048 tokens (wide rows: 64) at once, up to 65536 of fewer than 2^20 rows sorted by one launch
+    # up to 2048 tokens (wide rows: 64) at once, up to 32768 of fewer than 2^20 rows sorted by one launch
     "a wavefront's own row": (32, 1, 24),
     "a shared row": (33, 1, 24),
     "most at once": (2048, 5, 512),
@@ -47,8 +47,12 @@ CASES = {  # tokens, vocabulary, width
     "most wide rows at once": (64, 300, 4096),
     "one more wide row": (65, 300, 520),
     "wider rows": (64, 7, 4104),
-    "most in one sort": (65536, 1003, 8),
-    "one more than one sort": (65537, 1003, 8),
+    "most in one sort": (32768, 1003, 8),
+    "one more than one sort": (32769, 1003, 8),
+    "most in one sort, many rows": (32767, 2 ** 19, 8),
+    "one more than that": (32768, 2 ** 19, 8),
+    "eight workgroups' blocks": (65536, 1003, 8),
+    "one more than those": (65537, 1003, 8),
     "most rows of one sort": (3000, 2 ** 20 - 1, 8),
     "one more row": (50, 2 ** 20, 8),
 }
