@@ -23,7 +23,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .embedding import _check_tokens, _device_of, _row_stride, _rows, _type_code
+from .embedding import _check_tokens, _dense, _device_of, _row_stride, _rows, _type_code
 from .matrix_state import _check_dense, _layout, _On, _on_device, _ptr, _workspace
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
@@ -127,7 +127,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, h, weight, target, scale, reduction):
-        h, weight = _rows(h), _rows(weight)
+        h, weight, target = _rows(h), _rows(weight), _dense(target)
         loss, lse = linear_cross_entropy_forward(h, weight, target, scale, reduction)
         ctx.save_for_backward(h, weight, target, lse)
         ctx.args = (float(scale), reduction)
@@ -143,6 +143,6 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 
 
 def linear_cross_entropy(h, weight, target, scale: float = 1.0, reduction: str = "mean"):
-    """Differentiable loss; see linear_cross_entropy_forward.  h and weight that the
+    """Differentiable loss; see linear_cross_entropy_forward.  Operands that the
     library cannot read as they are, are copied."""
     return LinearCrossEntropyFunction.apply(h, weight, target, scale, reduction)

@@ -72,6 +72,12 @@ def _rows(t):
     return _readable(t if t.dim() == 2 else t.contiguous(), t)
 
 
+def _dense(t):
+    """Tokens or targets one after the other (a batch without its first or last token
+    is not); what is no tensor is left to the checks."""
+    return t.contiguous() if isinstance(t, torch.Tensor) else t
+
+
 @functools.lru_cache(maxsize=256)
 def _template(rows, dtype, other, tokens, token_dtype, vocabulary, scale):
     """The descriptor of a call, as bytes; rows: (shape, stride) of the table
@@ -154,6 +160,7 @@ class EmbedFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, table, tokens, scale, dtype):
+        tokens = _dense(tokens)
         out = embed_forward(_rows(table), tokens, scale, dtype)
         ctx.save_for_backward(tokens)
         ctx.args = (table.shape[0], float(scale), table.dtype)
@@ -169,5 +176,5 @@ class EmbedFunction(torch.autograd.Function):
 
 def embed(table, tokens, scale: float = 1.0, dtype=None):
     """Differentiable scale * table[tokens]; see embed_forward.  A table whose
-    rows are not 16-byte aligned is copied."""
+    rows are not 16-byte aligned, and tokens that are not contiguous, are copied."""
     return EmbedFunction.apply(table, tokens, scale, dtype)

@@ -256,6 +256,22 @@ def test_autograd(dtype, reduction):
     assert dh is None and torch.equal(part.grad, dw)
 
 
+def test_a_batch_without_its_first_targets():
+    h, w, target, _ = (t.to(DEV) for t in make(36, 24, 50, F32, 0.1))
+    target = target.view(4, 9)
+    leaf = h.view(4, 9, 24)[:, :-1].clone().requires_grad_()
+    loss = gs.linear_cross_entropy(leaf, w, target[:, 1:])
+    dense = target[:, 1:].contiguous()
+    want, lse = gs.linear_cross_entropy_forward(leaf.detach(), w, dense)
+    assert torch.equal(loss.detach(), want)
+    loss.backward()
+    dh, _ = gs.linear_cross_entropy_backward(leaf.detach(), w, dense, lse, torch.ones((), device=DEV),
+                                             wanted=(True, False))
+    assert torch.equal(leaf.grad, dh)
+    with pytest.raises(ValueError):
+        gs.linear_cross_entropy_forward(leaf.detach(), w, target[:, 1:])
+
+
 def test_other_stream_and_graph():
     h, w, target, _ = (t.to(DEV) for t in make(300, 136, 1003, BF, 0.2))
     d = torch.ones((), device=DEV)

@@ -176,6 +176,18 @@ def test_autograd(dtype):
     assert not frozen.requires_grad
 
 
+def test_a_batch_without_its_last_tokens():
+    gen = torch.Generator().manual_seed(7)
+    table = torch.randn(11, 16, generator=gen).to(DEV).requires_grad_()
+    t = torch.randint(0, 11, (3, 9), generator=gen).to(DEV)
+    y = gs.embed(table, t[:, :-1])
+    assert torch.equal(y, table.detach()[t[:, :-1]])
+    y.sum().backward()
+    assert torch.equal(table.grad[:, 0].long(), torch.bincount(t[:, :-1].reshape(-1), minlength=11))
+    with pytest.raises(ValueError):
+        gs.embed_forward(table.detach(), t[:, :-1])
+
+
 def test_other_stream_and_graph():
     gen = torch.Generator(device=DEV).manual_seed(7)
     t = torch.randint(0, 90, (2500,), generator=gen, device=DEV)
