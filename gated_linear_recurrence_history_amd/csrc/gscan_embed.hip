@@ -128,7 +128,9 @@ __device__ __forceinline__ void rank_items(SortLds &s, uint32_t (&item)[ITEMS], 
         const uint64_t some = __ballot(in);
         item[j] = d << 16;
         if (!some) continue;
-        const uint64_t peers = peers_of(d, some, bits);
+        // often all of them are one frequent token (32768 tokens of 32000 rows 54 -> 48 us)
+        const uint32_t d0 = __builtin_amdgcn_readlane(d, __builtin_ctzll(some));
+        const uint64_t peers = __ballot(in && d == d0) == some ? some : peers_of(d, some, bits);
         const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(peers >> 32),
                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)peers, 0u));
         uint32_t seen = 0;
