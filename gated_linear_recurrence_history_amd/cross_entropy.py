@@ -10,7 +10,9 @@ gscan_linear_cross_entropy_forward):
 
 h [..., width] and weight [vocabulary, width] (as torch.nn.Linear keeps it)
 share a type, float32 or bfloat16; the width is a multiple of 8 up to 65536,
-the vocabulary any size.  target [...]: int32 or int64, contiguous; a token
+the vocabulary any size.  Rows may lie any multiple of 16 bytes up to 2^21
+elements apart; `linear_cross_entropy` copies h or weights whose rows are further
+apart.  target [...]: int32 or int64, contiguous; a token
 whose target is outside the vocabulary (-100, say) does not count: its loss and
 lse are zero, and what its row of h holds reaches nothing.
 """
@@ -23,7 +25,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .embedding import _check_tokens, _dense, _device_of, _row_stride, _rows, _type_code
+from .embedding import _check_tokens, _dense, _device_of, _product_rows, _row_stride, _type_code
 from .matrix_state import _check_dense, _layout, _On, _on_device, _ptr, _workspace
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
@@ -127,7 +129,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, h, weight, target, scale, reduction):
-        h, weight, target = _rows(h), _rows(weight), _dense(target)
+        h, weight, target = _product_rows(h), _product_rows(weight), _dense(target)
         loss, lse = linear_cross_entropy_forward(h, weight, target, scale, reduction)
         ctx.save_for_backward(h, weight, target, lse)
         ctx.args = (float(scale), reduction)

@@ -64,12 +64,24 @@ def _device_of(t, name):
     return t.device
 
 
-def _rows(t):
+# Elements between rows, at most: of a table and its output's gradient, of the matrix products.
+_FURTHEST, _PRODUCTS_FURTHEST = 1 << 31, 1 << 21
+
+
+def _rows(t, furthest=_FURTHEST):
     """t as the library reads it: copied where its rows lie on no multiple of 16
-    bytes or at no single stride; what is no tensor is left to the checks."""
+    bytes, at no single stride or too far apart (the last token of each long sequence, or
+    a gradient that comes as such a slice); what is no tensor is left to the checks."""
     if not isinstance(t, torch.Tensor):
         return t
-    return _readable(t if t.dim() == 2 else t.contiguous(), t)
+    t = _readable(t if t.dim() == 2 else t.contiguous(), t)
+    if t.dim() == 2 and _outer_strides(*_layout(t))[0] > furthest:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _product_rows(t):
+    return _rows(t, _PRODUCTS_FURTHEST)
 
 
 def _dense(t):
@@ -176,5 +188,6 @@ class EmbedFunction(torch.autograd.Function):
 
 def embed(table, tokens, scale: float = 1.0, dtype=None):
     """Differentiable scale * table[tokens]; see embed_forward.  A table whose
-    rows are not 16-byte aligned, and tokens that are not contiguous, are copied."""
+    rows are not 16-byte aligned or more than 2^31 elements apart, and tokens that are
+    not contiguous, are copied."""
     return EmbedFunction.apply(table, tokens, scale, dtype)

@@ -10,7 +10,8 @@ it.  Argument marshalling only.
 x [..., width], w_gate, w_up [inner, width] (as torch.nn.Linear keeps them; both
 may be halves of one matrix), one type, float32 or bfloat16; width and inner
 are multiples of 8 up to 65536.  Rows may lie any multiple of 16 bytes up to
-2^21 elements apart.
+2^21 elements apart; `gated_projection` copies operands and upstream gradients
+whose rows are further apart.
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .embedding import _device_of, _row_stride, _rows, _type_code
+from .embedding import _device_of, _product_rows, _row_stride, _type_code
 from .matrix_state import _check_dense, _layout, _On, _on_device, _ptr, _workspace
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -134,7 +135,7 @@ class GatedProjectionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, activation):
-        x, w_gate, w_up = _rows(x), _rows(w_gate), _rows(w_up)
+        x, w_gate, w_up = _product_rows(x), _product_rows(w_gate), _product_rows(w_up)
         out = gated_projection_forward(x, w_gate, w_up, activation)
         ctx.save_for_backward(x, w_gate, w_up)
         ctx.activation = activation
@@ -145,7 +146,7 @@ class GatedProjectionFunction(torch.autograd.Function):
     def backward(ctx, d_out):
         x, w_gate, w_up = ctx.saved_tensors
         need = ctx.needs_input_grad
-        g = gated_projection_backward(x, w_gate, w_up, _rows(d_out.to(x.dtype)), ctx.activation,
+        g = gated_projection_backward(x, w_gate, w_up, _product_rows(d_out.to(x.dtype)), ctx.activation,
                                       (need[0], need[1] or need[2]))
         return tuple(t if n else None for t, n in zip(g, need)) + (None,)
 
