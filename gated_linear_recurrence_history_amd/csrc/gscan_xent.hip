@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kLThreads) gscan_xent_list_kernel(XentArgs a, 
     }
     if (!first_group || tid) return;
     *l.count = (int32_t)done;
-    if (BWD && a.reduction) *l.factor = a.scale * *a.dloss / (a.reduction == 2 && done ? (float)done : 1.f);
+    // (no token: sums of nothing are zero, also times a gradient that is no number)
+    if (BWD && a.reduction) *l.factor = done ? a.scale * *a.dloss / (a.reduction == 2 ? (float)done : 1.f) : 0.f;
 }
 
 // A token's partial results: 16 tokens, 16 lanes each.

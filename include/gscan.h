@@ -541,8 +541,9 @@ size_t gscan_gated_projection_backward_workspace_bytes(const gscan_gated_project
  *   lse[n] = log sum over v of exp(scale * <h_n, weight_v>)
  *   loss[n] = lse[n] - scale * <h_n, weight_target[n]>
  * A token whose target is outside 0 .. vocabulary - 1 does not count: its loss
- * and lse are zero, it has no part in any gradient (its own is zero), and
- * nothing that its row of h holds, NaN included, reaches anything.  loss is
+ * and lse are zero, it has no part in any gradient (its own is zero, and d_weight
+ * is zero where none counts, whatever d_loss is), and nothing that its row of h
+ * holds, NaN included, reaches anything.  loss is
  * fp32: [tokens] (GSCAN_LOSS_EACH), or one value, the sum over the tokens that
  * count or their mean (zero where none counts).
  * Backward: dh [tokens][width] and d_weight [vocabulary][width] (overwritten;
