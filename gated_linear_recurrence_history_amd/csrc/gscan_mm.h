@@ -116,11 +116,13 @@ __device__ __forceinline__ void store4(void *p, int64_t i, const f4 &x)
 }
 
 // (maximum, sum of powers of two relative to it) of two sets joined, logits in
-// powers of two.  An empty set is (-inf, 0).
+// powers of two.  An empty set is (-inf, 0); relative to an infinite maximum means relative
+// to zero, so that the sum is zero, infinite, or NaN if a logit is.
+__device__ __forceinline__ float lse_base(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
 __device__ __forceinline__ void join_lse(float &m, float &s, float m2, float s2)
 {
     const float top = fmaxf(m, m2);
-    const float base = top == -INFINITY ? 0.f : top;
+    const float base = lse_base(top);
     s = s * exp2_(m - base) + s2 * exp2_(m2 - base);
     m = top;
 }
@@ -254,7 +256,7 @@ __device__ __forceinline__ void epilogue(const MmArgs &a, f16v (&acc)[MI][NI], i
 #pragma unroll
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float base = top == -INFINITY ? 0.f : top;
+            const float base = lse_base(top);
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < MI; ++i)

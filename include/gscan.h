@@ -543,7 +543,8 @@ size_t gscan_gated_projection_backward_workspace_bytes(const gscan_gated_project
  * A token whose target is outside 0 .. vocabulary - 1 does not count: its loss
  * and lse are zero, it has no part in any gradient (its own is zero, and d_weight
  * is zero where none counts, whatever d_loss is), and nothing that its row of h
- * holds, NaN included, reaches anything.  loss is
+ * holds, NaN included, reaches anything.  A logit of plus infinity makes its
+ * token's lse infinite, a NaN NaN; other tokens' do not change.  loss is
  * fp32: [tokens] (GSCAN_LOSS_EACH), or one value, the sum over the tokens that
  * count or their mean (zero where none counts).
  * Backward: dh [tokens][width] and d_weight [vocabulary][width] (overwritten;
