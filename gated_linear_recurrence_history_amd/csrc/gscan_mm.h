@@ -95,26 +95,6 @@ __device__ __forceinline__ void activation(float a, int act, float &f, float &sl
     }
 }
 
-template <bool BF>
-__device__ __forceinline__ f4 load4(const void *p, int64_t i)
-{
-    if constexpr (BF) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
-        return f4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
-    } else {
-        return *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(p) + i);
-    }
-}
-template <bool BF>
-__device__ __forceinline__ void store4(void *p, int64_t i, const f4 &x)
-{
-    if constexpr (BF)
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
-            uint2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-    else
-        *reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i) = x;
-}
-
 // (maximum, sum of powers of two relative to it) of two sets joined, logits in
 // powers of two.  An empty set is (-inf, 0); relative to an infinite maximum means relative
 // to zero, so that the sum is zero, infinite, or NaN if a logit is.
@@ -172,7 +152,7 @@ __device__ __forceinline__ void store16(void *out, int64_t row, int m, const f4 
     } else {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            if (in(m + 8 * g)) store4<false>(out, row + m + 8 * g + 4 * hi, v[g]);
+            if (in(m + 8 * g)) *reinterpret_cast<f4 *>(reinterpret_cast<float *>(out) + row + m + 8 * g + 4 * hi) = v[g];
     }
 }
 
@@ -201,7 +181,8 @@ __device__ __forceinline__ void load16(const void *from, int64_t row, int m, f4 
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             v[g] = f4{};
-            if (in(m + 8 * g)) v[g] = load4<false>(from, row + m + 8 * g + 4 * hi);
+            if (in(m + 8 * g))
+                v[g] = *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(from) + row + m + 8 * g + 4 * hi);
         }
     }
 }
@@ -586,11 +567,13 @@ struct Work {
 struct MmShape {
     int m, n, groups, step, least, tile, part, join;
 };
-// 256 x 256, 128 x 128 or 128 (of m) x 64; fp32 has the latter two.
-constexpr MmShape kShapes[2][3] = {
-    {{256, 256, 256, 0, 0, 0, 0, 0}, {128, 128, 512, 4400, 2200, 3000, 37, 5000}, {128, 64, 768, 3300, 1100, 3000, 19, 5000}},
-    {{256, 256, 256, 1650, 1650, 5000, 150, 6000}, {128, 128, 512, 1050, 680, 2500, 37, 5000}, {128, 64, 768, 1170, 600, 2000, 19, 5000}},
-};
+// 0: 256 x 256 (bf16 only), 1: 128 x 128, 2: 128 (of m) x 64.
+constexpr MmShape kShapesF32[2] = {{128, 128, 512, 4400, 2200, 3000, 37, 5000}, {128, 64, 768, 3300, 1100, 3000, 19, 5000}};
+constexpr MmShape kShapesBf16[3] = {{256, 256, 256, 1650, 1650, 5000, 150, 6000},
+                                    {128, 128, 512, 1050, 680, 2500, 37, 5000},
+                                    {128, 64, 768, 1170, 600, 2000, 19, 5000}};
+constexpr int first_shape(bool bf) { return bf ? 0 : 1; }
+constexpr MmShape shape_of(bool bf, int i) { return bf ? kShapesBf16[i] : kShapesF32[i - 1]; }
 
 // ns of a step while n workgroups are at work, at most those that fit at once
 __host__ __device__ __forceinline__ int step_ns(const MmShape &c, int n)
@@ -727,7 +710,7 @@ __global__ void __launch_bounds__(64 * WM * WN, per_cu(NI, WM *WN) == 3 ? 3 : 2)
     const bool two = kTwo && a.a2;  // a second weight behind the first along k
     const int64_t part = two ? a.K1 : o.K;
     const int part_steps = (int)ceil_div(part, kStep);
-    constexpr MmShape kMine = kShapes[BF][kW == 8 ? 0 : NI == 2 ? 1 : 2];
+    constexpr MmShape kMine = shape_of(BF, kW == 8 ? 0 : NI == 2 ? 1 : 2);
     const Work work = divide_work(tm * tn, two ? 2 * part_steps : part_steps, kMine, a.parts);
 
     Tile<BF, RCA, kTA, kW> ta;
@@ -945,7 +928,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gscan_mm_join_kernel(MmArgs a
     const int i0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) / NI, j0 = kN == 1 ? 0 : (int)(blockIdx.x % kN) % NI;
     const Operands<L> o(a);
     const int tm = (int)ceil_div(a.M, kTM), tn = (int)ceil_div(o.N, kTN), d = (int)(blockIdx.x / kN);
-    constexpr MmShape kMine = kShapes[BF][WM * WN == 8 ? 0 : NI == 2 ? 1 : 2];
+    constexpr MmShape kMine = shape_of(BF, WM * WN == 8 ? 0 : NI == 2 ? 1 : 2);
     const Work work = divide_work(tm * tn, (int)steps_of(o.K, a.K1, kBK<BF>), kMine, a.parts);
     if (d >= work.left()) return;
     f16v acc[kI][kJ];
@@ -984,8 +967,8 @@ struct MmPlan {
 MmPlan plan_mm(int64_t M, int64_t N, int64_t K, int64_t K1, bool gated, bool limited, int dtype)
 {
     MmPlan best;
-    for (int i = dtype ? 0 : 1; i < 3; ++i) {
-        const MmShape &c = kShapes[dtype ? 1 : 0][i];
+    for (int i = first_shape(dtype); i < 3; ++i) {
+        const MmShape c = shape_of(dtype, i);
         MmPlan p;
         p.shape = i;
         p.work = plan_work((int)(ceil_div(M, gated ? c.m / 2 : c.m) * ceil_div(N, c.n)),
@@ -1051,7 +1034,7 @@ hipError_t launch_mm(MmArgs a, int dtype, void *partial, hipStream_t st)
 // Tiles of m: the partial results of EPI_LSE for each n.
 int64_t tiles_of_m(int64_t M, int64_t N, int64_t K, int dtype)
 {
-    return ceil_div(M, kShapes[dtype ? 1 : 0][plan_mm(M, N, K, 0, false, true, dtype).shape].m);
+    return ceil_div(M, shape_of(dtype, plan_mm(M, N, K, 0, false, true, dtype).shape).m);
 }
 
 }  // namespace
