@@ -46,9 +46,9 @@ constexpr int64_t kSBlock = kSThreads * kSItems;
 constexpr int64_t kSFew = 2048;        // tokens that are sorted and added up at once,
 constexpr int64_t kSWide = 64;         // of wide rows these,
 constexpr int kFewItems = (int)kSFew / kSThreads;
-// and that are sorted by one launch, of a table of fewer rows, and tokens times rows: 65536 of
-// 32000 rows took 86 us (77 by digits), 32768 of 2^19 146 (139), 32768 of 2^18 95 (100), 16384
-// of 2^20 144 (163).
+// and that are sorted by one launch, of a table of fewer rows, and tokens times rows.  The whole
+// gradient of 64 columns, fp32 of bf16: 65536 of 32000 rows took 86 us (77 by digits), 32768 of
+// 2^19 146 (139), 32768 of 2^18 95 (100), 16384 of 2^20 144 (163).
 constexpr int64_t kSSome = 32768, kSRows = int64_t(1) << 20, kSProduct = int64_t(1) << 34;
 constexpr int kLoadItems = 16;         // tokens that a lane requests together
 constexpr int kAlone = 32;             // few tokens: so many of a row are one wavefront's,

@@ -7,10 +7,11 @@
 // Forward: one kernel.  A tile holds the same columns of both products, so that
 // a lane has a and b of the same elements and neither reaches memory.
 // Backward: the same kernel again, whose epilogue leaves da | db (in the type of
-// the operands: the one rounding between the products), then a product for dx
-// over the columns of da and db in turn, and one for both weights' gradients.
-// 8192 tokens, 2048 x 2 x 5504: forward 328 us (1128 TFLOP/s); 4109 tokens, backward: 564 us
-// (985 TFLOP/s).
+// the operands: the one rounding between the products; unrounded they would need fp32
+// products, at a seventh of the rate), then a product for dx over the columns of da and db
+// in turn, and one for both weights' gradients.
+// 8192 tokens, 2048 x 2 x 5504: forward 325 us (1136 TFLOP/s); 4109 tokens, backward: 561 us
+// (991 TFLOP/s).
 #include "gscan_few.h"
 
 namespace gscan {

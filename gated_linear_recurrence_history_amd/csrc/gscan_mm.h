@@ -409,7 +409,9 @@ constexpr int kBK = 128 / kSize<BF>;  // k of a step
 constexpr uint32_t kNowhere = 0x7ffffff0u;  // past the end of every buffer
 
 // 64 lanes' 16 bytes at their offsets (and `more`) of the buffer, one after the other
-// from the LDS address on.  The wait for them is load_wait().
+// from the LDS address on.  The wait for them is load_wait().  (m0 is a reserved register: the
+// compiler keeps nothing in it, warns of it among the clobbers, and uses it nowhere else in
+// these kernels.)
 __device__ __forceinline__ void load_to_lds(const u4 &buffer, uint32_t offset, uint32_t more, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
@@ -563,7 +565,7 @@ struct Work {
 
 // One of the kernels' tiles, and what it takes, in ns: a step with all workgroups at
 // work, and at least; a tile besides its steps; a part's sums through memory (3.5
-// TB/s); the second kernel.  Measured at 300 to 8192 rows.
+// TB/s); the second kernel.  Measured at 300 to 8192 rows; fewer use the same figures.
 struct MmShape {
     int m, n, groups, step, least, tile, part, join;
 };
@@ -584,8 +586,9 @@ __host__ __device__ __forceinline__ int step_ns(const MmShape &c, int n)
 
 constexpr int kPartSteps = 4;   // at least so many steps to a part
 // Parts that the device may make where the host sees no reason to, as tokens that do not count
-// leave few tiles: a workgroup per CU (fp32 gradients of 1141 tokens, half of which count,
-// 1248 x 1134: SPARE).
+// leave few tiles: a workgroup per CU (fp32, 1141 tokens, half of which count, 1248 x 1134:
+// losses 66 -> 49 us, gradients 136 -> 108; where all count, 147 -> 152 by joins that find
+// nothing to do).
 constexpr int kSpare = 256;
 
 // The work with the tiles that are left divided into `parts` parts at most (tokens that

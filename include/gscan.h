@@ -551,7 +551,9 @@ size_t gscan_gated_projection_backward_workspace_bytes(const gscan_gated_project
  * either may be NULL: not wanted) for d_loss, of loss's shape, from the lse that
  * the forward left (not read for tokens that do not count).  The gradient of the
  * logits exists for a piece of the vocabulary at a time; with bf16 operands it
- * is rounded to bf16.
+ * is rounded to bf16.  The workspace holds that piece (up to 512 MiB, or 2048 columns
+ * of all tokens where that is more), a copy of h's rows and, with several pieces,
+ * dh in fp32.
  * Shapes: width a multiple of 8 up to 65536; any vocabulary >= 1 and tokens >=
  * 0, both below 2^31 - 128; vocabulary * width at most 2^40; tokens times
  * either at most 2^43; row strides up to 2^21 elements.
