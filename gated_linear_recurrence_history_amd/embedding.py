@@ -71,8 +71,9 @@ _FURTHEST, _PRODUCTS_FURTHEST = 1 << 31, 1 << 21
 def _rows(t, furthest=_FURTHEST):
     """t as the library reads it: copied where its rows lie on no multiple of 16
     bytes, at no single stride or too far apart (the last token of each long sequence, or
-    a gradient that comes as such a slice); what is no tensor is left to the checks."""
-    if not isinstance(t, torch.Tensor):
+    a gradient that comes as such a slice); what is no tensor, or has no dimension, is
+    left to the checks."""
+    if not isinstance(t, torch.Tensor) or t.dim() == 0:
         return t
     t = _readable(t if t.dim() == 2 else t.contiguous(), t)
     if t.dim() == 2 and _outer_strides(*_layout(t))[0] > furthest:

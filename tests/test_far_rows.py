@@ -39,3 +39,9 @@ def test_rows_of_the_embedding():
 def test_operands_of_other_layers_stay():
     x = rows(FAR + 8)
     assert matrix_state._readable(x, x) is x
+
+
+def test_a_number_is_refused_as_the_calls_refuse_it():
+    """No dimension at all: left to the checks, whose error it is."""
+    x = torch.tensor(1.0)
+    assert embedding._rows(x) is x

@@ -77,3 +77,11 @@ def test_upstream_gradients_that_are_slices(dtype):
     for t, g in zip((x, wg, wu), gs.gated_projection_backward(x.detach(), wg.detach(), wu.detach(),
                                                               d[:, 5].contiguous())):
         assert torch.equal(t.grad, g)
+
+
+def test_numbers_are_refused():
+    x, w, t = torch.ones((), device=DEV), torch.ones(8, 8, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    for call in (lambda: gs.embed(x, t), lambda: gs.gated_projection(x, w, w), lambda: gs.gated_projection(w, x, w),
+                 lambda: gs.linear_cross_entropy(x, w, t), lambda: gs.linear_cross_entropy(w, x, t)):
+        with pytest.raises(ValueError):
+            call()
